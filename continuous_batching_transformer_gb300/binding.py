@@ -25,6 +25,10 @@ NOALLOC_MAX_ROWS = 32
 NOALLOC_SCRATCH_BYTES = 20 << 20
 WEIGHTS_BF16, WEIGHTS_AFFINE4 = 0, 1
 DEV_OK, DEV_TOKEN_RANGE = 0, 1
+DEV_TIMEOUT, DEV_WORK_ITEM, DEV_PAGE_ID, DEV_PAGES, DEV_LENGTH, DEV_TOKENS = 2, 3, 4, 5, 6, 7
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+DTYPE_BF16, DTYPE_F32 = 0, 1
 
 # every entry point include/cbt.h declares
 EXPORTS = ["cbt_status_str", "cbt_engine_create", "cbt_engine_destroy", "cbt_slab_bytes",
@@ -35,7 +39,8 @@ EXPORTS = ["cbt_status_str", "cbt_engine_create", "cbt_engine_destroy", "cbt_sla
            "cbt_engine_timing", "cbt_greedy_head_noalloc", "cbt_kv_slab_copy_prefix",
            "cbt_kv_slab_share_prefix", "cbt_slab_bytes_kv8", "cbt_quantize_kv8",
            "cbt_slab_bytes_kvq", "cbt_quantize_kv", "cbt_engine_set_stamps", "cbt_engine_stamps",
-           "cbt_engine_test_stall"]
+           "cbt_engine_test_stall", "cbt_page_map", "cbt_rope_init", "cbt_rope_append",
+           "cbt_paged_attention", "cbt_paged_attention_workspace"]
 KCLASS_PROJ, KCLASS_ATTN, KCLASS_OTHER = 0, 1, 2
 
 
@@ -77,6 +82,50 @@ class Stats(ctypes.Structure):
                 ("slab_bytes_in_use", ctypes.c_int64), ("arena_bytes", ctypes.c_int64),
                 ("largest_free_bytes", ctypes.c_int64), ("scratch_bytes", ctypes.c_int64),
                 ("decode_steps", ctypes.c_int64), ("prefill_tokens", ctypes.c_int64)]
+
+
+class PagedKvDesc(ctypes.Structure):
+    _fields_ = [("pool", c_void), ("pool_bytes", ctypes.c_size_t), ("page_bytes", ctypes.c_int64),
+                ("k_offset", ctypes.c_int64), ("v_offset", ctypes.c_int64), ("n_pages", c_int32),
+                ("page_tokens", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32)]
+
+
+class PageMapArgs(ctypes.Structure):
+    _fields_ = [("block_table", c_void), ("max_pages", c_int32), ("page_tokens", c_int32),
+                ("n_pages", c_int32), ("rows", c_int32), ("kv_lens", c_void), ("new_lens", c_void),
+                ("free_pages", c_void), ("free_count", c_void), ("max_tokens", c_int32),
+                ("kv_lens_out", c_void), ("free_count_out", c_void), ("cu_q", c_void),
+                ("positions", c_void), ("slots", c_void), ("err", c_void)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("layout", c_int32), ("rot_dim", c_int32), ("scaling", c_int32),
+                ("original_len", c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("mscale", ctypes.c_double)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("mscale", ctypes.c_float), ("layout", c_int32),
+                ("rot_dim", c_int32), ("head_dim", c_int32)]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    _fields_ = [("kv", PagedKvDesc), ("rope", P(RopeDesc)), ("qkv", c_void), ("qkv_dtype", c_int32),
+                ("qkv_stride", ctypes.c_int64), ("tokens", c_int32), ("n_heads", c_int32),
+                ("q_gain", c_void), ("k_gain", c_void), ("eps", ctypes.c_float),
+                ("positions", c_void), ("slots", c_void), ("q_out", c_void),
+                ("q_stride", ctypes.c_int64), ("err", c_void)]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("kv", PagedKvDesc), ("block_table", c_void), ("max_pages", c_int32),
+                ("rows", c_int32), ("kv_lens", c_void), ("cu_q", c_void), ("tokens", c_int32),
+                ("max_q", c_int32), ("max_kv", c_int32), ("n_heads", c_int32), ("q", c_void),
+                ("q_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("window", c_int32),
+                ("sinks", c_int32), ("out", c_void), ("out_dtype", c_int32),
+                ("out_stride", ctypes.c_int64), ("workspace", c_void),
+                ("workspace_bytes", ctypes.c_size_t), ("err", c_void)]
 
 
 _lib = None
@@ -132,8 +181,15 @@ def lib():
         L.cbt_engine_stamps.argtypes = [c_void, c_int32, P(c_int32), c_void, c_void]
         L.cbt_engine_timing.argtypes = [c_void, c_int32, P(ctypes.c_double), P(ctypes.c_int64),
                                         P(ctypes.c_double)]
+        L.cbt_page_map.argtypes = [P(PageMapArgs), c_void]
+        L.cbt_rope_init.argtypes = [P(RopeConfig), c_int32, P(RopeDesc)]
+        L.cbt_rope_append.argtypes = [P(RopeAppendArgs), c_void]
+        L.cbt_paged_attention.argtypes = [P(PagedAttentionArgs), c_void]
+        L.cbt_paged_attention_workspace.argtypes = [P(PagedAttentionArgs)]
+        L.cbt_paged_attention_workspace.restype = ctypes.c_size_t
         for name in EXPORTS:
-            if name not in ("cbt_status_str", "cbt_slab_bytes", "cbt_slab_bytes_kv8",
+            if name not in ("cbt_paged_attention_workspace",
+                            "cbt_status_str", "cbt_slab_bytes", "cbt_slab_bytes_kv8",
                             "cbt_slab_bytes_kvq", "cbt_kernel_launches"):
                 getattr(L, name).restype = c_int32
         _lib = L
@@ -311,3 +367,26 @@ def engine_stamps(e: int, cap: int = 1024):
 
 def engine_test_stall(e: int, spin_limit: int) -> None:
     _check(lib().cbt_engine_test_stall(e, spin_limit), "cbt_engine_test_stall")
+
+
+# ---- operators on a paged KV cache (paged.py wraps them over tensors) ----------------------
+def page_map(args: PageMapArgs, stream: int = 0) -> None:
+    _check(lib().cbt_page_map(ctypes.byref(args), stream), "cbt_page_map")
+
+
+def rope_init(cfg: RopeConfig, head_dim: int) -> RopeDesc:
+    out = RopeDesc()
+    _check(lib().cbt_rope_init(ctypes.byref(cfg), head_dim, ctypes.byref(out)), "cbt_rope_init")
+    return out
+
+
+def rope_append(args: RopeAppendArgs, stream: int = 0) -> None:
+    _check(lib().cbt_rope_append(ctypes.byref(args), stream), "cbt_rope_append")
+
+
+def paged_attention(args: PagedAttentionArgs, stream: int = 0) -> None:
+    _check(lib().cbt_paged_attention(ctypes.byref(args), stream), "cbt_paged_attention")
+
+
+def paged_attention_workspace(args: PagedAttentionArgs) -> int:
+    return lib().cbt_paged_attention_workspace(ctypes.byref(args))

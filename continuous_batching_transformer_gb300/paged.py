@@ -1,0 +1,300 @@
+"""Operators on a paged KV cache, over torch tensors (see the paged section of include/cbt.h).
+
+For a model of one's own that keeps its KV cache in the engine's page layout: ``PagedKV`` describes
+a pool of pages, ``PageMap`` turns request lengths into block tables and slots, ``RopeAppend``
+normalises and rotates q and k and writes k and v into the pages, ``Attention`` reads them.  The
+handles check what they are given, borrow the tensors they were made with (which must outlive
+them) and queue their work on the current stream of the pool's device; lengths, tables and the
+free stack stay on the device, so a step can be captured in a CUDA graph.
+
+A step of one layer::
+
+    cache = PagedKV(pool, block_table, kv_lens, page_tokens=128, n_kv_heads=8, head_dim=128)
+    pages = PageMap(block_table, kv_lens, free_pages, free_count, page_tokens=128, max_tokens=8)
+    rope = Rope(128, theta=1e6)
+    append = RopeAppend(cache, rope, n_heads=32)
+    attn = Attention(cache, n_heads=32, max_kv=4096)
+    pages(new_lens)                                      # kv_lens and the free stack move on
+    append(0, qkv, pages.positions, pages.slots, q)      # qkv: [tokens, (32 + 2 * 8) * 128]
+    attn(0, q, out)                                      # one token per row
+    pages.check()                                        # synchronises; raises on device errors
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import binding as B
+
+DEV_ERRORS = {B.DEV_PAGE_ID: "page id outside the pool", B.DEV_PAGES: "too few free pages",
+              B.DEV_LENGTH: "row length out of range", B.DEV_TOKENS: "more tokens than max_tokens",
+              B.DEV_TIMEOUT: "a kernel's bounded wait ran out"}
+
+
+def page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int, n_layers: int = 1) -> int:
+    """Bytes of one page holding `n_layers` layers."""
+    return 4 * n_layers * n_kv_heads * page_tokens * head_dim
+
+
+def _tensor(t, what, dtype, device=None, dims=None):
+    """t, checked: a CUDA tensor of the type, on the device, contiguous with `dims` dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{what}: a {dtype} tensor is wanted")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{what}: is on {t.device}, not on {device or 'a GPU'}")
+    if dims is not None and (t.dim() != dims or not t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous tensor of {dims} dimensions is wanted")
+    return t
+
+
+def _rows(t, what, dtype, device, tokens, width):
+    """The row stride of t, [tokens, ...] with rows of `width` contiguous elements."""
+    _tensor(t, what, dtype, device)
+    if t.dim() < 2 or t.shape[0] != tokens or math.prod(t.shape[1:]) != width:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} is not {tokens} rows of {width}")
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != inner:
+            raise ValueError(f"{what}: rows are not contiguous (strides {t.stride()})")
+        inner *= n
+    return max(t.stride(0), width) if tokens <= 1 else t.stride(0)
+
+
+class _Device:
+    """Makes a device current for a call, and gives its current stream."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __call__(self, fn, args):
+        if torch.cuda.current_device() == self.device.index:
+            fn(args, torch.cuda.current_stream(self.device).cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                fn(args, torch.cuda.current_stream(self.device).cuda_stream)
+
+
+def _read_err(err: torch.Tensor) -> None:
+    code, info = err.tolist()
+    if code:
+        err.zero_()
+        raise B.CbtError(-10, f"paged operator: {DEV_ERRORS.get(code, code)} ({info})")
+
+
+class Rope:
+    """Rotary frequencies (cbt_rope_config).  layout "half" or "interleaved"; scaling "none",
+    "linear", "base" or "by_parts"."""
+
+    def __init__(self, head_dim: int, rot_dim: int | None = None, layout: str = "half",
+                 theta: float = 1e4, scaling: str = "none", factor: float = 1.0,
+                 original_len: int = 0, beta_fast: float = 0.0, beta_slow: float = 0.0,
+                 mscale: float = 0.0):
+        if layout not in B.ROPE_LAYOUTS or scaling not in B.ROPE_SCALINGS:
+            raise ValueError(f"layout {layout!r}, scaling {scaling!r}")
+        self.head_dim = head_dim
+        self.desc = B.rope_init(
+            B.RopeConfig(B.ROPE_LAYOUTS[layout], head_dim if rot_dim is None else rot_dim,
+                         B.ROPE_SCALINGS[scaling], original_len, theta, factor, beta_fast,
+                         beta_slow, mscale), head_dim)
+
+
+class PagedKV:
+    """A pool of pages, each holding K and V of `n_layers` layers for `page_tokens` positions.
+
+    pool         1-D contiguous bf16 or uint8 tensor, 256-byte aligned; its length gives the pages
+    block_table  int32 [rows, max_pages], kv_lens int32 [rows]: which pages a row holds and how
+                 many positions (both may be None for a cache that is only appended to by slot)
+    """
+
+    def __init__(self, pool, block_table, kv_lens, *, page_tokens: int, n_kv_heads: int,
+                 head_dim: int, n_layers: int = 1):
+        _tensor(pool, "pool", (torch.bfloat16, torch.uint8), dims=1)
+        self.device = pool.device
+        self.pool, self.block_table, self.kv_lens = pool, block_table, kv_lens
+        self.rows = 0
+        if block_table is not None or kv_lens is not None:
+            _tensor(block_table, "block_table", torch.int32, self.device, 2)
+            _tensor(kv_lens, "kv_lens", torch.int32, self.device, 1)
+            if kv_lens.shape[0] != block_table.shape[0]:
+                raise ValueError("block_table and kv_lens have different numbers of rows")
+            self.rows = block_table.shape[0]
+        self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
+        if min(page_tokens, n_kv_heads, head_dim, n_layers) <= 0:
+            raise ValueError("page_tokens, n_kv_heads, head_dim and n_layers are positive")
+        self.n_layers = n_layers
+        size = pool.numel() * pool.element_size()
+        step = page_bytes(page_tokens, n_kv_heads, head_dim, n_layers)
+        self.n_pages = size // step
+        if self.n_pages == 0:
+            raise ValueError(f"pool: {size} bytes hold no page of {step}")
+        block = step // (2 * n_layers)
+        self.layers = [B.PagedKvDesc(pool.data_ptr(), size, step, 2 * l * block, (2 * l + 1) * block,
+                                     self.n_pages, page_tokens, n_kv_heads, head_dim)
+                       for l in range(n_layers)]
+        self.err = torch.zeros(2, dtype=torch.int32, device=self.device)
+        self.call = _Device(self.device)
+
+    def check(self) -> None:
+        """Wait for the work queued on the current stream and raise if a kernel found an error."""
+        _read_err(self.err)
+
+
+class PageMap:
+    """Block tables and slot maps (cbt_page_map).
+
+    block_table, kv_lens  as in PagedKV; rewritten by every call
+    free_pages, free_count  int32 stack of free page ids and its count [1], or None, None: rows
+                 find the pages they grow into in their table already
+    n_pages      pages in the pool (ids are below it); free_pages' length where that is given
+    A call fills cu_q [rows + 1], positions and slots [max_tokens], tensors of the handle (or, at
+    construction, the caller's), which later calls overwrite."""
+
+    def __init__(self, block_table, kv_lens, free_pages, free_count, *, page_tokens: int,
+                 max_tokens: int, n_pages: int | None = None, cu_q=None, positions=None, slots=None):
+        _tensor(block_table, "block_table", torch.int32, dims=2)
+        dev = self.device = block_table.device
+        rows, max_pages = block_table.shape
+        self._vec(kv_lens, "kv_lens", rows)
+        if (free_pages is None) != (free_count is None):
+            raise ValueError("free_pages and free_count go together")
+        if free_pages is not None:
+            _tensor(free_pages, "free_pages", torch.int32, dev, 1)
+            self._vec(free_count, "free_count", 1)
+            if n_pages is not None and n_pages != free_pages.shape[0]:
+                raise ValueError("n_pages is not the length of free_pages")
+            n_pages = free_pages.shape[0]
+        if n_pages is None:
+            raise ValueError("n_pages is wanted where there is no free stack")
+        if max_tokens < 0:
+            raise ValueError("max_tokens is negative")
+
+        def new(t, what, n):
+            return torch.empty(n, dtype=torch.int32, device=dev) if t is None else self._vec(t, what, n)
+        self.cu_q = new(cu_q, "cu_q", rows + 1)
+        self.positions = new(positions, "positions", max_tokens)
+        self.slots = new(slots, "slots", max_tokens)
+        self.err = torch.zeros(2, dtype=torch.int32, device=dev)
+        self.rows = rows
+        self._keep = (block_table, kv_lens, free_pages, free_count)
+        opt = lambda t: None if t is None else t.data_ptr()
+        self.args = B.PageMapArgs(block_table.data_ptr(), max_pages, page_tokens, n_pages, rows,
+                                  kv_lens.data_ptr(), None, opt(free_pages), opt(free_count),
+                                  max_tokens, None, None, self.cu_q.data_ptr(),
+                                  self.positions.data_ptr(), self.slots.data_ptr(),
+                                  self.err.data_ptr())
+        self.call = _Device(dev)
+
+    def _vec(self, t, what, n):
+        _tensor(t, what, torch.int32, self.device, 1)
+        if t.shape[0] != n:
+            raise ValueError(f"{what}: {t.shape[0]} elements, {n} are wanted")
+        return t
+
+    def __call__(self, new_lens, kv_lens_out=None, free_count_out=None) -> None:
+        """One step: row b takes new_lens[b] more positions (negative: it retires).  The lengths
+        and the count afterwards go to kv_lens and free_count, or to the tensors given."""
+        a = self.args
+        a.new_lens = self._vec(new_lens, "new_lens", self.rows).data_ptr()
+        a.kv_lens_out = a.kv_lens if kv_lens_out is None else \
+            self._vec(kv_lens_out, "kv_lens_out", self.rows).data_ptr()
+        a.free_count_out = a.free_count if free_count_out is None else \
+            self._vec(free_count_out, "free_count_out", 1).data_ptr()
+        self.call(B.page_map, a)
+
+    def check(self) -> None:
+        _read_err(self.err)
+
+
+class RopeAppend:
+    """Per-head norm, rotary positions and KV append (cbt_rope_append).  rope None: no rotation."""
+
+    def __init__(self, cache: PagedKV, rope: Rope | None, *, n_heads: int, eps: float = 1e-6):
+        if rope is not None and rope.head_dim != cache.head_dim:
+            raise ValueError("rope and cache have different head_dim")
+        self.cache, self.rope, self.n_heads = cache, rope, n_heads
+        self.width = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim
+        self.args = B.RopeAppendArgs()
+        self.args.rope = None if rope is None else ctypes.pointer(rope.desc)
+        self.args.n_heads = n_heads
+        self.args.eps = eps
+        self.args.err = cache.err.data_ptr()
+
+    def __call__(self, layer: int, qkv, positions, slots, q_out, q_gain=None, k_gain=None) -> None:
+        """qkv [tokens, (n_heads + 2 n_kv_heads) * head_dim] bf16 or fp32, q_out [tokens, n_heads,
+        head_dim] (or two dimensions) bf16; rows may be strided.  positions and slots int32, at
+        least `tokens` long (the first `tokens` are used); gains bf16 [head_dim] or None."""
+        c, a = self.cache, self.args
+        tokens = qkv.shape[0]
+        a.kv = c.layers[layer]
+        a.qkv_stride = _rows(qkv, "qkv", (torch.bfloat16, torch.float32), c.device, tokens, self.width)
+        a.q_stride = _rows(q_out, "q_out", torch.bfloat16, c.device, tokens, self.n_heads * c.head_dim)
+        for t, what in ((positions, "positions"), (slots, "slots")):
+            if _tensor(t, what, torch.int32, c.device, 1).shape[0] < tokens:
+                raise ValueError(f"{what}: fewer than {tokens} elements")
+        for t, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+            if t is not None and _tensor(t, what, torch.bfloat16, c.device, 1).shape[0] != c.head_dim:
+                raise ValueError(f"{what}: {t.shape[0]} elements, {c.head_dim} are wanted")
+        a.qkv, a.q_out, a.tokens = qkv.data_ptr(), q_out.data_ptr(), tokens
+        a.qkv_dtype = B.DTYPE_F32 if qkv.dtype == torch.float32 else B.DTYPE_BF16
+        a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
+        a.q_gain = None if q_gain is None else q_gain.data_ptr()
+        a.k_gain = None if k_gain is None else k_gain.data_ptr()
+        c.call(B.rope_append, a)
+
+
+class Attention:
+    """Attention over the cache's pages (cbt_paged_attention), with a workspace of its own.
+
+    max_kv, max_q  upper bounds of a row's positions and query tokens
+    max_tokens     most rows of q in a call (default: the cache's rows, one token each)
+    window, sinks  0: causal; else position p sees j > p - window and j < sinks
+    Calls of one handle share its workspace: they may not overlap on the GPU (two streams, or two
+    captured graphs replayed side by side, take a handle each)."""
+
+    def __init__(self, cache: PagedKV, *, n_heads: int, max_kv: int, max_q: int = 1,
+                 max_tokens: int | None = None, window: int = 0, sinks: int = 0,
+                 scale: float | None = None):
+        if cache.block_table is None:
+            raise ValueError("the cache has no block table")
+        self.cache, self.n_heads = cache, n_heads
+        self.max_tokens = cache.rows if max_tokens is None else max_tokens
+        a = self.args = B.PagedAttentionArgs()
+        a.kv = cache.layers[0]
+        a.block_table, a.max_pages, a.rows = (cache.block_table.data_ptr(),
+                                              cache.block_table.shape[1], cache.rows)
+        a.kv_lens = cache.kv_lens.data_ptr()
+        a.tokens, a.max_q, a.max_kv, a.n_heads = self.max_tokens, max_q, max_kv, n_heads
+        a.scale = 1 / math.sqrt(cache.head_dim) if scale is None else scale
+        a.window, a.sinks = window, sinks
+        a.err = cache.err.data_ptr()
+        n = B.paged_attention_workspace(a)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+        a.workspace = self.workspace.data_ptr() if n else None
+        a.workspace_bytes = n
+
+    def __call__(self, layer: int, q, out, cu_q=None) -> None:
+        """q [tokens, n_heads, head_dim] (or two dimensions) bf16, out the same shape in bf16 or
+        fp32; rows may be strided.  cu_q int32 [rows + 1]: row b's query tokens; None: one each."""
+        c, a = self.cache, self.args
+        tokens = q.shape[0]
+        width = self.n_heads * c.head_dim
+        a.kv = c.layers[layer]
+        a.q_stride = _rows(q, "q", torch.bfloat16, c.device, tokens, width)
+        a.out_stride = _rows(out, "out", (torch.bfloat16, torch.float32), c.device, tokens, width)
+        if tokens > self.max_tokens:
+            raise ValueError(f"q: {tokens} rows, at most {self.max_tokens}")
+        if cu_q is None:
+            if tokens != c.rows:
+                raise ValueError(f"q: {tokens} rows for {c.rows} sequences and no cu_q")
+            if a.max_q != 1:
+                raise ValueError("a handle with max_q > 1 wants cu_q")
+            a.cu_q = None
+        else:
+            if _tensor(cu_q, "cu_q", torch.int32, c.device, 1).shape[0] != c.rows + 1:
+                raise ValueError(f"cu_q: {cu_q.shape[0]} elements, {c.rows + 1} are wanted")
+            a.cu_q = cu_q.data_ptr()
+        a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
+        a.out_dtype = B.DTYPE_F32 if out.dtype == torch.float32 else B.DTYPE_BF16
+        c.call(B.paged_attention, a)

@@ -74,6 +74,10 @@ typedef int32_t cbt_status;
 #define CBT_DEV_TOKEN_RANGE 1 /* a token id outside [0, vocab) */
 #define CBT_DEV_TIMEOUT 2     /* a kernel's bounded wait ran out; it stopped early (info: role) */
 #define CBT_DEV_WORK_ITEM 3   /* an attention work item its kernel cannot take (info: item) */
+#define CBT_DEV_PAGE_ID 4     /* a page id outside the pool (info: the row or token) */
+#define CBT_DEV_PAGES 5       /* too few free pages, or a free count out of range (info: missing) */
+#define CBT_DEV_LENGTH 6      /* a row's lengths are outside what the call allows (info: the row) */
+#define CBT_DEV_TOKENS 7      /* more new tokens than max_tokens (info: max_tokens) */
 
 #define CBT_WEIGHTS_BF16 0    /* bf16, row-major [out][in] */
 #define CBT_WEIGHTS_AFFINE4 1 /* 4-bit affine, see cbt_linear */
@@ -361,6 +365,203 @@ cbt_status cbt_engine_stamps(cbt_engine* e, int32_t cap, int32_t* n, int32_t* cl
  * scales, biases: device bf16 [rows][cols/group].  cols % group == 0.  Queued on `stream`. */
 cbt_status cbt_quantize_affine4(const void* w, int32_t rows, int32_t cols, int32_t group,
                                 void* packed, void* scales, void* biases, void* stream);
+
+/* ---- Operators on a caller-owned paged KV cache ------------------------------------------
+ * The parts of a step that deal with the KV cache, for callers that run a model of their own on
+ * caller-owned buffers: request lengths to block tables and slots (cbt_page_map), per-head
+ * norms, rotary positions and the append of K and V (cbt_rope_append), and attention over the
+ * pages (cbt_paged_attention).  Lengths, tables and the free stack live on the device and no
+ * call reads them on the host, so a whole step can be captured in a CUDA graph and replayed
+ * while sequences grow, join and retire.
+ *
+ * Conventions, besides those at the top of this file: all pointers are device pointers of the
+ * current device except the descriptor structs, which are read during the call only; work is
+ * queued on `stream` (cudaStream_t; NULL = legacy default) and nothing is allocated or
+ * synchronised.  `err` is a device int32 [2] the caller set to zero: the first error a kernel
+ * finds is left there as (CBT_DEV_* code, info) and stays until the caller clears it.  A call
+ * with nothing to do (rows or tokens 0) returns CBT_OK and queues nothing. */
+
+/* One layer's K and V in a pool of n_pages pages, page i at pool + i * page_bytes.  In a page, K
+ * starts at k_offset and V at v_offset bytes, each n_kv_heads blocks of page_tokens * head_dim
+ * bf16 in the layout of cbt_slab_bytes: K [position][head_dim], V [position / 64][head_dim][64].
+ * A pool whose pages are cbt_slab_bytes(cfg, page_tokens) bytes with k_offset = 2 * layer * n,
+ * v_offset = k_offset + n (n = n_kv_heads * page_tokens * head_dim * 2) is laid out as an
+ * engine's pages are.  pool, page_bytes and the offsets are multiples of 256 bytes; page_tokens
+ * is a multiple of 64; head_dim is 64 or 128; n_pages * page_tokens < 2^31 and pool_bytes <
+ * 128 * 2^31 (CBT_ERR_LIMIT); the last page's blocks end within pool_bytes. */
+typedef struct {
+  void* pool;
+  size_t pool_bytes;
+  int64_t page_bytes;
+  int64_t k_offset, v_offset;
+  int32_t n_pages, page_tokens, n_kv_heads, head_dim;
+} cbt_paged_kv;
+
+/* Block tables and slot maps from request lengths: one step's page bookkeeping on the device.
+ * Row b holds kv_lens[b] positions in pages block_table[b][0 .. ceil(kv_lens[b] / page_tokens)).
+ *   new_lens[b] > 0   the row grows by that many positions, taking the pages it lacks;
+ *   new_lens[b] == 0  the row stays as it is;
+ *   new_lens[b] < 0   the row retires: its pages return to the free stack, its length becomes 0.
+ * The free stack is free_pages[0 .. free_count[0]).  Retiring rows push their pages first, in
+ * row and then position order; growing rows then pop theirs from its top in the same order.
+ *   block_table  int32 [rows][max_pages]; entries taken are written, all others are left as
+ *                they are (a retired row's entries too).
+ *   free_pages   int32 [n_pages], or NULL: no page is taken or returned, growing rows find
+ *                every page in their table already (free_count and free_count_out are unused).
+ *   kv_lens_out, free_count_out  the lengths and the count afterwards; may be kv_lens and
+ *                free_count themselves.
+ *   cu_q         int32 [rows + 1]: exclusive prefix sums of the new tokens (row b's tokens are
+ *                [cu_q[b], cu_q[b + 1])).
+ *   positions, slots  int32 [max_tokens]: each new token's position in its row, and page id *
+ *                page_tokens + position % page_tokens.  Both are -1 past the last token; a slot
+ *                is -1 where its page id is outside [0, n_pages) (CBT_DEV_PAGE_ID, info: row).
+ * All or nothing: if a row's length is negative or would pass max_pages * page_tokens
+ * (CBT_DEV_LENGTH), the tokens pass max_tokens (CBT_DEV_TOKENS) or the stack is short or its
+ * count out of range (CBT_DEV_PAGES), then the lengths, count, table and stack stay as they
+ * were, cu_q is all zero and positions and slots are all -1, so the calls that follow find no
+ * tokens.
+ * Output arrays may not overlap anything else the call reads, but for the two named pairs.
+ * rows <= CBT_PAGE_MAP_MAX_ROWS (CBT_ERR_LIMIT); max_pages * page_tokens < 2^31 and n_pages *
+ * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_CUDA. */
+#define CBT_PAGE_MAP_MAX_ROWS 4096
+typedef struct {
+  int32_t* block_table;
+  int32_t max_pages, page_tokens, n_pages, rows;
+  const int32_t* kv_lens;
+  const int32_t* new_lens;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t max_tokens;
+  int32_t* kv_lens_out;
+  int32_t* free_count_out;
+  int32_t* cu_q;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* err;
+} cbt_page_map_args;
+cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream);
+
+/* Rotary position embedding.  Pair i < rot_dim / 2 of a head is (x[i], x[i + rot_dim / 2])
+ * (CBT_ROPE_HALF) or (x[2 i], x[2 i + 1]) (CBT_ROPE_INTERLEAVED), turned by position * f_i and
+ * multiplied by mscale; dims from rot_dim on pass through.  With u_i = theta^(-2 i / rot_dim)
+ * and s = factor:
+ *   CBT_ROPE_NONE      f_i = u_i
+ *   CBT_ROPE_LINEAR    f_i = u_i / s (positions interpolated)
+ *   CBT_ROPE_BASE      f_i = u_i with theta * s^(rot_dim / (rot_dim - 2)) for theta
+ *   CBT_ROPE_BY_PARTS  f_i = u_i (1 - r_i) + u_i / s r_i, r_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *                      lo = max(0, floor(c(beta_fast))), hi = min(rot_dim - 1, ceil(c(beta_slow))),
+ *                      c(n) = rot_dim ln(original_len / (2 pi n)) / (2 ln theta), hi taken as
+ *                      lo + 0.001 where it is not above lo: pairs that turn often over
+ *                      original_len positions keep their frequency, slow ones are interpolated
+ *                      (the published "YaRN" rule)
+ * mscale 0 stands for the form's own: 0.1 ln s + 1 by parts (s > 1), else 1.
+ * rot_dim is even, 2 <= rot_dim <= head_dim; theta > 1; factor >= 1; by parts also original_len >
+ * 0 and beta_fast > beta_slow > 0 (0, 0: 32 and 1).  CBT_ERR_INVALID otherwise. */
+#define CBT_ROPE_HALF 0
+#define CBT_ROPE_INTERLEAVED 1
+#define CBT_ROPE_NONE 0
+#define CBT_ROPE_LINEAR 1
+#define CBT_ROPE_BASE 2
+#define CBT_ROPE_BY_PARTS 3
+typedef struct {
+  int32_t layout, rot_dim, scaling, original_len;
+  double theta, factor, beta_fast, beta_slow, mscale;
+} cbt_rope_config;
+
+/* The frequencies a kernel turns by, filled on the host by cbt_rope_init: turns[i] = f_i / (2 pi)
+ * as a fraction of a turn in 64-bit fixed point, so position * turns[i] modulo 2^64 is the angle
+ * at any position without its whole turns. */
+typedef struct {
+  uint64_t turns[64];
+  float mscale;
+  int32_t layout, rot_dim, head_dim;
+} cbt_rope;
+cbt_status cbt_rope_init(const cbt_rope_config* c, int32_t head_dim, cbt_rope* out);
+
+/* Element types of the rows below */
+#define CBT_DTYPE_BF16 0
+#define CBT_DTYPE_F32 1
+
+/* Per-head norms, rotary positions and the KV append in one pass over QKV rows.  Token t's row
+ * holds n_heads q heads, n_kv_heads k heads and n_kv_heads v heads of head_dim.  Every q and k
+ * head is normalised (x / sqrt(mean(x^2) + eps) * gain, where a gain is given), then turned by
+ * positions[t]; q goes to q_out in bf16, k and v in bf16 to slot slots[t] of the cache.
+ *   qkv        bf16 or fp32 (qkv_dtype) [tokens], rows qkv_stride elements apart
+ *   q_gain, k_gain  bf16 [head_dim] or NULL (that norm is left out)
+ *   positions  int32 [tokens], >= 0 where the slot is
+ *   slots      int32 [tokens]; a token whose slot or position is negative is skipped: its q_out
+ *              row and the cache stay as they are.  A slot of n_pages * page_tokens or more is
+ *              skipped too (CBT_DEV_PAGE_ID, info: token).  Two tokens with one slot leave one
+ *              of the two there, unspecified which.
+ *   q_out      bf16 [tokens][n_heads * head_dim], rows q_stride elements apart; no overlap with qkv
+ * rope == NULL: no rotation.  Arithmetic is fp32 with one rounding to bf16 at the end.  qkv, q_out
+ * and the gains are 16-byte aligned, the strides multiples of 8 elements.  Errors: CBT_ERR_NULL,
+ * CBT_ERR_INVALID, CBT_ERR_UNSUPPORTED (head_dim), CBT_ERR_LIMIT, CBT_ERR_CUDA. */
+typedef struct {
+  cbt_paged_kv kv;
+  const cbt_rope* rope;
+  const void* qkv;
+  int32_t qkv_dtype;
+  int64_t qkv_stride;
+  int32_t tokens, n_heads;
+  const void* q_gain;
+  const void* k_gain;
+  float eps;
+  const int32_t* positions;
+  const int32_t* slots;
+  void* q_out;
+  int64_t q_stride;
+  int32_t* err;
+} cbt_rope_append_args;
+cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
+
+/* Attention over pages.  Row b has kv_lens[b] positions in the cache, the last n_b of them being
+ * its query tokens [cu_q[b], cu_q[b + 1]) (cu_q NULL: token b alone, tokens == rows).  The query at
+ * position p attends to positions j <= p with j > p - window or j < sinks (window 0: all j <= p):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j, q head h reading kv head h / (n_heads / n_kv_heads).
+ * A query that sees nothing (its row holds fewer positions than query tokens) gets zeros; out rows
+ * past cu_q[rows] are left as they are.  What masked positions hold, NaN and infinities among it,
+ * changes nothing.
+ *   block_table  int32 [rows][max_pages]
+ *   max_q, max_kv  upper bounds of n_b and kv_lens[b] that the caller vouches for: they size the
+ *                launch and the workspace.  A row above either, or with more positions than its
+ *                table, reports CBT_DEV_LENGTH; its outputs are unspecified.  So are those of a
+ *                row with a page id outside the pool among the pages it reads (CBT_DEV_PAGE_ID).
+ *   tokens       rows of q and out; a row whose cu_q range leaves [0, tokens] is skipped
+ *                (CBT_DEV_LENGTH)
+ *   q            bf16 [tokens][n_heads * head_dim], rows q_stride elements apart
+ *   out          bf16 or fp32 (out_dtype), rows out_stride elements apart; no overlap with q
+ *   workspace    cbt_paged_attention_workspace bytes, 256-byte aligned (NULL if that is 0).  Calls
+ *                that overlap on the GPU, graph replays among them, need workspaces of their own.
+ * scale is finite; window and sinks are >= 0 (sinks without a window change nothing).  Scores,
+ * softmax sums and outputs are accumulated in fp32.  A row's result does not depend on the other
+ * rows of the call.  n_heads / n_kv_heads <= 64, q and out 16-byte aligned, strides multiples of 8
+ * elements, kv.head_dim 64 or 128 (CBT_ERR_UNSUPPORTED); rows <= CBT_PAGED_ATTENTION_MAX_ROWS,
+ * max_kv + window and max_kv + sinks < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL,
+ * CBT_ERR_INVALID (a workspace that is too small among it), CBT_ERR_CUDA. */
+#define CBT_PAGED_ATTENTION_MAX_ROWS 4096
+typedef struct {
+  cbt_paged_kv kv;
+  const int32_t* block_table;
+  int32_t max_pages, rows;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int32_t tokens, max_q, max_kv, n_heads;
+  const void* q;
+  int64_t q_stride;
+  float scale;
+  int32_t window, sinks;
+  void* out;
+  int32_t out_dtype;
+  int64_t out_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* err;
+} cbt_paged_attention_args;
+cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream);
+/* Bytes of workspace the call described by a's sizes needs (pointers are not looked at); 0 where
+ * it needs none or the sizes are not supported. */
+size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
 
 /* ---- Greedy head without any allocation --------------------------------------------------
  * The pages have no counterpart to this call; it exists for callers that cannot allocate
