@@ -54,7 +54,9 @@ cbt_status attn_sizes(const cbt_paged_attention_args& a) {
   if (a.n_heads / a.kv.n_kv_heads > 64) return CBT_ERR_UNSUPPORTED;
   if (a.rows > CBT_PAGED_ATTENTION_MAX_ROWS || (int64_t)a.max_kv + a.window > INT32_MAX ||
       (int64_t)a.max_kv + a.sinks > INT32_MAX ||
-      (int64_t)a.n_heads * a.kv.head_dim > INT32_MAX / 4)
+      (int64_t)a.n_heads * a.kv.head_dim > INT32_MAX / 4 ||
+      // work items and grid dimensions stay below 2^31 and 65536
+      ((double)a.rows + a.tokens) * a.n_heads * (a.max_kv / 128.0 + 2) > (double)INT32_MAX)
     return CBT_ERR_LIMIT;
   return CBT_OK;
 }

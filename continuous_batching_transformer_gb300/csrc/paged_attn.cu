@@ -1,6 +1,6 @@
 // paged_attn.cu -- attention of ragged runs of query tokens over a paged KV cache, causal, with an
 // optional sliding window and first tokens that stay visible.
-#include "paged.h"
+#include "paged_attn.cuh"
 
 namespace {
 
@@ -71,9 +71,16 @@ __global__ void k_paged_attn(const PagedAttn a) {
 
 }  // namespace
 
-size_t paged_attn_workspace(const PagedAttn&) { return 0; }
+size_t paged_attn_workspace(const PagedAttn& a) {
+  return a.max_q == 1 ? paged_decode_workspace(a) : 0;
+}
 
 cudaError_t launch_paged_attn(const PagedAttn& a, cudaStream_t s) {
+  int dev = 0, num_sms = 0;
+  cudaError_t rc = cudaGetDevice(&dev);
+  if (rc == cudaSuccess) rc = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (rc != cudaSuccess) return rc;
+  if (a.max_q == 1) return launch_paged_decode(a, num_sms, s);
   const dim3 grid(a.tokens, (a.n_heads + 3) / 4);
   return a.kv.head_dim == 128 ? launch_pdl(k_paged_attn<128>, grid, dim3(128), 0, s, a)
                               : launch_pdl(k_paged_attn<64>, grid, dim3(128), 0, s, a);
