@@ -96,6 +96,10 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
 // {64, pair_rows, 2, K/64}, a box brings box_rows gate rows then the same up rows per block.
 bool make_tmap_kblocks(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows,
                        uint32_t nk, uint64_t pair_rows);
+// bf16 rows of `heads` heads, row_stride elements apart, as a 3-D map {head_dim, heads, tokens}: a
+// box brings 64 dims of box_heads heads of box_tokens tokens, each (token, head) a 128-byte row
+bool make_tmap_rows(CUtensorMap* m, const void* base, int head_dim, int heads, int tokens,
+                    long long row_stride, int box_heads, int box_tokens);
 // N tile for hi/lo (split) activations of n rows, and for plain bf16 activations
 int tc_split_bn(int n);
 int tc_plain_bn(int n);

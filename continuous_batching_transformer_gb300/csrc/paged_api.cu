@@ -86,6 +86,16 @@ PagedAttn attn_args(const cbt_paged_attention_args& a, const PagedKv& kv) {
   return p;
 }
 
+size_t attn_workspace(const PagedAttn& a) { return a.max_q == 1 ? paged_decode_workspace(a) : 0; }
+
+cudaError_t launch_attn(const PagedAttn& a, cudaStream_t s) {
+  if (a.max_q > 1) return launch_paged_prefill(a, s);
+  int dev = 0, num_sms = 0;
+  cudaError_t rc = cudaGetDevice(&dev);
+  if (rc == cudaSuccess) rc = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+  return rc == cudaSuccess ? launch_paged_decode(a, num_sms, s) : rc;
+}
+
 }  // namespace
 
 extern "C" cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream) {
@@ -193,7 +203,7 @@ extern "C" size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* 
   kv.page_tokens = a->kv.page_tokens;
   kv.n_kv_heads = a->kv.n_kv_heads;
   kv.head_dim = a->kv.head_dim;
-  return paged_attn_workspace(attn_args(*a, kv));
+  return attn_workspace(attn_args(*a, kv));
 }
 
 extern "C" cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream) {
@@ -210,8 +220,8 @@ extern "C" cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, voi
   if (!a->q || !a->out || !a->block_table || !a->kv_lens || !a->err) return CBT_ERR_NULL;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return CBT_ERR_INVALID;
   const PagedAttn p = attn_args(*a, kv);
-  const size_t need = paged_attn_workspace(p);
+  const size_t need = attn_workspace(p);
   if (need && !a->workspace) return CBT_ERR_NULL;
   if (need > a->workspace_bytes || !aligned(a->workspace, 256)) return CBT_ERR_INVALID;
-  return launch_paged_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
+  return launch_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
 }

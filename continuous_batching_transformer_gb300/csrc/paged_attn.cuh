@@ -90,8 +90,16 @@ CBT_D RowTokens row_tokens(const PagedAttn& a, int b) {
   return r;
 }
 
+// Visible keys among the 128 from k0 on, as 4 words of bits, for a query at position hi whose
+// window starts at lo (for a run of queries: the last one's position, the first one's window)
+CBT_D uint32_t ones_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+CBT_D void seen_bits(int k0, int hi, int lo, int sinks, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = k0 + 32 * i;
+    w[i] = ones_below(hi + 1 - b) & (~ones_below(lo - b) | ones_below(sinks - b));
+  }
+}
+
 // The pool as K rows of head_dim and as V^T rows of 64 keys (128 bytes)
 bool paged_maps(const PagedKv& kv, CUtensorMap* tk, CUtensorMap* tv);
-
-size_t paged_decode_workspace(const PagedAttn& a);
-cudaError_t launch_paged_decode(const PagedAttn& a, int num_sms, cudaStream_t s);
