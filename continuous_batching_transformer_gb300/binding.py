@@ -40,7 +40,7 @@ EXPORTS = ["cbt_status_str", "cbt_engine_create", "cbt_engine_destroy", "cbt_sla
            "cbt_kv_slab_share_prefix", "cbt_slab_bytes_kv8", "cbt_quantize_kv8",
            "cbt_slab_bytes_kvq", "cbt_quantize_kv", "cbt_engine_set_stamps", "cbt_engine_stamps",
            "cbt_engine_test_stall", "cbt_page_map", "cbt_rope_init", "cbt_rope_append",
-           "cbt_paged_attention", "cbt_paged_attention_workspace"]
+           "cbt_paged_attention", "cbt_paged_attention_workspace", "cbt_engine_set_attention"]
 KCLASS_PROJ, KCLASS_ATTN, KCLASS_OTHER = 0, 1, 2
 
 
@@ -128,6 +128,11 @@ class PagedAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("err", c_void)]
 
 
+class AttentionConfig(ctypes.Structure):
+    _fields_ = [("rope", P(RopeConfig)), ("q_norm", P(c_void)), ("k_norm", P(c_void)),
+                ("qk_norm_eps", ctypes.c_float), ("window", c_int32), ("sinks", c_int32)]
+
+
 _lib = None
 
 
@@ -181,6 +186,7 @@ def lib():
         L.cbt_engine_stamps.argtypes = [c_void, c_int32, P(c_int32), c_void, c_void]
         L.cbt_engine_timing.argtypes = [c_void, c_int32, P(ctypes.c_double), P(ctypes.c_int64),
                                         P(ctypes.c_double)]
+        L.cbt_engine_set_attention.argtypes = [c_void, P(AttentionConfig)]
         L.cbt_page_map.argtypes = [P(PageMapArgs), c_void]
         L.cbt_rope_init.argtypes = [P(RopeConfig), c_int32, P(RopeDesc)]
         L.cbt_rope_append.argtypes = [P(RopeAppendArgs), c_void]
@@ -367,6 +373,11 @@ def engine_stamps(e: int, cap: int = 1024):
 
 def engine_test_stall(e: int, spin_limit: int) -> None:
     _check(lib().cbt_engine_test_stall(e, spin_limit), "cbt_engine_test_stall")
+
+
+def engine_set_attention(e: int, cfg: AttentionConfig | None) -> None:
+    _check(lib().cbt_engine_set_attention(e, None if cfg is None else ctypes.byref(cfg)),
+           "cbt_engine_set_attention")
 
 
 # ---- operators on a paged KV cache (paged.py wraps them over tensors) ----------------------

@@ -10,6 +10,8 @@
 // capacity) to the device and then queues the whole forward pass on the engine stream.
 #include <cuda_runtime.h>
 
+#include <math.h>
+
 #include <algorithm>
 #include <atomic>
 #include <map>
@@ -21,6 +23,7 @@
 
 #include "cbt.h"
 #include "kernels.h"
+#include "paged.h"
 
 static std::atomic<long long> g_launches{0};
 long long kernel_launch_count() { return g_launches.load(); }
@@ -180,6 +183,24 @@ struct cbt_engine {
   size_t ev_used = 0;
   std::vector<TimeRec> recs;
 
+  // attention form set by cbt_engine_set_attention: the layers run the paged operators over the
+  // engine's pages.  Page ids are offsets in units of page_bytes (every extent of a bf16 paged
+  // engine is a page).  Per call the host writes the rows' page ids, lengths before the call and
+  // new tokens; k_page_map derives positions and slots on the device.
+  struct Form {
+    bool on = false;
+    cbt_rope rope;
+    std::vector<const uint16_t*> q_norm, k_norm;
+    float eps = 0.f;
+    int window = 0, sinks = 0;
+    int max_kv = 0, max_pages = 0;  // what table and ws are sized for (grown in powers of two)
+    int rows = 0, max_q = 0;        // of the call being queued
+    int32_t *table = nullptr, *lens = nullptr, *fresh = nullptr, *lens_out = nullptr;
+    int32_t *cu = nullptr, *positions = nullptr, *slots = nullptr;
+    uint8_t* ws = nullptr;
+    std::vector<int32_t> htable, hlens, hfresh;
+  } form;
+
   int qd() const { return cfg.n_heads * cfg.head_dim; }
   int kvd() const { return cfg.n_kv_heads * cfg.head_dim; }
 };
@@ -209,7 +230,7 @@ static void free_scratch(cbt_engine* e) {
                   e->rows,    e->err,      e->act_h, e->act_o, e->act_u,
                   e->items,    e->item_meta, e->att_o, e->att_ml, e->stage,
                   e->qtile,   e->ss,       e->qb,     e->pf_units, e->q4_arena, e->pagetab,
-                  e->tok_pages, e->kv8_jobs, e->q4x};
+                  e->tok_pages, e->kv8_jobs, e->q4x, e->form.table, e->form.lens, e->form.ws};
   for (void* q : ptrs)
     if (q) cudaFree(q);
 }
@@ -1203,6 +1224,220 @@ static bool tc_projection(cbt_engine* e, const CUtensorMap& wmap, const CUtensor
   return ok;
 }
 
+// ---- the attention form of cbt_engine_set_attention ------------------------------------------
+// keys the token at position pos reads
+static long long keys_seen(const cbt_engine* e, long long pos) {
+  const long long w = e->form.on ? e->form.window : 0;
+  return w && pos >= w ? w + std::min<long long>(e->form.sinks, pos + 1 - w) : pos + 1;
+}
+
+static PagedKv form_kv(const cbt_engine* e, int layer) {
+  const cbt_model_config& c = e->cfg;
+  PagedKv kv{};
+  const long long block = (long long)c.n_kv_heads * e->page * c.head_dim;
+  kv.pool = static_cast<uint16_t*>(e->p.kv_arena);
+  kv.pool_elems = (long long)(e->p.kv_arena_bytes / 2);
+  kv.page_elems = (long long)(e->page_bytes / 2);
+  kv.k_off = 2 * layer * block;
+  kv.v_off = kv.k_off + block;
+  kv.n_pages = (int)(e->p.kv_arena_bytes / e->page_bytes);
+  kv.page_tokens = e->page;
+  kv.n_kv_heads = c.n_kv_heads;
+  kv.head_dim = c.head_dim;
+  return kv;
+}
+
+static PagedAttn form_attn_args(const cbt_engine* e, int n, int layer, bool decode) {
+  const cbt_engine::Form& f = e->form;
+  PagedAttn a{};
+  a.kv = form_kv(e, layer);
+  a.table = f.table;
+  a.max_pages = f.max_pages;
+  a.rows = f.rows;
+  a.lens = f.lens_out;
+  a.cu = decode ? nullptr : f.cu;
+  a.tokens = n;
+  a.max_q = f.max_q;
+  a.max_kv = f.max_kv;
+  a.n_heads = e->cfg.n_heads;
+  a.q = e->qb;
+  a.q_ld = a.out_ld = e->qd();
+  a.scale = 1.f / sqrtf((float)e->cfg.head_dim);
+  a.window = f.window;
+  a.sinks = f.sinks;
+  a.out = e->o;
+  a.f32 = true;
+  a.ws = f.ws;
+  a.err = e->err;
+  return a;
+}
+
+static cudaError_t form_page_map(cbt_engine* e, int n) {
+  const cbt_engine::Form& f = e->form;
+  const PagedKv kv = form_kv(e, 0);
+  cbt_page_map_args a{};
+  a.block_table = f.table;
+  a.max_pages = f.max_pages;
+  a.page_tokens = kv.page_tokens;
+  a.n_pages = kv.n_pages;
+  a.rows = f.rows;
+  a.kv_lens = f.lens;
+  a.new_lens = f.fresh;
+  a.max_tokens = n;
+  a.kv_lens_out = f.lens_out;
+  a.cu_q = f.cu;
+  a.positions = f.positions;
+  a.slots = f.slots;
+  a.err = e->err;
+  return launch_page_map(a, e->stream);
+}
+
+static cudaError_t form_attention(cbt_engine* e, int n, int layer, bool decode) {
+  const cbt_engine::Form& f = e->form;
+  RopeAppend r{};
+  r.kv = form_kv(e, layer);
+  r.rope = f.rope;
+  r.qkv = e->qkv;
+  r.f32 = true;
+  r.qkv_ld = e->qd() + 2 * e->kvd();
+  r.tokens = n;
+  r.n_heads = e->cfg.n_heads;
+  r.q_gain = f.q_norm.empty() ? nullptr : f.q_norm[layer];
+  r.k_gain = f.k_norm.empty() ? nullptr : f.k_norm[layer];
+  r.eps = f.eps;
+  r.positions = f.positions;
+  r.slots = f.slots;
+  r.q_out = e->qb;
+  r.q_ld = e->qd();
+  r.err = e->err;
+  const cudaError_t rc = launch_paged_rope(r, e->stream);
+  return rc == cudaSuccess ? launch_paged_attn(form_attn_args(e, n, layer, decode), e->num_sms, e->stream)
+                           : rc;
+}
+
+// Before a call of K rows is queued: row r takes lens[r] tokens (one where lens is NULL).  Grows
+// the buffers for the longest row; the pages themselves are already there (prepare_writes).
+static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t* lens, int K) {
+  cbt_engine::Form& f = e->form;
+  const int mb = e->p.max_batch;
+  int longest = 0;
+  f.rows = K;
+  f.max_q = 1;
+  for (int r = 0; r < K; ++r) {
+    const int m = lens ? lens[r] : 1;
+    longest = std::max(longest, e->slabs[ids[r]].pos + m);
+    f.max_q = std::max(f.max_q, m);
+  }
+  cudaError_t rc = cudaSuccess;
+  if (longest > f.max_kv) {
+    long long cap = 1024;
+    while (cap < longest) cap *= 2;
+    // within what max_kv + window and max_kv + sinks may be
+    cap = std::min<long long>(cap, (long long)INT32_MAX - std::max(f.window, f.sinks));
+    if (cap < longest) return cudaErrorInvalidValue;
+    rc = cudaStreamSynchronize(e->stream);
+    drop_graphs(e);  // captured steps hold the old addresses and bounds
+    if (f.table) cudaFree(f.table);
+    if (f.ws) cudaFree(f.ws);
+    f.table = nullptr;
+    f.ws = nullptr;
+    f.max_kv = 0;
+    f.max_pages = (int)((cap + e->page - 1) / e->page);
+    if (rc == cudaSuccess)
+      rc = cudaMalloc(reinterpret_cast<void**>(&f.table), (size_t)mb * f.max_pages * sizeof(int32_t));
+    f.max_kv = (int)cap;
+    PagedAttn most = form_attn_args(e, mb, 0, true);  // a decode step of max_batch rows
+    most.rows = mb;
+    most.max_q = 1;
+    const size_t ws = paged_attn_workspace(most);
+    if (rc == cudaSuccess && ws) rc = cudaMalloc(reinterpret_cast<void**>(&f.ws), ws);
+    if (rc != cudaSuccess) {
+      f.max_kv = 0;
+      return rc;
+    }
+  }
+  f.htable.assign((size_t)K * f.max_pages, -1);
+  f.hlens.resize(K);
+  f.hfresh.resize(K);
+  for (int r = 0; r < K; ++r) {
+    const Slab& sl = e->slabs[ids[r]];
+    for (size_t p = 0; p < sl.pages.size() && p < (size_t)f.max_pages; ++p)
+      f.htable[(size_t)r * f.max_pages + p] = (int32_t)(sl.pages[p] / e->page_bytes);
+    f.hlens[r] = sl.pos;
+    f.hfresh[r] = lens ? lens[r] : 1;
+  }
+  rc = cudaMemcpyAsync(f.table, f.htable.data(), f.htable.size() * sizeof(int32_t),
+                       cudaMemcpyHostToDevice, e->stream);
+  if (rc == cudaSuccess)
+    rc = cudaMemcpyAsync(f.lens, f.hlens.data(), K * sizeof(int32_t), cudaMemcpyHostToDevice, e->stream);
+  if (rc == cudaSuccess)
+    rc = cudaMemcpyAsync(f.fresh, f.hfresh.data(), K * sizeof(int32_t), cudaMemcpyHostToDevice, e->stream);
+  return rc;
+}
+
+extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attention_config* c) {
+  if (!e) return CBT_ERR_NULL;
+  if (!e->slabs.empty()) return CBT_ERR_INVALID;
+  cbt_engine::Form& f = e->form;
+  if (!c) {
+    if (f.on) drop_graphs(e);
+    f.on = false;
+    return CBT_OK;
+  }
+  if (c->window < 0 || c->sinks < 0 || !(c->qk_norm_eps >= 0.f) || !(c->qk_norm_eps <= 3.4e38f))
+    return CBT_ERR_INVALID;
+  if (!e->page || e->quant() || !e->use_tc || e->p.max_batch > CBT_PAGED_ATTENTION_MAX_ROWS ||
+      e->cfg.n_heads / e->cfg.n_kv_heads > 64 || e->p.kv_arena_bytes >= (size_t)128 << 31 ||
+      (double)(e->p.kv_arena_bytes / e->page_bytes) * e->page > (double)INT32_MAX)
+    return CBT_ERR_UNSUPPORTED;
+  const cbt_rope_config own = {CBT_ROPE_HALF, e->cfg.head_dim, CBT_ROPE_NONE, 0, e->cfg.rope_theta,
+                               1.0, 0.0, 0.0, 0.0};
+  cbt_rope rope;
+  const cbt_status st = cbt_rope_init(c->rope ? c->rope : &own, e->cfg.head_dim, &rope);
+  if (st != CBT_OK) return st;
+  std::vector<const uint16_t*> norms[2];
+  const void* const* given[2] = {c->q_norm, c->k_norm};
+  for (int i = 0; i < 2; ++i)
+    for (int l = 0; given[i] && l < e->cfg.n_layers; ++l) {
+      if (!given[i][l]) return CBT_ERR_NULL;
+      if (reinterpret_cast<uintptr_t>(given[i][l]) & 15) return CBT_ERR_INVALID;
+      norms[i].push_back(static_cast<const uint16_t*>(given[i][l]));
+    }
+  if (!f.lens) {
+    const size_t mb = e->p.max_batch;
+    int32_t* p = nullptr;  // one allocation: lens, fresh, lens_out, cu, positions, slots
+    size_t tot = 0;
+    if (dmalloc(&p, 4 * (mb + 4) + 2 * (size_t)e->tmax, &tot) != cudaSuccess) {
+      cudaGetLastError();
+      return CBT_ERR_CUDA;
+    }
+    e->scratch_bytes += tot;
+    f.lens = p;
+    f.fresh = f.lens + mb + 4;
+    f.lens_out = f.fresh + mb + 4;
+    f.cu = f.lens_out + mb + 4;
+    f.positions = f.cu + mb + 4;
+    f.slots = f.positions + e->tmax;
+  }
+  drop_graphs(e);
+  f.on = true;
+  f.rope = rope;
+  f.q_norm = std::move(norms[0]);
+  f.k_norm = std::move(norms[1]);
+  f.eps = c->qk_norm_eps;
+  f.window = c->window;
+  f.sinks = c->sinks;
+  if (f.max_kv) {  // the workspace depends on the window: sized again by the next call
+    cudaStreamSynchronize(e->stream);
+    cudaFree(f.table);
+    if (f.ws) cudaFree(f.ws);
+    f.table = nullptr;
+    f.ws = nullptr;
+    f.max_kv = 0;
+  }
+  return CBT_OK;
+}
+
 // n tokens (decode rows or packed prefill tokens); n_out rows get logits: all n when
 // gather == false, else the n_out rows listed in e->last_idx.  total_keys = sum over the
 // tokens of (pos + 1), the KV positions attention reads per layer and kv head.
@@ -1237,6 +1472,7 @@ static cudaError_t forward(cbt_engine* e, int n, const int32_t* tokens, int max_
                     static_cast<const uint16_t*>(e->layers[0].attn_norm), fused ? e->act_h : nullptr,
                     lo, e->rows, c.head_dim, c.rope_theta, e->cosv, e->sinv, s);
   tend(e, t, 2.0 * n * d + 4.0 * n * d);
+  if (e->form.on) ok = form_page_map(e, n) == cudaSuccess;
   for (int l = 0; l < c.n_layers && ok; ++l) {
     const cbt_layer_weights& L = e->layers[l];
     const uint16_t* an = static_cast<const uint16_t*>(L.attn_norm);
@@ -1252,18 +1488,21 @@ static cudaError_t forward(cbt_engine* e, int n, const int32_t* tokens, int max_
     if (tcp)
       ok &= tc_projection(e, e->wmaps[l].qkv, e->wmaps_kb[l].qkv, e->q4w[l].qkv, &L.wqkv,
                           cbt_engine::kQ4xQkv, e->act_h, n, d, qd + 2 * kvd,
-                          fused ? (quant ? EPI_QKVQ : EPI_QKV) : EPI_STORE, e->qkv, qd + 2 * kvd, nullptr, 0, fused,
+                          fused && !e->form.on ? (quant ? EPI_QKVQ : EPI_QKV) : EPI_STORE, e->qkv, qd + 2 * kvd, nullptr, 0, fused,
                           nullptr, l);
     else
       projection(e, e->h, n, d, L.wqkv, qd + 2 * kvd, EPI_STORE, e->qkv);
     t = tbegin(e, CBT_KCLASS_ATTN);
     const bool tc_prefill = tcp && gather && e->pf_n > 0;
-    if (!fused)
+    if (!fused && !e->form.on)
       launch_rope_append(e->qkv, e->rows, n, l, c.n_heads, c.n_kv_heads, c.head_dim, e->cosv,
                          e->sinv, arena, (!gather && (tcp || quant)) ? e->qtile : nullptr,
                          tc_prefill ? e->qb : nullptr, e->qb_rows, s);
     uint8_t* arena8 = static_cast<uint8_t*>(e->p.kv_arena);
-    if (quant && !gather) {
+    if (e->form.on) {
+      ok &= form_attention(e, n, l, !gather) == cudaSuccess;
+      if (tcp) launch_f32_to_act(e->o, n, qd, e->act_o, lo, s);
+    } else if (quant && !gather) {
       // quantised KV decode: the fused QKV epilogue quantised each row's new K/V into its slab;
       // otherwise they went to the row's staging page (the RoPE kernel above) and are
       // quantised here.  Then split attention over the codes on the tensor cores and the merge
@@ -1550,7 +1789,7 @@ extern "C" cbt_status cbt_decode_step_batch(cbt_engine* e, const int32_t* ids, i
     }
     e->hslab[b] = &sl;
     max_keys = std::max(max_keys, sl.pos + 1);
-    total_keys += sl.pos + 1;
+    total_keys += keys_seen(e, sl.pos);
   }
   cudaError_t rc = cudaMemcpyAsync(e->rows, e->hrows.data(), sizeof(QueryRow) * B,
                                    cudaMemcpyHostToDevice, e->stream);
@@ -1567,7 +1806,8 @@ extern "C" cbt_status cbt_decode_step_batch(cbt_engine* e, const int32_t* ids, i
     }
     rc = upload_page_tables(e);
   }
-  if (rc == cudaSuccess && e->use_tc) rc = plan_decode_attention(e, B);
+  if (rc == cudaSuccess && e->form.on) rc = upload_form(e, ids, nullptr, B);
+  else if (rc == cudaSuccess && e->use_tc) rc = plan_decode_attention(e, B);
   if (rc == cudaSuccess && e->stamps_on) {  // begin slots to the maximum, end slots to 0
     rc = cudaMemset2DAsync(e->stamp_buf, 16, 0xFF, 8, kStampSlots, e->stream);
     if (rc == cudaSuccess)
@@ -1826,7 +2066,7 @@ static cbt_status prefill_impl(cbt_engine* e, const int32_t* ids, const int32_t*
     if ((long long)sl.pos + lens[s] > sl.cap) return CBT_ERR_CAPACITY;
     T += lens[s];
     max_keys = std::max(max_keys, sl.pos + lens[s]);
-    total_keys += (long long)lens[s] * sl.pos + (long long)lens[s] * (lens[s] + 1) / 2;
+    for (int j = 0; j < lens[s]; ++j) total_keys += keys_seen(e, sl.pos + j);
   }
   if (T > e->p.max_prefill_tokens) return CBT_ERR_TOKENS;
   std::vector<PageWrite> writes;
@@ -1858,7 +2098,8 @@ static cbt_status prefill_impl(cbt_engine* e, const int32_t* ids, const int32_t*
     rc = cudaMemcpyAsync(e->last_idx, e->hidx.data(), sizeof(int32_t) * K, cudaMemcpyHostToDevice,
                          e->stream);
   if (rc == cudaSuccess && e->page) rc = upload_page_tables(e);
-  if (rc == cudaSuccess) rc = plan_prefill_attention(e, ids, lens, K);
+  if (rc == cudaSuccess)
+    rc = e->form.on ? upload_form(e, ids, lens, K) : plan_prefill_attention(e, ids, lens, K);
   if (rc == cudaSuccess)
     rc = forward(e, (int)T, tokens, max_keys, total_keys, true, K, logits, next_tokens);
   if (rc != cudaSuccess) return rc == cudaErrorNotSupported ? CBT_ERR_UNSUPPORTED : CBT_ERR_CUDA;

@@ -54,7 +54,10 @@ struct PagedAttn {
   uint8_t* ws;
   int* err;
 };
-// one query token per row (max_q == 1), split over the cache's length; and ragged runs
+size_t paged_attn_workspace(const PagedAttn& a);
+cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s);
+// its two forms: one query token per row (max_q == 1), split over the cache's length, and ragged
+// runs of them
 size_t paged_decode_workspace(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, int num_sms, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedAttn& a, cudaStream_t s);

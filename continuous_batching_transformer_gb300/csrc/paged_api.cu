@@ -86,17 +86,20 @@ PagedAttn attn_args(const cbt_paged_attention_args& a, const PagedKv& kv) {
   return p;
 }
 
-size_t attn_workspace(const PagedAttn& a) { return a.max_q == 1 ? paged_decode_workspace(a) : 0; }
-
-cudaError_t launch_attn(const PagedAttn& a, cudaStream_t s) {
-  if (a.max_q > 1) return launch_paged_prefill(a, s);
-  int dev = 0, num_sms = 0;
-  cudaError_t rc = cudaGetDevice(&dev);
-  if (rc == cudaSuccess) rc = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
-  return rc == cudaSuccess ? launch_paged_decode(a, num_sms, s) : rc;
+// SMs of the current device
+cudaError_t sm_count(int* n) {
+  int dev = 0;
+  const cudaError_t rc = cudaGetDevice(&dev);
+  return rc == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : rc;
 }
 
 }  // namespace
+
+size_t paged_attn_workspace(const PagedAttn& a) { return a.max_q == 1 ? paged_decode_workspace(a) : 0; }
+
+cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s) {
+  return a.max_q > 1 ? launch_paged_prefill(a, s) : launch_paged_decode(a, num_sms, s);
+}
 
 extern "C" cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream) {
   if (!a) return CBT_ERR_NULL;
@@ -203,7 +206,7 @@ extern "C" size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* 
   kv.page_tokens = a->kv.page_tokens;
   kv.n_kv_heads = a->kv.n_kv_heads;
   kv.head_dim = a->kv.head_dim;
-  return attn_workspace(attn_args(*a, kv));
+  return paged_attn_workspace(attn_args(*a, kv));
 }
 
 extern "C" cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream) {
@@ -220,8 +223,11 @@ extern "C" cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, voi
   if (!a->q || !a->out || !a->block_table || !a->kv_lens || !a->err) return CBT_ERR_NULL;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return CBT_ERR_INVALID;
   const PagedAttn p = attn_args(*a, kv);
-  const size_t need = attn_workspace(p);
+  const size_t need = paged_attn_workspace(p);
   if (need && !a->workspace) return CBT_ERR_NULL;
   if (need > a->workspace_bytes || !aligned(a->workspace, 256)) return CBT_ERR_INVALID;
-  return launch_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != cudaSuccess) return CBT_ERR_CUDA;
+  return launch_paged_attn(p, num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK
+                                                                                         : CBT_ERR_CUDA;
 }

@@ -547,6 +547,7 @@ template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn& a, int num_sms,
                       cudaStream_t s) {
   const Layout lay = layout_of(a);
+  if (lay.max_runs > 1 && !a.ws) return cudaErrorInvalidValue;
   const size_t n = (size_t)a.rows * a.n_heads * lay.max_runs;
   float* po = reinterpret_cast<float*>(a.ws);
   float2* pml = reinterpret_cast<float2*>(a.ws + n * HD * sizeof(float));

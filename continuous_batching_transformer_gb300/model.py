@@ -15,6 +15,7 @@ import synth
 from synth.recipes import ModelShape
 
 from . import binding as B
+from .paged import Rope
 
 
 def config_struct(shape: ModelShape) -> B.ModelConfig:
@@ -106,6 +107,27 @@ class Engine:
         self.handle = B.engine_create(weights.cfg, weights.struct, params)
         self.max_batch = max_batch
         self.max_prefill_tokens = max_prefill_tokens
+
+    def set_attention(self, rope: Rope | None = None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                      window: int = 0, sinks: int = 0) -> None:
+        """The attention form of the layers from now on (cbt_engine_set_attention): rotary form,
+        per-head q and k norms (per layer a bf16 [head_dim] gain, or None), sliding window and
+        first positions that stay visible.  Paged bf16 engines, before any slab exists."""
+        L, hd = self.shape.n_layers, self.shape.head_dim
+        norms = []
+        for g in (q_norm, k_norm):
+            g = None if g is None else list(g)
+            for t in g or ():
+                if t.dtype != torch.bfloat16 or t.device != self.arena.device or t.shape != (hd,) or \
+                        not t.is_contiguous():
+                    raise ValueError(f"norm gains: bf16 [{hd}] tensors on {self.arena.device} are wanted")
+            if g is not None and len(g) != L:
+                raise ValueError(f"norm gains: {len(g)} of them for {L} layers")
+            norms.append(g)
+        arrays = [(ctypes.c_void_p * L)(*[t.data_ptr() for t in g]) if g else None for g in norms]
+        B.engine_set_attention(self.handle, B.AttentionConfig(
+            None if rope is None else ctypes.pointer(rope.config), *arrays, eps, window, sinks))
+        self._norms = norms  # the engine borrows the gains
 
     def close(self):
         if self.handle:

@@ -94,10 +94,10 @@ class Rope:
         if layout not in B.ROPE_LAYOUTS or scaling not in B.ROPE_SCALINGS:
             raise ValueError(f"layout {layout!r}, scaling {scaling!r}")
         self.head_dim = head_dim
-        self.desc = B.rope_init(
-            B.RopeConfig(B.ROPE_LAYOUTS[layout], head_dim if rot_dim is None else rot_dim,
-                         B.ROPE_SCALINGS[scaling], original_len, theta, factor, beta_fast,
-                         beta_slow, mscale), head_dim)
+        self.config = B.RopeConfig(B.ROPE_LAYOUTS[layout], head_dim if rot_dim is None else rot_dim,
+                                   B.ROPE_SCALINGS[scaling], original_len, theta, factor, beta_fast,
+                                   beta_slow, mscale)
+        self.desc = B.rope_init(self.config, head_dim)
 
 
 class PagedKV:

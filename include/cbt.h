@@ -372,7 +372,8 @@ cbt_status cbt_quantize_affine4(const void* w, int32_t rows, int32_t cols, int32
  * norms, rotary positions and the append of K and V (cbt_rope_append), and attention over the
  * pages (cbt_paged_attention).  Lengths, tables and the free stack live on the device and no
  * call reads them on the host, so a whole step can be captured in a CUDA graph and replayed
- * while sequences grow, join and retire.
+ * while sequences grow, join and retire.  An engine's own steps take the same rotary forms, norms,
+ * window and sinks through cbt_engine_set_attention, which runs these operators.
  *
  * Conventions, besides those at the top of this file: all pointers are device pointers of the
  * current device except the descriptor structs, which are read during the call only; work is
@@ -562,6 +563,27 @@ cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream);
 /* Bytes of workspace the call described by a's sizes needs (pointers are not looked at); 0 where
  * it needs none or the sizes are not supported. */
 size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
+
+/* The attention form of an engine's layers.  From now on every prefill and decode step of the
+ * engine normalises q and k per head, rotates them, appends K and V and attends as cbt_rope_append
+ * and cbt_paged_attention do, over the engine's own pages; NULL returns it to its built-in form
+ * (no norms, half rotation of the whole head by rope_theta, all earlier positions seen).
+ *   rope    rotary form (copied); NULL: the built-in one
+ *   q_norm, k_norm  host arrays [n_layers] of device bf16 [head_dim] gains (the array is copied,
+ *           the gains are borrowed), or NULL: that norm is left out
+ *   window, sinks  as in cbt_paged_attention
+ * q is rounded to bf16 for the attention.  Pages behind the window stay held.  Only before slabs
+ * exist (CBT_ERR_INVALID otherwise).  Needs a paged engine (kv_page_tokens > 0) with bf16 KV on the
+ * tensor-core path, max_batch <= CBT_PAGED_ATTENTION_MAX_ROWS and n_heads / n_kv_heads <= 64
+ * (CBT_ERR_UNSUPPORTED).  Errors leave the engine's form as it was. */
+typedef struct {
+  const cbt_rope_config* rope;
+  const void* const* q_norm;
+  const void* const* k_norm;
+  float qk_norm_eps;
+  int32_t window, sinks;
+} cbt_attention_config;
+cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attention_config* c);
 
 /* ---- Greedy head without any allocation --------------------------------------------------
  * The pages have no counterpart to this call; it exists for callers that cannot allocate

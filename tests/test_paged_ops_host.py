@@ -187,3 +187,9 @@ def test_handles_refuse_host_tensors():
     with pytest.raises(B.CbtError):
         paged.Rope(128, rot_dim=7)
     assert paged.page_bytes(128, 8, 128, 32) == 2 * 32 * 8 * 128 * 128 * 2
+
+
+def test_set_attention_refuses_a_null_engine(lib):
+    assert lib.cbt_engine_set_attention(None, None) == -2
+    c = B.AttentionConfig()
+    assert lib.cbt_engine_set_attention(None, ctypes.byref(c)) == -2
