@@ -382,7 +382,7 @@ def engine_set_attention(e: int, cfg: AttentionConfig | None) -> None:
 
 # ---- operators on a paged KV cache (paged.py wraps them over tensors) ----------------------
 def page_map(args: PageMapArgs, stream: int = 0) -> None:
-    _check(lib().cbt_page_map(ctypes.byref(args), stream), "cbt_page_map")
+    _check(lib().cbt_page_map(args, stream), "cbt_page_map")
 
 
 def rope_init(cfg: RopeConfig, head_dim: int) -> RopeDesc:
@@ -392,11 +392,11 @@ def rope_init(cfg: RopeConfig, head_dim: int) -> RopeDesc:
 
 
 def rope_append(args: RopeAppendArgs, stream: int = 0) -> None:
-    _check(lib().cbt_rope_append(ctypes.byref(args), stream), "cbt_rope_append")
+    _check(lib().cbt_rope_append(args, stream), "cbt_rope_append")
 
 
 def paged_attention(args: PagedAttentionArgs, stream: int = 0) -> None:
-    _check(lib().cbt_paged_attention(ctypes.byref(args), stream), "cbt_paged_attention")
+    _check(lib().cbt_paged_attention(args, stream), "cbt_paged_attention")
 
 
 def paged_attention_workspace(args: PagedAttentionArgs) -> int:

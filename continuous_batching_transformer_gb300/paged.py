@@ -38,42 +38,68 @@ def page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int, n_layers: int =
     return 4 * n_layers * n_kv_heads * page_tokens * head_dim
 
 
-def _tensor(t, what, dtype, device=None, dims=None):
-    """t, checked: a CUDA tensor of the type, on the device, contiguous with `dims` dimensions."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{what}: a {dtype} tensor is wanted")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{what}: is on {t.device}, not on {device or 'a GPU'}")
-    if dims is not None and (t.dim() != dims or not t.is_contiguous()):
-        raise ValueError(f"{what}: a contiguous tensor of {dims} dimensions is wanted")
+def _bad(t, what, dtypes, index, dims=None):
+    """Raises what is wrong with t."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{what}: a tensor of {' or '.join(map(str, dtypes))} is wanted")
+    if t.get_device() < 0 or (index is not None and t.get_device() != index):
+        raise ValueError(f"{what}: is on {t.device}, not on {'a GPU' if index is None else f'cuda:{index}'}")
+    raise ValueError(f"{what}: a contiguous tensor of {dims} dimensions is wanted, not one of shape "
+                     f"{tuple(t.shape)} and strides {t.stride()}")
+
+
+def _tensor(t, what, dtypes, index=None, dims=None):
+    """t, checked: a tensor of one of the types, on GPU `index` (None: any), contiguous with `dims`
+    dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() < 0 or \
+            (index is not None and t.get_device() != index) or \
+            (dims is not None and (t.dim() != dims or not t.is_contiguous())):
+        _bad(t, what, dtypes, index, dims)
     return t
 
 
-def _rows(t, what, dtype, device, tokens, width):
+def _vec(t, what, index, n=None):
+    """t's address: a contiguous int32 vector on GPU `index`, of n elements where n is given."""
+    if t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 1 or not t.is_contiguous():
+        _bad(t, what, _I32, index, 1)
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{what}: {t.numel()} elements, {n} are wanted")
+    return t.data_ptr()
+
+
+def _rows(t, what, dtypes, index, tokens, width):
     """The row stride of t, [tokens, ...] with rows of `width` contiguous elements."""
-    _tensor(t, what, dtype, device)
-    if t.dim() < 2 or t.shape[0] != tokens or math.prod(t.shape[1:]) != width:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} is not {tokens} rows of {width}")
+    if t.dtype not in dtypes or t.get_device() != index:
+        _bad(t, what, dtypes, index)
+    shape = t.shape
+    if t.is_contiguous() and len(shape) >= 2 and shape[0] == tokens and t.numel() == tokens * width:
+        return width
+    if len(shape) < 2 or shape[0] != tokens or math.prod(shape[1:]) != width:
+        raise ValueError(f"{what}: shape {tuple(shape)} is not {tokens} rows of {width}")
     inner = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if n > 1 and s != inner:
             raise ValueError(f"{what}: rows are not contiguous (strides {t.stride()})")
         inner *= n
     return max(t.stride(0), width) if tokens <= 1 else t.stride(0)
 
 
-class _Device:
-    """Makes a device current for a call, and gives its current stream."""
+_I32, _BF16, _ROWS = (torch.int32,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
 
-    def __init__(self, device):
-        self.device = device
+
+class _Device:
+    """Queues a call on a device's current stream, with that device current."""
+
+    def __init__(self, index):
+        self.index = index
 
     def __call__(self, fn, args):
-        if torch.cuda.current_device() == self.device.index:
-            fn(args, torch.cuda.current_stream(self.device).cuda_stream)
+        # the stream's handle alone: torch.cuda.current_stream builds an object around it (1 us)
+        if torch.cuda.current_device() == self.index:
+            fn(args, torch._C._cuda_getCurrentRawStream(self.index))
         else:
-            with torch.cuda.device(self.device):
-                fn(args, torch.cuda.current_stream(self.device).cuda_stream)
+            with torch.cuda.device(self.index):
+                fn(args, torch._C._cuda_getCurrentRawStream(self.index))
 
 
 def _read_err(err: torch.Tensor) -> None:
@@ -112,11 +138,12 @@ class PagedKV:
                  head_dim: int, n_layers: int = 1):
         _tensor(pool, "pool", (torch.bfloat16, torch.uint8), dims=1)
         self.device = pool.device
+        self.index = pool.get_device()
         self.pool, self.block_table, self.kv_lens = pool, block_table, kv_lens
         self.rows = 0
         if block_table is not None or kv_lens is not None:
-            _tensor(block_table, "block_table", torch.int32, self.device, 2)
-            _tensor(kv_lens, "kv_lens", torch.int32, self.device, 1)
+            _tensor(block_table, "block_table", _I32, self.index, 2)
+            _tensor(kv_lens, "kv_lens", _I32, self.index, 1)
             if kv_lens.shape[0] != block_table.shape[0]:
                 raise ValueError("block_table and kv_lens have different numbers of rows")
             self.rows = block_table.shape[0]
@@ -134,7 +161,7 @@ class PagedKV:
                                      self.n_pages, page_tokens, n_kv_heads, head_dim)
                        for l in range(n_layers)]
         self.err = torch.zeros(2, dtype=torch.int32, device=self.device)
-        self.call = _Device(self.device)
+        self.call = _Device(self.index)
 
     def check(self) -> None:
         """Wait for the work queued on the current stream and raise if a kernel found an error."""
@@ -153,15 +180,15 @@ class PageMap:
 
     def __init__(self, block_table, kv_lens, free_pages, free_count, *, page_tokens: int,
                  max_tokens: int, n_pages: int | None = None, cu_q=None, positions=None, slots=None):
-        _tensor(block_table, "block_table", torch.int32, dims=2)
-        dev = self.device = block_table.device
+        _tensor(block_table, "block_table", _I32, dims=2)
+        self.index = block_table.get_device()
         rows, max_pages = block_table.shape
-        self._vec(kv_lens, "kv_lens", rows)
+        _vec(_tensor(kv_lens, "kv_lens", _I32, self.index), "kv_lens", self.index, rows)
         if (free_pages is None) != (free_count is None):
             raise ValueError("free_pages and free_count go together")
         if free_pages is not None:
-            _tensor(free_pages, "free_pages", torch.int32, dev, 1)
-            self._vec(free_count, "free_count", 1)
+            _tensor(free_pages, "free_pages", _I32, self.index, 1)
+            _vec(_tensor(free_count, "free_count", _I32, self.index), "free_count", self.index, 1)
             if n_pages is not None and n_pages != free_pages.shape[0]:
                 raise ValueError("n_pages is not the length of free_pages")
             n_pages = free_pages.shape[0]
@@ -171,11 +198,14 @@ class PageMap:
             raise ValueError("max_tokens is negative")
 
         def new(t, what, n):
-            return torch.empty(n, dtype=torch.int32, device=dev) if t is None else self._vec(t, what, n)
+            if t is None:
+                return torch.empty(n, dtype=torch.int32, device=block_table.device)
+            _vec(_tensor(t, what, _I32, self.index), what, self.index, n)
+            return t
         self.cu_q = new(cu_q, "cu_q", rows + 1)
         self.positions = new(positions, "positions", max_tokens)
         self.slots = new(slots, "slots", max_tokens)
-        self.err = torch.zeros(2, dtype=torch.int32, device=dev)
+        self.err = torch.zeros(2, dtype=torch.int32, device=block_table.device)
         self.rows = rows
         self._keep = (block_table, kv_lens, free_pages, free_count)
         opt = lambda t: None if t is None else t.data_ptr()
@@ -184,23 +214,17 @@ class PageMap:
                                   max_tokens, None, None, self.cu_q.data_ptr(),
                                   self.positions.data_ptr(), self.slots.data_ptr(),
                                   self.err.data_ptr())
-        self.call = _Device(dev)
-
-    def _vec(self, t, what, n):
-        _tensor(t, what, torch.int32, self.device, 1)
-        if t.shape[0] != n:
-            raise ValueError(f"{what}: {t.shape[0]} elements, {n} are wanted")
-        return t
+        self.call = _Device(self.index)
 
     def __call__(self, new_lens, kv_lens_out=None, free_count_out=None) -> None:
         """One step: row b takes new_lens[b] more positions (negative: it retires).  The lengths
         and the count afterwards go to kv_lens and free_count, or to the tensors given."""
-        a = self.args
-        a.new_lens = self._vec(new_lens, "new_lens", self.rows).data_ptr()
+        a, dev = self.args, self.index
+        a.new_lens = _vec(new_lens, "new_lens", dev, self.rows)
         a.kv_lens_out = a.kv_lens if kv_lens_out is None else \
-            self._vec(kv_lens_out, "kv_lens_out", self.rows).data_ptr()
+            _vec(kv_lens_out, "kv_lens_out", dev, self.rows)
         a.free_count_out = a.free_count if free_count_out is None else \
-            self._vec(free_count_out, "free_count_out", 1).data_ptr()
+            _vec(free_count_out, "free_count_out", dev, 1)
         self.call(B.page_map, a)
 
     def check(self) -> None:
@@ -215,6 +239,8 @@ class RopeAppend:
             raise ValueError("rope and cache have different head_dim")
         self.cache, self.rope, self.n_heads = cache, rope, n_heads
         self.width = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim
+        self.q_width = n_heads * cache.head_dim
+        self._layer = None
         self.args = B.RopeAppendArgs()
         self.args.rope = None if rope is None else ctypes.pointer(rope.desc)
         self.args.n_heads = n_heads
@@ -226,22 +252,27 @@ class RopeAppend:
         head_dim] (or two dimensions) bf16; rows may be strided.  positions and slots int32, at
         least `tokens` long (the first `tokens` are used); gains bf16 [head_dim] or None."""
         c, a = self.cache, self.args
-        tokens = qkv.shape[0]
-        a.kv = c.layers[layer]
-        a.qkv_stride = _rows(qkv, "qkv", (torch.bfloat16, torch.float32), c.device, tokens, self.width)
-        a.q_stride = _rows(q_out, "q_out", torch.bfloat16, c.device, tokens, self.n_heads * c.head_dim)
-        for t, what in ((positions, "positions"), (slots, "slots")):
-            if _tensor(t, what, torch.int32, c.device, 1).shape[0] < tokens:
-                raise ValueError(f"{what}: fewer than {tokens} elements")
-        for t, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-            if t is not None and _tensor(t, what, torch.bfloat16, c.device, 1).shape[0] != c.head_dim:
-                raise ValueError(f"{what}: {t.shape[0]} elements, {c.head_dim} are wanted")
-        a.qkv, a.q_out, a.tokens = qkv.data_ptr(), q_out.data_ptr(), tokens
-        a.qkv_dtype = B.DTYPE_F32 if qkv.dtype == torch.float32 else B.DTYPE_BF16
-        a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
-        a.q_gain = None if q_gain is None else q_gain.data_ptr()
-        a.k_gain = None if k_gain is None else k_gain.data_ptr()
+        dev = c.index
+        a.tokens = tokens = qkv.shape[0]
+        if layer != self._layer:
+            a.kv = c.layers[layer]
+            self._layer = layer
+        a.qkv_stride = _rows(qkv, "qkv", _ROWS, dev, tokens, self.width)
+        a.q_stride = _rows(q_out, "q_out", _BF16, dev, tokens, self.q_width)
+        a.positions = _vec(positions, "positions", dev)
+        a.slots = _vec(slots, "slots", dev)
+        if positions.numel() < tokens or slots.numel() < tokens:
+            raise ValueError(f"positions and slots: fewer than {tokens} elements")
+        a.q_gain = None if q_gain is None else self._gain(q_gain, "q_gain")
+        a.k_gain = None if k_gain is None else self._gain(k_gain, "k_gain")
+        a.qkv, a.q_out = qkv.data_ptr(), q_out.data_ptr()
+        a.qkv_dtype = B.DTYPE_F32 if qkv.dtype is torch.float32 else B.DTYPE_BF16
         c.call(B.rope_append, a)
+
+    def _gain(self, t, what):
+        if _tensor(t, what, _BF16, self.cache.index, 1).numel() != self.cache.head_dim:
+            raise ValueError(f"{what}: {t.numel()} elements, {self.cache.head_dim} are wanted")
+        return t.data_ptr()
 
 
 class Attention:
@@ -259,6 +290,8 @@ class Attention:
         if cache.block_table is None:
             raise ValueError("the cache has no block table")
         self.cache, self.n_heads = cache, n_heads
+        self.width = n_heads * cache.head_dim
+        self._layer = None
         self.max_tokens = cache.rows if max_tokens is None else max_tokens
         a = self.args = B.PagedAttentionArgs()
         a.kv = cache.layers[0]
@@ -278,11 +311,13 @@ class Attention:
         """q [tokens, n_heads, head_dim] (or two dimensions) bf16, out the same shape in bf16 or
         fp32; rows may be strided.  cu_q int32 [rows + 1]: row b's query tokens; None: one each."""
         c, a = self.cache, self.args
+        dev = c.index
         tokens = q.shape[0]
-        width = self.n_heads * c.head_dim
-        a.kv = c.layers[layer]
-        a.q_stride = _rows(q, "q", torch.bfloat16, c.device, tokens, width)
-        a.out_stride = _rows(out, "out", (torch.bfloat16, torch.float32), c.device, tokens, width)
+        if layer != self._layer:
+            a.kv = c.layers[layer]
+            self._layer = layer
+        a.q_stride = _rows(q, "q", _BF16, dev, tokens, self.width)
+        a.out_stride = _rows(out, "out", _ROWS, dev, tokens, self.width)
         if tokens > self.max_tokens:
             raise ValueError(f"q: {tokens} rows, at most {self.max_tokens}")
         if cu_q is None:
@@ -292,9 +327,7 @@ class Attention:
                 raise ValueError("a handle with max_q > 1 wants cu_q")
             a.cu_q = None
         else:
-            if _tensor(cu_q, "cu_q", torch.int32, c.device, 1).shape[0] != c.rows + 1:
-                raise ValueError(f"cu_q: {cu_q.shape[0]} elements, {c.rows + 1} are wanted")
-            a.cu_q = cu_q.data_ptr()
+            a.cu_q = _vec(cu_q, "cu_q", dev, c.rows + 1)
         a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
-        a.out_dtype = B.DTYPE_F32 if out.dtype == torch.float32 else B.DTYPE_BF16
+        a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
         c.call(B.paged_attention, a)
