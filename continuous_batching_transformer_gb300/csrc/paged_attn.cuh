@@ -61,13 +61,22 @@ CBT_D void wait_timeout(int* err, volatile int* abort_flag, int where) {
   *abort_flag = 1;
   set_device_error(err, CBT_DEV_TIMEOUT, 400 + where);
 }
+// Bounded wait for a phase.  While it is incomplete the thread is suspended for up to a microsecond
+// a poll: spinning warps take issue slots from those that work.
 CBT_D bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  for (uint32_t i = 0; i < tc::kSpinLimit; ++i) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023) == 1023 && *abort_flag) return false;
-    if (i > 256) __nanosleep(32);
+#pragma unroll 1
+  for (uint32_t i = 0; i < 1u << 22; ++i) {
+    if (tc::mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    if (*abort_flag) return false;
   }
   return false;
+}
+
+// The same for the copies in flight at exit, which an abort does not call off
+CBT_D void wait_landed(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < 1u << 22; ++i)
+    if (tc::mbar_try_wait_sleep(bar, parity, 1000)) return;
 }
 
 // The query tokens of row b: [t0, t0 + n) of the call's rows, the last at position len - 1.
@@ -90,12 +99,13 @@ CBT_D RowTokens row_tokens(const PagedAttn& a, int b) {
   return r;
 }
 
-// Visible keys among the 128 from k0 on, as 4 words of bits, for a query at position hi whose
+// Visible keys among the 32 W from k0 on, as W words of bits, for a query at position hi whose
 // window starts at lo (for a run of queries: the last one's position, the first one's window)
 CBT_D uint32_t ones_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
-CBT_D void seen_bits(int k0, int hi, int lo, int sinks, uint32_t (&w)[4]) {
+template <int W>
+CBT_D void seen_bits(int k0, int hi, int lo, int sinks, uint32_t (&w)[W]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < W; ++i) {
     const int b = k0 + 32 * i;
     w[i] = ones_below(hi + 1 - b) & (~ones_below(lo - b) | ones_below(sinks - b));
   }

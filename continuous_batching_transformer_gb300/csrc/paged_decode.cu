@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
       }
     }
     // no copies in flight at exit
-    if (nk) tc::mbar_wait(kfull, (nk - 1) & 1);
-    if (nv) tc::mbar_wait(vfull, (nv - 1) & 1);
+    if (nk) wait_landed(kfull, (nk - 1) & 1);
+    if (nv) wait_landed(vfull, (nv - 1) & 1);
   } else {
     uint32_t n = 0;  // chunks done
     bool ok = true;

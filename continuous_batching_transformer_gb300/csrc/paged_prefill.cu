@@ -8,8 +8,8 @@
 //   softmax         one thread per row: the whole row of S in registers, running maximum and sum
 //   O += P V        tcgen05.mma 128 x head_dim x 128, P read from tensor memory as bf16 where S was
 // O stays in tensor memory for the whole unit.  A row's reference maximum is raised (and its O
-// rescaled) only when a block exceeds it by more than 2^kSlack, so O is rarely touched; the weights
-// stay below 2^kSlack, exact in what they are divided by.  P is rounded to bf16 once (2^-9 of each
+// rescaled) only when a block exceeds it by more than 2^kSlack, so O is rarely touched, and weights
+// stay below 2^kSlack.  P is rounded to bf16 once (2^-9 of each
 // weight on average less), everything else is fp32.
 //
 // Bound by the tensor cores and, close behind, the exponentials.  The two tiles of a unit run half
@@ -26,7 +26,8 @@ namespace {
 constexpr int kBlk = 128;
 constexpr int kBox = 16384;     // [128 rows][64 bf16], swizzled
 constexpr int kKStages = 3, kVStages = 2;
-constexpr int kThreads = 384;   // warps: tiles, issuer 0, issuer 1, V; 4..7 and 8..11 softmax
+constexpr int kThreads = 640;   // warps: tiles, issuer 0, issuer 1, V; 4..11 and 12..19 softmax
+constexpr int kSoft = 256;      // softmax threads of a tile
 constexpr float kSlack = 8.f;
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane
@@ -49,6 +50,8 @@ CBT_D void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 2^-n for a whole n >= 0 (n NaN or beyond the range: 0)
+CBT_D float pow2_down(float n) { return n <= 126.f ? __int_as_float((127 - (int)n) << 23) : 0.f; }
 CBT_D void tma_load_q(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int head, int tok) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -56,6 +59,27 @@ CBT_D void tma_load_q(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int
       "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(head), "r"(tok)
       : "memory");
 }
+
+CBT_D float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Barrier over a tile's softmax threads: 2 if any of them set bit 1 of v, else 1 if any set bit 0
+CBT_D uint32_t tile_vote(int id, uint32_t v) {
+  if (!tc::named_bar_any(id, kSoft, v != 0)) return 0;
+  return tc::named_bar_any(id, kSoft, (v & 2) != 0) ? 2 : 1;
+}
+
+// A shared-memory matrix descriptor (tc::sdesc_sw128) as two words: the high one is the same for
+// every tile, the low one counts in 16-byte units and is moved by additions.
+CBT_D uint32_t desc_lo(const void* p) { return (uint32_t)tc::sdesc_sw128(tc::smem_u32(p)); }
+CBT_D uint64_t desc(uint32_t lo) {
+  constexpr uint32_t hi = (uint32_t)((((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61)) >> 32);
+  return ((uint64_t)hi << 32) | lo;
+}
+// the k-th 16-deep step of a tile whose 64-column boxes are `box` bytes apart
+CBT_HD constexpr uint32_t step_of(int k, int box) { return (uint32_t)((k >> 2) * (box >> 4) + 2 * (k & 3)); }
 
 struct Unit {
   int b, t0, n;  // row; its query tokens [t0, t0 + n) of this unit, n = -1: no unit
@@ -85,12 +109,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kTile);
   uint64_t *qfull = bars, *kfull = bars + 1, *kempty = kfull + kKStages;
   uint64_t *vfull = kempty + kKStages, *vready = vfull + kVStages, *vempty = vready + kVStages;
-  uint64_t *s_full = vempty + kVStages, *p_full = s_full + 2, *o_full = p_full + 2;
-  constexpr int kBars = 1 + 2 * kKStages + 3 * kVStages + 6;
+  uint64_t *s_full = vempty + kVStages, *p_full = s_full + 2, *o_full = p_full + 4;
+  uint64_t* turn = o_full + 2;  // [tile]: its issuer may issue
+  constexpr int kBars = 1 + 2 * kKStages + 3 * kVStages + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* unit = reinterpret_cast<Unit*>(tmem_slot + 2);
-  int* wsum = reinterpret_cast<int*>(unit + 1);  // [12]
+  int* wsum = reinterpret_cast<int*>(unit + 1);                         // [20]
+  float* xchg = reinterpret_cast<float*>(sV + kVStages * kTile + 512);  // [tile][128 rows]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
@@ -98,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % Hkv;
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
-    for (int i = 0; i < kKStages; ++i) tc::mbar_init(&kempty[i], 2);
+    for (int i = 0; i < kKStages; ++i) tc::mbar_init(&kempty[i], 2);  // both issuers
     for (int i = 0; i < kVStages; ++i) tc::mbar_init(&vempty[i], 2);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], kSoft / 32);  // [tile][part]
     *abort_flag = 0;
     unit->n = -1;
     tc::mbar_fence_init();
@@ -108,55 +134,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tma_prefetch_desc(&tk);
     tc::tma_prefetch_desc(&tv);
   }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
   pdl_wait();
   pdl_launch();
   // ---- this CTA's unit: units are counted over the rows, thread by thread
   {
     const int per = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
-    int mine = 0;
-    for (int r = r0; r < r1; ++r) {
-      const RowTokens row = row_tokens(a, r);
-      if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, r);
-      if (row.n > 0) mine += (row.n + 2 * TQ - 1) / (2 * TQ);
-    }
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    int at = before + inc - mine;
-    const int u = total - 1 - (int)(blockIdx.x / Hkv);  // last units first
-    if (u >= at && u < at + mine) {
+    int mine = 0, at = 0, u = -1;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {  // count, then find (rolled: the code is run once a CTA)
+#pragma unroll 1
       for (int r = r0; r < r1; ++r) {
         const RowTokens row = row_tokens(a, r);
         const int k = row.n > 0 ? (row.n + 2 * TQ - 1) / (2 * TQ) : 0;
-        if (u < at + k) {
+        if (pass == 0) {
+          if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, r);
+          mine += k;
+        } else if (u >= at && u < at + k) {
           const int first = (u - at) * 2 * TQ;
           *unit = Unit{r, row.t0 + first, min(2 * TQ, row.n - first), row.len - row.n + first};
-          break;
         }
         at += k;
       }
+      if (pass) break;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      // lane w: warp w's sum
+      const int ws = lane < kThreads / 32 ? wsum[lane] : 0;
+      const int total = __reduce_add_sync(0xffffffffu, ws);
+      at = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + inc - mine;
+      u = total - 1 - (int)(blockIdx.x / Hkv);  // last units first
+      if (u < at || u >= at + mine) break;
     }
   }
-  __syncthreads();
-  const Unit un = *unit;
-  if (un.n < 0) return;  // more CTAs than units (the whole block leaves)
-  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  const Unit un = *unit;
   const uint32_t tmem = *tmem_slot;
+  if (un.n < 0) {  // more CTAs than units (the whole block leaves)
+    if (warp == 1) tc::tmem_dealloc(tmem, kTmem);
+    return;
+  }
 
   // positions of the unit's and of each tile's last token, and the blocks they need
   const int pl = un.p0 + un.n - 1;
@@ -173,7 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- tile requests
     const uint64_t pol = tc::policy_evict_last();
     const int P = a.kv.page_tokens;
-    uint32_t nk = 0, nv = 0;
+    int nk = 0, nv = 0;  // tiles requested
+    int ks = 0, vs = 0;  // stages and phases of K and V
+    uint32_t kp = 0, vp = 0;
     bool ok = true;
     if (lane == 0 && seen.n) {
       const int tiles = un.n > TQ ? 2 : 1;
@@ -183,128 +211,141 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < nKh; ++h)
           tma_load_q(sQ + x * kTile + h * kBox, &tq, qfull, h * 64, g * G, un.t0 + x * TQ);
     }
-    // the tile rows of block i's halves: lanes 0 and 1 look the pages up
-    struct Where {
-      unsigned halves;
-      int k0, k1, v0, v1;
-    };
-    auto where = [&](int i) {
-      const int key = seen.chunk(i) * kBlk + 64 * lane;
-      int krow = 0, vrow = 0;
-      bool want = false;
-      if (lane < 2) {
-        const int last = min(key + 63, pl);
-        want = key <= pl && (!a.window || last >= lo_win || key < a.sinks);
-        if (want) {
-          const int pg = key / P, o = key - pg * P;
-          int id = a.table[(size_t)un.b * a.max_pages + pg];
-          if (id < 0 || id >= a.kv.n_pages) {
-            set_device_error(a.err, CBT_DEV_PAGE_ID, un.b);
-            id = 0;  // a page that exists: the row's outputs are unspecified
+    // K runs one block ahead of V.  Lanes 0 and 1 look up the pages of a block's halves.
+    unsigned halves = 0, halves_v = 0;
+    int kr[2], vr[2], vnext[2] = {0, 0};
+#pragma unroll 1
+    for (int i = 0; i <= seen.n && seen.n && ok; ++i) {
+      if (i < seen.n) {
+        const int key = seen.chunk(i) * kBlk + 64 * lane;
+        int krow = 0, vrow = 0;
+        bool want = false;
+        if (lane < 2) {
+          want = key <= pl && (!a.window || min(key + 63, pl) >= lo_win || key < a.sinks);
+          if (want) {
+            const int pg = key / P, o = key - pg * P;
+            int id = a.table[(size_t)un.b * a.max_pages + pg];
+            if (id < 0 || id >= a.kv.n_pages) {
+              set_device_error(a.err, CBT_DEV_PAGE_ID, un.b);
+              id = 0;  // a page that exists: the row's outputs are unspecified
+            }
+            krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
+            vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
           }
-          krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
-          vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
+        }
+        halves = __ballot_sync(0xffffffffu, want);
+        for (int e = 0; e < 2; ++e) {
+          kr[e] = __shfl_sync(0xffffffffu, krow, e);
+          vr[e] = __shfl_sync(0xffffffffu, vrow, e);
+        }
+        if (lane == 0) {
+          ok = wait_or_abort(&kempty[ks], kp ^ 1, abort_flag);
+          if (ok) {
+            tc::mbar_expect_tx(&kfull[ks], __popc(halves) * 64 * HD * 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int h = 0; h < nKh; ++h)
+                if (halves >> e & 1)
+                  tc::tma_load_2d(sK + ks * kTile + h * kBox + e * 8192, &tk, &kfull[ks], h * 64, kr[e], pol);
+            ++nk;
+          }
+          ks = ks + 1 == kKStages ? 0 : ks + 1;
+          kp ^= ks == 0;
         }
       }
-      Where w;
-      w.halves = __ballot_sync(0xffffffffu, want);
-      w.k0 = krow;
-      w.v0 = vrow;
-      w.k1 = __shfl_sync(0xffffffffu, krow, 1);
-      w.v1 = __shfl_sync(0xffffffffu, vrow, 1);
-      return w;
-    };
-    auto load_k = [&](int i, const Where& w) {  // lane 0
-      const int st = i % kKStages;
-      if (!wait_or_abort(&kempty[st], ((i / kKStages) & 1) ^ 1, abort_flag)) return false;
-      tc::mbar_expect_tx(&kfull[st], __popc(w.halves) * 64 * HD * 2);
-      ++nk;
-      uint8_t* dst = sK + st * kTile;
+      if (i > 0 && lane == 0 && ok) {
+        ok = wait_or_abort(&vempty[vs], vp ^ 1, abort_flag);
+        if (ok) {
+          tc::mbar_expect_tx(&vfull[vs], __popc(halves_v) * 64 * HD * 2);
 #pragma unroll
-      for (int h = 0; h < nKh; ++h) {
-        if (w.halves & 1) tc::tma_load_2d(dst + h * kBox, &tk, &kfull[st], h * 64, w.k0, pol);
-        if (w.halves & 2) tc::tma_load_2d(dst + h * kBox + 8192, &tk, &kfull[st], h * 64, w.k1, pol);
+          for (int e = 0; e < 2; ++e)
+            if (halves_v >> e & 1)
+              tc::tma_load_2d(sV + vs * kTile + e * kVBox, &tv, &vfull[vs], 0, vnext[e], pol);
+          ++nv;
+        }
+        vs = vs + 1 == kVStages ? 0 : vs + 1;
+        vp ^= vs == 0;
       }
-      return true;
-    };
-    auto load_v = [&](int i, const Where& w) {
-      const int st = i % kVStages;
-      if (!wait_or_abort(&vempty[st], ((i / kVStages) & 1) ^ 1, abort_flag)) return false;
-      tc::mbar_expect_tx(&vfull[st], __popc(w.halves) * 64 * HD * 2);
-      ++nv;
-      uint8_t* dst = sV + st * kTile;
-      if (w.halves & 1) tc::tma_load_2d(dst, &tv, &vfull[st], 0, w.v0, pol);
-      if (w.halves & 2) tc::tma_load_2d(dst + kVBox, &tv, &vfull[st], 0, w.v1, pol);
-      return true;
-    };
-    // K runs one block ahead of V
-    Where cur{}, nxt{};
-    if (seen.n) {
-      cur = where(0);
-      if (lane == 0) ok = load_k(0, cur);
-    }
-    for (int i = 0; i < seen.n && ok; ++i) {
-      if (i + 1 < seen.n) {
-        nxt = where(i + 1);
-        if (lane == 0) ok = load_k(i + 1, nxt);
-      }
-      if (lane == 0 && ok) ok = load_v(i, cur);
-      cur = nxt;
+      halves_v = halves;
+      vnext[0] = vr[0];
+      vnext[1] = vr[1];
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (lane == 0) {
       if (!ok) wait_timeout(a.err, abort_flag, 11);
       // no copies in flight at exit
-      if (seen.n) tc::mbar_wait(qfull, 0);
-      for (uint32_t i = 0; i < (uint32_t)kKStages && i < nk; ++i)
-        tc::mbar_wait(&kfull[(nk - 1 - i) % kKStages], ((nk - 1 - i) / kKStages) & 1);
-      for (uint32_t i = 0; i < (uint32_t)kVStages && i < nv; ++i)
-        tc::mbar_wait(&vfull[(nv - 1 - i) % kVStages], ((nv - 1 - i) / kVStages) & 1);
+      if (seen.n) wait_landed(qfull, 0);
+#pragma unroll 1
+      for (int i = max(0, nk - kKStages); i < nk; ++i)
+        wait_landed(&kfull[i % kKStages], (i / kKStages) & 1);
+#pragma unroll 1
+      for (int i = max(0, nv - kVStages); i < nv; ++i)
+        wait_landed(&vfull[i % kVStages], (i / kVStages) & 1);
     }
   } else if (warp <= 2) {
-    // ---- MMA issue of tile x
-    if (lane == 0) {
-      const int x = warp - 1;
+    // ---- MMA issue of tile x: PV of its last block, then S of its next.  The two issuers take
+    // turns, each waiting for its operands while the other issues, so that while one tile's pair
+    // of products runs the other's softmax does (left alone, the tiles fall into step).
+    if (lane == 0 && seen.n) {
+      const int x = warp - 1, last = tile_last(x);
       const Seen mine = tile_seen(x);
-      const int last = tile_last(x);
       const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
-      bool ok = seen.n == 0 || wait_or_abort(qfull, 0, abort_flag);
-      uint32_t acc = 0, np = 0;
-      for (int i = 0; i < seen.n && ok; ++i) {
-        const int ks = i % kKStages, vs = i % kVStages;
-        const bool need = needs(mine, last, seen.chunk(i));
-        ok = wait_or_abort(&kfull[ks], (i / kKStages) & 1, abort_flag);
+      const uint32_t dq = desc_lo(sQ + x * kTile), dk = desc_lo(sK), dv = desc_lo(sV);
+      uint32_t acc = 0, np = 0;  // O holds something; phase of p_full
+      bool owed = false;         // the tile saw the block before: its PV is due
+      int ks = 0, vs = 0;        // stages and phases of K and V
+      uint32_t kp = 0, vp = 0;
+      bool ok = wait_or_abort(qfull, 0, abort_flag);
+      for (int i = 0; i <= seen.n && ok; ++i) {
+        const bool need = i < seen.n && needs(mine, last, seen.chunk(i));
+        if (i < seen.n) ok = wait_or_abort(&kfull[ks], kp, abort_flag);
+        if (i > 0) ok = ok && wait_or_abort(&vready[vs], vp, abort_flag);
+        if (owed) ok = ok && wait_or_abort(&p_full[2 * x], np, abort_flag);
+        if (x || i) ok = ok && wait_or_abort(&turn[x], x ? i & 1 : (i & 1) ^ 1, abort_flag);
         if (!ok) break;
-        if (!need) {  // this tile sees nothing of the block: pass its stages on
-          tc::mbar_arrive(&kempty[ks]);
-          ok = wait_or_abort(&vready[vs], (i / kVStages) & 1, abort_flag);
-          if (ok) tc::mbar_arrive(&vempty[vs]);
-          continue;
-        }
         tc::tc_fence_after();
+        if (owed) {
+          // the weights come in two parts: the first 32 keys of either half, then the rest
+          const uint32_t v = dv + vs * (kTile >> 4);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint64_t ad =
-              tc::sdesc_sw128(tc::smem_u32(sQ + x * kTile + (k >> 2) * kBox)) + 2 * (k & 3);
-          const uint64_t bd =
-              tc::sdesc_sw128(tc::smem_u32(sK + ks * kTile + (k >> 2) * kBox)) + 2 * (k & 3);
-          tc::mma_bf16(s_tm, ad, bd, kIdescS, k > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(&s_full[x]);
-        tc::mma_commit(&kempty[ks]);
-        ok = wait_or_abort(&p_full[x], np & 1, abort_flag) &&
-             wait_or_abort(&vready[vs], (i / kVStages) & 1, abort_flag);
-        if (!ok) break;
-        ++np;
-        tc::tc_fence_after();
+          for (int part = 0; part < 2; ++part) {
+            if (part) {
+              ok = wait_or_abort(&p_full[2 * x + 1], np, abort_flag);
+              if (!ok) break;
+              tc::tc_fence_after();
+            }
 #pragma unroll
-        for (int k = 0; k < kBlk / 16; ++k) {
-          const uint64_t bd =
-              tc::sdesc_sw128(tc::smem_u32(sV + vs * kTile + (k >> 2) * kVBox)) + 2 * (k & 3);
-          tc::mma_bf16_ta(o_tm, s_tm + 8 * k, bd, kIdescO, (acc || k > 0) ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {
+              const int k = 2 * part + (j & 1) + 4 * (j >> 1);  // 16-key step
+              tc::mma_bf16_ta(o_tm, s_tm + 64 * (k >> 2) + 8 * (k & 3), desc(v + step_of(k, kVBox)),
+                              kIdescO, (acc || part || j > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          np ^= 1;
+          acc = 1;
         }
-        acc = 1;
-        tc::mma_commit(&vempty[vs]);
+        if (need) {
+          const uint32_t kd = dk + ks * (kTile >> 4);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            tc::mma_bf16(s_tm, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox)), kIdescS,
+                         k > 0 ? 1u : 0u);
+          tc::mma_commit(&s_full[x]);
+        }
+        tc::mbar_arrive(&turn[x ^ 1]);
+        owed = need;
+        if (i < seen.n) {
+          tc::mma_commit(&kempty[ks]);
+          ks = ks + 1 == kKStages ? 0 : ks + 1;
+          kp ^= ks == 0;
+        }
+        if (i > 0) {
+          tc::mma_commit(&vempty[vs]);
+          vs = vs + 1 == kVStages ? 0 : vs + 1;
+          vp ^= vs == 0;
+        }
       }
       if (ok) tc::mma_commit(&o_full[x]);
       else wait_timeout(a.err, abort_flag, 12);
@@ -341,125 +382,186 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 13);
   } else {
-    // ---- softmax of tile x: thread = row
-    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    // ---- softmax of tile x: two threads per row, thread `half` of them for 64 keys of a block and
+    // half of O's columns.  They share the reference m; their sums are joined at the end.
+    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
     const Seen mine = tile_seen(x);
     const int last = tile_last(x);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + x * 128 + lane_off, o_tm = tmem + 256 + x * HD + lane_off;
-    const int tok = x * TQ + row / G;          // token of the unit
+    const uint32_t s_tm = tmem + x * 128 + 64 * half + lane_off;
+    const uint32_t o_tm = tmem + 256 + x * HD + half * (HD / 2) + lane_off;
+    volatile float* cell = xchg + x * kBlk + row;  // where the row's two threads meet
+    const int tok = x * TQ + row / G;              // token of the unit
     const bool live = row < TQ * G && tok < un.n;
-    const int p = live ? un.p0 + tok : -1;     // -1: sees nothing
+    const int p = live ? un.p0 + tok : -1;         // -1: sees nothing
     // rows that hold no token are left unmasked: what they compute is not stored
     const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
     const int sinks = a.window ? a.sinks : 0;
-    const float scale2 = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
+    // Scores in units of log2.  A negative scale negates them first, so that the largest product is
+    // the largest score's; a zero scale stands for one that leaves every weight 1 (a masked -inf
+    // must stay -inf).
+    const bool negate = a.scale < 0.f;
+    const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
     uint32_t ns = 0;
     bool ok = true;
     for (int i = 0; i < seen.n && ok; ++i) {
       const int c = seen.chunk(i);
       if (!needs(mine, last, c)) continue;
       ok = wait_or_abort(&s_full[x], ns & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       tc::tc_fence_after();
-      uint32_t s[128];
+      const int k0 = c * kBlk + 64 * half;
+      // every row sees every key of the half, or keys are masked one by one
+      const bool whole = __all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64));
+      // Scores are read twice, 32 at a time, rather than kept: kept they take the registers that
+      // everything else then spills, to a first-level cache that shared memory has left tiny.
+      auto scores = [&](int k, uint32_t(&s)[32]) {
+        tmem_ld32(s_tm + k, s);
+        tc::tmem_ld_wait();
+        if (negate) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(s_tm + 32 * k, s + 32 * k);
-      tc::tmem_ld_wait();
-      const int k0 = c * kBlk;
-      uint32_t bits[4];
-      seen_bits(k0, hi, lo, sinks, bits);
-      const bool whole = __all_sync(0xffffffffu, (bits[0] & bits[1] & bits[2] & bits[3]) == 0xFFFFFFFFu);
-      float mx = -INFINITY;
-      if (whole) {
-#pragma unroll
-        for (int k = 0; k < 128; ++k) {
-          const float v = __uint_as_float(s[k]) * scale2;
-          s[k] = __float_as_uint(v);
-          mx = fmaxf(mx, v);
+          for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
         }
-      } else {
+        if (!whole) {
+          uint32_t bits[1];
+          seen_bits(k0 + k, hi, lo, sinks, bits);
 #pragma unroll
-        for (int k = 0; k < 128; ++k) {
-          const float v = (bits[k >> 5] >> (k & 31)) & 1 ? __uint_as_float(s[k]) * scale2 : -INFINITY;
-          s[k] = __float_as_uint(v);
-          mx = fmaxf(mx, v);
+          for (int e = 0; e < 32; ++e)
+            if (!((bits[0] >> e) & 1)) s[e] = 0xFF800000u;  // -inf
         }
-      }
-      if (ns == 0) {
-        m = mx;
-      } else {
-        const bool up = mx > m + kSlack;  // m = -inf: the row's first visible keys
-        if (__any_sync(0xffffffffu, up)) {
-          // the MMAs into O have completed: S of this block was issued after them
-          const float f = up ? ex2(m - mx) : 1.f;
-          if (up) m = mx;
-          l *= f;
+      };
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int k = 0; k < HD; k += 16) {
+      for (int k = 0; k < 64; k += 32) {
+        uint32_t s[32];
+        scores(k, s);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+      }
+      float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale2;
+      // does any row of the tile exceed its reference by more than 2^kSlack, or see its first keys?
+      const bool up = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
+      const uint32_t vote = tile_vote(1 + x, (ok ? 0u : 2u) | (up ? 1u : 0u));
+      if (vote == 2) {  // a wait that ran out makes the whole tile leave
+        ok = false;
+        break;
+      }
+      if (vote) {
+        if (half) *cell = top;
+        tc::named_bar_sync(1 + x, kSoft);
+        if (!half) *cell = top = fmaxf(top, *cell);
+        tc::named_bar_sync(1 + x, kSoft);
+        if (half) top = *cell;
+        // Such rows raise it, to a whole number: what the old one has scaled is multiplied by a
+        // power of two, which rounds nothing.  The MMAs into O have completed: S was issued after
+        // them.
+        const bool raise = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
+        const float next = raise ? ceilf(top) : m;
+        const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
+        m = next;
+        l *= f;
+        if (ns) {
+#pragma unroll 1
+          for (int d = 0; d < HD / 2; d += 16) {
             uint32_t o[16];
-            tc::tmem_ld16(o_tm + k, o);
+            tc::tmem_ld16(o_tm + d, o);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(o_tm + k, o);
+            tmem_st16(o_tm + d, o);
           }
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 128; k += 32) {
-        uint32_t pk[16];
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int k = 0; k < 64; k += 32) {
+        uint32_t s[32], pk[16];
+        scores(k, s);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2(__uint_as_float(s[k + 2 * e]) - ref);
-          const float p1 = ex2(__uint_as_float(s[k + 2 * e + 1]) - ref);
-          sum += p0 + p1;
+          const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale2, -ref));
+          const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -ref));
+          part[e & 3] += p0;
+          part[(e + 2) & 3] += p1;
           pk[e] = pack_bf16(p0, p1);
         }
-        tmem_st16(s_tm + k / 2, pk);
+        tmem_st16(s_tm + k / 2, pk);  // over scores of this thread that have been read
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + (k >> 5)]);
       }
-      l += sum;
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_full[x]);
+      l += (part[0] + part[1]) + (part[2] + part[3]);
       ++ns;
     }
     if (ok && ns) {
       ok = wait_or_abort(&o_full[x], 0, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      if (half) *cell = l;
+      ok = !(tile_vote(1 + x, ok ? 0u : 2u) & 2);
+      if (!half) *cell = l = l + *cell;
+      tc::named_bar_sync(1 + x, kSoft);
+      if (half) l = *cell;
       tc::tc_fence_after();
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 14);
     if (ok) {
+      // Out through shared memory (Q's tile, no longer read): a lane holds a row, and its row alone
+      // would touch a cache line a lane; turned around, a warp's store fills whole lines.
       const float inv = p >= 0 ? 1.f / l : 0.f;
-      const long long at = (long long)(un.t0 + tok) * a.out_ld + (long long)(g * G + row % G) * HD;
+      uint8_t* stage = sQ + x * kTile + ((warp - 4) & 7) * (kTile / 8);  // [32 rows][kLine bytes]
+      const int size = a.f32 ? 4 : 2;
+      const long long at =
+          ((long long)(un.t0 + tok) * a.out_ld + (long long)(g * G + row % G) * HD + half * (HD / 2)) * size;
+      constexpr int kLine = HD;  // bytes of a row at a time: 128 (head_dim 128) or 64
 #pragma unroll 1
-      for (int k = 0; k < HD; k += 16) {
-        uint32_t o[16];
-        if (ns) {
-          tc::tmem_ld16(o_tm + k, o);
+      for (int k = 0; k < HD / 2 * size; k += kLine) {  // byte k of the row's half
+#pragma unroll
+        for (int b = 0; b < kLine; b += 32) {
+          // 8 fp32 or 16 bf16 values
+          uint32_t o[16];
+          uint4 w[2];
+          const int col = (k + b) / size;
+          if (a.f32) {
+            if (ns) tc::tmem_ld8(o_tm + col, o);
+          } else {
+            if (ns) tc::tmem_ld16(o_tm + col, o);
+          }
           tc::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[e] = p >= 0 ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          if (a.f32) {
+            w[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            w[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              h[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            w[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            w[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int u = b / 16 + e;  // 16-byte unit of the row, swizzled by the row
+            *reinterpret_cast<uint4*>(stage + lane * kLine + ((u ^ (lane & (kLine / 16 - 1))) << 4)) = w[e];
+          }
         }
-        float v[16];
+        __syncwarp();
+        constexpr int kUnits = kLine / 16, kRows = 32 / kUnits;
+        const int u = lane % kUnits;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = p >= 0 ? __uint_as_float(o[e]) * inv : 0.f;
-        if (!live) continue;
-        if (a.f32) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + k);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + k);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+        for (int r0 = 0; r0 < 32; r0 += kRows) {
+          const int r = r0 + lane / kUnits;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kLine + ((u ^ (r & (kUnits - 1))) << 4));
+          const long long to = __shfl_sync(0xffffffffu, at, r);
+          if (__shfl_sync(0xffffffffu, (int)live, r))
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to + k + u * 16) = w;
         }
+        __syncwarp();
       }
     }
     tc::tc_fence_before();
@@ -474,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const PagedAttn& a, cudaStream_t s) {
-  constexpr size_t smem = 1024 + (2 + kKStages + kVStages) * (HD / 64) * kBox + 512;
+  constexpr size_t smem = 1024 + (2 + kKStages + kVStages) * (HD / 64) * kBox + 512 + 2 * kBlk * sizeof(float);
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t rc = cudaFuncSetAttribute(k_paged_prefill<HD>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
