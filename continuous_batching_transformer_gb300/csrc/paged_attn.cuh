@@ -9,20 +9,21 @@
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Keys the query at position p sees: j <= p with j > p - window or j < sinks (window 0: all).
-// They lie in the 128-key chunks [0, ns) (sinks below the window's first chunk) and [ws, last].
+// They lie in the C-key chunks [0, ns) (sinks below the window's first chunk) and [ws, last].
 struct Seen {
   int ns, ws, n;  // n chunks in all
   CBT_HD int chunk(int i) const { return i < ns ? i : ws + i - ns; }
 };
 CBT_HD int first_in_window(int p, int window) { return window && p >= window ? p - window + 1 : 0; }
 // chunks that any of the queries at positions [p0, p1] sees (p1 < 0: none)
+template <int C>
 CBT_HD Seen seen_chunks(int p0, int p1, int window, int sinks) {
   Seen s{0, 0, 0};
   if (p1 < 0) return s;
-  s.ws = first_in_window(p0 < 0 ? 0 : p0, window) / 128;
-  const int sc = (int)(((long long)sinks + 127) / 128);
+  s.ws = first_in_window(p0 < 0 ? 0 : p0, window) / C;
+  const int sc = (int)(((long long)sinks + C - 1) / C);
   s.ns = sc < s.ws ? sc : s.ws;
-  s.n = s.ns + p1 / 128 - s.ws + 1;
+  s.n = s.ns + p1 / C - s.ws + 1;
   return s;
 }
 CBT_HD bool sees(int j, int p, int window, int sinks) {
@@ -55,6 +56,16 @@ CBT_D uint4 key_mask(uint32_t bits) {
   m.z = ((bits & 16) ? 0xFFFFu : 0u) | ((bits & 32) ? 0xFFFF0000u : 0u);
   m.w = ((bits & 64) ? 0xFFFFu : 0u) | ((bits & 128) ? 0xFFFF0000u : 0u);
   return m;
+}
+
+// What follows lets the compiler see that a value is the same in the whole warp, and that one
+// thread runs a branch: matrix instructions take their operands from uniform registers, and moving
+// them there from a lane's costs more than the instruction.
+CBT_D int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+CBT_D bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 CBT_D void wait_timeout(int* err, volatile int* abort_flag, int where) {

@@ -74,7 +74,7 @@ struct Cursor {
       row = row_tokens(a, b);
       if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, b);
       if (row.n == 1) {
-        seen = seen_chunks(row.len - 1, row.len - 1, a.window, a.sinks);
+        seen = seen_chunks<kSub>(row.len - 1, row.len - 1, a.window, a.sinks);
         n = runs_of(seen.n) * per_row;
       }
     }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(128)
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RowTokens row = row_tokens(a, b);
   if (row.n != 1) return;
-  const Seen seen = seen_chunks(row.len - 1, row.len - 1, a.window, a.sinks);
+  const Seen seen = seen_chunks<kSub>(row.len - 1, row.len - 1, a.window, a.sinks);
   const int runs = runs_of(seen.n);
   if (runs == 1) return;
   const size_t base = ((size_t)b * a.n_heads + h) * layout_of(a).max_runs;

@@ -23,11 +23,11 @@
 
 namespace {
 
-constexpr int kBlk = 128;
+constexpr int kRows = 128;      // tensor-core rows of a tile
+constexpr int kStep = 64;       // keys of a step
 constexpr int kBox = 16384;     // [128 rows][64 bf16], swizzled
-constexpr int kKStages = 3, kVStages = 2;
-constexpr int kThreads = 640;   // warps: tiles, issuer 0, issuer 1, V; 4..11 and 12..19 softmax
-constexpr int kSoft = 256;      // softmax threads of a tile
+constexpr int kKStages = 6, kVStages = 4;
+constexpr int kThreads = 384;   // warps: tiles, issuer 0, issuer 1, V; 4..7 and 8..11 softmax
 constexpr float kSlack = 8.f;
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane
@@ -65,12 +65,6 @@ CBT_D float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Barrier over a tile's softmax threads: 2 if any of them set bit 1 of v, else 1 if any set bit 0
-CBT_D uint32_t tile_vote(int id, uint32_t v) {
-  if (!tc::named_bar_any(id, kSoft, v != 0)) return 0;
-  return tc::named_bar_any(id, kSoft, (v & 2) != 0) ? 2 : 1;
-}
-
 // A shared-memory matrix descriptor (tc::sdesc_sw128) as two words: the high one is the same for
 // every tile, the low one counts in 16-byte units and is moved by additions.
 CBT_D uint32_t desc_lo(const void* p) { return (uint32_t)tc::sdesc_sw128(tc::smem_u32(p)); }
@@ -86,47 +80,41 @@ struct Unit {
   int p0;        // position of token t0 (may be negative)
 };
 
-// Blocks the tile with tokens at positions [p0, p1] needs
-CBT_D bool needs(const Seen& s, int p1, int c) {
-  return s.n > 0 && (c < s.ns || (c >= s.ws && c <= p1 / kBlk));
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttn a) {
   constexpr int nKh = HD / 64;
-  constexpr uint32_t kTile = nKh * kBox;     // a Q, K or V tile
-  constexpr int kVBox = HD * 128;            // V^T of 64 keys
-  constexpr uint32_t kIdescS = tc::idesc_bf16(128, 128), kIdescO = tc::idesc_bf16(128, HD);
-  constexpr uint32_t kTmem = 512;            // S0, S1 (P over them) in columns 0..255, O0, O1
+  constexpr uint32_t kTile = nKh * kBox;     // a Q tile
+  constexpr uint32_t kKV = kStep * HD * 2;   // K or V of a step
+  constexpr uint32_t kIdescS = tc::idesc_bf16(128, kStep), kIdescO = tc::idesc_bf16(128, HD);
+  constexpr uint32_t kTmem = 512;  // S (P over it): tile x, buffer b at 128 x + 64 b; O: 256 + HD x
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sQ = smem;                     // [tile][64-dim half][128 rows]
-  uint8_t* sK = sQ + 2 * kTile;           // [stage][64-dim half][128 keys]
-  uint8_t* sV = sK + kKStages * kTile;    // [stage][64-key half][HD dims]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kTile);
+  uint8_t* sK = sQ + 2 * kTile;           // [stage][64-dim half][64 keys]
+  uint8_t* sV = sK + kKStages * kKV;      // [stage][HD dims][64 keys]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kKV);
   uint64_t *qfull = bars, *kfull = bars + 1, *kempty = kfull + kKStages;
   uint64_t *vfull = kempty + kKStages, *vready = vfull + kVStages, *vempty = vready + kVStages;
-  uint64_t *s_full = vempty + kVStages, *p_full = s_full + 2, *o_full = p_full + 4;
-  uint64_t* turn = o_full + 2;  // [tile]: its issuer may issue
-  constexpr int kBars = 1 + 2 * kKStages + 3 * kVStages + 10;
+  // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
+  uint64_t *s_full = vempty + kVStages, *p_full = s_full + 4, *pv_done = p_full + 4;
+  constexpr int kBars = 1 + 2 * kKStages + 3 * kVStages + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* unit = reinterpret_cast<Unit*>(tmem_slot + 2);
-  int* wsum = reinterpret_cast<int*>(unit + 1);                         // [20]
-  float* xchg = reinterpret_cast<float*>(sV + kVStages * kTile + 512);  // [tile][128 rows]
+  int* wsum = reinterpret_cast<int*>(unit + 1);  // [12]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
-  const int TQ = kBlk / G;  // tokens per tile
+  const int TQ = kRows / G;  // tokens per tile
   const int g = blockIdx.x % Hkv;
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
     for (int i = 0; i < kKStages; ++i) tc::mbar_init(&kempty[i], 2);  // both issuers
     for (int i = 0; i < kVStages; ++i) tc::mbar_init(&vempty[i], 2);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], kSoft / 32);  // [tile][part]
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);         // a tile's softmax warps
     *abort_flag = 0;
     unit->n = -1;
     tc::mbar_fence_init();
@@ -177,100 +165,87 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const Unit un = *unit;
-  const uint32_t tmem = *tmem_slot;
+  const Unit un{uniform(unit->b), uniform(unit->t0), uniform(unit->n), uniform(unit->p0)};
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   if (un.n < 0) {  // more CTAs than units (the whole block leaves)
     if (warp == 1) tc::tmem_dealloc(tmem, kTmem);
     return;
   }
 
-  // positions of the unit's and of each tile's last token, and the blocks they need
-  const int pl = un.p0 + un.n - 1;
-  const Seen seen = seen_chunks(un.p0, pl, a.window, a.sinks);
-  auto tile_first = [&](int x) { return un.p0 + x * TQ; };
-  auto tile_last = [&](int x) { return min(pl, un.p0 + (x + 1) * TQ - 1); };
-  auto tile_seen = [&](int x) {
-    return tile_last(x) < tile_first(x) ? Seen{0, 0, 0}
-                                        : seen_chunks(tile_first(x), tile_last(x), a.window, a.sinks);
+  // The unit's steps are the 64-key chunks that any of its queries sees; a tile takes part in those
+  // that its own see.
+  const int pl = un.p0 + un.n - 1;  // position of the last token
+  const int lo_win = first_in_window(max(0, un.p0), a.window), sinks = a.window ? a.sinks : 0;
+  const Seen seen = seen_chunks<kStep>(un.p0, pl, a.window, a.sinks);
+  struct TileKeys {
+    int last, lo;  // positions of the tile's last token and of its first token's window
+    CBT_D bool need(int key, int sinks) const { return key <= last && (key + kStep > lo || key < sinks); }
   };
-  const int lo_win = first_in_window(max(0, un.p0), a.window);
+  auto tile_keys = [&](int x) {
+    const int first = un.p0 + x * TQ;
+    return TileKeys{x * TQ < un.n ? min(pl, first + TQ - 1) : -1, first_in_window(max(0, first), a.window)};
+  };
 
   if (warp == 0) {
-    // ---- tile requests
+    // ---- tile requests.  Per step: lanes 0 and 1 wait for its K stage and for the V stage of kAhead
+    // steps before, lane 0 requests both.  The pages of 32 steps are looked up at once, a lane each
+    // (one dependent load a step held every step up by some 2200 cycles, as the whole kernel took).
+    constexpr int kAhead = 2;
     const uint64_t pol = tc::policy_evict_last();
     const int P = a.kv.page_tokens;
-    int nk = 0, nv = 0;  // tiles requested
     int ks = 0, vs = 0;  // stages and phases of K and V
     uint32_t kp = 0, vp = 0;
+    int nk = 0, nv = 0;  // steps requested
+    int krow = 0, vrow = 0, vlast[kAhead] = {0, 0};
     bool ok = true;
-    if (lane == 0 && seen.n) {
+    if (seen.n && lane == 0) {
       const int tiles = un.n > TQ ? 2 : 1;
       tc::mbar_expect_tx(qfull, tiles * nKh * G * TQ * 128);
+#pragma unroll 1
       for (int x = 0; x < tiles; ++x)
-#pragma unroll
         for (int h = 0; h < nKh; ++h)
           tma_load_q(sQ + x * kTile + h * kBox, &tq, qfull, h * 64, g * G, un.t0 + x * TQ);
     }
-    // K runs one block ahead of V.  Lanes 0 and 1 look up the pages of a block's halves.
-    unsigned halves = 0, halves_v = 0;
-    int kr[2], vr[2], vnext[2] = {0, 0};
 #pragma unroll 1
-    for (int i = 0; i <= seen.n && seen.n && ok; ++i) {
-      if (i < seen.n) {
-        const int key = seen.chunk(i) * kBlk + 64 * lane;
-        int krow = 0, vrow = 0;
-        bool want = false;
-        if (lane < 2) {
-          want = key <= pl && (!a.window || min(key + 63, pl) >= lo_win || key < a.sinks);
-          if (want) {
-            const int pg = key / P, o = key - pg * P;
-            int id = a.table[(size_t)un.b * a.max_pages + pg];
-            if (id < 0 || id >= a.kv.n_pages) {
-              set_device_error(a.err, CBT_DEV_PAGE_ID, un.b);
-              id = 0;  // a page that exists: the row's outputs are unspecified
-            }
-            krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
-            vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
-          }
+    for (int i = 0; i < seen.n + kAhead && seen.n; ++i) {
+      if ((i & 31) == 0 && i + lane < seen.n) {
+        const int key = seen.chunk(i + lane) * kStep, pg = key / P, o = key - pg * P;
+        int id = a.table[(size_t)un.b * a.max_pages + pg];
+        if (id < 0 || id >= a.kv.n_pages) {
+          set_device_error(a.err, CBT_DEV_PAGE_ID, un.b);
+          id = 0;  // a page that exists: the row's outputs are unspecified
         }
-        halves = __ballot_sync(0xffffffffu, want);
-        for (int e = 0; e < 2; ++e) {
-          kr[e] = __shfl_sync(0xffffffffu, krow, e);
-          vr[e] = __shfl_sync(0xffffffffu, vrow, e);
-        }
-        if (lane == 0) {
-          ok = wait_or_abort(&kempty[ks], kp ^ 1, abort_flag);
-          if (ok) {
-            tc::mbar_expect_tx(&kfull[ks], __popc(halves) * 64 * HD * 2);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int h = 0; h < nKh; ++h)
-                if (halves >> e & 1)
-                  tc::tma_load_2d(sK + ks * kTile + h * kBox + e * 8192, &tk, &kfull[ks], h * 64, kr[e], pol);
-            ++nk;
-          }
-          ks = ks + 1 == kKStages ? 0 : ks + 1;
-          kp ^= ks == 0;
-        }
+        krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
+        vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
       }
-      if (i > 0 && lane == 0 && ok) {
-        ok = wait_or_abort(&vempty[vs], vp ^ 1, abort_flag);
-        if (ok) {
-          tc::mbar_expect_tx(&vfull[vs], __popc(halves_v) * 64 * HD * 2);
+      const bool has_k = i < seen.n, has_v = i >= kAhead;
+      const int kr = __shfl_sync(0xffffffffu, krow, i & 31), vr = __shfl_sync(0xffffffffu, vrow, i & 31);
+      const bool mine = lane == 0 ? has_k : lane == 1 && has_v;
+      ok = !mine || wait_or_abort(lane ? &vempty[vs] : &kempty[ks], (lane ? vp : kp) ^ 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (has_k) {
+        if (elect_one()) {
+          tc::mbar_expect_tx(&kfull[ks], kKV);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (halves_v >> e & 1)
-              tc::tma_load_2d(sV + vs * kTile + e * kVBox, &tv, &vfull[vs], 0, vnext[e], pol);
-          ++nv;
+          for (int h = 0; h < nKh; ++h)
+            tc::tma_load_2d(sK + ks * kKV + h * (kBox / 2), &tk, &kfull[ks], h * 64, kr, pol);
         }
+        ++nk;
+        ks = ks + 1 == kKStages ? 0 : ks + 1;
+        kp ^= ks == 0;
+      }
+      if (has_v) {
+        if (elect_one()) {
+          tc::mbar_expect_tx(&vfull[vs], kKV);
+          tc::tma_load_2d(sV + vs * kKV, &tv, &vfull[vs], 0, vlast[0], pol);
+        }
+        ++nv;
         vs = vs + 1 == kVStages ? 0 : vs + 1;
         vp ^= vs == 0;
       }
-      halves_v = halves;
-      vnext[0] = vr[0];
-      vnext[1] = vr[1];
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      vlast[0] = vlast[1];
+      vlast[1] = vr;
     }
     if (lane == 0) {
       if (!ok) wait_timeout(a.err, abort_flag, 11);
@@ -284,92 +259,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_landed(&vfull[i % kVStages], (i / kVStages) & 1);
     }
   } else if (warp <= 2) {
-    // ---- MMA issue of tile x: PV of its last block, then S of its next.  The two issuers take
-    // turns, each waiting for its operands while the other issues, so that while one tile's pair
-    // of products runs the other's softmax does (left alone, the tiles fall into step).
-    if (lane == 0 && seen.n) {
-      const int x = warp - 1, last = tile_last(x);
-      const Seen mine = tile_seen(x);
+    // ---- MMA issue of tile x.  Two S buffers: the next step's scores are there before the softmax
+    // asks for them, and it never waits for its own P V.
+    if (seen.n) {
+      const int x = warp - 1;
+      const TileKeys mine = tile_keys(x);
       const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
       const uint32_t dq = desc_lo(sQ + x * kTile), dk = desc_lo(sK), dv = desc_lo(sV);
-      uint32_t acc = 0, np = 0;  // O holds something; phase of p_full
-      bool owed = false;         // the tile saw the block before: its PV is due
-      int ks = 0, vs = 0;        // stages and phases of K and V
+      int ns = 0, np = 0;  // S and PV issued
+      int ks = 0, vs = 0;  // stages and phases of K and V
       uint32_t kp = 0, vp = 0;
       bool ok = wait_or_abort(qfull, 0, abort_flag);
-      for (int i = 0; i <= seen.n && ok; ++i) {
-        const bool need = i < seen.n && needs(mine, last, seen.chunk(i));
-        if (i < seen.n) ok = wait_or_abort(&kfull[ks], kp, abort_flag);
-        if (i > 0) ok = ok && wait_or_abort(&vready[vs], vp, abort_flag);
-        if (owed) ok = ok && wait_or_abort(&p_full[2 * x], np, abort_flag);
-        if (x || i) ok = ok && wait_or_abort(&turn[x], x ? i & 1 : (i & 1) ^ 1, abort_flag);
-        if (!ok) break;
-        tc::tc_fence_after();
-        if (owed) {
-          // the weights come in two parts: the first 32 keys of either half, then the rest
-          const uint32_t v = dv + vs * (kTile >> 4);
+      ok = __all_sync(0xffffffffu, ok);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {  // by the whole warp
+        ok = ok && __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+      };
+      auto next_k = [&]() {
+        ks = ks + 1 == kKStages ? 0 : ks + 1;
+        kp ^= ks == 0;
+      };
+      auto next_v = [&]() {
+        vs = vs + 1 == kVStages ? 0 : vs + 1;
+        vp ^= vs == 0;
+      };
+      auto pv = [&]() {
+        if (elect_one()) {
+          const uint32_t v = dv + vs * (kKV >> 4), pt = s_tm + 64 * (np & 1);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            if (part) {
-              ok = wait_or_abort(&p_full[2 * x + 1], np, abort_flag);
-              if (!ok) break;
-              tc::tc_fence_after();
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int k = 2 * part + (j & 1) + 4 * (j >> 1);  // 16-key step
-              tc::mma_bf16_ta(o_tm, s_tm + 64 * (k >> 2) + 8 * (k & 3), desc(v + step_of(k, kVBox)),
-                              kIdescO, (acc || part || j > 0) ? 1u : 0u);
-            }
-          }
-          if (!ok) break;
-          np ^= 1;
-          acc = 1;
-        }
-        if (need) {
-          const uint32_t kd = dk + ks * (kTile >> 4);
-#pragma unroll
-          for (int k = 0; k < HD / 16; ++k)
-            tc::mma_bf16(s_tm, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox)), kIdescS,
-                         k > 0 ? 1u : 0u);
-          tc::mma_commit(&s_full[x]);
-        }
-        tc::mbar_arrive(&turn[x ^ 1]);
-        owed = need;
-        if (i < seen.n) {
-          tc::mma_commit(&kempty[ks]);
-          ks = ks + 1 == kKStages ? 0 : ks + 1;
-          kp ^= ks == 0;
-        }
-        if (i > 0) {
+          for (int k = 0; k < kStep / 16; ++k)
+            tc::mma_bf16_ta(o_tm, pt + 8 * k, desc(v + 2 * k), kIdescO, (np || k > 0) ? 1u : 0u);
+          tc::mma_commit(&pv_done[2 * x + (np & 1)]);
           tc::mma_commit(&vempty[vs]);
-          vs = vs + 1 == kVStages ? 0 : vs + 1;
-          vp ^= vs == 0;
+        }
+        next_v();
+        ++np;
+      };
+#pragma unroll 1
+      for (int i = 0; i <= seen.n && ok; ++i) {
+        const bool end = i == seen.n, need = !end && mine.need(seen.chunk(i) * kStep, sinks);
+        if (need) {
+          const bool due = ns - np == 2;  // the buffer's last weights are multiplied first
+          if (due) {
+            wait(&p_full[2 * x + (np & 1)], (np >> 1) & 1);
+            wait(&vready[vs], vp);
+          }
+          wait(&kfull[ks], kp);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (due) pv();
+          if (elect_one()) {
+            const uint32_t kd = dk + ks * (kKV >> 4), st = s_tm + 64 * (ns & 1);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              tc::mma_bf16(st, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox / 2)), kIdescS,
+                           k > 0 ? 1u : 0u);
+            tc::mma_commit(&s_full[2 * x + (ns & 1)]);
+            tc::mma_commit(&kempty[ks]);
+          }
+          ++ns;
+          next_k();
+        } else {  // at the end, and where the tile sits a step out, all products due are issued
+#pragma unroll 1
+          while (ok && np < ns) {
+            wait(&p_full[2 * x + (np & 1)], (np >> 1) & 1);
+            wait(&vready[vs], vp);
+            tc::tc_fence_after();
+            if (ok) pv();
+          }
+          if (end || !ok) break;
+          wait(&kfull[ks], kp);
+          wait(&vready[vs], vp);
+          if (ok && lane == 0) {  // pass the step's stages on
+            tc::mbar_arrive(&kempty[ks]);
+            tc::mbar_arrive(&vempty[vs]);
+          }
+          next_k();
+          next_v();
         }
       }
-      if (ok) tc::mma_commit(&o_full[x]);
-      else wait_timeout(a.err, abort_flag, 12);
+      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 12);
     }
   } else if (warp == 3) {
     // ---- V of keys that no query of the unit sees is cleared
     bool ok = true;
+    int vs = 0;
+    uint32_t vp = 0;
+#pragma unroll 1
     for (int i = 0; i < seen.n && ok; ++i) {
-      const int st = i % kVStages;
-      ok = wait_or_abort(&vfull[st], (i / kVStages) & 1, abort_flag);
+      ok = wait_or_abort(&vfull[vs], vp, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      uint32_t bits[4];
-      seen_bits(seen.chunk(i) * kBlk, pl, lo_win, a.window ? a.sinks : 0, bits);
-      if ((bits[0] & bits[1] & bits[2] & bits[3]) != 0xFFFFFFFFu) {
-        uint8_t* v = sV + st * kTile;
+      uint32_t bits[2];
+      seen_bits(seen.chunk(i) * kStep, pl, lo_win, sinks, bits);
+      if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
+        uint8_t* v = sV + vs * kKV;
 #pragma unroll 1
-        for (int u = 0; u < 16; ++u) {  // 8 keys
-          const uint32_t m8 = ((u < 4 ? bits[0] : u < 8 ? bits[1] : u < 12 ? bits[2] : bits[3]) >>
-                               (8 * (u & 3))) & 0xFFu;
+        for (int u = 0; u < 8; ++u) {  // 8 keys
+          const uint32_t m8 = ((u < 4 ? bits[0] : bits[1]) >> (8 * (u & 3))) & 0xFFu;
           if (m8 == 0xFFu) continue;
           const uint4 mk = key_mask(m8);
           for (int d = lane; d < HD; d += 32) {
-            uint4* p = reinterpret_cast<uint4*>(v + (u >> 3) * kVBox + d * 128 + (((u & 7) ^ (d & 7)) << 4));
+            uint4* p = reinterpret_cast<uint4*>(v + d * 128 + ((u ^ (d & 7)) << 4));
             uint4 z = make_uint4(0, 0, 0, 0);
             if (m8) z = *p;
             *p = make_uint4(z.x & mk.x, z.y & mk.y, z.z & mk.z, z.w & mk.w);
@@ -378,93 +368,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) tc::mbar_arrive(&vready[st]);
+      if (lane == 0) tc::mbar_arrive(&vready[vs]);
+      vs = vs + 1 == kVStages ? 0 : vs + 1;
+      vp ^= vs == 0;
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 13);
   } else {
-    // ---- softmax of tile x: two threads per row, thread `half` of them for 64 keys of a block and
-    // half of O's columns.  They share the reference m; their sums are joined at the end.
-    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const Seen mine = tile_seen(x);
-    const int last = tile_last(x);
+    // ---- softmax of tile x: thread = row
+    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const TileKeys mine = tile_keys(x);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + x * 128 + 64 * half + lane_off;
-    const uint32_t o_tm = tmem + 256 + x * HD + half * (HD / 2) + lane_off;
-    volatile float* cell = xchg + x * kBlk + row;  // where the row's two threads meet
-    const int tok = x * TQ + row / G;              // token of the unit
+    const uint32_t s_tm = tmem + x * 128 + lane_off, o_tm = tmem + 256 + x * HD + lane_off;
+    const int tok = x * TQ + row / G;          // token of the unit
     const bool live = row < TQ * G && tok < un.n;
-    const int p = live ? un.p0 + tok : -1;         // -1: sees nothing
+    const int p = live ? un.p0 + tok : -1;     // -1: sees nothing
     // rows that hold no token are left unmasked: what they compute is not stored
     const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
-    const int sinks = a.window ? a.sinks : 0;
     // Scores in units of log2.  A negative scale negates them first, so that the largest product is
     // the largest score's; a zero scale stands for one that leaves every weight 1 (a masked -inf
     // must stay -inf).
     const bool negate = a.scale < 0.f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
-    uint32_t ns = 0;
+    int ns = 0;                    // steps done
     bool ok = true;
-    for (int i = 0; i < seen.n && ok; ++i) {
-      const int c = seen.chunk(i);
-      if (!needs(mine, last, c)) continue;
-      ok = wait_or_abort(&s_full[x], ns & 1, abort_flag);
-      tc::tc_fence_after();
-      const int k0 = c * kBlk + 64 * half;
-      // every row sees every key of the half, or keys are masked one by one
-      const bool whole = __all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64));
-      // Scores are read twice, 32 at a time, rather than kept: kept they take the registers that
-      // everything else then spills, to a first-level cache that shared memory has left tiny.
-      auto scores = [&](int k, uint32_t(&s)[32]) {
-        tmem_ld32(s_tm + k, s);
-        tc::tmem_ld_wait();
-        if (negate) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
-        }
-        if (!whole) {
-          uint32_t bits[1];
-          seen_bits(k0 + k, hi, lo, sinks, bits);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((bits[0] >> e) & 1)) s[e] = 0xFF800000u;  // -inf
-        }
-      };
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-      for (int k = 0; k < 64; k += 32) {
-        uint32_t s[32];
-        scores(k, s);
+    for (int i = 0; i < seen.n && ok; ++i) {
+      const int k0 = seen.chunk(i) * kStep;
+      if (!mine.need(k0, sinks)) continue;
+      const int b = ns & 1;
+      ok = wait_or_abort(&s_full[2 * x + b], (ns >> 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint32_t s[64];
+      tmem_ld32(s_tm + 64 * b, s);
+      tmem_ld32(s_tm + 64 * b + 32, s + 32);
+      tc::tmem_ld_wait();
+      if (negate) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        for (int e = 0; e < 64; ++e) s[e] ^= 0x80000000u;
       }
-      float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale2;
-      // does any row of the tile exceed its reference by more than 2^kSlack, or see its first keys?
+      // every row sees every key of the step, or keys are masked one by one
+      if (!__all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64))) {
+        uint32_t bits[2];
+        seen_bits(k0, hi, lo, sinks, bits);
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (!((bits[e >> 5] >> (e & 31)) & 1)) s[e] = 0xFF800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale2;
       const bool up = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
-      const uint32_t vote = tile_vote(1 + x, (ok ? 0u : 2u) | (up ? 1u : 0u));
-      if (vote == 2) {  // a wait that ran out makes the whole tile leave
-        ok = false;
-        break;
-      }
-      if (vote) {
-        if (half) *cell = top;
-        tc::named_bar_sync(1 + x, kSoft);
-        if (!half) *cell = top = fmaxf(top, *cell);
-        tc::named_bar_sync(1 + x, kSoft);
-        if (half) top = *cell;
-        // Such rows raise it, to a whole number: what the old one has scaled is multiplied by a
-        // power of two, which rounds nothing.  The MMAs into O have completed: S was issued after
-        // them.
-        const bool raise = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
-        const float next = raise ? ceilf(top) : m;
+      if (__any_sync(0xffffffffu, up)) {
+        // Rows that exceed their reference by more than 2^kSlack, or see their first keys, raise
+        // it, to a whole number: what the old one has scaled is multiplied by a power of two,
+        // which rounds nothing.
+        const float next = up ? ceilf(top) : m;
         const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
         m = next;
         l *= f;
         if (ns) {
+          ok = wait_or_abort(&pv_done[2 * x + (b ^ 1)], ((ns - 1) >> 1) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::tc_fence_after();
 #pragma unroll 1
-          for (int d = 0; d < HD / 2; d += 16) {
+          for (int d = 0; d < HD; d += 16) {
             uint32_t o[16];
             tc::tmem_ld16(o_tm + d, o);
             tc::tmem_ld_wait();
@@ -476,34 +449,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float ref = m == -INFINITY ? 0.f : m;
       float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int k = 0; k < 64; k += 32) {
-        uint32_t s[32], pk[16];
-        scores(k, s);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale2, -ref));
-          const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -ref));
-          part[e & 3] += p0;
-          part[(e + 2) & 3] += p1;
-          pk[e] = pack_bf16(p0, p1);
-        }
-        tmem_st16(s_tm + k / 2, pk);  // over scores of this thread that have been read
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + (k >> 5)]);
+      for (int e = 0; e < 32; ++e) {
+        const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale2, -ref));
+        const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -ref));
+        part[e & 3] += p0;
+        part[(e + 2) & 3] += p1;
+        s[e] = pack_bf16(p0, p1);
       }
+      tc::tmem_st32(s_tm + 64 * b, s);  // over the scores
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
       l += (part[0] + part[1]) + (part[2] + part[3]);
       ++ns;
     }
-    if (ok && ns) {
-      ok = wait_or_abort(&o_full[x], 0, abort_flag);
-      if (half) *cell = l;
-      ok = !(tile_vote(1 + x, ok ? 0u : 2u) & 2);
-      if (!half) *cell = l = l + *cell;
-      tc::named_bar_sync(1 + x, kSoft);
-      if (half) l = *cell;
+    if (ok && seen.n) {
+      // O is complete (a tile that saw nothing: Q has landed), so Q's tile is free
+      ok = ns ? wait_or_abort(&pv_done[2 * x + ((ns - 1) & 1)], ((ns - 1) >> 1) & 1, abort_flag)
+              : wait_or_abort(qfull, 0, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
       tc::tc_fence_after();
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 14);
@@ -511,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Out through shared memory (Q's tile, no longer read): a lane holds a row, and its row alone
       // would touch a cache line a lane; turned around, a warp's store fills whole lines.
       const float inv = p >= 0 ? 1.f / l : 0.f;
-      uint8_t* stage = sQ + x * kTile + ((warp - 4) & 7) * (kTile / 8);  // [32 rows][kLine bytes]
+      uint8_t* stage = sQ + x * kTile + quarter * (kTile / 4);  // [32 rows][kLine bytes]
       const int size = a.f32 ? 4 : 2;
       const long long at =
-          ((long long)(un.t0 + tok) * a.out_ld + (long long)(g * G + row % G) * HD + half * (HD / 2)) * size;
+          ((long long)(un.t0 + tok) * a.out_ld + (long long)(g * G + row % G) * HD) * size;
       constexpr int kLine = HD;  // bytes of a row at a time: 128 (head_dim 128) or 64
 #pragma unroll 1
-      for (int k = 0; k < HD / 2 * size; k += kLine) {  // byte k of the row's half
+      for (int k = 0; k < HD * size; k += kLine) {  // byte k of the row
 #pragma unroll
         for (int b = 0; b < kLine; b += 32) {
           // 8 fp32 or 16 bf16 values
@@ -551,10 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        constexpr int kUnits = kLine / 16, kRows = 32 / kUnits;
+        constexpr int kUnits = kLine / 16;
         const int u = lane % kUnits;
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kRows) {
+        for (int r0 = 0; r0 < 32; r0 += 32 / kUnits) {
           const int r = r0 + lane / kUnits;
           const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kLine + ((u ^ (r & (kUnits - 1))) << 4));
           const long long to = __shfl_sync(0xffffffffu, at, r);
@@ -576,12 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const PagedAttn& a, cudaStream_t s) {
-  constexpr size_t smem = 1024 + (2 + kKStages + kVStages) * (HD / 64) * kBox + 512 + 2 * kBlk * sizeof(float);
+  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + (kKStages + kVStages) * kStep * HD * 2 + 512;
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t rc = cudaFuncSetAttribute(k_paged_prefill<HD>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (rc != cudaSuccess) return rc;
-  const int G = a.n_heads / a.kv.n_kv_heads, run = 2 * (kBlk / G);
+  const int G = a.n_heads / a.kv.n_kv_heads, run = 2 * (kRows / G);
   // most units: every row may end in a partly filled one
   const long long by_tokens = (long long)a.tokens / run + a.rows;
   const long long by_rows = (long long)a.rows * ((a.max_q + run - 1) / run);
@@ -596,7 +562,7 @@ cudaError_t launch_paged_prefill(const PagedAttn& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   const int G = a.n_heads / a.kv.n_kv_heads;
   if (!paged_maps(a.kv, &tk, &tv) ||
-      !make_tmap_rows(&tq, a.q, a.kv.head_dim, a.n_heads, a.tokens, a.q_ld, G, kBlk / G))
+      !make_tmap_rows(&tq, a.q, a.kv.head_dim, a.n_heads, a.tokens, a.q_ld, G, kRows / G))
     return cudaErrorInvalidValue;
   return a.kv.head_dim == 128 ? launch_hd<128>(tq, tk, tv, a, s) : launch_hd<64>(tq, tk, tv, a, s);
 }
