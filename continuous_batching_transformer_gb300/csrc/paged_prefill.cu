@@ -26,7 +26,8 @@ namespace {
 constexpr int kRows = 128;      // tensor-core rows of a tile
 constexpr int kStep = 64;       // keys of a step
 constexpr int kBox = 16384;     // [128 rows][64 bf16], swizzled
-constexpr int kKStages = 6, kVStages = 4;
+constexpr int kStages = 5;
+constexpr int kLag = 2;         // a stage holds K of a step and V of the step kLag before it
 constexpr int kThreads = 384;   // warps: tiles, issuer 0, issuer 1, V; 4..7 and 8..11 softmax
 constexpr float kSlack = 8.f;
 
@@ -94,13 +95,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   uint8_t* sQ = smem;                     // [tile][64-dim half][128 rows]
   uint8_t* sK = sQ + 2 * kTile;           // [stage][64-dim half][64 keys]
-  uint8_t* sV = sK + kKStages * kKV;      // [stage][HD dims][64 keys]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kVStages * kKV);
-  uint64_t *qfull = bars, *kfull = bars + 1, *kempty = kfull + kKStages;
-  uint64_t *vfull = kempty + kKStages, *vready = vfull + kVStages, *vempty = vready + kVStages;
+  uint8_t* sV = sK + kStages * kKV;       // [stage][HD dims][64 keys]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kStages * kKV);
+  // a stage has landed, its V is clean, both tiles are done with it
+  uint64_t *qfull = bars, *full = bars + 1, *ready = full + kStages, *empty = ready + kStages;
   // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
-  uint64_t *s_full = vempty + kVStages, *p_full = s_full + 4, *pv_done = p_full + 4;
-  constexpr int kBars = 1 + 2 * kKStages + 3 * kVStages + 12;
+  uint64_t *s_full = empty + kStages, *p_full = s_full + 4, *pv_done = p_full + 4;
+  constexpr int kBars = 1 + 3 * kStages + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* unit = reinterpret_cast<Unit*>(tmem_slot + 2);
@@ -112,9 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % Hkv;
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
-    for (int i = 0; i < kKStages; ++i) tc::mbar_init(&kempty[i], 2);  // both issuers
-    for (int i = 0; i < kVStages; ++i) tc::mbar_init(&vempty[i], 2);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);         // a tile's softmax warps
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2);  // both issuers
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);       // a tile's softmax warps
     *abort_flag = 0;
     unit->n = -1;
     tc::mbar_fence_init();
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pl = un.p0 + un.n - 1;  // position of the last token
   const int lo_win = first_in_window(max(0, un.p0), a.window), sinks = a.window ? a.sinks : 0;
   const Seen seen = seen_chunks<kStep>(un.p0, pl, a.window, a.sinks);
+  const int stages = seen.n ? seen.n + kLag : 0;
   struct TileKeys {
     int last, lo;  // positions of the tile's last token and of its first token's window
     CBT_D bool need(int key, int sinks) const { return key <= last && (key + kStep > lo || key < sinks); }
@@ -187,16 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---- tile requests.  Per step: lanes 0 and 1 wait for its K stage and for the V stage of kAhead
-    // steps before, lane 0 requests both.  The pages of 32 steps are looked up at once, a lane each
-    // (one dependent load a step held every step up by some 2200 cycles, as the whole kernel took).
-    constexpr int kAhead = 2;
+    // ---- tile requests: per stage K of a step and V of the step kLag before.  The pages of 32 steps
+    // are looked up at once, a lane each (one dependent load a step was as long as the step).
     const uint64_t pol = tc::policy_evict_last();
     const int P = a.kv.page_tokens;
-    int ks = 0, vs = 0;  // stages and phases of K and V
-    uint32_t kp = 0, vp = 0;
-    int nk = 0, nv = 0;  // steps requested
-    int krow = 0, vrow = 0, vlast[kAhead] = {0, 0};
+    int st = 0, n = 0;  // stage, stages requested
+    uint32_t ph = 0;
+    int krow = 0, vrow = 0, vlag[kLag] = {0, 0};
     bool ok = true;
     if (seen.n && lane == 0) {
       const int tiles = un.n > TQ ? 2 : 1;
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_q(sQ + x * kTile + h * kBox, &tq, qfull, h * 64, g * G, un.t0 + x * TQ);
     }
 #pragma unroll 1
-    for (int i = 0; i < seen.n + kAhead && seen.n; ++i) {
+    for (int i = 0; i < stages; ++i) {
       if ((i & 31) == 0 && i + lane < seen.n) {
         const int key = seen.chunk(i + lane) * kStep, pg = key / P, o = key - pg * P;
         int id = a.table[(size_t)un.b * a.max_pages + pg];
@@ -218,141 +216,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
         vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
       }
-      const bool has_k = i < seen.n, has_v = i >= kAhead;
       const int kr = __shfl_sync(0xffffffffu, krow, i & 31), vr = __shfl_sync(0xffffffffu, vrow, i & 31);
-      const bool mine = lane == 0 ? has_k : lane == 1 && has_v;
-      ok = !mine || wait_or_abort(lane ? &vempty[vs] : &kempty[ks], (lane ? vp : kp) ^ 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], ph ^ 1, abort_flag));
       if (!ok) break;
-      if (has_k) {
-        if (elect_one()) {
-          tc::mbar_expect_tx(&kfull[ks], kKV);
+      const bool has_k = i < seen.n, has_v = i >= kLag;
+      if (elect_one()) {
+        tc::mbar_expect_tx(&full[st], (has_k ? kKV : 0) + (has_v ? kKV : 0));
+        if (has_k) {
 #pragma unroll
           for (int h = 0; h < nKh; ++h)
-            tc::tma_load_2d(sK + ks * kKV + h * (kBox / 2), &tk, &kfull[ks], h * 64, kr, pol);
+            tc::tma_load_2d(sK + st * kKV + h * (kBox / 2), &tk, &full[st], h * 64, kr, pol);
         }
-        ++nk;
-        ks = ks + 1 == kKStages ? 0 : ks + 1;
-        kp ^= ks == 0;
+        if (has_v) tc::tma_load_2d(sV + st * kKV, &tv, &full[st], 0, vlag[0], pol);
       }
-      if (has_v) {
-        if (elect_one()) {
-          tc::mbar_expect_tx(&vfull[vs], kKV);
-          tc::tma_load_2d(sV + vs * kKV, &tv, &vfull[vs], 0, vlast[0], pol);
-        }
-        ++nv;
-        vs = vs + 1 == kVStages ? 0 : vs + 1;
-        vp ^= vs == 0;
-      }
-      vlast[0] = vlast[1];
-      vlast[1] = vr;
+      ++n;
+      st = st + 1 == kStages ? 0 : st + 1;
+      ph ^= st == 0;
+      vlag[0] = vlag[1];
+      vlag[1] = vr;
     }
     if (lane == 0) {
       if (!ok) wait_timeout(a.err, abort_flag, 11);
       // no copies in flight at exit
       if (seen.n) wait_landed(qfull, 0);
 #pragma unroll 1
-      for (int i = max(0, nk - kKStages); i < nk; ++i)
-        wait_landed(&kfull[i % kKStages], (i / kKStages) & 1);
-#pragma unroll 1
-      for (int i = max(0, nv - kVStages); i < nv; ++i)
-        wait_landed(&vfull[i % kVStages], (i / kVStages) & 1);
+      for (int i = max(0, n - kStages); i < n; ++i) wait_landed(&full[i % kStages], (i / kStages) & 1);
     }
   } else if (warp <= 2) {
-    // ---- MMA issue of tile x.  Two S buffers: the next step's scores are there before the softmax
-    // asks for them, and it never waits for its own P V.
+    // ---- MMA issue of tile x: per stage P V of the step kLag before, then S of the step into the
+    // buffer this freed.  So a step's scores are there before the softmax asks for them, and it
+    // never waits for its own P V.
     if (seen.n) {
       const int x = warp - 1;
       const TileKeys mine = tile_keys(x);
       const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
       const uint32_t dq = desc_lo(sQ + x * kTile), dk = desc_lo(sK), dv = desc_lo(sV);
-      int ns = 0, np = 0;  // S and PV issued
-      int ks = 0, vs = 0;  // stages and phases of K and V
-      uint32_t kp = 0, vp = 0;
-      bool ok = wait_or_abort(qfull, 0, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      auto wait = [&](uint64_t* bar, uint32_t parity) {  // by the whole warp
-        ok = ok && __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
-      };
-      auto next_k = [&]() {
-        ks = ks + 1 == kKStages ? 0 : ks + 1;
-        kp ^= ks == 0;
-      };
-      auto next_v = [&]() {
-        vs = vs + 1 == kVStages ? 0 : vs + 1;
-        vp ^= vs == 0;
-      };
-      auto pv = [&]() {
-        if (elect_one()) {
-          const uint32_t v = dv + vs * (kKV >> 4), pt = s_tm + 64 * (np & 1);
-#pragma unroll
-          for (int k = 0; k < kStep / 16; ++k)
-            tc::mma_bf16_ta(o_tm, pt + 8 * k, desc(v + 2 * k), kIdescO, (np || k > 0) ? 1u : 0u);
-          tc::mma_commit(&pv_done[2 * x + (np & 1)]);
-          tc::mma_commit(&vempty[vs]);
-        }
-        next_v();
-        ++np;
-      };
+      int st = 0;
+      uint32_t ph = 0, pp = 0;  // phases of the stages, and of p_full (bit b: buffer b)
+      uint32_t took = 0;        // bit j: the tile took part in the step j before this one
+      uint32_t acc = 0;
+      bool ok = __all_sync(0xffffffffu, wait_or_abort(qfull, 0, abort_flag));
 #pragma unroll 1
-      for (int i = 0; i <= seen.n && ok; ++i) {
-        const bool end = i == seen.n, need = !end && mine.need(seen.chunk(i) * kStep, sinks);
-        if (need) {
-          const bool due = ns - np == 2;  // the buffer's last weights are multiplied first
+      for (int i = 0; i < stages && ok; ++i) {
+        const int b = i & 1;
+        const bool need = i < seen.n && mine.need(seen.chunk(i) * kStep, sinks), due = took >> (kLag - 1) & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&ready[st], ph, abort_flag));
+        if (due) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&p_full[2 * x + b], pp >> b & 1, abort_flag));
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (elect_one()) {
           if (due) {
-            wait(&p_full[2 * x + (np & 1)], (np >> 1) & 1);
-            wait(&vready[vs], vp);
+            const uint32_t v = dv + st * (kKV >> 4);
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k)
+              tc::mma_bf16_ta(o_tm, s_tm + 64 * b + 8 * k, desc(v + 2 * k), kIdescO, (acc || k > 0) ? 1u : 0u);
+            tc::mma_commit(&pv_done[2 * x + b]);
           }
-          wait(&kfull[ks], kp);
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (due) pv();
-          if (elect_one()) {
-            const uint32_t kd = dk + ks * (kKV >> 4), st = s_tm + 64 * (ns & 1);
+          if (need) {
+            const uint32_t kd = dk + st * (kKV >> 4);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
-              tc::mma_bf16(st, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox / 2)), kIdescS,
+              tc::mma_bf16(s_tm + 64 * b, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox / 2)), kIdescS,
                            k > 0 ? 1u : 0u);
-            tc::mma_commit(&s_full[2 * x + (ns & 1)]);
-            tc::mma_commit(&kempty[ks]);
+            tc::mma_commit(&s_full[2 * x + b]);
           }
-          ++ns;
-          next_k();
-        } else {  // at the end, and where the tile sits a step out, all products due are issued
-#pragma unroll 1
-          while (ok && np < ns) {
-            wait(&p_full[2 * x + (np & 1)], (np >> 1) & 1);
-            wait(&vready[vs], vp);
-            tc::tc_fence_after();
-            if (ok) pv();
-          }
-          if (end || !ok) break;
-          wait(&kfull[ks], kp);
-          wait(&vready[vs], vp);
-          if (ok && lane == 0) {  // pass the step's stages on
-            tc::mbar_arrive(&kempty[ks]);
-            tc::mbar_arrive(&vempty[vs]);
-          }
-          next_k();
-          next_v();
+          tc::mma_commit(&empty[st]);
         }
+        if (due) {
+          pp ^= 1u << b;
+          acc = 1;
+        }
+        took = took << 1 | (need ? 1u : 0u);
+        st = st + 1 == kStages ? 0 : st + 1;
+        ph ^= st == 0;
       }
       if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 12);
     }
   } else if (warp == 3) {
     // ---- V of keys that no query of the unit sees is cleared
     bool ok = true;
-    int vs = 0;
-    uint32_t vp = 0;
+    int st = 0;
+    uint32_t ph = 0;
 #pragma unroll 1
-    for (int i = 0; i < seen.n && ok; ++i) {
-      ok = wait_or_abort(&vfull[vs], vp, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+    for (int i = 0; i < stages && ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
       if (!ok) break;
-      uint32_t bits[2];
-      seen_bits(seen.chunk(i) * kStep, pl, lo_win, sinks, bits);
+      uint32_t bits[2] = {~0u, ~0u};
+      if (i >= kLag) seen_bits(seen.chunk(i - kLag) * kStep, pl, lo_win, sinks, bits);
       if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
-        uint8_t* v = sV + vs * kKV;
+        uint8_t* v = sV + st * kKV;
 #pragma unroll 1
         for (int u = 0; u < 8; ++u) {  // 8 keys
           const uint32_t m8 = ((u < 4 ? bits[0] : bits[1]) >> (8 * (u & 3))) & 0xFFu;
@@ -368,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_async_smem();
         __syncwarp();
       }
-      if (lane == 0) tc::mbar_arrive(&vready[vs]);
-      vs = vs + 1 == kVStages ? 0 : vs + 1;
-      vp ^= vs == 0;
+      if (lane == 0) tc::mbar_arrive(&ready[st]);
+      st = st + 1 == kStages ? 0 : st + 1;
+      ph ^= st == 0;
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 13);
   } else {
@@ -390,16 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool negate = a.scale < 0.f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
-    int ns = 0;                    // steps done
+    uint32_t sp = 0;               // phases of s_full to come (bit b: buffer b)
+    int done = -1;                 // the last step done
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < seen.n && ok; ++i) {
       const int k0 = seen.chunk(i) * kStep;
       if (!mine.need(k0, sinks)) continue;
-      const int b = ns & 1;
-      ok = wait_or_abort(&s_full[2 * x + b], (ns >> 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      const int b = i & 1;
+      ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
       if (!ok) break;
+      sp ^= 1u << b;
       tc::tc_fence_after();
       uint32_t s[64];
       tmem_ld32(s_tm + 64 * b, s);
@@ -431,9 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
         m = next;
         l *= f;
-        if (ns) {
-          ok = wait_or_abort(&pv_done[2 * x + (b ^ 1)], ((ns - 1) >> 1) & 1, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
+        if (done >= 0) {
+          // O is at rest once the last step's product is in it (S of this step, there already, was
+          // issued after those before)
+          const int d = done & 1;
+          ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ (d != b), abort_flag));
           if (!ok) break;
           tc::tc_fence_after();
 #pragma unroll 1
@@ -463,12 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
       l += (part[0] + part[1]) + (part[2] + part[3]);
-      ++ns;
+      done = i;
     }
     if (ok && seen.n) {
       // O is complete (a tile that saw nothing: Q has landed), so Q's tile is free
-      ok = ns ? wait_or_abort(&pv_done[2 * x + ((ns - 1) & 1)], ((ns - 1) >> 1) & 1, abort_flag)
-              : wait_or_abort(qfull, 0, abort_flag);
+      const int d = done & 1;
+      ok = done >= 0 ? wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ 1, abort_flag)
+                     : wait_or_abort(qfull, 0, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc::tc_fence_after();
     }
@@ -491,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 w[2];
           const int col = (k + b) / size;
           if (a.f32) {
-            if (ns) tc::tmem_ld8(o_tm + col, o);
+            if (done >= 0) tc::tmem_ld8(o_tm + col, o);
           } else {
-            if (ns) tc::tmem_ld16(o_tm + col, o);
+            if (done >= 0) tc::tmem_ld16(o_tm + col, o);
           }
           tc::tmem_ld_wait();
 #pragma unroll
@@ -542,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const PagedAttn& a, cudaStream_t s) {
-  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + (kKStages + kVStages) * kStep * HD * 2 + 512;
+  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + 2 * kStages * kStep * HD * 2 + 512;
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t rc = cudaFuncSetAttribute(k_paged_prefill<HD>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
