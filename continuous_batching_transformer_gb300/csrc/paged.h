@@ -60,4 +60,4 @@ cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s);
 // runs of them
 size_t paged_decode_workspace(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, int num_sms, cudaStream_t s);
-cudaError_t launch_paged_prefill(const PagedAttn& a, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s);

@@ -98,7 +98,7 @@ cudaError_t sm_count(int* n) {
 size_t paged_attn_workspace(const PagedAttn& a) { return a.max_q == 1 ? paged_decode_workspace(a) : 0; }
 
 cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s) {
-  return a.max_q > 1 ? launch_paged_prefill(a, s) : launch_paged_decode(a, num_sms, s);
+  return a.max_q > 1 ? launch_paged_prefill(a, num_sms, s) : launch_paged_decode(a, num_sms, s);
 }
 
 extern "C" cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream) {

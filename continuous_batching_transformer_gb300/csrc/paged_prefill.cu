@@ -61,6 +61,17 @@ CBT_D void tma_load_q(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int
       : "memory");
 }
 
+// 32 bytes to 16-byte aligned global memory; wide: 32-byte aligned
+CBT_D void store32(void* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 CBT_D float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -77,8 +88,36 @@ CBT_D uint64_t desc(uint32_t lo) {
 CBT_HD constexpr uint32_t step_of(int k, int box) { return (uint32_t)((k >> 2) * (box >> 4) + 2 * (k & 3)); }
 
 struct Unit {
-  int b, t0, n;  // row; its query tokens [t0, t0 + n) of this unit, n = -1: no unit
+  int b, t0, n;  // row; its query tokens [t0, t0 + n) of this unit
   int p0;        // position of token t0 (may be negative)
+  int g;         // kv head
+};
+constexpr int kUnits = 48;   // most units of a CTA
+constexpr int kRanked = 64;  // rows up to which they are ranked
+
+// What the roles derive from a unit.  Its steps are the 64-key chunks that any of its queries sees; a
+// tile takes part in those that its own see.
+struct Work {
+  Unit u;
+  int pl, lo_win;  // positions of the last token and of the first token's window
+  Seen seen;
+  int stages;      // steps, and kLag more
+  CBT_D Work(const Unit* s, const PagedAttn& a)
+      : u{uniform(s->b), uniform(s->t0), uniform(s->n), uniform(s->p0), uniform(s->g)} {
+    pl = u.p0 + u.n - 1;
+    lo_win = first_in_window(max(0, u.p0), a.window);
+    seen = seen_chunks<kStep>(u.p0, pl, a.window, a.sinks);
+    stages = seen.n ? seen.n + kLag : 0;
+  }
+};
+struct TileKeys {
+  int last, lo;  // positions of the tile's last token and of its first token's window
+  CBT_D TileKeys(const Work& w, const PagedAttn& a, int x, int TQ) {
+    const int first = w.u.p0 + x * TQ;
+    last = x * TQ < w.u.n ? min(w.pl, first + TQ - 1) : -1;
+    lo = first_in_window(max(0, first), a.window);
+  }
+  CBT_D bool need(int key, int sinks) const { return key <= last && (key + kStep > lo || key < sinks); }
 };
 
 template <int HD>
@@ -101,22 +140,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *qfull = bars, *full = bars + 1, *ready = full + kStages, *empty = ready + kStages;
   // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
   uint64_t *s_full = empty + kStages, *p_full = s_full + 4, *pv_done = p_full + 4;
-  constexpr int kBars = 1 + 3 * kStages + 12;
+  uint64_t* qempty = pv_done + 4;         // both tiles' S of a unit are done
+  constexpr int kBars = 2 + 3 * kStages + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Unit* unit = reinterpret_cast<Unit*>(tmem_slot + 2);
-  int* wsum = reinterpret_cast<int*>(unit + 1);  // [12]
+  int* wsum = reinterpret_cast<int*>(tmem_slot + 2);     // [12]
+  Unit* units = reinterpret_cast<Unit*>(wsum + 12);      // [kUnits]
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
   const int TQ = kRows / G;  // tokens per tile
-  const int g = blockIdx.x % Hkv;
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2);  // both issuers
     for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);       // a tile's softmax warps
+    tc::mbar_init(qempty, 2);
     *abort_flag = 0;
-    unit->n = -1;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tq);
     tc::tma_prefetch_desc(&tk);
@@ -125,67 +164,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
   pdl_wait();
   pdl_launch();
-  // ---- this CTA's unit: units are counted over the rows, thread by thread
-  {
+  const int grid = gridDim.x;
+  auto item_of = [&](int round) {  // items are below 2^31, one round past them in 32 bits too
+    return (unsigned)round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x);
+  };
+  // tokens / (2 TQ), by multiplication where that is exact (a dividend below 2^24, a divisor of 256
+  // at most): a division a row and unit was a third of the search
+  const unsigned inv = 0xFFFFFFFFu / (2 * TQ) + 1;
+  auto in_units = [&](int n) { return n >> 24 ? n / (2 * TQ) : 2 * TQ == 1 ? n : (int)__umulhi(n, inv); };
+  // ---- this CTA's units.  Items are (unit, kv head), dealt to the CTAs forth and back.  With few rows
+  // the units are ranked by their last position (the longest first), each by a thread that counts
+  // the units before it; with many they are taken as they come, the rows' last units first: there
+  // are enough of them then to even out.  (Four 1024-token prompts: 56 us unranked.)
+  int total = 0;
+  auto units_of = [&](int n) { return n > 0 ? in_units(n - 1) + 1 : 0; };
+  if (a.rows <= kRanked) {
+    struct Row {
+      int t0, n, p0, k;  // query tokens, their number, the first one's position, units
+    };
+    Row* rows = reinterpret_cast<Row*>(sQ);  // before Q lands there
+    if (tid < a.rows) {
+      const RowTokens row = row_tokens(a, tid);
+      if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, tid);
+      rows[tid] = Row{row.t0, max(0, row.n), row.len - row.n, units_of(row.n)};
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = 0; r < a.rows; ++r) total += rows[r].k;
+#pragma unroll 1
+    for (int q = tid; q < total; q += kThreads) {
+      int r = 0, first = q;  // unit `first` of row r
+      for (; first >= rows[r].k; ++r) first -= rows[r].k;
+      const Row me = rows[r];
+      const int end = min(me.n, (first + 1) * 2 * TQ), last = me.p0 + end - 1;
+      int rank = 0;
+#pragma unroll 1
+      for (int o = 0; o < a.rows; ++o) {
+        const Row w = rows[o];
+        // units of row o that end at position t or later
+        auto from = [&](int t) {
+          const int d = t - w.p0 + 1;  // tokens up to t
+          return d > w.n ? 0 : w.k - (d > 0 ? in_units(d - 1) : 0);
+        };
+        rank += from(last + (o < r ? 0 : 1));
+      }
+      unsigned round = (unsigned)rank * Hkv / grid;
+      int at = rank * Hkv - round * grid;
+#pragma unroll 1
+      for (int g = 0; g < Hkv; ++g, ++at) {
+        if (at == grid) {
+          at = 0;
+          ++round;
+        }
+        if (at == (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x) && round < kUnits)
+          units[round] = Unit{r, me.t0 + first * 2 * TQ, end - first * 2 * TQ, me.p0 + first * 2 * TQ, g};
+      }
+    }
+    tc::fence_proxy_async_smem();  // Q is written over the rows by the async proxy
+  } else {
     const int per = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
-    int mine = 0, at = 0, u = -1;
+    int mine = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {  // count, then find (rolled: the code is run once a CTA)
-#pragma unroll 1
-      for (int r = r0; r < r1; ++r) {
-        const RowTokens row = row_tokens(a, r);
-        const int k = row.n > 0 ? (row.n + 2 * TQ - 1) / (2 * TQ) : 0;
-        if (pass == 0) {
-          if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, r);
-          mine += k;
-        } else if (u >= at && u < at + k) {
-          const int first = (u - at) * 2 * TQ;
-          *unit = Unit{r, row.t0 + first, min(2 * TQ, row.n - first), row.len - row.n + first};
-        }
-        at += k;
-      }
-      if (pass) break;
-      int inc = mine;
+    for (int r = r0; r < r1; ++r) {
+      const RowTokens row = row_tokens(a, r);
+      if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, r);
+      mine += units_of(row.n);
+    }
+    int inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    const int ws = lane < kThreads / 32 ? wsum[lane] : 0;  // lane w: warp w's sum
+    total = __reduce_add_sync(0xffffffffu, ws);
+    const int begin = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + inc - mine;
+#pragma unroll 1
+    for (int round = 0; round < kUnits; ++round) {
+      const unsigned it = item_of(round);
+      if (it >= (unsigned)(total * Hkv)) break;
+      const int u = total - 1 - (int)(it / Hkv);
+      int at = begin;
+      if (u >= begin && u < begin + mine) {
+#pragma unroll 1
+        for (int r = r0; r < r1; ++r) {
+          const RowTokens row = row_tokens(a, r);
+          const int k = units_of(row.n), first = (u - at) * 2 * TQ;
+          if (u >= at && u < at + k)
+            units[round] = Unit{r, row.t0 + first, min(2 * TQ, row.n - first), row.len - row.n + first,
+                                (int)(it % Hkv)};
+          at += k;
+        }
       }
-      if (lane == 31) wsum[warp] = inc;
-      __syncthreads();
-      // lane w: warp w's sum
-      const int ws = lane < kThreads / 32 ? wsum[lane] : 0;
-      const int total = __reduce_add_sync(0xffffffffu, ws);
-      at = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + inc - mine;
-      u = total - 1 - (int)(blockIdx.x / Hkv);  // last units first
-      if (u < at || u >= at + mine) break;
     }
   }
+  int count = 0;  // only the last round is not full
+  while (count < kUnits && item_of(count) < (unsigned)(total * Hkv)) ++count;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const Unit un{uniform(unit->b), uniform(unit->t0), uniform(unit->n), uniform(unit->p0)};
+  count = uniform(count);
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-  if (un.n < 0) {  // more CTAs than units (the whole block leaves)
-    if (warp == 1) tc::tmem_dealloc(tmem, kTmem);
-    return;
-  }
-
-  // The unit's steps are the 64-key chunks that any of its queries sees; a tile takes part in those
-  // that its own see.
-  const int pl = un.p0 + un.n - 1;  // position of the last token
-  const int lo_win = first_in_window(max(0, un.p0), a.window), sinks = a.window ? a.sinks : 0;
-  const Seen seen = seen_chunks<kStep>(un.p0, pl, a.window, a.sinks);
-  const int stages = seen.n ? seen.n + kLag : 0;
-  struct TileKeys {
-    int last, lo;  // positions of the tile's last token and of its first token's window
-    CBT_D bool need(int key, int sinks) const { return key <= last && (key + kStep > lo || key < sinks); }
-  };
-  auto tile_keys = [&](int x) {
-    const int first = un.p0 + x * TQ;
-    return TileKeys{x * TQ < un.n ? min(pl, first + TQ - 1) : -1, first_in_window(max(0, first), a.window)};
-  };
+  const int sinks = a.window ? a.sinks : 0;
 
   if (warp == 0) {
     // ---- tile requests: per stage K of a step and V of the step kLag before.  The pages of 32 steps
@@ -193,52 +276,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol = tc::policy_evict_last();
     const int P = a.kv.page_tokens;
     int st = 0, n = 0;  // stage, stages requested
-    uint32_t ph = 0;
-    int krow = 0, vrow = 0, vlag[kLag] = {0, 0};
+    uint32_t ph = 0, qp = 0;
+    int qn = 0;         // units whose Q was requested
     bool ok = true;
-    if (seen.n && lane == 0) {
-      const int tiles = un.n > TQ ? 2 : 1;
-      tc::mbar_expect_tx(qfull, tiles * nKh * G * TQ * 128);
 #pragma unroll 1
-      for (int x = 0; x < tiles; ++x)
-        for (int h = 0; h < nKh; ++h)
-          tma_load_q(sQ + x * kTile + h * kBox, &tq, qfull, h * 64, g * G, un.t0 + x * TQ);
-    }
+    for (int k = 0; k < count && ok; ++k) {
+      const Work w(units + k, a);
+      if (!w.stages) continue;
+      int krow = 0, vrow = 0, vlag[kLag] = {0, 0};
 #pragma unroll 1
-    for (int i = 0; i < stages; ++i) {
-      if ((i & 31) == 0 && i + lane < seen.n) {
-        const int key = seen.chunk(i + lane) * kStep, pg = key / P, o = key - pg * P;
-        int id = a.table[(size_t)un.b * a.max_pages + pg];
-        if (id < 0 || id >= a.kv.n_pages) {
-          set_device_error(a.err, CBT_DEV_PAGE_ID, un.b);
-          id = 0;  // a page that exists: the row's outputs are unspecified
+      for (int i = 0; i < w.stages; ++i) {
+        if ((i & 31) == 0 && i + lane < w.seen.n) {
+          const int key = w.seen.chunk(i + lane) * kStep, pg = key / P, o = key - pg * P;
+          int id = a.table[(size_t)w.u.b * a.max_pages + pg];
+          if (id < 0 || id >= a.kv.n_pages) {
+            set_device_error(a.err, CBT_DEV_PAGE_ID, w.u.b);
+            id = 0;  // a page that exists: the row's outputs are unspecified
+          }
+          krow = (int)(paged_k(a.kv, id, w.u.g, o, 0) / HD);
+          vrow = (int)(paged_v(a.kv, id, w.u.g, o, 0) / 64);
         }
-        krow = (int)(paged_k(a.kv, id, g, o, 0) / HD);
-        vrow = (int)(paged_v(a.kv, id, g, o, 0) / 64);
-      }
-      const int kr = __shfl_sync(0xffffffffu, krow, i & 31), vr = __shfl_sync(0xffffffffu, vrow, i & 31);
-      ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], ph ^ 1, abort_flag));
-      if (!ok) break;
-      const bool has_k = i < seen.n, has_v = i >= kLag;
-      if (elect_one()) {
-        tc::mbar_expect_tx(&full[st], (has_k ? kKV : 0) + (has_v ? kKV : 0));
-        if (has_k) {
+        if (i == 0) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
+          if (!ok) break;
+          qp ^= 1;
+          ++qn;
+          if (lane == 0) {
+            const int tiles = w.u.n > TQ ? 2 : 1;
+            tc::mbar_expect_tx(qfull, tiles * nKh * G * TQ * 128);
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x)
+              for (int h = 0; h < nKh; ++h)
+                tma_load_q(sQ + x * kTile + h * kBox, &tq, qfull, h * 64, w.u.g * G, w.u.t0 + x * TQ);
+          }
+          __syncwarp();
+        }
+        const int kr = __shfl_sync(0xffffffffu, krow, i & 31), vr = __shfl_sync(0xffffffffu, vrow, i & 31);
+        ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], ph ^ 1, abort_flag));
+        if (!ok) break;
+        const bool has_k = i < w.seen.n, has_v = i >= kLag;
+        if (elect_one()) {
+          tc::mbar_expect_tx(&full[st], (has_k ? kKV : 0) + (has_v ? kKV : 0));
+          if (has_k) {
 #pragma unroll
-          for (int h = 0; h < nKh; ++h)
-            tc::tma_load_2d(sK + st * kKV + h * (kBox / 2), &tk, &full[st], h * 64, kr, pol);
+            for (int h = 0; h < nKh; ++h)
+              tc::tma_load_2d(sK + st * kKV + h * (kBox / 2), &tk, &full[st], h * 64, kr, pol);
+          }
+          if (has_v) tc::tma_load_2d(sV + st * kKV, &tv, &full[st], 0, vlag[0], pol);
         }
-        if (has_v) tc::tma_load_2d(sV + st * kKV, &tv, &full[st], 0, vlag[0], pol);
+        ++n;
+        st = st + 1 == kStages ? 0 : st + 1;
+        ph ^= st == 0;
+        vlag[0] = vlag[1];
+        vlag[1] = vr;
       }
-      ++n;
-      st = st + 1 == kStages ? 0 : st + 1;
-      ph ^= st == 0;
-      vlag[0] = vlag[1];
-      vlag[1] = vr;
     }
     if (lane == 0) {
       if (!ok) wait_timeout(a.err, abort_flag, 11);
       // no copies in flight at exit
-      if (seen.n) wait_landed(qfull, 0);
+      if (qn) wait_landed(qfull, (qn - 1) & 1);
 #pragma unroll 1
       for (int i = max(0, n - kStages); i < n; ++i) wait_landed(&full[i % kStages], (i / kStages) & 1);
     }
@@ -246,20 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- MMA issue of tile x: per stage P V of the step kLag before, then S of the step into the
     // buffer this freed.  So a step's scores are there before the softmax asks for them, and it
     // never waits for its own P V.
-    if (seen.n) {
-      const int x = warp - 1;
-      const TileKeys mine = tile_keys(x);
-      const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
-      const uint32_t dq = desc_lo(sQ + x * kTile), dk = desc_lo(sK), dv = desc_lo(sV);
-      int st = 0;
-      uint32_t ph = 0, pp = 0;  // phases of the stages, and of p_full (bit b: buffer b)
-      uint32_t took = 0;        // bit j: the tile took part in the step j before this one
-      uint32_t acc = 0;
-      bool ok = __all_sync(0xffffffffu, wait_or_abort(qfull, 0, abort_flag));
+    const int x = warp - 1;
+    const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
+    const uint32_t dq = desc_lo(sQ + x * kTile), dk = desc_lo(sK), dv = desc_lo(sV);
+    int st = 0;
+    uint32_t ph = 0, pp = 0, qp = 0;  // phases of the stages, of p_full (bit b: buffer b) and of Q
+    bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < stages && ok; ++i) {
+    for (int k = 0; k < count && ok; ++k) {
+      const Work w(units + k, a);
+      if (!w.stages) continue;
+      const TileKeys mine(w, a, x, TQ);
+      uint32_t took = 0;  // bit j: the tile took part in the step j before this one
+      uint32_t acc = 0;   // O holds something of this unit
+      ok = __all_sync(0xffffffffu, wait_or_abort(qfull, qp, abort_flag));
+      qp ^= 1;
+#pragma unroll 1
+      for (int i = 0; i < w.stages && ok; ++i) {
         const int b = i & 1;
-        const bool need = i < seen.n && mine.need(seen.chunk(i) * kStep, sinks), due = took >> (kLag - 1) & 1;
+        const bool need = i < w.seen.n && mine.need(w.seen.chunk(i) * kStep, sinks);
+        const bool due = took >> (kLag - 1) & 1;
         ok = __all_sync(0xffffffffu, wait_or_abort(&ready[st], ph, abort_flag));
         if (due) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&p_full[2 * x + b], pp >> b & 1, abort_flag));
         if (!ok) break;
@@ -268,19 +370,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (due) {
             const uint32_t v = dv + st * (kKV >> 4);
 #pragma unroll
-            for (int k = 0; k < kStep / 16; ++k)
-              tc::mma_bf16_ta(o_tm, s_tm + 64 * b + 8 * k, desc(v + 2 * k), kIdescO, (acc || k > 0) ? 1u : 0u);
+            for (int e = 0; e < kStep / 16; ++e)
+              tc::mma_bf16_ta(o_tm, s_tm + 64 * b + 8 * e, desc(v + 2 * e), kIdescO, (acc || e > 0) ? 1u : 0u);
             tc::mma_commit(&pv_done[2 * x + b]);
           }
           if (need) {
             const uint32_t kd = dk + st * (kKV >> 4);
 #pragma unroll
-            for (int k = 0; k < HD / 16; ++k)
-              tc::mma_bf16(s_tm + 64 * b, desc(dq + step_of(k, kBox)), desc(kd + step_of(k, kBox / 2)), kIdescS,
-                           k > 0 ? 1u : 0u);
+            for (int e = 0; e < HD / 16; ++e)
+              tc::mma_bf16(s_tm + 64 * b, desc(dq + step_of(e, kBox)), desc(kd + step_of(e, kBox / 2)), kIdescS,
+                           e > 0 ? 1u : 0u);
             tc::mma_commit(&s_full[2 * x + b]);
           }
           tc::mma_commit(&empty[st]);
+          if (i == w.seen.n - 1) tc::mma_commit(qempty);
         }
         if (due) {
           pp ^= 1u << b;
@@ -290,202 +393,185 @@ __global__ void __launch_bounds__(kThreads, 1)
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0;
       }
-      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 12);
     }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 12);
   } else if (warp == 3) {
     // ---- V of keys that no query of the unit sees is cleared
     bool ok = true;
     int st = 0;
     uint32_t ph = 0;
 #pragma unroll 1
-    for (int i = 0; i < stages && ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
-      if (!ok) break;
-      uint32_t bits[2] = {~0u, ~0u};
-      if (i >= kLag) seen_bits(seen.chunk(i - kLag) * kStep, pl, lo_win, sinks, bits);
-      if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
-        uint8_t* v = sV + st * kKV;
+    for (int k = 0; k < count && ok; ++k) {
+      const Work w(units + k, a);
 #pragma unroll 1
-        for (int u = 0; u < 8; ++u) {  // 8 keys
-          const uint32_t m8 = ((u < 4 ? bits[0] : bits[1]) >> (8 * (u & 3))) & 0xFFu;
-          if (m8 == 0xFFu) continue;
-          const uint4 mk = key_mask(m8);
-          for (int d = lane; d < HD; d += 32) {
-            uint4* p = reinterpret_cast<uint4*>(v + d * 128 + ((u ^ (d & 7)) << 4));
-            uint4 z = make_uint4(0, 0, 0, 0);
-            if (m8) z = *p;
-            *p = make_uint4(z.x & mk.x, z.y & mk.y, z.z & mk.z, z.w & mk.w);
+      for (int i = 0; i < w.stages && ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
+        if (!ok) break;
+        uint32_t bits[2] = {~0u, ~0u};
+        if (i >= kLag) seen_bits(w.seen.chunk(i - kLag) * kStep, w.pl, w.lo_win, sinks, bits);
+        if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
+          uint8_t* v = sV + st * kKV;
+#pragma unroll 1
+          for (int u = 0; u < 8; ++u) {  // 8 keys
+            const uint32_t m8 = ((u < 4 ? bits[0] : bits[1]) >> (8 * (u & 3))) & 0xFFu;
+            if (m8 == 0xFFu) continue;
+            const uint4 mk = key_mask(m8);
+            for (int d = lane; d < HD; d += 32) {
+              uint4* p = reinterpret_cast<uint4*>(v + d * 128 + ((u ^ (d & 7)) << 4));
+              uint4 z = make_uint4(0, 0, 0, 0);
+              if (m8) z = *p;
+              *p = make_uint4(z.x & mk.x, z.y & mk.y, z.z & mk.z, z.w & mk.w);
+            }
           }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ready[st]);
+        st = st + 1 == kStages ? 0 : st + 1;
+        ph ^= st == 0;
       }
-      if (lane == 0) tc::mbar_arrive(&ready[st]);
-      st = st + 1 == kStages ? 0 : st + 1;
-      ph ^= st == 0;
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 13);
   } else {
     // ---- softmax of tile x: thread = row
     const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const TileKeys mine = tile_keys(x);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tmem + x * 128 + lane_off, o_tm = tmem + 256 + x * HD + lane_off;
-    const int tok = x * TQ + row / G;          // token of the unit
-    const bool live = row < TQ * G && tok < un.n;
-    const int p = live ? un.p0 + tok : -1;     // -1: sees nothing
-    // rows that hold no token are left unmasked: what they compute is not stored
-    const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
     // Scores in units of log2.  A negative scale negates them first, so that the largest product is
     // the largest score's; a zero scale stands for one that leaves every weight 1 (a masked -inf
     // must stay -inf).
     const bool negate = a.scale < 0.f;
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
-    float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
-    uint32_t sp = 0;               // phases of s_full to come (bit b: buffer b)
-    int done = -1;                 // the last step done
+    uint32_t sp = 0;  // phases of s_full to come (bit b: buffer b)
     bool ok = true;
+    // rows of out on 32-byte boundaries: whole sectors a store
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.out_ld % (a.f32 ? 8 : 16) == 0;
 #pragma unroll 1
-    for (int i = 0; i < seen.n && ok; ++i) {
-      const int k0 = seen.chunk(i) * kStep;
-      if (!mine.need(k0, sinks)) continue;
-      const int b = i & 1;
-      ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
-      if (!ok) break;
-      sp ^= 1u << b;
-      tc::tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32(s_tm + 64 * b, s);
-      tmem_ld32(s_tm + 64 * b + 32, s + 32);
-      tc::tmem_ld_wait();
-      if (negate) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] ^= 0x80000000u;
-      }
-      // every row sees every key of the step, or keys are masked one by one
-      if (!__all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64))) {
-        uint32_t bits[2];
-        seen_bits(k0, hi, lo, sinks, bits);
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (!((bits[e >> 5] >> (e & 31)) & 1)) s[e] = 0xFF800000u;  // -inf
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale2;
-      const bool up = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
-      if (__any_sync(0xffffffffu, up)) {
-        // Rows that exceed their reference by more than 2^kSlack, or see their first keys, raise
-        // it, to a whole number: what the old one has scaled is multiplied by a power of two,
-        // which rounds nothing.
-        const float next = up ? ceilf(top) : m;
-        const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
-        m = next;
-        l *= f;
-        if (done >= 0) {
-          // O is at rest once the last step's product is in it (S of this step, there already, was
-          // issued after those before)
-          const int d = done & 1;
-          ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ (d != b), abort_flag));
-          if (!ok) break;
-          tc::tc_fence_after();
+    for (int unit = 0; unit < count && ok; ++unit) {
+      const Work w(units + unit, a);
+      const TileKeys mine(w, a, x, TQ);
+      const int tok = x * TQ + row / G;  // token of the unit
+      const bool live = row < TQ * G && tok < w.u.n;
+      const int p = live ? w.u.p0 + tok : -1;  // -1: sees nothing
+      // rows that hold no token are left unmasked: what they compute is not stored
+      const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
+      float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
+      int done = -1;                 // the last step done
 #pragma unroll 1
-          for (int d = 0; d < HD; d += 16) {
-            uint32_t o[16];
-            tc::tmem_ld16(o_tm + d, o);
-            tc::tmem_ld_wait();
+      for (int i = 0; i < w.seen.n && ok; ++i) {
+        const int k0 = w.seen.chunk(i) * kStep;
+        if (!mine.need(k0, sinks)) continue;
+        const int b = i & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
+        if (!ok) break;
+        sp ^= 1u << b;
+        tc::tc_fence_after();
+        uint32_t s[64];
+        tmem_ld32(s_tm + 64 * b, s);
+        tmem_ld32(s_tm + 64 * b + 32, s + 32);
+        tc::tmem_ld_wait();
+        if (negate) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(o_tm + d, o);
+          for (int e = 0; e < 64; ++e) s[e] ^= 0x80000000u;
+        }
+        // every row sees every key of the step, or keys are masked one by one
+        if (!__all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64))) {
+          uint32_t bits[2];
+          seen_bits(k0, hi, lo, sinks, bits);
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((bits[e >> 5] >> (e & 31)) & 1)) s[e] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale2;
+        const bool up = m == -INFINITY ? top > -INFINITY : top > m + kSlack;
+        if (__any_sync(0xffffffffu, up)) {
+          // Rows that exceed their reference by more than 2^kSlack, or see their first keys, raise
+          // it, to a whole number: what the old one has scaled is multiplied by a power of two,
+          // which rounds nothing.
+          const float next = up ? ceilf(top) : m;
+          const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
+          m = next;
+          l *= f;
+          if (done >= 0) {
+            // O is at rest once the last step's product is in it (S of this step, there already, was
+            // issued after those before)
+            const int d = done & 1;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ (d != b), abort_flag));
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_tm + d, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_tm + d, o);
+            }
           }
         }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+        const float ref = m == -INFINITY ? 0.f : m;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale2, -ref));
-        const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -ref));
-        part[e & 3] += p0;
-        part[(e + 2) & 3] += p1;
-        s[e] = pack_bf16(p0, p1);
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale2, -ref));
+          const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -ref));
+          part[e & 3] += p0;
+          part[(e + 2) & 3] += p1;
+          s[e] = pack_bf16(p0, p1);
+        }
+        tc::tmem_st32(s_tm + 64 * b, s);  // over the scores
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
+        l += (part[0] + part[1]) + (part[2] + part[3]);
+        done = i;
       }
-      tc::tmem_st32(s_tm + 64 * b, s);  // over the scores
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
-      l += (part[0] + part[1]) + (part[2] + part[3]);
-      done = i;
-    }
-    if (ok && seen.n) {
-      // O is complete (a tile that saw nothing: Q has landed), so Q's tile is free
-      const int d = done & 1;
-      ok = done >= 0 ? wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ 1, abort_flag)
-                     : wait_or_abort(qfull, 0, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::tc_fence_after();
-    }
-    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 14);
-    if (ok) {
-      // Out through shared memory (Q's tile, no longer read): a lane holds a row, and its row alone
-      // would touch a cache line a lane; turned around, a warp's store fills whole lines.
+      // The row goes straight out (through shared memory and in whole lines it took as long).  O is
+      // not written again before this tile hands in weights of the next unit.
+      if (ok && done >= 0) {
+        const int d = done & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ 1, abort_flag));
+        tc::tc_fence_after();
+      }
+      if (!ok) break;
       const float inv = p >= 0 ? 1.f / l : 0.f;
-      uint8_t* stage = sQ + x * kTile + quarter * (kTile / 4);  // [32 rows][kLine bytes]
-      const int size = a.f32 ? 4 : 2;
-      const long long at =
-          ((long long)(un.t0 + tok) * a.out_ld + (long long)(g * G + row % G) * HD) * size;
-      constexpr int kLine = HD;  // bytes of a row at a time: 128 (head_dim 128) or 64
+      const long long at = (long long)(w.u.t0 + tok) * a.out_ld + (long long)(w.u.g * G + row % G) * HD;
 #pragma unroll 1
-      for (int k = 0; k < HD * size; k += kLine) {  // byte k of the row
-#pragma unroll
-        for (int b = 0; b < kLine; b += 32) {
-          // 8 fp32 or 16 bf16 values
-          uint32_t o[16];
-          uint4 w[2];
-          const int col = (k + b) / size;
-          if (a.f32) {
-            if (done >= 0) tc::tmem_ld8(o_tm + col, o);
-          } else {
-            if (done >= 0) tc::tmem_ld16(o_tm + col, o);
-          }
+      for (int k = 0; k < HD; k += 16) {
+        uint32_t o[16];
+        if (done >= 0) {
+          tc::tmem_ld16(o_tm + k, o);
           tc::tmem_ld_wait();
+        }
+        float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = p >= 0 ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          if (a.f32) {
-            w[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            w[1] = make_uint4(o[4], o[5], o[6], o[7]);
-          } else {
+        for (int e = 0; e < 16; ++e) v[e] = p >= 0 ? __uint_as_float(o[e]) * inv : 0.f;
+        if (!live) continue;
+        if (a.f32) {
+          float* dst = static_cast<float*>(a.out) + at + k;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
             uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              h[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            w[0] = make_uint4(h[0], h[1], h[2], h[3]);
-            w[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int j = 0; j < 8; ++j) h[j] = __float_as_uint(v[e + j]);
+            store32(dst + e, h, wide);
           }
+        } else {
+          uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int u = b / 16 + e;  // 16-byte unit of the row, swizzled by the row
-            *reinterpret_cast<uint4*>(stage + lane * kLine + ((u ^ (lane & (kLine / 16 - 1))) << 4)) = w[e];
-          }
+          for (int j = 0; j < 8; ++j) h[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          store32(static_cast<uint16_t*>(a.out) + at + k, h, wide);
         }
-        __syncwarp();
-        constexpr int kUnits = kLine / 16;
-        const int u = lane % kUnits;
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 32 / kUnits) {
-          const int r = r0 + lane / kUnits;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kLine + ((u ^ (r & (kUnits - 1))) << 4));
-          const long long to = __shfl_sync(0xffffffffu, at, r);
-          if (__shfl_sync(0xffffffffu, (int)live, r))
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to + k + u * 16) = w;
-        }
-        __syncwarp();
       }
+      tc::tc_fence_before();
     }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 14);
     tc::tc_fence_before();
   }
   __syncthreads();
@@ -497,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                      const PagedAttn& a, cudaStream_t s) {
-  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + 2 * kStages * kStep * HD * 2 + 512;
+                      const PagedAttn& a, int num_sms, cudaStream_t s) {
+  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + 2 * kStages * kStep * HD * 2 + 1536;
   static_assert(smem <= 227 * 1024, "shared memory budget");
   const cudaError_t rc = cudaFuncSetAttribute(k_paged_prefill<HD>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -508,17 +594,19 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const long long by_tokens = (long long)a.tokens / run + a.rows;
   const long long by_rows = (long long)a.rows * ((a.max_q + run - 1) / run);
   const long long units = by_tokens < by_rows ? by_tokens : by_rows;
-  return launch_pdl(k_paged_prefill<HD>, dim3((unsigned)(units * a.kv.n_kv_heads)), dim3(kThreads), smem, s,
-                    tq, tk, tv, a);
+  const long long items = units * a.kv.n_kv_heads, least = (items + kUnits - 1) / kUnits;
+  const long long grid = items < num_sms ? items : least > num_sms ? least : num_sms;
+  return launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_prefill(const PagedAttn& a, cudaStream_t s) {
+cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   const int G = a.n_heads / a.kv.n_kv_heads;
   if (!paged_maps(a.kv, &tk, &tv) ||
       !make_tmap_rows(&tq, a.q, a.kv.head_dim, a.n_heads, a.tokens, a.q_ld, G, kRows / G))
     return cudaErrorInvalidValue;
-  return a.kv.head_dim == 128 ? launch_hd<128>(tq, tk, tv, a, s) : launch_hd<64>(tq, tk, tv, a, s);
+  return a.kv.head_dim == 128 ? launch_hd<128>(tq, tk, tv, a, num_sms, s)
+                              : launch_hd<64>(tq, tk, tv, a, num_sms, s);
 }
