@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
   float* red2 = red + 32;
   float* l_run = red2 + 32;                             // [8]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Layout lay = layout_of(a);
   const int per_row = a.kv.n_kv_heads * lay.groups;
   if (tid == 0) {
@@ -186,66 +186,94 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   pdl_wait();
   pdl_launch();
   Cursor cur;
   cur.load(a, per_row, 0, 0);
 
   if (warp == 4) {
-    // ---- tile requests: K, then V of each chunk
+    // ---- tile requests: K, then V of each chunk.  The next chunk's pages are looked up while V's
+    // buffer is awaited, so that K's stays empty for a wait only.
     const uint64_t pol = tc::policy_evict_first();
-    uint32_t n = 0, nk = 0, nv = 0;  // chunks, and tiles of K and of V requested (lane 0)
+    uint32_t n = 0, nk = 0, nv = 0;  // chunks, and tiles of K and of V requested
     bool ok = true;
     const int P = a.kv.page_tokens;
-    for (int it = blockIdx.x; ok && cur.seek(a, per_row, it); it += gridDim.x) {
-      const Item w = item_at(cur, a, lay.groups, it);
-      for (int i = w.i0; i < w.i1 && ok; ++i, ++n) {
-        const int c = w.seen.chunk(i);
-        // lanes 0 and 1: the page of each 64-key half, -1 where no key of it is seen
-        const int k0 = c * kSub + 64 * lane;
-        int krow = 0, vrow = 0;
-        bool want = false;
-        if (lane < 2) {
-          want = k0 <= w.p && (sees(k0, w.p, a.window, a.sinks) ||
-                               sees(min(k0 + 63, w.p), w.p, a.window, a.sinks));
-          if (want) {
-            const int pg = k0 / P, o = k0 - pg * P;
-            int id = a.table[(size_t)w.b * a.max_pages + pg];
-            if (id < 0 || id >= a.kv.n_pages) {
-              set_device_error(a.err, CBT_DEV_PAGE_ID, w.b);
-              id = 0;  // a page that exists: the row's outputs are unspecified
-            }
-            krow = (int)(paged_k(a.kv, id, w.g, o, 0) / HD);
-            vrow = (int)(paged_v(a.kv, id, w.g, o, 0) / 64);
-          }
-        }
-        const unsigned halves = __ballot_sync(0xffffffffu, want);
-        const int kr1 = __shfl_sync(0xffffffffu, krow, 1), vr1 = __shfl_sync(0xffffffffu, vrow, 1);
-        if (lane == 0) {
-          const uint32_t bytes = __popc(halves) * 64 * HD * 2;
-          ok = wait_or_abort(kempty, (n & 1) ^ 1, abort_flag);
-          if (ok) {
-            tc::mbar_expect_tx(kfull, bytes);
-            ++nk;
-#pragma unroll
-            for (int h = 0; h < nKh; ++h) {
-              if (halves & 1) tc::tma_load_2d(sK + h * kBox, &tk, kfull, h * 64, krow, pol);
-              if (halves & 2) tc::tma_load_2d(sK + h * kBox + 8192, &tk, kfull, h * 64, kr1, pol);
-            }
-            ok = wait_or_abort(vempty, (n & 1) ^ 1, abort_flag);
-            if (ok) {
-              tc::mbar_expect_tx(vfull, bytes);
-              ++nv;
-              if (halves & 1) tc::tma_load_2d(sV, &tv, vfull, 0, vrow, pol);
-              if (halves & 2) tc::tma_load_2d(sV + kBox, &tv, vfull, 0, vr1, pol);
-            }
-          }
-          if (!ok) wait_timeout(a.err, abort_flag, 1);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      }
+    // a chunk's halves of 64 keys that hold a key the query sees, and their rows in the two maps
+    struct Chunk {
+      unsigned halves;
+      int k[2], v[2];
+    };
+    int it = blockIdx.x, i = 0;
+    bool have = cur.seek(a, per_row, it);
+    Item w{};
+    if (have) {
+      w = item_at(cur, a, lay.groups, it);
+      i = w.i0;
     }
+    auto next = [&]() {  // halves 0: no chunk is left
+      Chunk c{};
+      while (have && i >= w.i1) {
+        it += gridDim.x;
+        have = cur.seek(a, per_row, it);
+        if (have) {
+          w = item_at(cur, a, lay.groups, it);
+          i = w.i0;
+        }
+      }
+      if (!have) return c;
+      // lanes 0 and 1: a half each
+      const int k0 = w.seen.chunk(i++) * kSub + 64 * lane;
+      int krow = 0, vrow = 0;
+      const bool want = lane < 2 && k0 <= w.p && (sees(k0, w.p, a.window, a.sinks) ||
+                                                   sees(min(k0 + 63, w.p), w.p, a.window, a.sinks));
+      if (want) {
+        const int pg = k0 / P, o = k0 - pg * P;
+        int id = a.table[(size_t)w.b * a.max_pages + pg];
+        if (id < 0 || id >= a.kv.n_pages) {
+          set_device_error(a.err, CBT_DEV_PAGE_ID, w.b);
+          id = 0;  // a page that exists: the row's outputs are unspecified
+        }
+        krow = (int)(paged_k(a.kv, id, w.g, o, 0) / HD);
+        vrow = (int)(paged_v(a.kv, id, w.g, o, 0) / 64);
+      }
+      c.halves = __ballot_sync(0xffffffffu, want);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c.k[e] = __shfl_sync(0xffffffffu, krow, e);
+        c.v[e] = __shfl_sync(0xffffffffu, vrow, e);
+      }
+      return c;
+    };
+    Chunk c = next();
+#pragma unroll 1
+    for (; c.halves; ++n) {
+      const uint32_t bytes = __popc(c.halves) * 64 * HD * 2;
+      ok = __all_sync(0xffffffffu, wait_or_abort(kempty, (n & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (elect_one()) {
+        tc::mbar_expect_tx(kfull, bytes);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int h = 0; h < nKh; ++h)
+            if (c.halves >> e & 1)
+              tc::tma_load_2d(sK + h * kBox + e * (kBox / 2), &tk, kfull, h * 64, c.k[e], pol);
+      }
+      ++nk;
+      const Chunk nxt = next();
+      ok = __all_sync(0xffffffffu, wait_or_abort(vempty, (n & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (elect_one()) {
+        tc::mbar_expect_tx(vfull, bytes);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (c.halves >> e & 1) tc::tma_load_2d(sV + e * kBox, &tv, vfull, 0, c.v[e], pol);
+      }
+      ++nv;
+      c = nxt;
+    }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 1);
     // no copies in flight at exit
     if (nk) wait_landed(kfull, (nk - 1) & 1);
     if (nv) wait_landed(vfull, (nv - 1) & 1);
@@ -290,11 +318,11 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
       tc::named_bar_sync(1, kCompute);
 
       for (int i = w.i0; i < w.i1; ++i, ++n) {
-        if (tid == 0 || tid == 32) {
-          const int iss = tid >> 5;
-          if (!wait_or_abort(kfull, n & 1, abort_flag)) {
-            wait_timeout(a.err, abort_flag, 2);
-          } else {
+        if (warp < kIssuers) {
+          const int iss = warp;
+          if (!__all_sync(0xffffffffu, wait_or_abort(kfull, n & 1, abort_flag))) {
+            if (lane == 0) wait_timeout(a.err, abort_flag, 2);
+          } else if (elect_one()) {
             tc::tc_fence_after();
             constexpr int kSteps = HD / 16 / kIssuers;
 #pragma unroll
@@ -391,11 +419,11 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
             if (h == tid) sc = scl[h];
           l_run[tid] = l_run[tid] * sc + red2[tid] + red2[8 + tid] + red2[16 + tid] + red2[24 + tid];
         }
-        if (tid == 0 || tid == 32) {
-          const int iss = tid >> 5;
-          if (!wait_or_abort(vfull, n & 1, abort_flag)) {
-            wait_timeout(a.err, abort_flag, 4);
-          } else {
+        if (warp < kIssuers) {
+          const int iss = warp;
+          if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
+            if (lane == 0) wait_timeout(a.err, abort_flag, 4);
+          } else if (elect_one()) {
             tc::tc_fence_after();
             constexpr int kSteps = kSub / 16 / kIssuers;
 #pragma unroll
