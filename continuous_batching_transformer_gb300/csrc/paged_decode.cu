@@ -15,9 +15,13 @@
 //
 // Work is dealt on the device from the rows' lengths, so a captured launch stays valid while they
 // grow: a persistent grid walks items (row, kv head, group of 8 q heads, run of chunks), each warp
-// finding its item's row from prefix sums over 32 rows at a time kept in registers.  A run is one
-// chunk, or two from kLongChunks visible chunks on; it depends on the row alone, and so does the
-// order in which k_paged_merge adds the runs' (max, sum, output).  Rows of one run are finished here.
+// finding its item's row from prefix sums over 32 rows at a time kept in registers.  A run's length
+// depends on the row alone, and so does the order in which k_paged_merge adds the runs' (max, sum,
+// output).  Rows of one run are finished here.
+//
+// Measured on one GB300 (graph replays): 32 rows of 8192 to 16384 positions, 32 / 8 heads of 128, 245
+// us = 6.7 TB/s, all of the measured copy rate; 8 rows of 512 to 4096 15.6 us, where 2.5 chunks a CTA
+// do not divide evenly and the join takes 3 us.
 #include "paged_attn.cuh"
 
 namespace {
@@ -28,13 +32,23 @@ constexpr int kCompute = 128;  // warps 0..3; warp 4 requests tiles
 constexpr int kCtasPerSm = 3;
 constexpr int kIssuers = 2;    // threads that issue half of each contraction's MMAs
 constexpr uint32_t kTmemCols = 64;
-constexpr int kLongChunks = 64;
 constexpr int kGroup = 8;      // q heads per item
 
-CBT_HD int chunks_per_run(int n) { return n >= kLongChunks ? 2 : 1; }
+// Chunks of a run, by the chunks n that the row sees alone (so that its result does not depend on the
+// other rows).  Longer runs halve the partial outputs and their join; shorter ones spread a few rows
+// over the SMs: in us, 32 rows of 64 to 128 chunks 244 by fours, 251 by twos; one row of 64 chunks
+// 11.3 by fours, 10.4 by twos; 16 rows of 33 chunks 47.0 by twos, 48.3 singly.  Up to three chunks are
+// one run, which needs no join (one row of two chunks 6.4 against 7.4).
+CBT_HD int chunks_per_run(int n) { return n >= 96 ? 4 : n >= 32 ? 2 : n > 3 ? 1 : n > 0 ? n : 1; }
 CBT_HD int runs_of(int n) {  // a row that sees nothing has one run, which writes its zeros
   const int per = chunks_per_run(n);
   return n <= 0 ? 1 : (n + per - 1) / per;
+}
+CBT_HD int most_runs(int n) {  // of any row that sees n chunks or fewer
+  int r = runs_of(n);
+  if (n >= 32) r = r > 31 ? r : 31;
+  if (n >= 96) r = r > 48 ? r : 48;
+  return r;
 }
 
 struct Layout {
@@ -49,10 +63,7 @@ __host__ __device__ inline Layout layout_of(const PagedAttn& a) {
     const long long w = ((long long)a.sinks + kSub - 1) / kSub + (a.window + kSub - 2) / kSub + 1;
     n = w < n ? (int)w : n;
   }
-  // runs_of is not monotone at kLongChunks
-  int r = runs_of(n);
-  if (n >= kLongChunks) r = r > kLongChunks - 1 ? r : kLongChunks - 1;
-  return {(G + kGroup - 1) / kGroup, r};
+  return {(G + kGroup - 1) / kGroup, most_runs(n)};
 }
 
 // The rows' items in flat order, walked forward by a whole warp: lane i keeps row w0 + i and the
@@ -188,7 +199,6 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
   tc::tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   pdl_wait();
-  pdl_launch();
   Cursor cur;
   cur.load(a, per_row, 0, 0);
 
@@ -484,6 +494,8 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
       tc::named_bar_sync(1, kCompute);
     }
   }
+  // Only now: the join's blocks, resident early, slowed the streaming down by a fifth (301 us for 250)
+  pdl_launch();
   tc::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
