@@ -23,10 +23,16 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
 
-struct Sums {  // 64-bit: the lengths are checked row by row, their sums are not yet
-  long long tok, take, back;
+// Sums that stop at kFull instead of overflowing: the lengths are checked row by row, their sums are
+// not yet
+constexpr unsigned kFull = 0x7FFFFFFFu;
+struct Sums {
+  unsigned tok, take, back;
 };
-CBT_D Sums operator+(Sums a, Sums b) { return {a.tok + b.tok, a.take + b.take, a.back + b.back}; }
+CBT_D unsigned add_full(unsigned a, unsigned b) { return min(a + b, kFull); }
+CBT_D Sums operator+(Sums a, Sums b) {
+  return {add_full(a.tok, b.tok), add_full(a.take, b.take), add_full(a.back, b.back)};
+}
 CBT_D Sums shfl_up(Sums v, int o) {
   return {__shfl_up_sync(0xffffffffu, v.tok, o), __shfl_up_sync(0xffffffffu, v.take, o),
           __shfl_up_sync(0xffffffffu, v.back, o)};
@@ -51,14 +57,29 @@ CBT_D int find_row(const int* pre, int n, int i) {
   return lo;
 }
 
+// n / d for 0 <= n < 2^31 as a multiplication: with 2^(s - 1) < d <= 2^s and m = ceil(2^(31 + s) / d),
+// n m / 2^(31 + s) exceeds n / d by less than n / 2^31 / d, too little to reach the next whole number
+struct Divide {
+  unsigned m, s;
+};
+Divide divide_by(unsigned d) {
+  unsigned s = 0;
+  while ((1ull << s) < d) ++s;
+  return {(unsigned)(((1ull << (31 + s)) + d - 1) / d), s};
+}
+CBT_D int quotient(int n, Divide d) { return d.s ? (int)(__umulhi(n, d.m) >> (d.s - 1)) : n; }
+
 template <int C>
-__global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a) {
+__global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a, const Divide page) {
   extern __shared__ int sm[];
   const int B = a.rows, P = a.page_tokens;
+  // pages of n positions; the most a row may have, max_pages * P, is below 2^31
+  auto pages = [&](int n) { return n > 0 ? quotient(n - 1, page) + 1 : 0; };
   int* cu = sm;              // [B + 1] new tokens
   int* take = sm + B + 1;    // [B + 1] pages to take
   int* back = take + B + 1;  // [B + 1] pages to return
   int* len = back + B + 1;   // [B] lengths before the call
+  int* held = len + B;       // [B] and pages
   __shared__ Sums wtot[kThreads / 32];
   __shared__ int bad_row;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -73,6 +94,11 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   const int per = (B + kThreads - 1) / kThreads;
   const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
   const long long most = (long long)a.max_pages * P;
+  auto row_sums = [&](int n, int w) {
+    const int h = pages(n);
+    return Sums{w > 0 ? (unsigned)w : 0u, pool && w > 0 ? (unsigned)(pages(n + w) - h) : 0u,
+                pool && w < 0 ? (unsigned)h : 0u};
+  };
   Sums mine = {0, 0, 0};
   for (int r = r0; r < r1; ++r) {
     const int n = a.kv_lens[r], w = a.new_lens[r];
@@ -80,42 +106,39 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
       atomicMin(&bad_row, r);
       continue;
     }
-    const int held = (int)(((long long)n + P - 1) / P);
-    mine.tok += w > 0 ? w : 0;
-    mine.take += pool && w > 0 ? (int)(((long long)n + w + P - 1) / P) - held : 0;
-    mine.back += pool && w < 0 ? held : 0;
+    mine = mine + row_sums(n, w);
   }
   Sums inc = warp_scan(mine, lane);
   if (lane == 31) wtot[warp] = inc;
   __syncthreads();
   if (warp == 0) wtot[lane] = warp_scan(wtot[lane], lane);
   __syncthreads();
+  const Sums tot = wtot[kThreads / 32 - 1];
+  // the sums before this thread's rows (used only where none is full)
   Sums run = warp ? wtot[warp - 1] + inc : inc;
   run = {run.tok - mine.tok, run.take - mine.take, run.back - mine.back};
-  const Sums tot = wtot[kThreads / 32 - 1];
   const int count = pool ? *a.free_count : 0;
   int code = 0, info = 0;
   if (bad_row != INT_MAX) {
     code = CBT_DEV_LENGTH;
     info = bad_row;
-  } else if (tot.tok > a.max_tokens) {
+  } else if (tot.tok > (unsigned)a.max_tokens || tot.tok == kFull) {
     code = CBT_DEV_TOKENS;
     info = a.max_tokens;
-  } else if (pool && (count < 0 || count + tot.back > a.n_pages || tot.take > count + tot.back)) {
+  } else if (pool && (count < 0 || count + (long long)tot.back > a.n_pages ||
+                      (long long)tot.take > count + (long long)tot.back)) {
     code = CBT_DEV_PAGES;
-    info = (int)min((long long)INT_MAX, max(0ll, tot.take - count - tot.back));
+    info = (int)min((long long)INT_MAX, max(0ll, (long long)tot.take - count - tot.back));
   }
   if (code == 0) {
     for (int r = r0; r < r1; ++r) {
       const int n = a.kv_lens[r], w = a.new_lens[r];
-      const int held = (int)(((long long)n + P - 1) / P);
       cu[r] = (int)run.tok;
       take[r] = (int)run.take;
       back[r] = (int)run.back;
       len[r] = n;
-      run.tok += w > 0 ? w : 0;
-      run.take += pool && w > 0 ? (int)(((long long)n + w + P - 1) / P) - held : 0;
-      run.back += pool && w < 0 ? held : 0;
+      held[r] = pages(n);
+      run = run + row_sums(n, w);
     }
     if (tid == 0) {
       cu[B] = (int)tot.tok;
@@ -127,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   const int t0 = rank * kThreads + tid;
   constexpr int kStep = C * kThreads;
   if (code == 0 && pool) {  // push the retiring rows' pages
-    for (int i = t0; i < tot.back; i += kStep) {
+    for (int i = t0; i < (int)tot.back; i += kStep) {
       const int r = find_row(back, B, i);
       const int id = a.block_table[(size_t)r * a.max_pages + (i - back[r])];
       if (id < 0 || id >= a.n_pages) set_device_error(a.err, CBT_DEV_PAGE_ID, r);
@@ -157,36 +180,56 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   }
   const int top = (int)(count + tot.back) - 1;
   if (pool) {
-    for (int i = t0; i < tot.take; i += kStep) {
+    for (int i = t0; i < (int)tot.take; i += kStep) {
       const int r = find_row(take, B, i);
-      const int held = (int)(((long long)len[r] + P - 1) / P);
-      a.block_table[(size_t)r * a.max_pages + held + (i - take[r])] = __ldcg(a.free_pages + top - i);
+      a.block_table[(size_t)r * a.max_pages + held[r] + (i - take[r])] = __ldcg(a.free_pages + top - i);
     }
   }
-  for (int t = t0; t < a.max_tokens; t += kStep) {
-    int pos = -1, slot = -1;
-    if (t < cu[B]) {
-      const int r = find_row(cu, B, t);
-      pos = len[r] + t - cu[r];
-      const int pg = pos / P;
-      const int held = (int)(((long long)len[r] + P - 1) / P);
-      // a page taken by this call is read from the stack, not from the table being written
-      const int id = pool && pg >= held ? __ldcg(a.free_pages + top - (take[r] + pg - held))
-                                        : a.block_table[(size_t)r * a.max_pages + pg];
-      if (id < 0 || id >= a.n_pages) set_device_error(a.err, CBT_DEV_PAGE_ID, r);
-      else slot = id * P + (pos - pg * P);
+  // tokens, four of a thread's at a time: their searches and page loads overlap
+  const int n_tok = cu[B];
+  int step0 = 1;
+  while (2 * step0 < B) step0 *= 2;
+  constexpr int kAtOnce = 4;
+  for (int tb = t0; tb < a.max_tokens; tb += kAtOnce * kStep) {
+    int r[kAtOnce] = {}, pos[kAtOnce], off[kAtOnce], id[kAtOnce];
+    for (int s = step0; s > 0; s >>= 1) {
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (r[e] + s < B && cu[r[e] + s] <= tb + e * kStep) r[e] += s;
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int t = tb + e * kStep;
+      pos[e] = id[e] = -1;
+      off[e] = 0;
+      if (t < n_tok) {
+        const int n = len[r[e]];
+        pos[e] = n + t - cu[r[e]];
+        const int pg = quotient(pos[e], page), h = held[r[e]];
+        off[e] = pos[e] - pg * P;
+        // a page taken by this call is read from the stack, not from the table being written
+        id[e] = __ldcg(pool && pg >= h ? a.free_pages + top - (take[r[e]] + pg - h)
+                                       : a.block_table + (size_t)r[e] * a.max_pages + pg);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int t = tb + e * kStep;
+      if (t >= a.max_tokens) break;
+      const bool good = id[e] >= 0 && id[e] < a.n_pages;
+      if (t < n_tok && !good) set_device_error(a.err, CBT_DEV_PAGE_ID, r[e]);
+      a.positions[t] = pos[e];
+      a.slots[t] = good ? id[e] * P + off[e] : -1;
+    }
   }
 }
 
 template <int C>
 cudaError_t launch(const cbt_page_map_args& a, cudaStream_t s) {
-  const size_t smem = ((size_t)a.rows * 4 + 3) * sizeof(int);
+  const size_t smem = ((size_t)a.rows * 5 + 3) * sizeof(int);
   if (smem > 48 * 1024) {
     cudaError_t rc = cudaFuncSetAttribute(k_page_map<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (4 * CBT_PAGE_MAP_MAX_ROWS + 3) * (int)sizeof(int));
+                                          (5 * CBT_PAGE_MAP_MAX_ROWS + 3) * (int)sizeof(int));
     if (rc != cudaSuccess) return rc;
   }
   cudaLaunchConfig_t cfg = {};
@@ -204,7 +247,7 @@ cudaError_t launch(const cbt_page_map_args& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, k_page_map<C>, a);
+  return cudaLaunchKernelEx(&cfg, k_page_map<C>, a, divide_by(a.page_tokens));
 }
 
 }  // namespace

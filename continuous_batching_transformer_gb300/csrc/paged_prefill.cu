@@ -163,7 +163,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
   pdl_wait();
-  pdl_launch();
   const int grid = gridDim.x;
   auto item_of = [&](int round) {  // items are below 2^31, one round past them in 32 bits too
     return (unsigned)round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x);
@@ -574,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 14);
     tc::tc_fence_before();
   }
+  pdl_launch();
   __syncthreads();
   if (warp == 1) {
     tc::tc_fence_after();

@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 5)
     k_rope_append(const __grid_constant__ RopeAppend a, int qk_blocks, int runs, int per) {
   extern __shared__ __align__(16) uint8_t sm[];
   pdl_wait();
-  pdl_launch();
   if ((int)blockIdx.x < qk_blocks) {
     const int warp = threadIdx.x >> 5;
     const long long w = (long long)blockIdx.x * kWarps + warp;
@@ -311,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 5)
     const int b = blockIdx.x - qk_blocks;
     append_v<HD, F32>(a, b / a.kv.n_kv_heads * kVTokens, b % a.kv.n_kv_heads, sm);
   }
+  pdl_launch();
 }
 
 template <int HD, bool F32, int MODE>
