@@ -198,6 +198,7 @@ struct cbt_engine {
     int32_t *table = nullptr, *lens = nullptr, *fresh = nullptr, *lens_out = nullptr;
     int32_t *cu = nullptr, *positions = nullptr, *slots = nullptr;
     uint8_t* ws = nullptr;
+    size_t ws_bytes = 0;
     std::vector<int32_t> htable, hlens, hfresh;
   } form;
 
@@ -1268,6 +1269,7 @@ static PagedAttn form_attn_args(const cbt_engine* e, int n, int layer, bool deco
   a.out = e->o;
   a.f32 = true;
   a.ws = f.ws;
+  a.ws_bytes = f.ws_bytes;
   a.err = e->err;
   return a;
 }
@@ -1349,8 +1351,9 @@ static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t*
     PagedAttn most = form_attn_args(e, mb, 0, true);  // a decode step of max_batch rows
     most.rows = mb;
     most.max_q = 1;
-    const size_t ws = paged_attn_workspace(most);
-    if (rc == cudaSuccess && ws) rc = cudaMalloc(reinterpret_cast<void**>(&f.ws), ws);
+    const size_t ws = std::max(paged_attn_workspace(most), paged_prefill_most_workspace(e->cfg.head_dim));
+    if (rc == cudaSuccess) rc = cudaMalloc(reinterpret_cast<void**>(&f.ws), ws);
+    f.ws_bytes = ws;
     if (rc != cudaSuccess) {
       f.max_kv = 0;
       return rc;

@@ -52,6 +52,7 @@ struct PagedAttn {
   bool f32;
   long long out_ld;
   uint8_t* ws;
+  size_t ws_bytes;
   int* err;
 };
 size_t paged_attn_workspace(const PagedAttn& a);
@@ -60,4 +61,6 @@ cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s);
 // runs of them
 size_t paged_decode_workspace(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, int num_sms, cudaStream_t s);
+size_t paged_prefill_workspace(const PagedAttn& a);
+size_t paged_prefill_most_workspace(int head_dim);  // of any call with tokens <= rows * max_q
 cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s);

@@ -55,8 +55,10 @@ cbt_status attn_sizes(const cbt_paged_attention_args& a) {
   if (a.rows > CBT_PAGED_ATTENTION_MAX_ROWS || (int64_t)a.max_kv + a.window > INT32_MAX ||
       (int64_t)a.max_kv + a.sinks > INT32_MAX ||
       (int64_t)a.n_heads * a.kv.head_dim > INT32_MAX / 4 ||
-      // work items and grid dimensions stay below 2^31 and 65536
-      ((double)a.rows + a.tokens) * a.n_heads * (a.max_kv / 128.0 + 2) > (double)INT32_MAX)
+      // work items and grid dimensions stay below 2^31; one token per row: an item for every 128 keys
+      ((double)a.rows + a.tokens) * a.n_heads >= (double)(1 << 29) ||
+      (a.max_q == 1 &&
+       ((double)a.rows + a.tokens) * a.n_heads * (a.max_kv / 128.0 + 2) > (double)INT32_MAX))
     return CBT_ERR_LIMIT;
   return CBT_OK;
 }
@@ -82,6 +84,7 @@ PagedAttn attn_args(const cbt_paged_attention_args& a, const PagedKv& kv) {
   p.f32 = a.out_dtype == CBT_DTYPE_F32;
   p.out_ld = a.out_stride;
   p.ws = static_cast<uint8_t*>(a.workspace);
+  p.ws_bytes = a.workspace_bytes;
   p.err = a.err;
   return p;
 }
@@ -95,9 +98,12 @@ cudaError_t sm_count(int* n) {
 
 }  // namespace
 
-size_t paged_attn_workspace(const PagedAttn& a) { return a.max_q == 1 ? paged_decode_workspace(a) : 0; }
+size_t paged_attn_workspace(const PagedAttn& a) {
+  return a.max_q == 1 ? paged_decode_workspace(a) : paged_prefill_workspace(a);
+}
 
 cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s) {
+  if (paged_attn_workspace(a) > a.ws_bytes) return cudaErrorInvalidValue;
   return a.max_q > 1 ? launch_paged_prefill(a, num_sms, s) : launch_paged_decode(a, num_sms, s);
 }
 

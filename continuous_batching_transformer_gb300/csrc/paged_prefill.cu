@@ -3,22 +3,25 @@
 // A unit is a run of query tokens of one row and one kv head, as two tiles of 128 tensor-core rows.
 // A tile's rows are (token, q head) pairs: the q heads that read the kv head lie next to each other,
 // so a tile holds 128 / G tokens with all G of their heads, a decode row or a short chunk fills its
-// tile with heads, and one K and V tile serves all of them.  Per 128-key block and tile:
-//   S = Q K^T       tcgen05.mma 128 x 128 x head_dim into tensor memory
+// tile with heads, and one K and V tile serves all of them.  Per step of 64 keys and tile:
+//   S = Q K^T       tcgen05.mma 128 x 64 x head_dim into tensor memory
 //   softmax         one thread per row: the whole row of S in registers, running maximum and sum
-//   O += P V        tcgen05.mma 128 x head_dim x 128, P read from tensor memory as bf16 where S was
-// O stays in tensor memory for the whole unit.  A row's reference maximum is raised (and its O
-// rescaled) only when a block exceeds it by more than 2^kSlack, so O is rarely touched, and weights
-// stay below 2^kSlack.  P is rounded to bf16 once (2^-9 of each
-// weight on average less), everything else is fp32.
+//   O += P V        tcgen05.mma 128 x head_dim x 64, P read from tensor memory as bf16 where S was
+// O stays in tensor memory for the whole unit.  A row's reference is its maximum so far, rounded up to
+// a whole number of powers of two and raised (with a rescaling of O, exact) only when a step exceeds
+// it by more than 2^kSlack: O is rarely touched, and weights stay below 2^kSlack.  P is rounded to
+// bf16 once (at most 2^-8 of each weight, as the tensor cores take it), everything else is fp32.
 //
-// Bound by the tensor cores and, close behind, the exponentials.  The two tiles of a unit run half
-// a block out of step, each with an issuer thread and a softmax warpgroup of its own: one's MMAs
-// run under the other's softmax.  K and V tiles come through two TMA maps over the whole pool (64
-// keys a request, each from its own page) into rings of three and two stages.  A warp of its own
-// clears V of keys that no query of the unit sees (what lies there may not be finite) before the
-// MMA reads it.  One CTA per unit; units are found on the device from the rows' lengths, the rows'
-// last units (the longest) first.
+// Long units are bound by the tensor cores and, close behind, the exponentials; a unit of one tile
+// by its own chain of S, softmax and P V (0.7 to 0.8 us a step).  Each tile has an issuer warp and a
+// softmax warpgroup of its own and two buffers of S, so that one step's MMAs run under another's
+// softmax.  K and V come through two TMA maps over the whole pool (64 keys a request, each from its own
+// page) into one ring of stages; a stage holds K of a step and V of the step kLag before it, which is
+// when that is needed, so that an issuer waits once a step.  A warp of its own clears V of keys that
+// no query of the unit sees (what lies there may not be finite) before the MMA reads it.  CTAs stay
+// for several units, which they find from the rows' lengths: the longest first, dealt back and forth.
+// Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 41 us (830 TFLOP/s); four chunks
+// of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 169 us (1095 TFLOP/s).
 #include "paged_attn.cuh"
 
 namespace {
@@ -91,9 +94,30 @@ struct Unit {
   int b, t0, n;  // row; its query tokens [t0, t0 + n) of this unit
   int p0;        // position of token t0 (may be negative)
   int g;         // kv head
+  int s0, s1;    // the steps [s0, s1) of the unit that this item takes
+  int run;       // which of the unit's runs they are
 };
 constexpr int kUnits = 48;   // most units of a CTA
 constexpr int kRanked = 64;  // rows up to which they are ranked
+
+// Few units over long contexts: a unit's steps are cut into up to `runs` runs of kRunSteps steps or
+// more, taken by different CTAs and joined by k_prefill_merge, where all runs find an SM at once.
+// Whole and cut, rows of 4 tokens, 32 q and 8 kv heads of 128: one over 2000 positions 28 and 16 us, over
+// 131072 1460 and 100 us (5.4 TB/s of K and V); eight over 4096 54 and 40 us.  One of 512 tokens over
+// 16384: 203 and 142 us.  With runs of 16 steps the first takes 21 us.  With twice as many items,
+// two rounds: 114 us for the second, 97 us for a prompt of 1024 (34 us whole, as here).
+constexpr int kRunSteps = 8;
+constexpr int kFewItems = 152;  // items that the runs may make: one for each SM
+CBT_HD int ceil_div(int n, int d) { return (n + d - 1) / d; }
+// The steps of each run of a unit, the last one's aside, and how many runs hold any: every one of them
+// is written, and those behind are not read.
+CBT_HD int run_length(int steps, int runs) {
+  const int most = ceil_div(steps, kRunSteps);
+  return most <= 1 ? (steps > 0 ? steps : 1) : ceil_div(steps, runs < most ? runs : most);
+}
+CBT_HD int run_count(int steps, int runs) {
+  return steps > 0 ? ceil_div(steps, run_length(steps, runs)) : 1;
+}
 
 // What the roles derive from a unit.  Its steps are the 64-key chunks that any of its queries sees; a
 // tile takes part in those that its own see.
@@ -101,14 +125,17 @@ struct Work {
   Unit u;
   int pl, lo_win;  // positions of the last token and of the first token's window
   Seen seen;
-  int stages;      // steps, and kLag more
+  int steps, stages;  // steps of the item, and kLag more
   CBT_D Work(const Unit* s, const PagedAttn& a)
-      : u{uniform(s->b), uniform(s->t0), uniform(s->n), uniform(s->p0), uniform(s->g)} {
+      : u{uniform(s->b), uniform(s->t0), uniform(s->n), uniform(s->p0), uniform(s->g), uniform(s->s0),
+          uniform(s->s1)} {
     pl = u.p0 + u.n - 1;
     lo_win = first_in_window(max(0, u.p0), a.window);
     seen = seen_chunks<kStep>(u.p0, pl, a.window, a.sinks);
-    stages = seen.n ? seen.n + kLag : 0;
+    steps = u.s1 - u.s0;
+    stages = steps > 0 ? steps + kLag : 0;
   }
+  CBT_D int key(int i) const { return seen.chunk(u.s0 + i) * kStep; }  // the first of step i
 };
 struct TileKeys {
   int last, lo;  // positions of the tile's last token and of its first token's window
@@ -123,7 +150,8 @@ struct TileKeys {
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttn a) {
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttn a,
+                    const int runs, float* __restrict__ part_o, float2* __restrict__ part_ml) {
   constexpr int nKh = HD / 64;
   constexpr uint32_t kTile = nKh * kBox;     // a Q tile
   constexpr uint32_t kKV = kStep * HD * 2;   // K or V of a step
@@ -207,16 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         rank += from(last + (o < r ? 0 : 1));
       }
-      unsigned round = (unsigned)rank * Hkv / grid;
-      int at = rank * Hkv - round * grid;
+      const int p0 = me.p0 + first * 2 * TQ;
+      const int steps = seen_chunks<kStep>(p0, last, a.window, a.sinks).n;
+      const int per = run_length(steps, runs), cuts = run_count(steps, runs);
+      unsigned round = (unsigned)rank * (Hkv * runs) / grid;
+      int at = rank * (Hkv * runs) - round * grid;
 #pragma unroll 1
-      for (int g = 0; g < Hkv; ++g, ++at) {
+      for (int e = 0; e < Hkv * runs; ++e, ++at) {
         if (at == grid) {
           at = 0;
           ++round;
         }
-        if (at == (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x) && round < kUnits)
-          units[round] = Unit{r, me.t0 + first * 2 * TQ, end - first * 2 * TQ, me.p0 + first * 2 * TQ, g};
+        if (at == (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x) && round < kUnits) {
+          const int g = e / runs, run = e - g * runs;  // past the unit's last run: no tokens, no steps
+          units[round] = Unit{r, me.t0 + first * 2 * TQ, run < cuts ? end - first * 2 * TQ : 0, p0, g,
+                              min(run * per, steps), min((run + 1) * per, steps), run};
+        }
       }
     }
     tc::fence_proxy_async_smem();  // Q is written over the rows by the async proxy
@@ -252,16 +286,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = r0; r < r1; ++r) {
           const RowTokens row = row_tokens(a, r);
           const int k = units_of(row.n), first = (u - at) * 2 * TQ;
-          if (u >= at && u < at + k)
-            units[round] = Unit{r, row.t0 + first, min(2 * TQ, row.n - first), row.len - row.n + first,
-                                (int)(it % Hkv)};
+          if (u >= at && u < at + k) {
+            const int n = min(2 * TQ, row.n - first), p0 = row.len - row.n + first;
+            units[round] = Unit{r, row.t0 + first, n, p0, (int)(it % Hkv), 0,
+                                seen_chunks<kStep>(p0, p0 + n - 1, a.window, a.sinks).n, 0};
+          }
           at += k;
         }
       }
     }
   }
   int count = 0;  // only the last round is not full
-  while (count < kUnits && item_of(count) < (unsigned)(total * Hkv)) ++count;
+  while (count < kUnits && item_of(count) < (unsigned)(total * Hkv * runs)) ++count;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -285,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int krow = 0, vrow = 0, vlag[kLag] = {0, 0};
 #pragma unroll 1
       for (int i = 0; i < w.stages; ++i) {
-        if ((i & 31) == 0 && i + lane < w.seen.n) {
-          const int key = w.seen.chunk(i + lane) * kStep, pg = key / P, o = key - pg * P;
+        if ((i & 31) == 0 && i + lane < w.steps) {
+          const int key = w.key(i + lane), pg = key / P, o = key - pg * P;
           int id = a.table[(size_t)w.u.b * a.max_pages + pg];
           if (id < 0 || id >= a.kv.n_pages) {
             set_device_error(a.err, CBT_DEV_PAGE_ID, w.u.b);
@@ -313,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kr = __shfl_sync(0xffffffffu, krow, i & 31), vr = __shfl_sync(0xffffffffu, vrow, i & 31);
         ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], ph ^ 1, abort_flag));
         if (!ok) break;
-        const bool has_k = i < w.seen.n, has_v = i >= kLag;
+        const bool has_k = i < w.steps, has_v = i >= kLag;
         if (elect_one()) {
           tc::mbar_expect_tx(&full[st], (has_k ? kKV : 0) + (has_v ? kKV : 0));
           if (has_k) {
@@ -359,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < w.stages && ok; ++i) {
         const int b = i & 1;
-        const bool need = i < w.seen.n && mine.need(w.seen.chunk(i) * kStep, sinks);
+        const bool need = i < w.steps && mine.need(w.key(i), sinks);
         const bool due = took >> (kLag - 1) & 1;
         ok = __all_sync(0xffffffffu, wait_or_abort(&ready[st], ph, abort_flag));
         if (due) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&p_full[2 * x + b], pp >> b & 1, abort_flag));
@@ -382,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mma_commit(&s_full[2 * x + b]);
           }
           tc::mma_commit(&empty[st]);
-          if (i == w.seen.n - 1) tc::mma_commit(qempty);
+          if (i == w.steps - 1) tc::mma_commit(qempty);
         }
         if (due) {
           pp ^= 1u << b;
@@ -407,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
         if (!ok) break;
         uint32_t bits[2] = {~0u, ~0u};
-        if (i >= kLag) seen_bits(w.seen.chunk(i - kLag) * kStep, w.pl, w.lo_win, sinks, bits);
+        if (i >= kLag) seen_bits(w.key(i - kLag), w.pl, w.lo_win, sinks, bits);
         if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {
           uint8_t* v = sV + st * kKV;
 #pragma unroll 1
@@ -457,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;  // the reference (a maximum so far, rounded up) and the sum
       int done = -1;                 // the last step done
 #pragma unroll 1
-      for (int i = 0; i < w.seen.n && ok; ++i) {
-        const int k0 = w.seen.chunk(i) * kStep;
+      for (int i = 0; i < w.steps && ok; ++i) {
+        const int k0 = w.key(i);
         if (!mine.need(k0, sinks)) continue;
         const int b = i & 1;
         ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
@@ -539,8 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
       }
       if (!ok) break;
-      const float inv = p >= 0 ? 1.f / l : 0.f;
-      const long long at = (long long)(w.u.t0 + tok) * a.out_ld + (long long)(w.u.g * G + row % G) * HD;
+      // a run of several hands over O as it is, with its reference and sum
+      const int head = w.u.g * G + row % G;
+      const size_t part = ((size_t)(w.u.t0 + tok) * H + head) * runs + units[unit].run;
+      const float inv = runs > 1 ? 1.f : p >= 0 ? 1.f / l : 0.f;
+      if (runs > 1 && live) part_ml[part] = make_float2(m, l);
+      const long long at = (long long)(w.u.t0 + tok) * a.out_ld + (long long)head * HD;
 #pragma unroll 1
       for (int k = 0; k < HD; k += 16) {
         uint32_t o[16];
@@ -552,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = p >= 0 ? __uint_as_float(o[e]) * inv : 0.f;
         if (!live) continue;
-        if (a.f32) {
-          float* dst = static_cast<float*>(a.out) + at + k;
+        if (a.f32 || runs > 1) {
+          float* dst = runs > 1 ? part_o + part * HD + k : static_cast<float*>(a.out) + at + k;
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             uint32_t h[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[j] = __float_as_uint(v[e + j]);
-            store32(dst + e, h, wide);
+            store32(dst + e, h, wide || runs > 1);
           }
         } else {
           uint32_t h[8];
@@ -581,6 +621,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the runs of a (token, q head), a block each: every warp finds the common reference and sum,
+// a lane per run, then takes every fourth run's O, HD / 32 dims a lane; the warps' sums are added in
+// order.  (One warp that took the runs one after the other waited a trip to memory for each: 33 us
+// more for 37 runs of four tokens and 32 heads.)
+template <int HD>
+__global__ void __launch_bounds__(128)
+    k_prefill_merge(const __grid_constant__ PagedAttn a, const int runs, const float* __restrict__ part_o,
+                    const float2* __restrict__ part_ml) {
+  constexpr int R = HD / 32;
+  __shared__ float sums[4][HD];
+  pdl_wait();
+  pdl_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = (int)(blockIdx.x / a.n_heads), h = (int)(blockIdx.x - (unsigned)t * a.n_heads);
+  int lo = 0, hi = a.rows;  // the row of token t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const RowTokens row = row_tokens(a, lo);
+  if (row.n <= 0 || t < row.t0 || t >= row.t0 + row.n) return;  // the whole block
+  const int width = 2 * (kRows / (a.n_heads / a.kv.n_kv_heads)), first = (t - row.t0) / width * width;
+  const int p0 = row.len - row.n + first, pl = row.len - row.n + min(row.n, first + width) - 1;
+  const int count = run_count(seen_chunks<kStep>(p0, pl, a.window, a.sinks).n, runs);
+  const size_t base = (size_t)blockIdx.x * runs;
+  float m = -INFINITY, l = 0.f, acc[R];
+  for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(part_ml + base + i).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const float2 v = i0 + lane < count ? __ldcg(part_ml + base + i0 + lane) : make_float2(-INFINITY, 0.f);
+    const float mine = v.x == -INFINITY ? 0.f : ex2(v.x - m);  // 0: a run of which the token sees nothing
+    l += mine == 0.f ? 0.f : v.y * mine;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float wgt = __shfl_sync(0xffffffffu, mine, j + warp);
+      if (i0 + j + warp >= count) continue;
+      const float* o = part_o + (base + i0 + j + warp) * HD + lane;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float x = __ldcg(o + 32 * r);
+        acc[r] = wgt == 0.f ? acc[r] : fmaf(x, wgt, acc[r]);  // what such a run left is not a number
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int r = 0; r < R; ++r) sums[warp][32 * r + lane] = acc[r];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= HD) return;
+  const float x = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
+  const float y = m == -INFINITY ? 0.f : x / l;
+  const long long at = t * a.out_ld + (long long)h * HD + d;
+  if (a.f32) static_cast<float*>(a.out)[at] = y;
+  else static_cast<uint16_t*>(a.out)[at] = round_bf16(y);
+}
+
+// The most runs a unit is cut into (1: none), from the call's sizes alone
+int runs_for(const PagedAttn& a) {
+  const int width = 2 * (kRows / (a.n_heads / a.kv.n_kv_heads));  // tokens of a unit
+  const long long items = (long long)a.rows * (((long long)a.max_q + width - 1) / width) * a.kv.n_kv_heads;
+  if (a.rows > kRanked || items <= 0 || items > kFewItems / 2) return 1;
+  long long keys = a.max_kv;  // that a unit sees at most
+  if (a.window) {
+    const long long some = (long long)a.window + width + a.sinks + 2 * kStep;
+    keys = keys < some ? keys : some;
+  }
+  return run_count((int)((keys + kStep - 1) / kStep), (int)(kFewItems / items));
+}
+
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const PagedAttn& a, int num_sms, cudaStream_t s) {
@@ -594,12 +710,29 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const long long by_tokens = (long long)a.tokens / run + a.rows;
   const long long by_rows = (long long)a.rows * ((a.max_q + run - 1) / run);
   const long long units = by_tokens < by_rows ? by_tokens : by_rows;
-  const long long items = units * a.kv.n_kv_heads, least = (items + kUnits - 1) / kUnits;
+  const int runs = runs_for(a);
+  const long long items = units * a.kv.n_kv_heads * runs, least = (items + kUnits - 1) / kUnits;
   const long long grid = items < num_sms ? items : least > num_sms ? least : num_sms;
-  return launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a);
+  float* po = reinterpret_cast<float*>(a.ws);
+  const size_t parts = (size_t)a.tokens * a.n_heads * runs;
+  float2* pml = reinterpret_cast<float2*>(a.ws + parts * HD * sizeof(float));
+  const cudaError_t launched =
+      launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, po, pml);
+  if (launched != cudaSuccess || runs == 1) return launched;
+  const long long pairs = (long long)a.tokens * a.n_heads;
+  return launch_pdl(k_prefill_merge<HD>, dim3((unsigned)pairs), dim3(128), 0, s, a, runs, po, pml);
 }
 
 }  // namespace
+
+size_t paged_prefill_workspace(const PagedAttn& a) {
+  const int runs = runs_for(a);
+  return runs == 1 ? 0 : (size_t)a.tokens * a.n_heads * runs * (a.kv.head_dim * sizeof(float) + sizeof(float2));
+}
+// of tokens <= rows * max_q: a row of a tile each for the most items
+size_t paged_prefill_most_workspace(int head_dim) {
+  return (size_t)kFewItems * 2 * kRows * (head_dim * sizeof(float) + sizeof(float2));
+}
 
 cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s) {
   CUtensorMap tq, tk, tv;

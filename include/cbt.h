@@ -521,8 +521,9 @@ cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
  * position p attends to positions j <= p with j > p - window or j < sinks (window 0: all j <= p):
  *   out = sum_j softmax_j(scale * q . k_j) v_j, q head h reading kv head h / (n_heads / n_kv_heads).
  * A query that sees nothing (its row holds fewer positions than query tokens) gets zeros; out rows
- * past cu_q[rows] are left as they are.  What masked positions hold, NaN and infinities among it,
- * changes nothing.
+ * past cu_q[rows] are left as they are.  What positions hold that no query token of the row sees,
+ * NaN and infinities among it, changes nothing.  (V that is not finite where one query token of a
+ * row sees it may reach the row's other query tokens: their weight of it is 0, and 0 * NaN is NaN.)
  *   block_table  int32 [rows][max_pages]
  *   max_q, max_kv  upper bounds of n_b and kv_lens[b] that the caller vouches for: they size the
  *                launch and the workspace.  A row above either, or with more positions than its
@@ -535,11 +536,15 @@ cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
  *   workspace    cbt_paged_attention_workspace bytes, 256-byte aligned (NULL if that is 0).  Calls
  *                that overlap on the GPU, graph replays among them, need workspaces of their own.
  * scale is finite; window and sinks are >= 0 (sinks without a window change nothing).  Scores,
- * softmax sums and outputs are accumulated in fp32.  A row's result does not depend on the other
- * rows of the call.  n_heads / n_kv_heads <= 64, q and out 16-byte aligned, strides multiples of 8
+ * softmax sums and outputs are accumulated in fp32, in an order that the sizes fix: the same call
+ * gives the same bits again.  What the other rows hold never changes a row's result.  With max_q
+ * == 1 neither does how many there are; with more, rows, max_q and max_kv decide whether long rows
+ * are summed in several runs, so calls of different sizes may differ in the last bits.
+ * n_heads / n_kv_heads <= 64, q and out 16-byte aligned, strides multiples of 8
  * elements, kv.head_dim 64 or 128 (CBT_ERR_UNSUPPORTED); rows <= CBT_PAGED_ATTENTION_MAX_ROWS,
- * max_kv + window and max_kv + sinks < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL,
- * CBT_ERR_INVALID (a workspace that is too small among it), CBT_ERR_CUDA. */
+ * max_kv + window and max_kv + sinks < 2^31, (rows + tokens) * n_heads < 2^29 and with max_q == 1
+ * (rows + tokens) * n_heads * (max_kv / 128 + 2) < 2^31 (CBT_ERR_LIMIT).  Other errors:
+ * CBT_ERR_NULL, CBT_ERR_INVALID (a workspace that is too small among it), CBT_ERR_CUDA. */
 #define CBT_PAGED_ATTENTION_MAX_ROWS 4096
 typedef struct {
   cbt_paged_kv kv;
