@@ -6,6 +6,9 @@
 
 namespace {
 
+// most tokens or pages of a call: the kernels' 32-bit counters step past the last by less than this
+constexpr int32_t kMostTokens = 1 << 30;
+
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // checks a descriptor and converts it to elements
@@ -112,7 +115,8 @@ extern "C" cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream) {
   if (a->rows < 0 || a->max_pages <= 0 || a->page_tokens <= 0 || a->n_pages <= 0 || a->max_tokens < 0)
     return CBT_ERR_INVALID;
   if (a->rows > CBT_PAGE_MAP_MAX_ROWS || (int64_t)a->max_pages * a->page_tokens > INT32_MAX ||
-      (int64_t)a->n_pages * a->page_tokens > INT32_MAX)
+      (int64_t)a->n_pages * a->page_tokens > INT32_MAX ||
+      a->max_tokens > kMostTokens || a->n_pages > kMostTokens)
     return CBT_ERR_LIMIT;
   if (a->rows == 0) return CBT_OK;
   if (!a->block_table || !a->kv_lens || !a->new_lens || !a->kv_lens_out || !a->cu_q || !a->err ||
@@ -181,7 +185,7 @@ extern "C" cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* strea
       (a->rope && !rope_ok(*a->rope, hd)))
     return CBT_ERR_INVALID;
   // 65535: the launch's limit on its second grid dimension, far above any head count in use
-  if (width > INT32_MAX / 4 || (int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads > 65535)
+  if (a->tokens > kMostTokens || width > INT32_MAX / 4 || (int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads > 65535)
     return CBT_ERR_LIMIT;
   if (a->tokens == 0) return CBT_OK;
   if (!a->qkv || !a->q_out || !a->positions || !a->slots || !a->err) return CBT_ERR_NULL;

@@ -81,7 +81,7 @@ def _rows(t, what, dtypes, index, tokens, width):
         if n > 1 and s != inner:
             raise ValueError(f"{what}: rows are not contiguous (strides {t.stride()})")
         inner *= n
-    return max(t.stride(0), width) if tokens <= 1 else t.stride(0)
+    return width if tokens <= 1 else t.stride(0)  # of a single row no stride is used
 
 
 _I32, _BF16, _ROWS = (torch.int32,), (torch.bfloat16,), (torch.bfloat16, torch.float32)

@@ -422,8 +422,8 @@ typedef struct {
  * were, cu_q is all zero and positions and slots are all -1, so the calls that follow find no
  * tokens.
  * Output arrays may not overlap anything else the call reads, but for the two named pairs.
- * rows <= CBT_PAGE_MAP_MAX_ROWS (CBT_ERR_LIMIT); max_pages * page_tokens < 2^31 and n_pages *
- * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_CUDA. */
+ * rows <= CBT_PAGE_MAP_MAX_ROWS, max_tokens and n_pages <= 2^30, max_pages * page_tokens < 2^31
+ * and n_pages * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_CUDA. */
 #define CBT_PAGE_MAP_MAX_ROWS 4096
 typedef struct {
   int32_t* block_table;
@@ -492,12 +492,13 @@ cbt_status cbt_rope_init(const cbt_rope_config* c, int32_t head_dim, cbt_rope* o
  *   positions  int32 [tokens], >= 0 where the slot is
  *   slots      int32 [tokens]; a token whose slot or position is negative is skipped: its q_out
  *              row and the cache stay as they are.  A slot of n_pages * page_tokens or more is
- *              skipped too (CBT_DEV_PAGE_ID, info: token).  Two tokens with one slot leave one
- *              of the two there, unspecified which.
+ *              skipped too (CBT_DEV_PAGE_ID, info: token).  Where two tokens have one slot, each
+ *              element of K and V there is one or the other's, unspecified which.
  *   q_out      bf16 [tokens][n_heads * head_dim], rows q_stride elements apart; no overlap with qkv
  * rope == NULL: no rotation.  Arithmetic is fp32 with one rounding to bf16 at the end.  qkv, q_out
  * and the gains are 16-byte aligned, the strides multiples of 8 elements.  Errors: CBT_ERR_NULL,
- * CBT_ERR_INVALID, CBT_ERR_UNSUPPORTED (head_dim), CBT_ERR_LIMIT, CBT_ERR_CUDA. */
+ * CBT_ERR_INVALID, CBT_ERR_UNSUPPORTED (head_dim), CBT_ERR_LIMIT (tokens above 2^30, n_heads + 2
+ * n_kv_heads above 65535), CBT_ERR_CUDA. */
 typedef struct {
   cbt_paged_kv kv;
   const cbt_rope* rope;

@@ -193,3 +193,46 @@ def test_set_attention_refuses_a_null_engine(lib):
     assert lib.cbt_engine_set_attention(None, None) == -2
     c = B.AttentionConfig()
     assert lib.cbt_engine_set_attention(None, ctypes.byref(c)) == -2
+
+
+def test_sizes_past_the_kernels_counters_are_refused(lib):
+    """Each call also lacks its err, so that none could be queued if its sizes were taken."""
+    def page_map(**kw):
+        a = B.PageMapArgs()
+        d = dict(block_table=FAKE, max_pages=8, page_tokens=1, n_pages=32, rows=4, kv_lens=FAKE,
+                 new_lens=FAKE, max_tokens=8, kv_lens_out=FAKE, cu_q=FAKE, positions=FAKE, slots=FAKE)
+        for k, v in {**d, **kw}.items():
+            setattr(a, k, v)
+        return lib.cbt_page_map(ctypes.byref(a), None)
+    for ok in (dict(), dict(max_tokens=1 << 30), dict(n_pages=1 << 30)):
+        assert page_map(**ok) == -2, ok
+    for bad in (dict(max_tokens=(1 << 30) + 1), dict(max_tokens=2 ** 31 - 1), dict(n_pages=(1 << 30) + 1)):
+        assert page_map(**bad) == -12, bad
+
+    def append(tokens):
+        a = B.RopeAppendArgs()
+        a.kv = kv_desc()
+        for k, v in dict(qkv=FAKE, qkv_stride=(8 + 4) * 128, tokens=tokens, n_heads=8, eps=1e-6,
+                         positions=FAKE, slots=FAKE, q_out=FAKE, q_stride=1024).items():
+            setattr(a, k, v)
+        return lib.cbt_rope_append(ctypes.byref(a), None)
+    assert append(1 << 30) == -2
+    assert append((1 << 30) + 1) == -12 and append(2 ** 31 - 1) == -12
+
+
+def test_sizes_of_multi_token_calls(lib):
+    big = dict(n_heads=16, rows=1, tokens=65536, max_q=65536, max_kv=1 << 20, max_pages=1 << 20, cu_q=FAKE,
+               q_stride=2048, out_stride=2048, err=None)
+    rc = lambda **kw: lib.cbt_paged_attention(ctypes.byref(attn_args(**{**big, **kw})), None)
+    size = lambda **kw: lib.cbt_paged_attention_workspace(ctypes.byref(attn_args(**{**big, **kw})))
+    assert rc() == -2                                     # taken, but for err
+    assert rc(tokens=(1 << 25)) == -12 and rc(tokens=2 ** 31 - 1) == -12
+    assert size() == 0                                    # units enough to stay whole
+    # few tokens over long rows are cut: a workspace, which is looked for before the launch
+    few = dict(tokens=4, max_q=4, err=FAKE)
+    n = size(**few)
+    assert 0 < n <= 152 * 256 * (128 * 4 + 8)
+    assert size(**{**few, "max_kv": 500}) == 0
+    assert size(**{**few, "window": 200}) <= n and size(**{**few, "tokens": 3}) <= n
+    assert rc(**few, workspace_bytes=n - 1) == -1
+    assert rc(**few, workspace=None) == -2
