@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kCompute + 32, kCtasPerSm)
         float ps[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float p = valid ? ex2(s[h] - m_run[h]) : 0.f;
+          // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
+          const float p = valid ? ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h])) : 0.f;
           const uint16_t hi = round_bf16(p);
           *reinterpret_cast<uint16_t*>(sP + sw128_offset(h, tid, 2048)) = hi;
           *reinterpret_cast<uint16_t*>(sP + sw128_offset(8 + h, tid, 2048)) =
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(128)
       o[1] = f.y;
     }
     const float mn = fmaxf(m, v.x);
-    const float sc = m == -INFINITY ? 0.f : ex2(m - mn), wgt = ex2(v.x - mn);
+    // m = -inf: no run yet, or runs whose scores are all -inf
+    const float sc = m == -INFINITY ? 0.f : ex2(m - mn), wgt = v.x == -INFINITY ? 0.f : ex2(v.x - mn);
     l = fmaf(l, sc, v.y * wgt);
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = fmaf(acc[r], sc, o[r] * wgt);

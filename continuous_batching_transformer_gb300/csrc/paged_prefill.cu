@@ -678,7 +678,8 @@ __global__ void __launch_bounds__(128)
   const int d = threadIdx.x;
   if (d >= HD) return;
   const float x = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
-  const float y = m == -INFINITY ? 0.f : x / l;
+  // a token before the row's first position sees nothing
+  const float y = row.len - row.n + t - row.t0 < 0 ? 0.f : x / l;
   const long long at = t * a.out_ld + (long long)h * HD + d;
   if (a.f32) static_cast<float*>(a.out)[at] = y;
   else static_cast<uint16_t*>(a.out)[at] = round_bf16(y);

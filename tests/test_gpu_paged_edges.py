@@ -172,3 +172,31 @@ def test_pages_past_32_bit_offsets():
         o = s % page
         assert torch.equal(K[0, :, o], x[t, H:H + kv])
         assert torch.equal(V[0, :, o // 64, :, o % 64], x[t, H + kv:])
+
+
+@pytest.mark.parametrize("new", [1, 3, 200])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_infinite_scores(new, hd):
+    """A score of -inf is a weight of 0, wherever it falls: all that a run of the row's keys holds (the
+    last key, alone in its chunk), the first keys, a chunk in the middle.  A query all of whose scores
+    are -inf has no softmax: NaN."""
+    page, H = 64, 4
+    for n, hidden in ((641, [640]), (641, range(0, 130)), (1300, range(128, 256)), (70, [0]), (1, [0])):
+        if n < new:
+            continue
+        c = R.Cache([(n - new, new)], kv=2, hd=hd, page=page, window=0, sinks=0, seed=3, device=dev())
+        K = R.k_view(c.pool, c.n_pages, 1, 2, page, hd)
+        for j in hidden:
+            K[int(c.table[0, j // page]), :, j % page, 0] = float("-inf")
+            c.k[0][:, j, 0] = float("-inf")
+        q = torch.randn(new, H, hd, device=dev()).to(torch.bfloat16)
+        q[..., 0] = q[..., 0].abs() + 0.5
+        cache = paged.PagedKV(c.pool, c.table, c.lens, page_tokens=page, n_kv_heads=2, head_dim=hd)
+        for max_q in {new, 20000 if new > 1 else 1}:  # cut and whole
+            out = torch.zeros(new, H, hd, device=dev())
+            paged.Attention(cache, n_heads=H, max_kv=n, max_q=max_q, max_tokens=new)(0, q, out, cu_q=c.cu)
+            cache.check()
+            if n == 1:
+                assert torch.isnan(out).all()
+            else:
+                check_attention(out, *c.expected(q, 0, 0, hd ** -0.5), torch.float32)
