@@ -19,8 +19,9 @@
 // depends on the row alone, and so does the order in which k_paged_merge adds the runs' (max, sum,
 // output).  Rows of one run are finished here.
 //
-// Measured on one GB300 (graph replays): 32 rows of 8192 to 16384 positions, 32 / 8 heads of 128, 245
-// us = 6.7 TB/s, all of the measured copy rate; 8 rows of 512 to 4096 15.6 us, where 2.5 chunks a CTA
+// Measured on one GB300 (graph replays): 32 rows of 8192 to 16384 positions, 32 / 8 heads of 128, 244
+// to 252 us = 6.5 to 6.7 TB/s, 95 to 99 % of the measured copy rate; 16 of them through a window of
+// 4096 47.4 us (5.7 TB/s); 8 rows of 512 to 4096 15.6 us, where 2.5 chunks a CTA
 // do not divide evenly and the join takes 3 us.
 #include "paged_attn.cuh"
 

