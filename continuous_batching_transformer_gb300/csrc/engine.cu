@@ -2069,7 +2069,10 @@ static cbt_status prefill_impl(cbt_engine* e, const int32_t* ids, const int32_t*
     if ((long long)sl.pos + lens[s] > sl.cap) return CBT_ERR_CAPACITY;
     T += lens[s];
     max_keys = std::max(max_keys, sl.pos + lens[s]);
-    for (int j = 0; j < lens[s]; ++j) total_keys += keys_seen(e, sl.pos + j);
+    if (e->form.on && e->form.window)
+      for (int j = 0; j < lens[s]; ++j) total_keys += keys_seen(e, sl.pos + j);
+    else
+      total_keys += (long long)lens[s] * sl.pos + (long long)lens[s] * (lens[s] + 1) / 2;
   }
   if (T > e->p.max_prefill_tokens) return CBT_ERR_TOKENS;
   std::vector<PageWrite> writes;

@@ -235,3 +235,27 @@ def test_refusals():
     plain = Engine(w, arena_bytes=64 << 20, max_batch=4, max_prefill_tokens=64, page_tokens=128)
     outs2, _ = run(plain, w.shape, lens, 2)
     assert all(np.array_equal(x, y) for x, y in zip(outs, outs2))
+
+
+def test_few_tokens_after_long_prompts():
+    """A few tokens admitted behind a long context, whose keys are taken in several runs, next to a row
+    that has none yet; then decode steps over both."""
+    ensure_built()
+    w, m = weights(SHAPES["hd128-gqa"])
+    fm = FORMS["norm"]
+    eng, gains = make_engine(w, fm, arena=256 << 20)
+    n, few = 1300, 5
+    t = np.random.default_rng(7).integers(0, w.shape.vocab, n + few + 2).astype(np.int32)
+    u = np.random.default_rng(8).integers(0, w.shape.vocab, 4).astype(np.int32)
+    a, b = eng.kv_slab_alloc(2000), eng.kv_slab_alloc(100)
+    one, two = (torch.empty(k, w.shape.vocab, device="cuda") for k in (1, 2))
+    for i in range(0, n, 500):
+        eng.prefill_segmented([a], [min(500, n - i)], to_dev(t[i:min(n, i + 500)]), one)
+    ref, ref2 = reference(m, t, fm, gains), reference(m, u, fm, gains)
+    check_logits(one.cpu().numpy(), ref[n - 1:n], TOL["bf16"], "long prompt")
+    eng.prefill_segmented([a, b], [few, 2], to_dev(np.concatenate([t[n:n + few], u[:2]])), two)
+    check_logits(two.cpu().numpy(), np.stack([ref[n + few - 1], ref2[1]]), TOL["bf16"], "few tokens")
+    for s in range(2):
+        eng.decode_step_batch([a, b], to_dev(np.array([t[n + few + s], u[2 + s]], np.int32)), two)
+        check_logits(two.cpu().numpy(), np.stack([ref[n + few + s], ref2[2 + s]]), TOL["bf16"], f"step {s}")
+    assert eng.device_error() == (0, 0)
