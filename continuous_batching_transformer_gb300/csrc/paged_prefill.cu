@@ -22,6 +22,8 @@
 // for several units, which they find from the rows' lengths: the longest first, dealt back and forth.
 // Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 41 us (830 TFLOP/s); four chunks
 // of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 169 us (1095 TFLOP/s).
+#include <math.h>
+
 #include "paged_attn.cuh"
 
 namespace {
@@ -101,13 +103,13 @@ constexpr int kUnits = 48;   // most units of a CTA
 constexpr int kRanked = 64;  // rows up to which they are ranked
 
 // Few units over long contexts: a unit's steps are cut into up to `runs` runs of kRunSteps steps or
-// more, taken by different CTAs and joined by k_prefill_merge, where all runs find an SM at once.
+// more, taken by different CTAs and joined by k_prefill_merge (runs_for decides).
 // Whole and cut, rows of 4 tokens, 32 q and 8 kv heads of 128: one over 2000 positions 28 and 16 us, over
-// 131072 1460 and 100 us (5.4 TB/s of K and V); eight over 4096 54 and 40 us.  One of 512 tokens over
-// 16384: 203 and 142 us.  With runs of 16 steps the first takes 21 us.  With twice as many items,
-// two rounds: 114 us for the second, 97 us for a prompt of 1024 (34 us whole, as here).
+// 131072 1460 and 100 us (5.4 TB/s of K and V); ten over 8192 101 and 78 us.  One row of 512 tokens over
+// 16384: 203 and 121 us.  With runs of 16 steps the first takes 21 us.
 constexpr int kRunSteps = 8;
-constexpr int kFewItems = 152;  // items that the runs may make: one for each SM
+constexpr int kSms = 152, kMostRuns = 64;
+constexpr int kMostItems = 4 * kSms;  // that the runs may make
 CBT_HD int ceil_div(int n, int d) { return (n + d - 1) / d; }
 // The steps of each run of a unit, the last one's aside, and how many runs hold any: every one of them
 // is written, and those behind are not read.
@@ -621,11 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the runs of a (token, q head), a block each: every warp finds the common reference and sum,
-// a lane per run, then takes every fourth run's O, HD / 32 dims a lane; the warps' sums are added in
-// order.  (One warp that took the runs one after the other waited a trip to memory for each: 33 us
-// more for 37 runs of four tokens and 32 heads.)
-template <int HD>
+// Joins the runs of a (token, q head), W warps each: every warp finds the common reference and sum, a
+// lane per run, then takes every W-th run's O, HD / 32 dims a lane; four warps' sums are added in
+// order.  Four where few pairs have many runs and each one's chain of loads counts: 20 pairs of 12 runs
+// 15.6 us with four and 17.2 with one, 2880 of 12 37.1 and 39.1.  One otherwise: 4096 pairs of 9 runs 30.7
+// and 27.6, 512 pairs of 4 22.5 and 20.2, 19200 of 5 176 and 156.
+template <int HD, int W>
 __global__ void __launch_bounds__(128)
     k_prefill_merge(const __grid_constant__ PagedAttn a, const int runs, const float* __restrict__ part_o,
                     const float2* __restrict__ part_ml) {
@@ -633,20 +636,21 @@ __global__ void __launch_bounds__(128)
   __shared__ float sums[4][HD];
   pdl_wait();
   pdl_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = (int)(blockIdx.x / a.n_heads), h = (int)(blockIdx.x - (unsigned)t * a.n_heads);
-  int lo = 0, hi = a.rows;  // the row of token t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const RowTokens row = row_tokens(a, lo);
-  if (row.n <= 0 || t < row.t0 || t >= row.t0 + row.n) return;  // the whole block
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = W == 4 ? warp : 0;
+  const unsigned pair = W == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
+  const int t = (int)(pair / a.n_heads), h = (int)(pair - (unsigned)t * a.n_heads);
+  if (t >= a.tokens) return;
+  // the last of the kRanked or fewer rows that starts at t or before
+  const unsigned r0 = __ballot_sync(0xffffffffu, lane < a.rows && a.cu[min(lane, a.rows)] <= t);
+  const unsigned r1 = __ballot_sync(0xffffffffu, lane + 32 < a.rows && a.cu[min(lane + 32, a.rows)] <= t);
+  const int b = __popc(r0) + __popc(r1) - 1;
+  if (b < 0) return;
+  const RowTokens row = row_tokens(a, b);
+  if (row.n <= 0 || t < row.t0 || t >= row.t0 + row.n) return;  // all warps of the pair
   const int width = 2 * (kRows / (a.n_heads / a.kv.n_kv_heads)), first = (t - row.t0) / width * width;
   const int p0 = row.len - row.n + first, pl = row.len - row.n + min(row.n, first + width) - 1;
   const int count = run_count(seen_chunks<kStep>(p0, pl, a.window, a.sinks).n, runs);
-  const size_t base = (size_t)blockIdx.x * runs;
+  const size_t base = (size_t)pair * runs;
   float m = -INFINITY, l = 0.f, acc[R];
   for (int i = lane; i < count; i += 32) m = fmaxf(m, __ldcg(part_ml + base + i).x);
 #pragma unroll
@@ -658,44 +662,80 @@ __global__ void __launch_bounds__(128)
     const float2 v = i0 + lane < count ? __ldcg(part_ml + base + i0 + lane) : make_float2(-INFINITY, 0.f);
     const float mine = v.x == -INFINITY ? 0.f : ex2(v.x - m);  // 0: a run of which the token sees nothing
     l += mine == 0.f ? 0.f : v.y * mine;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float wgt = __shfl_sync(0xffffffffu, mine, j + warp);
-      if (i0 + j + warp >= count) continue;
-      const float* o = part_o + (base + i0 + j + warp) * HD + lane;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float x = __ldcg(o + 32 * r);
-        acc[r] = wgt == 0.f ? acc[r] : fmaf(x, wgt, acc[r]);  // what such a run left is not a number
+    const int n = min(32, count - i0);
+#pragma unroll 4
+    for (int j = sub; j < n; j += W) {
+      const float wgt = __shfl_sync(0xffffffffu, mine, j);
+      const float* o = part_o + (base + i0 + j) * HD + lane * R;
+      float x[R];
+      if (R == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
+        x[0] = f.x;
+        x[1] = f.y;
+        x[R - 2] = f.z;
+        x[R - 1] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
+        x[0] = f.x;
+        x[1] = f.y;
       }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        acc[r] = wgt == 0.f ? acc[r] : fmaf(x[r], wgt, acc[r]);  // what such a run left is not a number
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (W == 4) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) sums[warp][32 * r + lane] = acc[r];
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= HD) return;
-  const float x = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
-  // a token before the row's first position sees nothing
-  const float y = row.len - row.n + t - row.t0 < 0 ? 0.f : x / l;
-  const long long at = t * a.out_ld + (long long)h * HD + d;
-  if (a.f32) static_cast<float*>(a.out)[at] = y;
-  else static_cast<uint16_t*>(a.out)[at] = round_bf16(y);
-}
-
-// The most runs a unit is cut into (1: none), from the call's sizes alone
-int runs_for(const PagedAttn& a) {
-  const int width = 2 * (kRows / (a.n_heads / a.kv.n_kv_heads));  // tokens of a unit
-  const long long items = (long long)a.rows * (((long long)a.max_q + width - 1) / width) * a.kv.n_kv_heads;
-  if (a.rows > kRanked || items <= 0 || items > kFewItems / 2) return 1;
-  long long keys = a.max_kv;  // that a unit sees at most
-  if (a.window) {
-    const long long some = (long long)a.window + width + a.sinks + 2 * kStep;
-    keys = keys < some ? keys : some;
+    for (int r = 0; r < R; ++r) sums[warp][lane * R + r] = acc[r];
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int d = lane * R + r;
+      acc[r] = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
+    }
   }
-  return run_count((int)((keys + kStep - 1) / kStep), (int)(kFewItems / items));
+  // a token before the row's first position sees nothing
+  const bool nothing = row.len - row.n + t - row.t0 < 0;
+  const long long at = t * a.out_ld + (long long)h * HD + lane * R;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float y = nothing ? 0.f : acc[r] / l;
+    if (a.f32) static_cast<float*>(a.out)[at + r] = y;
+    else static_cast<uint16_t*>(a.out)[at + r] = round_bf16(y);
+  }
+}
+constexpr int kFewPairs = 20 * kSms, kManyRuns = 8;  // up to, and above which, they have four warps
+
+// The most runs a unit is cut into (1: none), from rows, max_q and max_kv alone: the number that should
+// take the least time, counted in steps (0.75 us).  Items go to the SMs in rounds; each costs its steps,
+// 5 more to start and end, and the writing of its partial outputs (45 bytes a ns); the join costs 6
+// and the reading of them all (5000 bytes a ns).  Over 25 shapes the cut so chosen was at worst 2 % behind
+// whole (two rows of 700 tokens over 6000: 157 to 159 and 155 to 156 us).  One item for each SM instead:
+// ten rows of 4 over 8192 stay whole, 101 for 78 us.
+int runs_for(const PagedAttn& a) {
+  const int G = a.n_heads / a.kv.n_kv_heads, width = 2 * (kRows / G);  // tokens of a unit
+  const long long units = (long long)a.rows * (((long long)a.max_q + width - 1) / width) * a.kv.n_kv_heads;
+  if (a.rows > kRanked || units <= 0 || units > kMostItems / 2) return 1;
+  double keys = a.max_kv;  // that a unit sees at most
+  if (a.window) keys = fmin(keys, (double)a.window + width + a.sinks + 2 * kStep);
+  const int steps = (int)((keys + kStep - 1) / kStep);
+  const double step_ns = 750, row_bytes = a.kv.head_dim * sizeof(float);
+  const double item = 5 + fmin((double)a.max_q * G, 2 * kRows) * row_bytes / 45 / step_ns;
+  // (not a.tokens: a call of fewer tokens must not need more workspace)
+  const double join = (double)a.rows * a.max_q * a.n_heads * row_bytes / 5000 / step_ns;
+  int best = 1;
+  double least = (double)((units + kSms - 1) / kSms) * (steps + 5);
+  for (int n = 2; n <= kMostRuns && n * units <= kMostItems && (n - 1) * kRunSteps < steps; ++n) {
+    const double t = (double)((n * units + kSms - 1) / kSms) * ((double)steps / n + item) + 6 + n * join;
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
 }
 
 template <int HD>
@@ -721,7 +761,9 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
       launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, po, pml);
   if (launched != cudaSuccess || runs == 1) return launched;
   const long long pairs = (long long)a.tokens * a.n_heads;
-  return launch_pdl(k_prefill_merge<HD>, dim3((unsigned)pairs), dim3(128), 0, s, a, runs, po, pml);
+  if (pairs <= kFewPairs && runs > kManyRuns)
+    return launch_pdl(k_prefill_merge<HD, 4>, dim3((unsigned)pairs), dim3(128), 0, s, a, runs, po, pml);
+  return launch_pdl(k_prefill_merge<HD, 1>, dim3((unsigned)((pairs + 3) / 4)), dim3(128), 0, s, a, runs, po, pml);
 }
 
 }  // namespace
@@ -732,7 +774,7 @@ size_t paged_prefill_workspace(const PagedAttn& a) {
 }
 // of tokens <= rows * max_q: a row of a tile each for the most items
 size_t paged_prefill_most_workspace(int head_dim) {
-  return (size_t)kFewItems * 2 * kRows * (head_dim * sizeof(float) + sizeof(float2));
+  return (size_t)kMostItems * 2 * kRows * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s) {

@@ -236,3 +236,13 @@ def test_sizes_of_multi_token_calls(lib):
     assert size(**{**few, "window": 200}) <= n and size(**{**few, "tokens": 3}) <= n
     assert rc(**few, workspace_bytes=n - 1) == -1
     assert rc(**few, workspace=None) == -2
+
+
+def test_a_call_of_fewer_tokens_needs_no_more_workspace(lib):
+    """A workspace for the most tokens serves every call with the same bounds."""
+    for rows, max_q, max_kv in ((1, 4096, 100000), (3, 200, 40000), (10, 4, 8192), (64, 7, 3000), (1, 2, 1 << 20)):
+        kw = dict(rows=rows, max_q=max_q, max_kv=max_kv, cu_q=FAKE)
+        most = rows * max_q
+        sizes = [lib.cbt_paged_attention_workspace(ctypes.byref(attn_args(**kw, tokens=t)))
+                 for t in sorted({1, 2, 3, most // 7 + 1, most // 2 + 1, most - 1, most})]
+        assert sizes == sorted(sizes), kw
