@@ -20,8 +20,8 @@
 // when that is needed, so that an issuer waits once a step.  A warp of its own clears V of keys that
 // no query of the unit sees (what lies there may not be finite) before the MMA reads it.  CTAs stay
 // for several units, which they find from the rows' lengths: the longest first, dealt back and forth.
-// Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 41 us (830 TFLOP/s); four chunks
-// of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 169 us (1095 TFLOP/s).
+// Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 40.7 us (845 TFLOP/s); four
+// chunks of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 168.5 us (1100 TFLOP/s).
 #include <math.h>
 
 #include "paged_attn.cuh"
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work w(units + k, a);
       if (!w.stages) continue;
       int krow = 0, vrow = 0, vlag[kLag] = {0, 0};
+      const int q_at = qn ? kLag : 0;  // the step before which Q is asked for
 #pragma unroll 1
       for (int i = 0; i < w.stages; ++i) {
         if ((i & 31) == 0 && i + lane < w.steps) {
@@ -333,7 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           krow = (int)(paged_k(a.kv, id, w.u.g, o, 0) / HD);
           vrow = (int)(paged_v(a.kv, id, w.u.g, o, 0) / 64);
         }
-        if (i == 0) {
+        // Q once both tiles have had the last unit's.  K of the first steps needs only stages that the last
+        // unit has left, so after the first unit it is asked for before (four prompts of 1024 tokens
+        // 41.5 to 40.7 us; for the first unit it would only be in Q's way).
+        if (i == q_at) {
           ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
           if (!ok) break;
           qp ^= 1;
