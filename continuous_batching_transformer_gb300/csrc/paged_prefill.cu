@@ -20,8 +20,9 @@
 // when that is needed, so that an issuer waits once a step.  A warp of its own clears V of keys that
 // no query of the unit sees (what lies there may not be finite) before the MMA reads it.  CTAs stay
 // for several units, which they find from the rows' lengths: the longest first, dealt back and forth.
-// Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 40.7 us (845 TFLOP/s); four
-// chunks of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 168.5 us (1100 TFLOP/s).
+// Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 40.7 to 41.1 us (840 TFLOP/s);
+// four chunks of 500 to 1030 tokens over 3000 to 9000 positions, window 4096, 168.5 to 169.8 us (1095
+// TFLOP/s).
 #include <math.h>
 
 #include "paged_attn.cuh"
