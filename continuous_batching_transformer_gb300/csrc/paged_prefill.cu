@@ -103,6 +103,21 @@ struct Unit {
 constexpr int kUnits = 48;   // most units of a CTA
 constexpr int kRanked = 64;  // rows up to which they are ranked
 
+// Shared memory: the tiles of Q, K and V, then this
+constexpr int kBars = 2 + 3 * kStages + 12;
+struct Tail {
+  uint64_t bars[kBars];
+  uint32_t tmem_slot;
+  int abort_flag;
+  int warp_sums[kThreads / 32];
+  Unit units[kUnits];
+};
+template <int HD>
+constexpr size_t smem_bytes() {  // 1024: the base is rounded up to the tiles' alignment
+  return 1024 + 2 * (HD / 64) * kBox + 2 * kStages * kStep * HD * 2 + sizeof(Tail);
+}
+static_assert(smem_bytes<64>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024, "shared memory");
+
 // Few units over long contexts: a unit's steps are cut into up to `runs` runs of kRunSteps steps or
 // more, taken by different CTAs and joined by k_prefill_merge (runs_for decides).
 // Whole and cut, rows of 4 tokens, 32 q and 8 kv heads of 128: one over 2000 positions 28 and 16 us, over
@@ -166,17 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;                     // [tile][64-dim half][128 rows]
   uint8_t* sK = sQ + 2 * kTile;           // [stage][64-dim half][64 keys]
   uint8_t* sV = sK + kStages * kKV;       // [stage][HD dims][64 keys]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kStages * kKV);
+  Tail& tail = *reinterpret_cast<Tail*>(sV + kStages * kKV);
+  uint64_t* bars = tail.bars;
   // a stage has landed, its V is clean, both tiles are done with it
   uint64_t *qfull = bars, *full = bars + 1, *ready = full + kStages, *empty = ready + kStages;
   // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
   uint64_t *s_full = empty + kStages, *p_full = s_full + 4, *pv_done = p_full + 4;
   uint64_t* qempty = pv_done + 4;         // both tiles' S of a unit are done
-  constexpr int kBars = 2 + 3 * kStages + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* wsum = reinterpret_cast<int*>(tmem_slot + 2);     // [12]
-  Unit* units = reinterpret_cast<Unit*>(wsum + 12);      // [kUnits]
+  uint32_t* tmem_slot = &tail.tmem_slot;
+  volatile int* abort_flag = &tail.abort_flag;
+  int* wsum = tail.warp_sums;
+  Unit* units = tail.units;
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
@@ -213,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int t0, n, p0, k;  // query tokens, their number, the first one's position, units
     };
     Row* rows = reinterpret_cast<Row*>(sQ);  // before Q lands there
+    static_assert(kRanked * sizeof(Row) <= 2 * kTile, "rows fit where Q goes");
     if (tid < a.rows) {
       const RowTokens row = row_tokens(a, tid);
       if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, tid);
@@ -746,8 +762,7 @@ int runs_for(const PagedAttn& a) {
 template <int HD>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const PagedAttn& a, int num_sms, cudaStream_t s) {
-  constexpr size_t smem = 1024 + 2 * (HD / 64) * kBox + 2 * kStages * kStep * HD * 2 + 1536;
-  static_assert(smem <= 227 * 1024, "shared memory budget");
+  constexpr size_t smem = smem_bytes<HD>();
   const cudaError_t rc = cudaFuncSetAttribute(k_paged_prefill<HD>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (rc != cudaSuccess) return rc;
