@@ -661,13 +661,18 @@ __global__ void __launch_bounds__(128)
   const unsigned pair = W == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
   const int t = (int)(pair / a.n_heads), h = (int)(pair - (unsigned)t * a.n_heads);
   if (t >= a.tokens) return;
-  // the last of the kRanked or fewer rows that starts at t or before
-  const unsigned r0 = __ballot_sync(0xffffffffu, lane < a.rows && a.cu[min(lane, a.rows)] <= t);
-  const unsigned r1 = __ballot_sync(0xffffffffu, lane + 32 < a.rows && a.cu[min(lane + 32, a.rows)] <= t);
-  const int b = __popc(r0) + __popc(r1) - 1;
-  if (b < 0) return;
-  const RowTokens row = row_tokens(a, b);
-  if (row.n <= 0 || t < row.t0 || t >= row.t0 + row.n) return;  // all warps of the pair
+  // the row that holds t, among kRanked or fewer: a lane looks at two of them (the ranges need not lie in
+  // the rows' order, and some may be no ranges)
+  auto look = [&](int r) { return r < a.rows ? row_tokens(a, r) : RowTokens{0, -1, 0, true}; };
+  const RowTokens lo = look(lane), hi = look(lane + 32);
+  const unsigned in_lo = __ballot_sync(0xffffffffu, lo.n > 0 && t >= lo.t0 && t - lo.t0 < lo.n);
+  const unsigned in_hi = __ballot_sync(0xffffffffu, hi.n > 0 && t >= hi.t0 && t - hi.t0 < hi.n);
+  if (!(in_lo | in_hi)) return;  // all warps of the pair
+  const int src = __ffs(in_lo ? in_lo : in_hi) - 1;
+  RowTokens row{};
+  row.t0 = __shfl_sync(0xffffffffu, in_lo ? lo.t0 : hi.t0, src);
+  row.n = __shfl_sync(0xffffffffu, in_lo ? lo.n : hi.n, src);
+  row.len = __shfl_sync(0xffffffffu, in_lo ? lo.len : hi.len, src);
   const int width = 2 * (kRows / (a.n_heads / a.kv.n_kv_heads)), first = (t - row.t0) / width * width;
   const int p0 = row.len - row.n + first, pl = row.len - row.n + min(row.n, first + width) - 1;
   const int count = run_count(seen_chunks<kStep>(p0, pl, a.window, a.sinks).n, runs);

@@ -1,11 +1,14 @@
 """Calls of the operators on a paged KV cache that the documentation allows and that lie off the usual
-path: CTAs that hold every unit they may."""
+path: CTAs that hold every unit they may, ranges of tokens that are none.  Tolerances are those of
+tests/test_gpu_paged_ops."""
 import pytest
 import torch
 
+from continuous_batching_transformer_gb300 import binding as B
 from continuous_batching_transformer_gb300 import paged
+from tests import paged_reference as R
 from tests.gpu_harness import ensure_built
-from tests.paged_reference import BF16_STEP
+from tests.test_gpu_paged_ops import check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -49,5 +52,32 @@ def test_ctas_full_of_units(rows, hd):
     row = [b for b in range(rows) for _ in range(new[b])]
     pos = [lens[b] - new[b] + i for b in range(rows) for i in range(new[b])]
     want = V[table[row, 0].long(), :, :, torch.tensor(pos, device=dev())]
-    tol = (2 * BF16_STEP + 2.0 ** -15) * want.float().abs()
+    tol = (2 * R.BF16_STEP + 2.0 ** -15) * want.float().abs()
     assert ((out.float() - want.float()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("cut", [True, False])
+@pytest.mark.parametrize("cu,good", [([0, 5, 1000, 10, 15], [0, 3]),    # rows 1 and 2 leave the call's tokens
+                                     ([10, 15, 3, 8], [0, 2]),          # in another order
+                                     ([-1, 4, 9, 2 ** 31 - 1, 12, 15], [1, 4]),
+                                     ([-2 ** 31, 0, 5, -2 ** 31, 12, 15], [1, 4])])
+def test_bad_ranges_in_the_middle(cu, good, cut):
+    """A row whose range of tokens is no range is reported and skipped, whether the others' long rows
+    are cut into runs or not; the tokens that no row takes stay as they are."""
+    n = len(cu) - 1
+    c = R.Cache([(3000 + 100 * b, 5) for b in range(n)], kv=2, hd=64, page=64, window=0, sinks=0, seed=4,
+                device=dev())
+    q = torch.randn(15, 8, 64, device=dev()).to(torch.bfloat16)
+    out = torch.full((15, 8, 64), 7.0, device=dev())
+    cache = paged.PagedKV(c.pool, c.table, c.lens, page_tokens=64, n_kv_heads=2, head_dim=64)
+    paged.Attention(cache, n_heads=8, max_kv=3500, max_q=5 if cut else 20000, max_tokens=15)(0, q, out, cu_q=i32(cu))
+    torch.cuda.synchronize()
+    assert cache.err.tolist()[0] == B.DEV_LENGTH and cache.err.tolist()[1] not in good
+    left = set(range(15))
+    for b in good:
+        t = range(cu[b], cu[b + 1])
+        first = 3000 + 100 * b + 5 - len(t)  # the last of them is the row's last position
+        ref, mag = R.attention(q[cu[b]:cu[b + 1]].double().cpu().numpy(), c.k[b], c.v[b], first, 0, 0, 64 ** -0.5)
+        check_attention(out[cu[b]:cu[b + 1]], ref, mag, torch.float32)
+        left -= set(t)
+    assert (out[sorted(left)] == 7.0).all()
