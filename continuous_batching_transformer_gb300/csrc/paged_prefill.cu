@@ -169,7 +169,7 @@ template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttn a,
-                    const int runs, float* __restrict__ part_o, float2* __restrict__ part_ml) {
+                    const int runs, const int most, float* __restrict__ part_o, float2* __restrict__ part_ml) {
   constexpr int nKh = HD / 64;
   constexpr uint32_t kTile = nKh * kBox;     // a Q tile
   constexpr uint32_t kKV = kStep * HD * 2;   // K or V of a step
@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the units are ranked by their last position (the longest first), each by a thread that counts
   // the units before it; with many they are taken as they come, the rows' last units first: there
   // are enough of them then to even out.  (Four 1024-token prompts: 56 us unranked.)
+  // Rows whose ranges of tokens overlap may hold more units than the `most` that the launch and the
+  // counters here are sized for: none is done then (some range runs backwards, which is reported).
   int total = 0;
   auto units_of = [&](int n) { return n > 0 ? in_units(n - 1) + 1 : 0; };
   if (a.rows <= kRanked) {
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
 #pragma unroll 1
     for (int r = 0; r < a.rows; ++r) total += rows[r].k;
+    if (total > most) total = 0;
 #pragma unroll 1
     for (int q = tid; q < total; q += kThreads) {
       int r = 0, first = q;  // unit `first` of row r
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = r0; r < r1; ++r) {
       const RowTokens row = row_tokens(a, r);
       if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, r);
-      mine += units_of(row.n);
+      mine = min(mine + units_of(row.n), most + 1);
     }
     int inc = mine;
 #pragma unroll
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ws = lane < kThreads / 32 ? wsum[lane] : 0;  // lane w: warp w's sum
     total = __reduce_add_sync(0xffffffffu, ws);
     const int begin = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + inc - mine;
+    if (total > most) total = 0;
 #pragma unroll 1
     for (int round = 0; round < kUnits; ++round) {
       const unsigned it = item_of(round);
@@ -783,7 +787,8 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const size_t parts = (size_t)a.tokens * a.n_heads * runs;
   float2* pml = reinterpret_cast<float2*>(a.ws + parts * HD * sizeof(float));
   const cudaError_t launched =
-      launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, po, pml);
+      launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, (int)units, po,
+                 pml);
   if (launched != cudaSuccess || runs == 1) return launched;
   const long long pairs = (long long)a.tokens * a.n_heads;
   if (pairs <= kFewPairs && runs > kManyRuns)

@@ -530,8 +530,9 @@ cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
  *                launch and the workspace.  A row above either, or with more positions than its
  *                table, reports CBT_DEV_LENGTH; its outputs are unspecified.  So are those of a
  *                row with a page id outside the pool among the pages it reads (CBT_DEV_PAGE_ID).
- *   tokens       rows of q and out; a row whose cu_q range leaves [0, tokens] is skipped
- *                (CBT_DEV_LENGTH)
+ *   tokens       rows of q and out; a row whose cu_q range leaves [0, tokens] or runs backwards is
+ *                skipped (CBT_DEV_LENGTH).  Where the ranges of other rows overlap (which takes one
+ *                that runs backwards), the call's outputs are unspecified.
  *   q            bf16 [tokens][n_heads * head_dim], rows q_stride elements apart
  *   out          bf16 or fp32 (out_dtype), rows out_stride elements apart; no overlap with q
  *   workspace    cbt_paged_attention_workspace bytes, 256-byte aligned (NULL if that is 0).  Calls

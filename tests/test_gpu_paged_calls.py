@@ -81,3 +81,30 @@ def test_bad_ranges_in_the_middle(cu, good, cut):
         check_attention(out[cu[b]:cu[b + 1]], ref, mag, torch.float32)
         left -= set(t)
     assert (out[sorted(left)] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,max_kv", [(63, 4000), (63, 64), (4095, 64)])
+def test_ranges_that_overlap(rows, max_kv):
+    """Every other row takes all of the call's tokens, many more units than its launch is made for: it
+    is reported, nothing but the call's rows is written, and the next call is right."""
+    tokens, hd = 200, 64
+    pool = torch.randn(2 * 2 * 64 * hd, device=dev()).to(torch.bfloat16)
+    table = torch.zeros(rows, 1 + max_kv // 64, dtype=torch.int32, device=dev())
+    lens = torch.full((rows,), max_kv, dtype=torch.int32, device=dev())
+    cache = paged.PagedKV(pool, table, lens, page_tokens=64, n_kv_heads=1, head_dim=hd)
+    attn = paged.Attention(cache, n_heads=4, max_kv=max_kv, max_q=tokens, max_tokens=tokens + 5)
+    q = torch.randn(tokens + 5, 4, hd, device=dev()).to(torch.bfloat16)
+    out = torch.full((tokens + 9, 4, hd), 7.0, device=dev())
+    attn(0, q, out[:tokens + 5], cu_q=i32([0, tokens] * ((rows + 1) // 2)))
+    torch.cuda.synchronize()
+    assert (out[tokens:] == 7.0).all()
+    assert cache.err.tolist()[0] == B.DEV_LENGTH and cache.err.tolist()[1] % 2 == 1
+    cache.err.zero_()
+    attn(0, q, out[:tokens + 5], cu_q=i32([0] * rows + [tokens]))
+    cache.check()
+    K, V = (R.k_view(pool, 2, 1, 1, 64, hd)[0], R.v_view(pool, 2, 1, 1, 64, hd)[0])
+    n = max_kv // 64
+    k = K.double().cpu().repeat(1, n + 1, 1)[:, :max_kv].numpy()
+    v = V.permute(0, 1, 3, 2).reshape(1, 64, hd).double().cpu().repeat(1, n + 1, 1)[:, :max_kv].numpy()
+    check_attention(out[:tokens], *R.attention(q[:tokens].double().cpu().numpy(), k, v, max_kv - tokens, 0, 0,
+                                               hd ** -0.5), torch.float32)
