@@ -15,7 +15,7 @@ import synth
 from synth.recipes import ModelShape
 
 from . import binding as B
-from .paged import Rope
+from .paged import Rope, size32
 
 
 def config_struct(shape: ModelShape) -> B.ModelConfig:
@@ -114,6 +114,7 @@ class Engine:
         per-head q and k norms (per layer a bf16 [head_dim] gain, or None), sliding window and
         first positions that stay visible.  Paged bf16 engines, before any slab exists."""
         L, hd = self.shape.n_layers, self.shape.head_dim
+        window, sinks = size32(window, "window"), size32(sinks, "sinks")
         norms = []
         for g in (q_norm, k_norm):
             g = None if g is None else list(g)

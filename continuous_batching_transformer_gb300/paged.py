@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import torch
 
@@ -36,6 +37,14 @@ DEV_ERRORS = {B.DEV_PAGE_ID: "page id outside the pool", B.DEV_PAGES: "too few f
 def page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int, n_layers: int = 1) -> int:
     """Bytes of one page holding `n_layers` layers."""
     return 4 * n_layers * n_kv_heads * page_tokens * head_dim
+
+
+def size32(v, what: str) -> int:
+    """v, a whole number that a 32-bit field holds (ctypes cuts others without a word)."""
+    n = operator.index(v)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{what}: {n} does not fit 32 bits")
+    return n
 
 
 def _bad(t, what, dtypes, index, dims=None):
@@ -119,10 +128,11 @@ class Rope:
                  mscale: float = 0.0):
         if layout not in B.ROPE_LAYOUTS or scaling not in B.ROPE_SCALINGS:
             raise ValueError(f"layout {layout!r}, scaling {scaling!r}")
-        self.head_dim = head_dim
-        self.config = B.RopeConfig(B.ROPE_LAYOUTS[layout], head_dim if rot_dim is None else rot_dim,
-                                   B.ROPE_SCALINGS[scaling], original_len, theta, factor, beta_fast,
-                                   beta_slow, mscale)
+        self.head_dim = size32(head_dim, "head_dim")
+        self.config = B.RopeConfig(B.ROPE_LAYOUTS[layout],
+                                   head_dim if rot_dim is None else size32(rot_dim, "rot_dim"),
+                                   B.ROPE_SCALINGS[scaling], size32(original_len, "original_len"), theta,
+                                   factor, beta_fast, beta_slow, mscale)
         self.desc = B.rope_init(self.config, head_dim)
 
 
@@ -136,6 +146,9 @@ class PagedKV:
 
     def __init__(self, pool, block_table, kv_lens, *, page_tokens: int, n_kv_heads: int,
                  head_dim: int, n_layers: int = 1):
+        for n, what in ((page_tokens, "page_tokens"), (n_kv_heads, "n_kv_heads"), (head_dim, "head_dim"),
+                        (n_layers, "n_layers")):
+            size32(n, what)
         _tensor(pool, "pool", (torch.bfloat16, torch.uint8), dims=1)
         self.device = pool.device
         self.index = pool.get_device()
@@ -180,6 +193,9 @@ class PageMap:
 
     def __init__(self, block_table, kv_lens, free_pages, free_count, *, page_tokens: int,
                  max_tokens: int, n_pages: int | None = None, cu_q=None, positions=None, slots=None):
+        for n, what in ((page_tokens, "page_tokens"), (max_tokens, "max_tokens"),
+                        (0 if n_pages is None else n_pages, "n_pages")):
+            size32(n, what)
         _tensor(block_table, "block_table", _I32, dims=2)
         self.index = block_table.get_device()
         rows, max_pages = block_table.shape
@@ -237,7 +253,7 @@ class RopeAppend:
     def __init__(self, cache: PagedKV, rope: Rope | None, *, n_heads: int, eps: float = 1e-6):
         if rope is not None and rope.head_dim != cache.head_dim:
             raise ValueError("rope and cache have different head_dim")
-        self.cache, self.rope, self.n_heads = cache, rope, n_heads
+        self.cache, self.rope, self.n_heads = cache, rope, size32(n_heads, "n_heads")
         self.width = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim
         self.q_width = n_heads * cache.head_dim
         self._layer = None
@@ -289,6 +305,10 @@ class Attention:
                  scale: float | None = None):
         if cache.block_table is None:
             raise ValueError("the cache has no block table")
+        for n, what in ((n_heads, "n_heads"), (max_kv, "max_kv"), (max_q, "max_q"),
+                        (0 if max_tokens is None else max_tokens, "max_tokens"), (window, "window"),
+                        (sinks, "sinks")):
+            size32(n, what)
         self.cache, self.n_heads = cache, n_heads
         self.width = n_heads * cache.head_dim
         self._layer = None
