@@ -115,6 +115,8 @@ class Engine:
         first positions that stay visible.  Paged bf16 engines, before any slab exists."""
         L, hd = self.shape.n_layers, self.shape.head_dim
         window, sinks = size32(window, "window"), size32(sinks, "sinks")
+        if rope is not None and rope.head_dim != hd:
+            raise ValueError(f"rope: head_dim {rope.head_dim}, the engine's is {hd}")
         norms = []
         for g in (q_norm, k_norm):
             g = None if g is None else list(g)

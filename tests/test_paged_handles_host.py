@@ -49,3 +49,11 @@ def test_sizes_are_whole_numbers():
     for bad in (4.0, "4", None):
         with pytest.raises(TypeError):
             paged.RopeAppend(cache_stub(), None, n_heads=bad)
+
+
+def test_an_engine_refuses_the_rope_of_another_head_size():
+    engine = SimpleNamespace(shape=SimpleNamespace(n_layers=1, head_dim=128), arena=torch.zeros(1), handle=None)
+    with pytest.raises(ValueError, match="head_dim"):
+        model.Engine.set_attention(engine, paged.Rope(64))
+    with pytest.raises(B.CbtError):  # taken, but for the missing engine
+        model.Engine.set_attention(engine, paged.Rope(128, rot_dim=64))
