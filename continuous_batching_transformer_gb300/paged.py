@@ -7,6 +7,11 @@ handles check what they are given, borrow the tensors they were made with (which
 them) and queue their work on the current stream of the pool's device; lengths, tables and the
 free stack stay on the device, so a step can be captured in a CUDA graph.
 
+The workspace, error words and outputs that a handle makes itself may be used on any stream of the
+device, and are kept from reuse while queued work needs them, also where the handle goes before.  A
+captured graph holds their addresses alone: its handles have to outlive it.  Order between streams that
+use one handle, and the caller's own tensors, are the caller's to keep.
+
 A step of one layer::
 
     cache = PagedKV(pool, block_table, kv_lens, page_tokens=128, n_kv_heads=8, head_dim=128)
@@ -97,18 +102,49 @@ _I32, _BF16, _ROWS = (torch.int32,), (torch.bfloat16,), (torch.bfloat16, torch.f
 
 
 class _Device:
-    """Queues a call on a device's current stream, with that device current."""
+    """Queues a handle's calls on its device's current stream, with that device current.
 
-    def __init__(self, index):
-        self.index = index
+    own     device tensors that the handle made.  A stream other than the one they were made on waits
+            for that one before its first call, and is made known to torch's allocator, so that
+            their memory is not given away under queued work when the handle goes.
+    parent  of the handle's cache
+    Within a capture neither is done: a graph's first replay follows what the capture waited for, and a
+    graph has to be outlived by its handles."""
+
+    def __init__(self, index, own, parent=None):
+        self.index, self.own, self.parent = index, own, parent
+        with torch.cuda.device(index):
+            stream = torch.cuda.current_stream()
+            self.ready = None if torch.cuda.is_current_stream_capturing() else stream.record_event()
+        self.streams = {stream.cuda_stream}
+        if parent is not None:
+            parent.join(stream.cuda_stream)
+
+    def join(self, raw):
+        if raw in self.streams:
+            return
+        if self.parent is not None:
+            self.parent.join(raw)
+        with torch.cuda.device(self.index):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            stream = torch.cuda.current_stream()
+            if self.ready is not None:
+                stream.wait_event(self.ready)
+            for t in self.own:
+                t.record_stream(stream)
+        self.streams.add(raw)
 
     def __call__(self, fn, args):
         # the stream's handle alone: torch.cuda.current_stream builds an object around it (1 us)
+        raw = torch._C._cuda_getCurrentRawStream(self.index)
+        if raw not in self.streams:
+            self.join(raw)
         if torch.cuda.current_device() == self.index:
-            fn(args, torch._C._cuda_getCurrentRawStream(self.index))
+            fn(args, raw)
         else:
             with torch.cuda.device(self.index):
-                fn(args, torch._C._cuda_getCurrentRawStream(self.index))
+                fn(args, raw)
 
 
 def _read_err(err: torch.Tensor) -> None:
@@ -174,7 +210,7 @@ class PagedKV:
                                      self.n_pages, page_tokens, n_kv_heads, head_dim)
                        for l in range(n_layers)]
         self.err = torch.zeros(2, dtype=torch.int32, device=self.device)
-        self.call = _Device(self.index)
+        self.call = _Device(self.index, [self.err])
 
     def check(self) -> None:
         """Wait for the work queued on the current stream and raise if a kernel found an error."""
@@ -213,9 +249,12 @@ class PageMap:
         if max_tokens < 0:
             raise ValueError("max_tokens is negative")
 
+        own = []
+
         def new(t, what, n):
             if t is None:
-                return torch.empty(n, dtype=torch.int32, device=block_table.device)
+                own.append(torch.empty(n, dtype=torch.int32, device=block_table.device))
+                return own[-1]
             _vec(_tensor(t, what, _I32, self.index), what, self.index, n)
             return t
         self.cu_q = new(cu_q, "cu_q", rows + 1)
@@ -230,7 +269,7 @@ class PageMap:
                                   max_tokens, None, None, self.cu_q.data_ptr(),
                                   self.positions.data_ptr(), self.slots.data_ptr(),
                                   self.err.data_ptr())
-        self.call = _Device(self.index)
+        self.call = _Device(self.index, own + [self.err])
 
     def __call__(self, new_lens, kv_lens_out=None, free_count_out=None) -> None:
         """One step: row b takes new_lens[b] more positions (negative: it retires).  The lengths
@@ -326,6 +365,7 @@ class Attention:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
         a.workspace = self.workspace.data_ptr() if n else None
         a.workspace_bytes = n
+        self.call = _Device(cache.index, [self.workspace] if n else [], cache.call)
 
     def __call__(self, layer: int, q, out, cu_q=None) -> None:
         """q [tokens, n_heads, head_dim] (or two dimensions) bf16, out the same shape in bf16 or
@@ -350,4 +390,4 @@ class Attention:
             a.cu_q = _vec(cu_q, "cu_q", dev, c.rows + 1)
         a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
         a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
-        c.call(B.paged_attention, a)
+        self.call(B.paged_attention, a)

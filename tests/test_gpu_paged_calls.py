@@ -1,6 +1,6 @@
 """Calls of the operators on a paged KV cache that the documentation allows and that lie off the usual
-path: CTAs that hold every unit they may, ranges of tokens that are none.  Tolerances are those of
-tests/test_gpu_paged_ops."""
+path: CTAs that hold every unit they may, ranges of tokens that are none, handles that are
+dropped early and streams other than their own.  Tolerances are those of tests/test_gpu_paged_ops."""
 import pytest
 import torch
 
@@ -108,3 +108,70 @@ def test_ranges_that_overlap(rows, max_kv):
     v = V.permute(0, 1, 3, 2).reshape(1, 64, hd).double().cpu().repeat(1, n + 1, 1)[:, :max_kv].numpy()
     check_attention(out[:tokens], *R.attention(q[:tokens].double().cpu().numpy(), k, v, max_kv - tokens, 0, 0,
                                                hd ** -0.5), torch.float32)
+
+
+def busy():
+    torch.cuda._sleep(200_000_000)  # some 0.1 s
+
+
+def taken_from(ptrs, sizes):
+    """Whether new tensors of these sizes, made on the current stream, take any of the addresses."""
+    held = [torch.empty(n, dtype=torch.uint8, device=dev()) for n in sizes for _ in range(50)]
+    return {t.data_ptr() for t in held} & set(ptrs)
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_memory_of_dropped_handles(new):
+    """Handles that are dropped while another stream has yet to run their calls: what they made themselves
+    is not handed out again before."""
+    rows = [(3000, new), (2500, new)]
+    c = R.Cache(rows, kv=2, hd=128, page=128, window=0, sinks=0, seed=2, device=dev())
+    q = torch.randn(2 * new, 8, 128, device=dev()).to(torch.bfloat16)
+    out, want = torch.zeros(2 * new, 8, 128, device=dev()), torch.zeros(2 * new, 8, 128, device=dev())
+    table, lens, fresh = torch.zeros(2, 5, dtype=torch.int32, device=dev()), i32([0, 0]), i32([1, 2])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    def handles():
+        cache = paged.PagedKV(c.pool, c.table, c.lens, page_tokens=128, n_kv_heads=2, head_dim=128)
+        pm = paged.PageMap(table, lens, None, None, page_tokens=128, max_tokens=700, n_pages=4)
+        return cache, paged.Attention(cache, n_heads=8, max_kv=4096, max_q=new, max_tokens=2 * new), pm
+    cache, attn, pm = handles()
+    attn(0, q, want, cu_q=c.cu)
+    pm(fresh)  # (a kernel's first call loads it, which may wait for the device)
+    cache.check()
+    del cache, attn, pm
+    busy()
+    torch.cuda.synchronize()
+    cache, attn, pm = handles()
+    own = [cache.err, attn.workspace, pm.err, pm.cu_q, pm.positions, pm.slots]
+    ptrs, sizes = [t.data_ptr() for t in own], [t.numel() * t.element_size() for t in own]
+    with torch.cuda.stream(side):
+        busy()
+        attn(0, q, out, cu_q=c.cu)
+        pm(fresh)
+        done = side.record_event()
+    del cache, attn, pm, own
+    taken = taken_from(ptrs, sizes)
+    assert not done.query(), "the other stream was done too early for this test to see anything"
+    assert not taken
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_the_first_call_waits_for_the_error_word():
+    """A cache made on a stream that is busy: a call on another one waits until its error word is zeroed,
+    so that the error it finds is not wiped out afterwards."""
+    c = R.Cache([(100, 1)], kv=2, hd=64, page=64, window=0, sinks=0, seed=2, device=dev())
+    c.table.fill_(-1)
+    q = torch.randn(1, 4, 64, device=dev()).to(torch.bfloat16)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        busy()
+        cache = paged.PagedKV(c.pool, c.table, c.lens, page_tokens=64, n_kv_heads=2, head_dim=64)
+        attn = paged.Attention(cache, n_heads=4, max_kv=128)
+    attn(0, q, out)
+    torch.cuda.synchronize()
+    assert cache.err.tolist() == [B.DEV_PAGE_ID, 0]
