@@ -10,7 +10,7 @@ free stack stay on the device, so a step can be captured in a CUDA graph.
 The workspace, error words and outputs that a handle makes itself may be used on any stream of the
 device, and are kept from reuse while queued work needs them, also where the handle goes before.  A
 captured graph holds their addresses alone: its handles have to outlive it.  Order between streams that
-use one handle, and the caller's own tensors, are the caller's to keep.
+use one handle, and the caller's own tensors, are the caller's to keep.  Threads may share a handle.
 
 A step of one layer::
 
@@ -29,6 +29,7 @@ from __future__ import annotations
 import ctypes
 import math
 import operator
+import threading
 
 import torch
 
@@ -263,6 +264,7 @@ class PageMap:
         self.err = torch.zeros(2, dtype=torch.int32, device=block_table.device)
         self.rows = rows
         self._keep = (block_table, kv_lens, free_pages, free_count)
+        self._lock = threading.Lock()  # a call's arguments are its own until it is queued
         opt = lambda t: None if t is None else t.data_ptr()
         self.args = B.PageMapArgs(block_table.data_ptr(), max_pages, page_tokens, n_pages, rows,
                                   kv_lens.data_ptr(), None, opt(free_pages), opt(free_count),
@@ -275,12 +277,13 @@ class PageMap:
         """One step: row b takes new_lens[b] more positions (negative: it retires).  The lengths
         and the count afterwards go to kv_lens and free_count, or to the tensors given."""
         a, dev = self.args, self.index
-        a.new_lens = _vec(new_lens, "new_lens", dev, self.rows)
-        a.kv_lens_out = a.kv_lens if kv_lens_out is None else \
-            _vec(kv_lens_out, "kv_lens_out", dev, self.rows)
-        a.free_count_out = a.free_count if free_count_out is None else \
-            _vec(free_count_out, "free_count_out", dev, 1)
-        self.call(B.page_map, a)
+        with self._lock:
+            a.new_lens = _vec(new_lens, "new_lens", dev, self.rows)
+            a.kv_lens_out = a.kv_lens if kv_lens_out is None else \
+                _vec(kv_lens_out, "kv_lens_out", dev, self.rows)
+            a.free_count_out = a.free_count if free_count_out is None else \
+                _vec(free_count_out, "free_count_out", dev, 1)
+            self.call(B.page_map, a)
 
     def check(self) -> None:
         _read_err(self.err)
@@ -296,6 +299,7 @@ class RopeAppend:
         self.width = (n_heads + 2 * cache.n_kv_heads) * cache.head_dim
         self.q_width = n_heads * cache.head_dim
         self._layer = None
+        self._lock = threading.Lock()
         self.args = B.RopeAppendArgs()
         self.args.rope = None if rope is None else ctypes.pointer(rope.desc)
         self.args.n_heads = n_heads
@@ -308,21 +312,22 @@ class RopeAppend:
         least `tokens` long (the first `tokens` are used); gains bf16 [head_dim] or None."""
         c, a = self.cache, self.args
         dev = c.index
-        a.tokens = tokens = qkv.shape[0]
-        if layer != self._layer:
-            a.kv = c.layers[layer]
-            self._layer = layer
-        a.qkv_stride = _rows(qkv, "qkv", _ROWS, dev, tokens, self.width)
-        a.q_stride = _rows(q_out, "q_out", _BF16, dev, tokens, self.q_width)
-        a.positions = _vec(positions, "positions", dev)
-        a.slots = _vec(slots, "slots", dev)
-        if positions.numel() < tokens or slots.numel() < tokens:
-            raise ValueError(f"positions and slots: fewer than {tokens} elements")
-        a.q_gain = None if q_gain is None else self._gain(q_gain, "q_gain")
-        a.k_gain = None if k_gain is None else self._gain(k_gain, "k_gain")
-        a.qkv, a.q_out = qkv.data_ptr(), q_out.data_ptr()
-        a.qkv_dtype = B.DTYPE_F32 if qkv.dtype is torch.float32 else B.DTYPE_BF16
-        c.call(B.rope_append, a)
+        with self._lock:
+            a.tokens = tokens = qkv.shape[0]
+            if layer != self._layer:
+                a.kv = c.layers[layer]
+                self._layer = layer
+            a.qkv_stride = _rows(qkv, "qkv", _ROWS, dev, tokens, self.width)
+            a.q_stride = _rows(q_out, "q_out", _BF16, dev, tokens, self.q_width)
+            a.positions = _vec(positions, "positions", dev)
+            a.slots = _vec(slots, "slots", dev)
+            if positions.numel() < tokens or slots.numel() < tokens:
+                raise ValueError(f"positions and slots: fewer than {tokens} elements")
+            a.q_gain = None if q_gain is None else self._gain(q_gain, "q_gain")
+            a.k_gain = None if k_gain is None else self._gain(k_gain, "k_gain")
+            a.qkv, a.q_out = qkv.data_ptr(), q_out.data_ptr()
+            a.qkv_dtype = B.DTYPE_F32 if qkv.dtype is torch.float32 else B.DTYPE_BF16
+            c.call(B.rope_append, a)
 
     def _gain(self, t, what):
         if _tensor(t, what, _BF16, self.cache.index, 1).numel() != self.cache.head_dim:
@@ -351,6 +356,7 @@ class Attention:
         self.cache, self.n_heads = cache, n_heads
         self.width = n_heads * cache.head_dim
         self._layer = None
+        self._lock = threading.Lock()
         self.max_tokens = cache.rows if max_tokens is None else max_tokens
         a = self.args = B.PagedAttentionArgs()
         a.kv = cache.layers[0]
@@ -372,22 +378,23 @@ class Attention:
         fp32; rows may be strided.  cu_q int32 [rows + 1]: row b's query tokens; None: one each."""
         c, a = self.cache, self.args
         dev = c.index
-        tokens = q.shape[0]
-        if layer != self._layer:
-            a.kv = c.layers[layer]
-            self._layer = layer
-        a.q_stride = _rows(q, "q", _BF16, dev, tokens, self.width)
-        a.out_stride = _rows(out, "out", _ROWS, dev, tokens, self.width)
-        if tokens > self.max_tokens:
-            raise ValueError(f"q: {tokens} rows, at most {self.max_tokens}")
-        if cu_q is None:
-            if tokens != c.rows:
-                raise ValueError(f"q: {tokens} rows for {c.rows} sequences and no cu_q")
-            if a.max_q != 1:
-                raise ValueError("a handle with max_q > 1 wants cu_q")
-            a.cu_q = None
-        else:
-            a.cu_q = _vec(cu_q, "cu_q", dev, c.rows + 1)
-        a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
-        a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
-        self.call(B.paged_attention, a)
+        with self._lock:
+            tokens = q.shape[0]
+            if layer != self._layer:
+                a.kv = c.layers[layer]
+                self._layer = layer
+            a.q_stride = _rows(q, "q", _BF16, dev, tokens, self.width)
+            a.out_stride = _rows(out, "out", _ROWS, dev, tokens, self.width)
+            if tokens > self.max_tokens:
+                raise ValueError(f"q: {tokens} rows, at most {self.max_tokens}")
+            if cu_q is None:
+                if tokens != c.rows:
+                    raise ValueError(f"q: {tokens} rows for {c.rows} sequences and no cu_q")
+                if a.max_q != 1:
+                    raise ValueError("a handle with max_q > 1 wants cu_q")
+                a.cu_q = None
+            else:
+                a.cu_q = _vec(cu_q, "cu_q", dev, c.rows + 1)
+            a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
+            a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
+            self.call(B.paged_attention, a)

@@ -1,4 +1,8 @@
-"""CPU checks of the paged operators' Python handles: sizes that a 32-bit field cannot hold."""
+"""CPU checks of the paged operators' Python handles: sizes that a 32-bit field cannot hold, handles that
+threads share."""
+import ctypes
+import threading
+import time
 from types import SimpleNamespace
 
 import pytest
@@ -57,3 +61,56 @@ def test_an_engine_refuses_the_rope_of_another_head_size():
         model.Engine.set_attention(engine, paged.Rope(64))
     with pytest.raises(B.CbtError):  # taken, but for the missing engine
         model.Engine.set_attention(engine, paged.Rope(128, rot_dim=64))
+
+
+class SlowCall:
+    """In place of the launch: sees the arguments, lets other threads run, and sees them again."""
+
+    def __init__(self, *args):
+        self.torn = []
+        self.seen = set()
+
+    def join(self, raw):
+        pass
+
+    def __call__(self, fn, a):
+        look = lambda: tuple(getattr(a, n) for n, t in a._fields_ if t in (ctypes.c_void_p, ctypes.c_int32))
+        before = look()
+        time.sleep(0.001)
+        self.seen.add(before)
+        if look() != before:
+            self.torn.append(before)
+
+
+@pytest.mark.parametrize("kind", ["append", "attention", "map"])
+def test_threads_that_share_a_handle(kind, monkeypatch):
+    """A call's arguments are its own until it has been queued."""
+    monkeypatch.setattr(paged, "_Device", SlowCall)
+    monkeypatch.setattr(paged, "_tensor", lambda t, *a, **k: t)
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    bf = lambda *n: torch.zeros(*n, dtype=torch.bfloat16)
+    cache = cache_stub()
+    cache.call = SlowCall()
+    if kind == "append":
+        h = paged.RopeAppend(cache, None, n_heads=4)
+        make = lambda n: (0, bf(n, 8 * 64), i32(n), i32(n), bf(n, 4 * 64))
+    elif kind == "attention":
+        h = paged.Attention(cache, n_heads=4, max_kv=128, max_q=1, max_tokens=9)
+        make = lambda n: (0, bf(n, 4 * 64), bf(n, 4 * 64), i32(3))
+    else:
+        table = i32(2, 3)
+        h = paged.PageMap(table, i32(2), None, None, page_tokens=64, max_tokens=8, n_pages=8)
+        h.index = -1
+        make = lambda n: (i32(2), i32(2), None)
+    device = cache.call if kind == "append" else h.call
+
+    def work(n):
+        args = make(n)
+        for _ in range(20):
+            h(*args)
+    threads = [threading.Thread(target=work, args=(n,)) for n in (1, 2, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(device.seen) == 3 and not device.torn
