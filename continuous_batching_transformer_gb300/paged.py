@@ -226,7 +226,7 @@ class PageMap:
                  find the pages they grow into in their table already
     n_pages      pages in the pool (ids are below it); free_pages' length where that is given
     A call fills cu_q [rows + 1], positions and slots [max_tokens], tensors of the handle (or, at
-    construction, the caller's), which later calls overwrite."""
+    construction, the caller's), which later calls overwrite.  Until the first they name no token."""
 
     def __init__(self, block_table, kv_lens, free_pages, free_count, *, page_tokens: int,
                  max_tokens: int, n_pages: int | None = None, cu_q=None, positions=None, slots=None):
@@ -252,13 +252,13 @@ class PageMap:
 
         own = []
 
-        def new(t, what, n):
+        def new(t, what, n, none=-1):
             if t is None:
-                own.append(torch.empty(n, dtype=torch.int32, device=block_table.device))
+                own.append(torch.full((n,), none, dtype=torch.int32, device=block_table.device))
                 return own[-1]
             _vec(_tensor(t, what, _I32, self.index), what, self.index, n)
             return t
-        self.cu_q = new(cu_q, "cu_q", rows + 1)
+        self.cu_q = new(cu_q, "cu_q", rows + 1, 0)
         self.positions = new(positions, "positions", max_tokens)
         self.slots = new(slots, "slots", max_tokens)
         self.err = torch.zeros(2, dtype=torch.int32, device=block_table.device)
@@ -283,7 +283,14 @@ class PageMap:
                 _vec(kv_lens_out, "kv_lens_out", dev, self.rows)
             a.free_count_out = a.free_count if free_count_out is None else \
                 _vec(free_count_out, "free_count_out", dev, 1)
+            if self.rows == 0:  # queues nothing; no token is what the outputs say
+                self.call(self._none, a)
             self.call(B.page_map, a)
+
+    def _none(self, a, stream):
+        self.cu_q.zero_()
+        self.positions.fill_(-1)
+        self.slots.fill_(-1)
 
     def check(self) -> None:
         _read_err(self.err)

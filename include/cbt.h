@@ -421,6 +421,7 @@ typedef struct {
  * count out of range (CBT_DEV_PAGES), then the lengths, count, table and stack stay as they
  * were, cu_q is all zero and positions and slots are all -1, so the calls that follow find no
  * tokens.
+ * With rows 0 nothing is written, cu_q, positions and slots among it.
  * Output arrays may not overlap anything else the call reads, but for the two named pairs.
  * rows <= CBT_PAGE_MAP_MAX_ROWS, max_tokens and n_pages <= 2^30, max_pages * page_tokens < 2^31
  * and n_pages * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_CUDA. */

@@ -175,3 +175,22 @@ def test_the_first_call_waits_for_the_error_word():
     attn(0, q, out)
     torch.cuda.synchronize()
     assert cache.err.tolist() == [B.DEV_PAGE_ID, 0]
+
+
+@pytest.mark.parametrize("own", [True, False])
+def test_a_map_of_no_rows(own):
+    """No rows take no tokens: positions and slots say so, and the append that follows writes nothing."""
+    given = {} if own else dict(cu_q=i32([5]), positions=i32([3, 2, 1]), slots=i32([0, 1, 2]))
+    pm = paged.PageMap(i32([[0]])[:0], i32([]), None, None, page_tokens=64, max_tokens=3, n_pages=2, **given)
+    # (before any call the handle's own outputs name no token either)
+    assert not own or (pm.positions.tolist() == pm.slots.tolist() == [-1] * 3 and pm.cu_q.tolist() == [0])
+    pm(i32([]))
+    pm.check()
+    assert pm.cu_q.tolist() == [0] and pm.positions.tolist() == pm.slots.tolist() == [-1] * 3
+    pool = torch.full((2 * 2 * 64 * 64,), 7.0, dtype=torch.bfloat16, device=dev())
+    cache = paged.PagedKV(pool, None, None, page_tokens=64, n_kv_heads=1, head_dim=64)
+    qkv = torch.randn(3, 3 * 64, device=dev()).to(torch.bfloat16)
+    q = torch.full((3, 1, 64), 7.0, dtype=torch.bfloat16, device=dev())
+    paged.RopeAppend(cache, None, n_heads=1)(0, qkv, pm.positions, pm.slots, q)
+    cache.check()
+    assert (pool == 7.0).all() and (q == 7.0).all()
