@@ -8,9 +8,10 @@
 // binary search in the prefix sums in shared memory.
 //
 // Bound by latency: some KB are read and 8 bytes a token written, all of it one dependent chain of
-// loads, scans and the barrier: 3.0 us for 8 rows with a token each, 7.0 us for 256 rows, 24 prompts
-// among them, with 32768 tokens of room.  Eight CTAs once the tokens or rows would keep one CTA for several passes, one CTA
-// (no cluster barrier) below that.
+// loads, scans and the barrier: 3.0 us for 8 rows with a token each, 7.4 us for 256 rows, 24 prompts
+// and 9 retiring rows among them, with 32768 tokens of room (7.0 us without the check of the returned
+// ids across the cluster).  Eight CTAs once the tokens or rows would keep one CTA for several passes,
+// one CTA (no cluster barrier) below that.
 #include <cooperative_groups.h>
 
 #include <limits.h>
@@ -82,11 +83,11 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   int* len = back + B + 1;   // [B] lengths before the call
   int* held = len + B;       // [B] and pages
   __shared__ Sums wtot[kThreads / 32];
-  __shared__ int bad_row;
+  __shared__ int bad_row, bad_page;  // the first row with a bad length, and with a bad page to return
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = C > 1 ? (int)blockIdx.x : 0;
   const bool pool = a.free_pages != nullptr;
-  if (tid == 0) bad_row = INT_MAX;
+  if (tid == 0) bad_row = bad_page = INT_MAX;
   pdl_wait();
   pdl_launch();
   __syncthreads();
@@ -150,17 +151,33 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   __syncthreads();
   const int t0 = rank * kThreads + tid;
   constexpr int kStep = C * kThreads;
-  if (code == 0 && pool) {  // push the retiring rows' pages
+  const bool returns = code == 0 && tot.back > 0;  // the same in the whole cluster
+  if (returns) {  // push the retiring rows' pages, above the count: a bad one undoes them by leaving that
     for (int i = t0; i < (int)tot.back; i += kStep) {
       const int r = find_row(back, B, i);
       const int id = a.block_table[(size_t)r * a.max_pages + (i - back[r])];
-      if (id < 0 || id >= a.n_pages) set_device_error(a.err, CBT_DEV_PAGE_ID, r);
+      if (id < 0 || id >= a.n_pages) atomicMin(&bad_page, r);
       a.free_pages[count + i] = id;
     }
   }
   // every CTA has read the lengths and the count; pushed pages are visible to the whole cluster
   if (C > 1) cg::this_cluster().sync();
   else __syncthreads();
+  if (returns) {
+    if (warp == 0) {
+      const int r = lane >= C ? INT_MAX : C > 1 ? *cg::this_cluster().map_shared_rank(&bad_page, lane) : bad_page;
+      bad_row = __reduce_min_sync(0xffffffffu, r);
+    }
+    __syncthreads();
+    if (bad_row != INT_MAX) {
+      code = CBT_DEV_PAGE_ID;
+      info = bad_row;
+    }
+    if (C > 1) cg::this_cluster().barrier_arrive();  // awaited before the CTA, and bad_page, go
+  }
+  auto leave = [&] {
+    if (C > 1 && returns) cg::this_cluster().barrier_wait();
+  };
 
   if (rank == 0) {  // the state afterwards
     for (int r = r0; r < r1; ++r) {
@@ -177,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
   }
   if (code) {
     for (int t = t0; t < a.max_tokens; t += kStep) a.positions[t] = a.slots[t] = -1;
+    leave();
     return;
   }
   const int top = (int)(count + tot.back) - 1;
@@ -223,6 +241,7 @@ __global__ void __launch_bounds__(kThreads) k_page_map(const cbt_page_map_args a
       a.slots[t] = good ? id[e] * P + off[e] : -1;
     }
   }
+  leave();
 }
 
 template <int C>

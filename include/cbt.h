@@ -417,10 +417,11 @@ typedef struct {
  *                page_tokens + position % page_tokens.  Both are -1 past the last token; a slot
  *                is -1 where its page id is outside [0, n_pages) (CBT_DEV_PAGE_ID, info: row).
  * All or nothing: if a row's length is negative or would pass max_pages * page_tokens
- * (CBT_DEV_LENGTH), the tokens pass max_tokens (CBT_DEV_TOKENS) or the stack is short or its
- * count out of range (CBT_DEV_PAGES), then the lengths, count, table and stack stay as they
- * were, cu_q is all zero and positions and slots are all -1, so the calls that follow find no
- * tokens.
+ * (CBT_DEV_LENGTH), the tokens pass max_tokens (CBT_DEV_TOKENS), the stack is short or its count
+ * out of range (CBT_DEV_PAGES), or a page id that a retiring row returns is outside [0, n_pages)
+ * (CBT_DEV_PAGE_ID, info: the row), then the lengths, count, table and stack stay as they were
+ * (what free_pages holds from the count on is never specified), cu_q is all zero and positions and
+ * slots are all -1, so the calls that follow find no tokens.
  * With rows 0 nothing is written, cu_q, positions and slots among it.
  * Output arrays may not overlap anything else the call reads, but for the two named pairs.
  * rows <= CBT_PAGE_MAP_MAX_ROWS, max_tokens and n_pages <= 2^30, max_pages * page_tokens < 2^31

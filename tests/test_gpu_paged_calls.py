@@ -194,3 +194,44 @@ def test_a_map_of_no_rows(own):
     paged.RopeAppend(cache, None, n_heads=1)(0, qkv, pm.positions, pm.slots, q)
     cache.check()
     assert (pool == 7.0).all() and (q == 7.0).all()
+
+
+@pytest.mark.parametrize("rows", [5, 1500])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, "past", 2 ** 31 - 1])
+def test_a_page_id_that_may_not_be_returned(rows, bad):
+    """Rows that retire with an id outside the pool in their table: the call changes nothing, and no later
+    one is handed that id."""
+    page, mp = 64, 3
+    n_pages = rows * mp + 8
+    bad = n_pages if bad == "past" else bad
+    table = torch.arange(rows * mp, dtype=torch.int32, device=dev()).view(rows, mp)
+    lens = i32([130] * rows)
+    stack = i32(list(range(rows * mp, n_pages)) + [-7] * (rows * mp))
+    count = i32([8])
+    pm = paged.PageMap(table, lens, stack, count, page_tokens=page, max_tokens=2 * rows)
+    new = torch.where(torch.arange(rows, device=dev()) % 5 == 3, -1, 1).int()
+    last = (rows - 4) // 5 * 5 + 3
+    for where in ([3], [last], [last, 3]):
+        t = table.clone()
+        for r in where:
+            table[r, r % 3] = bad
+        before = [x.clone() for x in (table, lens, stack[:8], count)]
+        pm(new)
+        torch.cuda.synchronize()
+        assert pm.err.tolist() == [B.DEV_PAGE_ID, min(where)]
+        assert all(torch.equal(x, y) for x, y in zip(before, (table, lens, stack[:8], count)))
+        assert set(pm.cu_q.tolist()) == {0} and set(pm.positions.tolist()) == set(pm.slots.tolist()) == {-1}
+        pm.err.zero_()
+        table.copy_(t)
+    want = R.page_map(table.tolist(), lens.tolist(), new.tolist(), stack.tolist(), 8, page, 2 * rows)
+    pm(new)
+    pm.check()
+    t, l, s, c, cu, pos, slots = want
+    assert (table.tolist(), lens.tolist(), stack[:c].tolist(), count.tolist()) == (t, l, s[:c], [c])
+    assert (pm.cu_q.tolist(), pm.positions.tolist(), pm.slots.tolist()) == (cu, pos, slots)
+    # ids beyond a row's length are not looked at, nor those of rows that stay
+    table[3, 1:] = bad
+    table[0, 2] = bad
+    lens[3] = 5
+    pm(i32([0, 0, 0, -1] + [0] * (rows - 4)))
+    pm.check()
