@@ -1232,6 +1232,12 @@ static long long keys_seen(const cbt_engine* e, long long pos) {
   return w && pos >= w ? w + std::min<long long>(e->form.sinks, pos + 1 - w) : pos + 1;
 }
 
+// positions that all pages together hold, the most a row can have (below 2^30: a position takes 256
+// bytes or more of an arena below 2^38)
+static long long most_positions(const cbt_engine* e) {
+  return (long long)(e->p.kv_arena_bytes / e->page_bytes) * e->page;
+}
+
 static PagedKv form_kv(const cbt_engine* e, int layer) {
   const cbt_model_config& c = e->cfg;
   PagedKv kv{};
@@ -1334,9 +1340,7 @@ static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t*
   if (longest > f.max_kv) {
     long long cap = 1024;
     while (cap < longest) cap *= 2;
-    // within what max_kv + window and max_kv + sinks may be
-    cap = std::min<long long>(cap, (long long)INT32_MAX - std::max(f.window, f.sinks));
-    if (cap < longest) return cudaErrorInvalidValue;
+    cap = std::min(cap, std::max<long long>(longest, most_positions(e)));
     rc = cudaStreamSynchronize(e->stream);
     drop_graphs(e);  // captured steps hold the old addresses and bounds
     if (f.table) cudaFree(f.table);
@@ -1391,7 +1395,7 @@ extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attentio
     return CBT_ERR_INVALID;
   if (!e->page || e->quant() || !e->use_tc || e->p.max_batch > CBT_PAGED_ATTENTION_MAX_ROWS ||
       e->cfg.n_heads / e->cfg.n_kv_heads > 64 || e->p.kv_arena_bytes >= (size_t)128 << 31 ||
-      (double)(e->p.kv_arena_bytes / e->page_bytes) * e->page > (double)INT32_MAX)
+      most_positions(e) > INT32_MAX)
     return CBT_ERR_UNSUPPORTED;
   const cbt_rope_config own = {CBT_ROPE_HALF, e->cfg.head_dim, CBT_ROPE_NONE, 0, e->cfg.rope_theta,
                                1.0, 0.0, 0.0, 0.0};
@@ -1428,8 +1432,11 @@ extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attentio
   f.q_norm = std::move(norms[0]);
   f.k_norm = std::move(norms[1]);
   f.eps = c->qk_norm_eps;
-  f.window = c->window;
-  f.sinks = c->sinks;
+  // A window that no row can outgrow, or as many sinks, hides nothing.  Other windows and sinks are below
+  // 2^30, as max_kv is, so that their sums with it stay within what the kernels take.
+  const long long most = most_positions(e);
+  f.window = c->window < most && c->sinks < most ? c->window : 0;
+  f.sinks = f.window ? c->sinks : 0;
   if (f.max_kv) {  // the workspace depends on the window: sized again by the next call
     cudaStreamSynchronize(e->stream);
     cudaFree(f.table);

@@ -580,7 +580,8 @@ size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
  *   rope    rotary form (copied); NULL: the built-in one
  *   q_norm, k_norm  host arrays [n_layers] of device bf16 [head_dim] gains (the array is copied,
  *           the gains are borrowed), or NULL: that norm is left out
- *   window, sinks  as in cbt_paged_attention
+ *   window, sinks  as in cbt_paged_attention, any size: where either reaches the positions that all
+ *           of the arena's pages hold, every earlier position is seen
  * q is rounded to bf16 for the attention.  Pages behind the window stay held.  Of such an engine
  * cbt_engine_stamps records the projections alone.  Only before slabs
  * exist (CBT_ERR_INVALID otherwise).  Needs a paged engine (kv_page_tokens > 0) with bf16 KV on the
