@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "cbt.h"
+#include "form_buffers.h"
 #include "kernels.h"
 #include "paged.h"
 
@@ -193,12 +194,10 @@ struct cbt_engine {
     std::vector<const uint16_t*> q_norm, k_norm;
     float eps = 0.f;
     int window = 0, sinks = 0;
-    int max_kv = 0, max_pages = 0;  // what table and ws are sized for (grown in powers of two)
-    int rows = 0, max_q = 0;        // of the call being queued
-    int32_t *table = nullptr, *lens = nullptr, *fresh = nullptr, *lens_out = nullptr;
+    FormBuffers buf;          // table and workspace, grown with the rows
+    int rows = 0, max_q = 0;  // of the call being queued
+    int32_t *lens = nullptr, *fresh = nullptr, *lens_out = nullptr;
     int32_t *cu = nullptr, *positions = nullptr, *slots = nullptr;
-    uint8_t* ws = nullptr;
-    size_t ws_bytes = 0;
     std::vector<int32_t> htable, hlens, hfresh;
   } form;
 
@@ -231,7 +230,7 @@ static void free_scratch(cbt_engine* e) {
                   e->rows,    e->err,      e->act_h, e->act_o, e->act_u,
                   e->items,    e->item_meta, e->att_o, e->att_ml, e->stage,
                   e->qtile,   e->ss,       e->qb,     e->pf_units, e->q4_arena, e->pagetab,
-                  e->tok_pages, e->kv8_jobs, e->q4x, e->form.table, e->form.lens, e->form.ws};
+                  e->tok_pages, e->kv8_jobs, e->q4x, e->form.buf.table, e->form.lens, e->form.buf.ws};
   for (void* q : ptrs)
     if (q) cudaFree(q);
 }
@@ -1258,14 +1257,14 @@ static PagedAttn form_attn_args(const cbt_engine* e, int n, int layer, bool deco
   const cbt_engine::Form& f = e->form;
   PagedAttn a{};
   a.kv = form_kv(e, layer);
-  a.table = f.table;
-  a.max_pages = f.max_pages;
+  a.table = static_cast<const int32_t*>(f.buf.table);
+  a.max_pages = f.buf.max_pages;
   a.rows = f.rows;
   a.lens = f.lens_out;
   a.cu = decode ? nullptr : f.cu;
   a.tokens = n;
   a.max_q = f.max_q;
-  a.max_kv = f.max_kv;
+  a.max_kv = f.buf.max_kv;
   a.n_heads = e->cfg.n_heads;
   a.q = e->qb;
   a.q_ld = a.out_ld = e->qd();
@@ -1274,8 +1273,8 @@ static PagedAttn form_attn_args(const cbt_engine* e, int n, int layer, bool deco
   a.sinks = f.sinks;
   a.out = e->o;
   a.f32 = true;
-  a.ws = f.ws;
-  a.ws_bytes = f.ws_bytes;
+  a.ws = static_cast<uint8_t*>(f.buf.ws);
+  a.ws_bytes = f.buf.ws_bytes;
   a.err = e->err;
   return a;
 }
@@ -1284,8 +1283,8 @@ static cudaError_t form_page_map(cbt_engine* e, int n) {
   const cbt_engine::Form& f = e->form;
   const PagedKv kv = form_kv(e, 0);
   cbt_page_map_args a{};
-  a.block_table = f.table;
-  a.max_pages = f.max_pages;
+  a.block_table = static_cast<int32_t*>(f.buf.table);
+  a.max_pages = f.buf.max_pages;
   a.page_tokens = kv.page_tokens;
   a.n_pages = kv.n_pages;
   a.rows = f.rows;
@@ -1323,11 +1322,29 @@ static cudaError_t form_attention(cbt_engine* e, int n, int layer, bool decode) 
                            : rc;
 }
 
-// Before a call of K rows is queued: row r takes lens[r] tokens (one where lens is NULL).  Grows
-// the buffers for the longest row; the pages themselves are already there (prepare_writes).
-static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t* lens, int K) {
+// the device memory of grow_form, on an engine whose queued work and captured steps hold addresses
+namespace {
+struct FormMemory {
+  cbt_engine* e;
+  void* alloc(size_t n) {
+    void* p = nullptr;
+    if (cudaMalloc(&p, n) == cudaSuccess) return p;
+    cudaGetLastError();  // the step that comes next asks for the last error of its own launches
+    return nullptr;
+  }
+  void settle() {
+    cudaStreamSynchronize(e->stream);
+    drop_graphs(e);
+  }
+  void release(void* p) { cudaFree(p); }
+};
+}  // namespace
+
+// Before a call of K rows is queued: row r takes lens[r] tokens (one where lens is NULL; n in all).
+// Grows the buffers for the longest row and these rows' partial sums; the pages themselves are already
+// there (prepare_writes).
+static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t* lens, int K, int n) {
   cbt_engine::Form& f = e->form;
-  const int mb = e->p.max_batch;
   int longest = 0;
   f.rows = K;
   f.max_q = 1;
@@ -1336,45 +1353,27 @@ static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t*
     longest = std::max(longest, e->slabs[ids[r]].pos + m);
     f.max_q = std::max(f.max_q, m);
   }
-  cudaError_t rc = cudaSuccess;
-  if (longest > f.max_kv) {
-    long long cap = 1024;
-    while (cap < longest) cap *= 2;
-    cap = std::min(cap, std::max<long long>(longest, most_positions(e)));
-    rc = cudaStreamSynchronize(e->stream);
-    drop_graphs(e);  // captured steps hold the old addresses and bounds
-    if (f.table) cudaFree(f.table);
-    if (f.ws) cudaFree(f.ws);
-    f.table = nullptr;
-    f.ws = nullptr;
-    f.max_kv = 0;
-    f.max_pages = (int)((cap + e->page - 1) / e->page);
-    if (rc == cudaSuccess)
-      rc = cudaMalloc(reinterpret_cast<void**>(&f.table), (size_t)mb * f.max_pages * sizeof(int32_t));
-    f.max_kv = (int)cap;
-    PagedAttn most = form_attn_args(e, mb, 0, true);  // a decode step of max_batch rows
-    most.rows = mb;
-    most.max_q = 1;
-    const size_t ws = std::max(paged_attn_workspace(most), paged_prefill_most_workspace(e->cfg.head_dim));
-    if (rc == cudaSuccess) rc = cudaMalloc(reinterpret_cast<void**>(&f.ws), ws);
-    f.ws_bytes = ws;
-    if (rc != cudaSuccess) {
-      f.max_kv = 0;
-      return rc;
-    }
-  }
-  f.htable.assign((size_t)K * f.max_pages, -1);
+  auto ws_bytes = [&](int max_kv) {
+    PagedAttn a = form_attn_args(e, n, 0, lens == nullptr);
+    a.max_kv = max_kv;
+    return paged_attn_workspace(a);
+  };
+  FormMemory mem{e};
+  if (!grow_form(&f.buf, longest, most_positions(e), e->page, e->p.max_batch, ws_bytes, mem))
+    return cudaErrorMemoryAllocation;
+  const int max_pages = f.buf.max_pages;
+  f.htable.assign((size_t)K * max_pages, -1);
   f.hlens.resize(K);
   f.hfresh.resize(K);
   for (int r = 0; r < K; ++r) {
     const Slab& sl = e->slabs[ids[r]];
-    for (size_t p = 0; p < sl.pages.size() && p < (size_t)f.max_pages; ++p)
-      f.htable[(size_t)r * f.max_pages + p] = (int32_t)(sl.pages[p] / e->page_bytes);
+    for (size_t p = 0; p < sl.pages.size() && p < (size_t)max_pages; ++p)
+      f.htable[(size_t)r * max_pages + p] = (int32_t)(sl.pages[p] / e->page_bytes);
     f.hlens[r] = sl.pos;
     f.hfresh[r] = lens ? lens[r] : 1;
   }
-  rc = cudaMemcpyAsync(f.table, f.htable.data(), f.htable.size() * sizeof(int32_t),
-                       cudaMemcpyHostToDevice, e->stream);
+  cudaError_t rc = cudaMemcpyAsync(f.buf.table, f.htable.data(), f.htable.size() * sizeof(int32_t),
+                                   cudaMemcpyHostToDevice, e->stream);
   if (rc == cudaSuccess)
     rc = cudaMemcpyAsync(f.lens, f.hlens.data(), K * sizeof(int32_t), cudaMemcpyHostToDevice, e->stream);
   if (rc == cudaSuccess)
@@ -1387,7 +1386,10 @@ extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attentio
   if (!e->slabs.empty()) return CBT_ERR_INVALID;
   cbt_engine::Form& f = e->form;
   if (!c) {
-    if (f.on) drop_graphs(e);
+    if (f.on) {
+      cudaStreamSynchronize(e->stream);  // the gains are the caller's again
+      drop_graphs(e);
+    }
     f.on = false;
     return CBT_OK;
   }
@@ -1426,6 +1428,7 @@ extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attentio
     f.positions = f.cu + mb + 4;
     f.slots = f.positions + e->tmax;
   }
+  if (f.on) cudaStreamSynchronize(e->stream);  // the gains of before are the caller's again
   drop_graphs(e);
   f.on = true;
   f.rope = rope;
@@ -1437,14 +1440,6 @@ extern "C" cbt_status cbt_engine_set_attention(cbt_engine* e, const cbt_attentio
   const long long most = most_positions(e);
   f.window = c->window < most && c->sinks < most ? c->window : 0;
   f.sinks = f.window ? c->sinks : 0;
-  if (f.max_kv) {  // the workspace depends on the window: sized again by the next call
-    cudaStreamSynchronize(e->stream);
-    cudaFree(f.table);
-    if (f.ws) cudaFree(f.ws);
-    f.table = nullptr;
-    f.ws = nullptr;
-    f.max_kv = 0;
-  }
   return CBT_OK;
 }
 
@@ -1816,7 +1811,7 @@ extern "C" cbt_status cbt_decode_step_batch(cbt_engine* e, const int32_t* ids, i
     }
     rc = upload_page_tables(e);
   }
-  if (rc == cudaSuccess && e->form.on) rc = upload_form(e, ids, nullptr, B);
+  if (rc == cudaSuccess && e->form.on) rc = upload_form(e, ids, nullptr, B, B);
   else if (rc == cudaSuccess && e->use_tc) rc = plan_decode_attention(e, B);
   if (rc == cudaSuccess && e->stamps_on) {  // begin slots to the maximum, end slots to 0
     rc = cudaMemset2DAsync(e->stamp_buf, 16, 0xFF, 8, kStampSlots, e->stream);
@@ -2112,7 +2107,7 @@ static cbt_status prefill_impl(cbt_engine* e, const int32_t* ids, const int32_t*
                          e->stream);
   if (rc == cudaSuccess && e->page) rc = upload_page_tables(e);
   if (rc == cudaSuccess)
-    rc = e->form.on ? upload_form(e, ids, lens, K) : plan_prefill_attention(e, ids, lens, K);
+    rc = e->form.on ? upload_form(e, ids, lens, K, (int)T) : plan_prefill_attention(e, ids, lens, K);
   if (rc == cudaSuccess)
     rc = forward(e, (int)T, tokens, max_keys, total_keys, true, K, logits, next_tokens);
   if (rc != cudaSuccess) return rc == cudaErrorNotSupported ? CBT_ERR_UNSUPPORTED : CBT_ERR_CUDA;

@@ -62,5 +62,4 @@ cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s);
 size_t paged_decode_workspace(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, int num_sms, cudaStream_t s);
 size_t paged_prefill_workspace(const PagedAttn& a);
-size_t paged_prefill_most_workspace(int head_dim);  // of any call with tokens <= rows * max_q
 cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s);

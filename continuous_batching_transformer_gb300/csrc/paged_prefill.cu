@@ -802,10 +802,6 @@ size_t paged_prefill_workspace(const PagedAttn& a) {
   const int runs = runs_for(a);
   return runs == 1 ? 0 : (size_t)a.tokens * a.n_heads * runs * (a.kv.head_dim * sizeof(float) + sizeof(float2));
 }
-// of tokens <= rows * max_q: a row of a tile each for the most items
-size_t paged_prefill_most_workspace(int head_dim) {
-  return (size_t)kMostItems * 2 * kRows * (head_dim * sizeof(float) + sizeof(float2));
-}
 
 cudaError_t launch_paged_prefill(const PagedAttn& a, int num_sms, cudaStream_t s) {
   CUtensorMap tq, tk, tv;

@@ -583,9 +583,16 @@ size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
  *   window, sinks  as in cbt_paged_attention, any size: where either reaches the positions that all
  *           of the arena's pages hold, every earlier position is seen
  * q is rounded to bf16 for the attention.  Pages behind the window stay held.  Of such an engine
- * cbt_engine_stamps records the projections alone.  Only before slabs
- * exist (CBT_ERR_INVALID otherwise).  Needs a paged engine (kv_page_tokens > 0) with bf16 KV on the
- * tensor-core path, max_batch <= CBT_PAGED_ATTENTION_MAX_ROWS and n_heads / n_kv_heads <= 64
+ * cbt_engine_stamps records the projections alone.
+ * The calls' page table and the attention's partial sums grow inside the call that needs more, which
+ * waits for the stream.  The table takes 4 bytes for each page of
+ * the longest row, max_batch times; the sums of a decode step of B rows 4 * B * n_heads * head_dim bytes
+ * for every 512 positions of the longest row (every 128 below 4096), those of a prefill at most 84 MB.
+ * Where no memory is left the call returns CBT_ERR_CUDA and queues no step, and calls that fit
+ * what is there go on.
+ * Only before slabs exist (CBT_ERR_INVALID otherwise); a form that replaces one waits for the stream,
+ * and the gains of before are the caller's again.  Needs a paged engine (kv_page_tokens > 0) with bf16
+ * KV on the tensor-core path, max_batch <= CBT_PAGED_ATTENTION_MAX_ROWS and n_heads / n_kv_heads <= 64
  * (CBT_ERR_UNSUPPORTED).  Errors leave the engine's form as it was. */
 typedef struct {
   const cbt_rope_config* rope;

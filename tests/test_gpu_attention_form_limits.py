@@ -1,9 +1,10 @@
 """Engines with an attention form (cbt_engine_set_attention) at the ends of what it takes."""
 import numpy as np
 import pytest
+import torch
 
-from tests.gpu_harness import ensure_built
-from tests.test_gpu_attention_form import SHAPES, make_engine, run, weights
+from tests.gpu_harness import ensure_built, to_dev
+from tests.test_gpu_attention_form import FORMS, SHAPES, make_engine, run, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +25,43 @@ def test_windows_and_sinks_that_hide_nothing(form):
     outs, _ = run(make_engine(w, form)[0], w.shape, lens, steps, chunk=400)
     want, _ = run(make_engine(w, {})[0], w.shape, lens, steps, chunk=400)
     assert all(np.array_equal(a, b) for a, b in zip(outs, want))
+
+
+def test_growth_under_captured_steps():
+    """Rows that outgrow the table and the sums between captured decode steps: the same bits as from an
+    engine whose buffers were made for all of it before."""
+    w, _ = weights(SHAPES["hd128-gqa"])
+    s = w.shape
+    g = torch.Generator().manual_seed(2)
+    lens = [10, 900, 1500, 5000, 9000, 13000]
+    kv = torch.randn(2, s.n_layers, s.n_kv_heads, max(lens), s.head_dim, generator=g).to(torch.bfloat16).cuda()
+    toks = to_dev(np.arange(100, 100 + len(lens), dtype=np.int32))
+
+    def add(eng, n):
+        slab = eng.kv_slab_alloc(n + 100)
+        eng.import_kv(slab, kv[0, :, :, :n].contiguous(), kv[1, :, :, :n].contiguous(), n)
+        return slab
+
+    def steps(eng):
+        slabs, outs = [], []
+        for i, n in enumerate(lens):
+            slabs.append(add(eng, n))
+            for rows in ([i], list(range(i + 1))):
+                lg = torch.empty(len(rows), s.vocab, device="cuda")
+                for _ in range(2):  # the second replays what the first captured
+                    eng.decode_step_batch([slabs[r] for r in rows], toks[rows], lg)
+                    outs.append(lg.clone())
+        assert eng.device_error() == (0, 0)
+        eng.retire(slabs)
+        return outs
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        eng, _ = make_engine(w, FORMS["norm"], stream, arena=256 << 20)
+        grown = steps(eng)
+        eng, _ = make_engine(w, FORMS["norm"], stream, arena=256 << 20)
+        slabs = [add(eng, max(lens)) for _ in lens]
+        eng.decode_step_batch(slabs, toks, torch.empty(len(lens), s.vocab, device="cuda"))
+        eng.retire(slabs)
+        want = steps(eng)
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grown, want)) and torch.isfinite(grown[-1]).all()
