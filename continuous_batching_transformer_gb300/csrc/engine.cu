@@ -1359,8 +1359,10 @@ static cudaError_t upload_form(cbt_engine* e, const int32_t* ids, const int32_t*
     return paged_attn_workspace(a);
   };
   FormMemory mem{e};
+  const size_t before = f.buf.table_bytes + f.buf.ws_bytes;
   if (!grow_form(&f.buf, longest, most_positions(e), e->page, e->p.max_batch, ws_bytes, mem))
     return cudaErrorMemoryAllocation;
+  e->scratch_bytes += f.buf.table_bytes + f.buf.ws_bytes - before;
   const int max_pages = f.buf.max_pages;
   f.htable.assign((size_t)K * max_pages, -1);
   f.hlens.resize(K);

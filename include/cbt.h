@@ -585,7 +585,7 @@ size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
  * q is rounded to bf16 for the attention.  Pages behind the window stay held.  Of such an engine
  * cbt_engine_stamps records the projections alone.
  * The calls' page table and the attention's partial sums grow inside the call that needs more, which
- * waits for the stream.  The table takes 4 bytes for each page of
+ * waits for the stream; cbt_stats.scratch_bytes counts them.  The table takes 4 bytes for each page of
  * the longest row, max_batch times; the sums of a decode step of B rows 4 * B * n_heads * head_dim bytes
  * for every 512 positions of the longest row (every 128 below 4096), those of a prefill at most 84 MB.
  * Where no memory is left the call returns CBT_ERR_CUDA and queues no step, and calls that fit

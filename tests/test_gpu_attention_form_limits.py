@@ -65,3 +65,25 @@ def test_growth_under_captured_steps():
         want = steps(eng)
         torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(grown, want)) and torch.isfinite(grown[-1]).all()
+
+
+def test_scratch_bytes_count_what_grows():
+    """The table and the sums of a form are in the engine's statistics, and grow with the rows."""
+    w, _ = weights(SHAPES["hd128-gqa"])
+    s = w.shape
+    eng, _ = make_engine(w, FORMS["norm"], arena=256 << 20)
+    counted = [eng.stats().scratch_bytes]
+    kv = torch.zeros(2, s.n_layers, s.n_kv_heads, 13000, s.head_dim, dtype=torch.bfloat16, device="cuda")
+    lg = torch.empty(3, s.vocab, device="cuda")
+    for n in (900, 13000):
+        slabs = [eng.kv_slab_alloc(n + 1) for _ in range(3)]
+        for slab in slabs:
+            eng.import_kv(slab, kv[0, :, :, :n].contiguous(), kv[1, :, :, :n].contiguous(), n)
+        eng.decode_step_batch(slabs, to_dev(np.array([1, 2, 3], np.int32)), lg)
+        eng.retire(slabs)
+        # an entry a page of 8 rows, and partial sums: three rows of 4 heads, in runs of four chunks of 128
+        # keys (fewer of short rows), each of head_dim sums with a maximum and a weight
+        least = 8 * 4 * -(-(n + 1) // 128) + 3 * 4 * -(-(n + 1) // 512) * (4 * s.head_dim + 8)
+        counted.append(eng.stats().scratch_bytes)
+        assert counted[0] + least <= counted[-1] <= counted[0] + 16 * least
+    assert counted[0] < counted[1] < counted[2]
