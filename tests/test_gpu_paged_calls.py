@@ -1,6 +1,7 @@
 """Calls of the operators on a paged KV cache that the documentation allows and that lie off the usual
 path: CTAs that hold every unit they may, ranges of tokens that are none, handles that are
 dropped early and streams other than their own.  Tolerances are those of tests/test_gpu_paged_ops."""
+import numpy as np
 import pytest
 import torch
 
@@ -8,7 +9,7 @@ from continuous_batching_transformer_gb300 import binding as B
 from continuous_batching_transformer_gb300 import paged
 from tests import paged_reference as R
 from tests.gpu_harness import ensure_built
-from tests.test_gpu_paged_ops import check_attention
+from tests.test_gpu_paged_ops import STEPS, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -235,3 +236,95 @@ def test_a_page_id_that_may_not_be_returned(rows, bad):
     lens[3] = 5
     pm(i32([0, 0, 0, -1] + [0] * (rows - 4)))
     pm.check()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_served_batch_from_what_was_cached(graph):
+    """Steps of map, append and attention on device state, each part against 64 bits from what the part
+    before it really left: q and the new K and V from the QKV rows, the attention from the q and the
+    pages that it read.  So its tolerance is that of one call, which a lost sink, a window off by one or a
+    stale page passes by far."""
+    rows, H, kv, hd, page, window, sinks, layers, top, n_pages, mp = 4, 8, 2, 64, 64, 70, 3, 2, 128, 14, 6
+    g = torch.Generator(device=dev()).manual_seed(1)
+    table = torch.full((rows, mp), -1, dtype=torch.int32, device=dev())
+    lens, free, count = i32([0] * rows), i32(list(range(n_pages))), i32([n_pages])
+    pool = torch.zeros(n_pages * paged.page_bytes(page, kv, hd, layers) // 2, dtype=torch.bfloat16, device=dev())
+    cache = paged.PagedKV(pool, table, lens, page_tokens=page, n_kv_heads=kv, head_dim=hd, n_layers=layers)
+    pm = paged.PageMap(table, lens, free, count, page_tokens=page, max_tokens=top)
+    app = paged.RopeAppend(cache, paged.Rope(hd, theta=1e4), n_heads=H)
+    attn = paged.Attention(cache, n_heads=H, max_kv=page * mp, max_q=100, max_tokens=top, window=window, sinks=sinks)
+    gain = (1 + 0.1 * torch.randn(2, layers, hd, device=dev(), generator=g)).to(torch.bfloat16)
+    new = i32([0] * rows)
+    qkv = torch.zeros(layers, top, (H + 2 * kv) * hd, device=dev())
+    q = torch.zeros(layers, top, H, hd, dtype=torch.bfloat16, device=dev())
+    out = torch.zeros(layers, top, H, hd, device=dev())
+
+    def step():
+        pm(new)
+        for l in range(layers):
+            app(l, qkv[l], pm.positions, pm.slots, q[l], gain[0, l], gain[1, l])
+            attn(l, q[l], out[l], cu_q=pm.cu_q)
+    captured = None
+    f, m = R.rope_freqs(hd, 1e4, "none", 1.0, 0)
+    blind = {"sinks": 0, "late window": 0, "early window": 0, "stale key": 0}
+    held = [0] * rows
+    for n in STEPS:
+        new.copy_(i32(n))
+        qkv.copy_(torch.randn(qkv.shape, device=dev(), generator=g))
+        if graph and captured is None:
+            state = [t.clone() for t in (table, lens, free, count, pool)]
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                step()
+            torch.cuda.current_stream().wait_stream(side)
+            for t, v in zip((table, lens, free, count, pool), state):
+                t.copy_(v)
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                step()
+        out.fill_(9.0)
+        captured.replay() if graph else step()
+        pm.check()
+        cache.check()
+        held = [0 if k < 0 else h + k for h, k in zip(held, n)]
+        assert lens.tolist() == held
+        at = 0
+        for b in range(rows):
+            k, L = max(n[b], 0), held[b]
+            if not k:
+                continue
+            ids = table[b, :-(-L // page)].long()
+            pos = list(range(L - k, L))
+            for l in range(layers):
+                K = R.k_view(pool, n_pages, layers, kv, page, hd, l)[ids].permute(1, 0, 2, 3).reshape(kv, -1, hd)
+                V = R.v_view(pool, n_pages, layers, kv, page, hd, l)[ids].permute(1, 0, 2, 4, 3).reshape(kv, -1, hd)
+                K, V = K[:, :L].double().cpu().numpy(), V[:, :L].double().cpu().numpy()
+                x = qkv[l, at:at + k].double().cpu().numpy().reshape(k, H + 2 * kv, hd)
+                G = gain[:, l].double().cpu().numpy()
+                got_q = q[l, at:at + k].double().cpu().numpy()
+                for got, heads, gn in ((got_q, x[:, :H], G[0]),
+                                       (K[:, L - k:].transpose(1, 0, 2), x[:, H:H + kv], G[1])):
+                    ref = R.rope_heads(heads, gn, 1e-6, pos, hd, "half", f, m)
+                    # the rounding to bf16, and fp32 roundings relative to the head's largest value
+                    tol = R.BF16_STEP * np.abs(ref) + 2.0 ** -17 * np.abs(ref).max(-1, keepdims=True)
+                    assert (np.abs(got - ref) <= tol).all()
+                v_in = torch.from_numpy(x[:, H + kv:]).to(torch.bfloat16).double().numpy()
+                assert np.array_equal(V[:, L - k:].transpose(1, 0, 2), v_in)
+                o = out[l, at:at + k]
+                scale = hd ** -0.5
+                check_attention(o, *R.attention(got_q, K, V, L - k, window, sinks, scale), torch.float32)
+                # mistakes planted in the reference are seen
+                if L > window + sinks:
+                    stale = K.copy()
+                    stale[:, L - window // 2] = K[:, L - 1]
+                    for name, (K2, w2, s2) in {"sinks": (K, window, 0), "late window": (K, window - 1, sinks),
+                                               "early window": (K, window + 1, sinks),
+                                               "stale key": (stale, window, sinks)}.items():
+                        wrong = R.attention(got_q, K2, V, L - k, w2, s2, scale)
+                        with pytest.raises(AssertionError):
+                            check_attention(o, *wrong, torch.float32)
+                        blind[name] += 1
+            at += k
+        assert (out[:, at:] == 9.0).all()
+    assert all(v >= 10 for v in blind.values()), blind
