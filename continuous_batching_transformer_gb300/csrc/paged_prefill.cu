@@ -120,9 +120,9 @@ static_assert(smem_bytes<64>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024,
 
 // Few units over long contexts: a unit's steps are cut into up to `runs` runs of kRunSteps steps or
 // more, taken by different CTAs and joined by k_prefill_merge (runs_for decides).
-// Whole and cut, rows of 4 tokens, 32 q and 8 kv heads of 128: one over 2000 positions 28 and 16 us, over
-// 131072 1460 and 100 us (5.4 TB/s of K and V); ten over 8192 101 and 78 us.  One row of 512 tokens over
-// 16384: 203 and 121 us.  With runs of 16 steps the first takes 21 us.
+// Whole and cut, rows of 4 tokens, 32 q and 8 kv heads of 128: one over 2000 positions 28 and 17 us, over
+// 131072 1454 and 98 us (5.4 TB/s of K and V); ten over 8192 100 and 77 us.  One row of 512 tokens over
+// 16384: 202 and 121 us.  With runs of 16 steps the first takes 21 us.
 constexpr int kRunSteps = 8;
 constexpr int kSms = 152, kMostRuns = 64;
 constexpr int kMostItems = 4 * kSms;  // that the runs may make
@@ -169,7 +169,8 @@ template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttn a,
-                    const int runs, const int most, float* __restrict__ part_o, float2* __restrict__ part_ml) {
+                    const int runs, const int most, float* __restrict__ part_o,
+                    float2* __restrict__ part_ml) {
   constexpr int nKh = HD / 64;
   constexpr uint32_t kTile = nKh * kBox;     // a Q tile
   constexpr uint32_t kKV = kStep * HD * 2;   // K or V of a step
@@ -742,9 +743,11 @@ constexpr int kFewPairs = 20 * kSms, kManyRuns = 8;  // up to, and above which, 
 // The most runs a unit is cut into (1: none), from rows, max_q and max_kv alone: the number that should
 // take the least time, counted in steps (0.75 us).  Items go to the SMs in rounds; each costs its steps,
 // 5 more to start and end, and the writing of its partial outputs (45 bytes a ns); the join costs 6
-// and the reading of them all (5000 bytes a ns).  Over 25 shapes the cut so chosen was at worst 2 % behind
-// whole (two rows of 700 tokens over 6000: 157 to 159 and 155 to 156 us).  One item for each SM instead:
-// ten rows of 4 over 8192 stay whole, 101 for 78 us.
+// and the reading of them all (5000 bytes a ns).  Over 25 shapes whose bounds were the rows' own the cut so
+// chosen was at worst 2 % behind whole (two rows of 700 tokens over 6000: 157 and 155 us).  Bounds above
+// the rows mislead it: one prompt of 512 tokens takes 15 us, 27 with max_kv 8192 and 31 with 131072; and
+// rows of one token over 65536 next to that prompt stay whole, 735 us.  One item for each SM instead:
+// ten rows of 4 over 8192 stay whole, 100 for 77 us.
 int runs_for(const PagedAttn& a) {
   const int G = a.n_heads / a.kv.n_kv_heads, width = 2 * (kRows / G);  // tokens of a unit
   const long long units = (long long)a.rows * (((long long)a.max_q + width - 1) / width) * a.kv.n_kv_heads;
@@ -786,9 +789,8 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   float* po = reinterpret_cast<float*>(a.ws);
   const size_t parts = (size_t)a.tokens * a.n_heads * runs;
   float2* pml = reinterpret_cast<float2*>(a.ws + parts * HD * sizeof(float));
-  const cudaError_t launched =
-      launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, (int)units, po,
-                 pml);
+  const cudaError_t launched = launch_pdl(k_paged_prefill<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s,
+                                          tq, tk, tv, a, runs, (int)units, po, pml);
   if (launched != cudaSuccess || runs == 1) return launched;
   const long long pairs = (long long)a.tokens * a.n_heads;
   if (pairs <= kFewPairs && runs > kManyRuns)

@@ -3,10 +3,10 @@
 //
 // Every element is read once and written once as bf16: HBM is the floor.  8192 tokens of 32 q and 8
 // kv heads of 128 take 39.4 us = 5.1 TB/s, three quarters of the measured copy rate; 8 tokens of them
-// 3.4 us; 777 tokens of 12 and 4 heads of 64 5.1 us.  What keeps it from the rest is each token's chain (load, norm's reductions, store)
-// over the warps that fit: issue slots are 72 % taken, yet a form with a fifth fewer instructions
-// (gains held, two products an instruction) took 41 us, its registers having cost warps.  Two kinds
-// of block share a launch:
+// 3.4 us; 777 tokens of 12 and 4 heads of 64 5.1 us.  What keeps it from the rest is each token's
+// chain (load, norm's reductions, store) over the warps that fit: issue slots are 72 % taken, yet a
+// form with a fifth fewer instructions (gains held, two products an instruction) took 41 us, its
+// registers having cost warps.  Two kinds of block share a launch:
 // - q and k: a warp takes one token and a run of its heads.  A head is spread over head_dim / 8
 //   lanes, each with two groups of four dims chosen so that both members of its rotated pairs are
 //   its own (half layout: dims 4l.. of the first and of the second half), so the rotation needs no

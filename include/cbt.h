@@ -425,7 +425,8 @@ typedef struct {
  * With rows 0 nothing is written, cu_q, positions and slots among it.
  * Output arrays may not overlap anything else the call reads, but for the two named pairs.
  * rows <= CBT_PAGE_MAP_MAX_ROWS, max_tokens and n_pages <= 2^30, max_pages * page_tokens < 2^31
- * and n_pages * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_CUDA. */
+ * and n_pages * page_tokens < 2^31 (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID,
+ * CBT_ERR_CUDA. */
 #define CBT_PAGE_MAP_MAX_ROWS 4096
 typedef struct {
   int32_t* block_table;
@@ -529,9 +530,11 @@ cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
  * row sees it may reach the row's other query tokens: their weight of it is 0, and 0 * NaN is NaN.)
  *   block_table  int32 [rows][max_pages]
  *   max_q, max_kv  upper bounds of n_b and kv_lens[b] that the caller vouches for: they size the
- *                launch and the workspace.  A row above either, or with more positions than its
- *                table, reports CBT_DEV_LENGTH; its outputs are unspecified.  So are those of a
- *                row with a page id outside the pool among the pages it reads (CBT_DEV_PAGE_ID).
+ *                launch and the workspace, and with max_q > 1 they decide whether rows are cut into
+ *                runs (bounds far above the rows cost time, not results).  A row above either, or
+ *                with more positions than its table, reports CBT_DEV_LENGTH; its outputs are
+ *                unspecified.  So are those of a row with a page id outside the pool among the pages
+ *                it reads (CBT_DEV_PAGE_ID).
  *   tokens       rows of q and out; a row whose cu_q range leaves [0, tokens] or runs backwards is
  *                skipped (CBT_DEV_LENGTH).  Where the ranges of other rows overlap (which takes one
  *                that runs backwards), the call's outputs are unspecified.
@@ -541,9 +544,11 @@ cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream);
  *                that overlap on the GPU, graph replays among them, need workspaces of their own.
  * scale is finite; window and sinks are >= 0 (sinks without a window change nothing).  Scores,
  * softmax sums and outputs are accumulated in fp32, in an order that the sizes fix: the same call
- * gives the same bits again.  What the other rows hold never changes a row's result.  With max_q
- * == 1 neither does how many there are; with more, rows, max_q and max_kv decide whether long rows
- * are summed in several runs, so calls of different sizes may differ in the last bits.
+ * gives the same bits again.  The weights that multiply V have two bf16 parts (2^-16 relative) with
+ * max_q == 1, and are rounded to bf16 once (2^-8) with more, rows of one token among them.
+ * What the other rows hold never changes a row's result.  With max_q == 1 neither does how many there
+ * are; with more, rows, max_q and max_kv decide whether long rows are summed in several runs, so
+ * calls of different sizes may differ in the last bits.
  * n_heads / n_kv_heads <= 64, q and out 16-byte aligned, strides multiples of 8
  * elements, kv.head_dim 64 or 128 (CBT_ERR_UNSUPPORTED); rows <= CBT_PAGED_ATTENTION_MAX_ROWS,
  * max_kv + window and max_kv + sinks < 2^31, (rows + tokens) * n_heads < 2^29 and with max_q == 1
@@ -582,8 +587,9 @@ size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
  *           the gains are borrowed), or NULL: that norm is left out
  *   window, sinks  as in cbt_paged_attention, any size: where either reaches the positions that all
  *           of the arena's pages hold, every earlier position is seen
- * q is rounded to bf16 for the attention.  Pages behind the window stay held.  Of such an engine
- * cbt_engine_stamps records the projections alone.
+ * q is rounded to bf16 for the attention, and in a prefill (of more than a token a prompt) the
+ * softmax's weights too; the built-in form carries two parts of both.  Pages behind the window stay
+ * held.  Of such an engine cbt_engine_stamps records the projections alone.
  * The calls' page table and the attention's partial sums grow inside the call that needs more, which
  * waits for the stream; cbt_stats.scratch_bytes counts them.  The table takes 4 bytes for each page of
  * the longest row, max_batch times; the sums of a decode step of B rows 4 * B * n_heads * head_dim bytes
