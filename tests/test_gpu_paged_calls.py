@@ -112,7 +112,7 @@ def test_ranges_that_overlap(rows, max_kv):
 
 
 def busy():
-    torch.cuda._sleep(200_000_000)  # some 0.1 s
+    torch.cuda._sleep(1_000_000_000)  # some 0.5 s, for the host to be ahead of
 
 
 def taken_from(ptrs, sizes):
