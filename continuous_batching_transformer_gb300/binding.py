@@ -40,7 +40,9 @@ EXPORTS = ["cbt_status_str", "cbt_engine_create", "cbt_engine_destroy", "cbt_sla
            "cbt_kv_slab_share_prefix", "cbt_slab_bytes_kv8", "cbt_quantize_kv8",
            "cbt_slab_bytes_kvq", "cbt_quantize_kv", "cbt_engine_set_stamps", "cbt_engine_stamps",
            "cbt_engine_test_stall", "cbt_page_map", "cbt_rope_init", "cbt_rope_append",
-           "cbt_paged_attention", "cbt_paged_attention_workspace", "cbt_engine_set_attention"]
+           "cbt_paged_attention", "cbt_paged_attention_workspace", "cbt_engine_set_attention",
+           "cbt_rope_append_fp8", "cbt_paged_read_fp8", "cbt_paged_attention_fp8",
+           "cbt_paged_attention_fp8_workspace"]
 KCLASS_PROJ, KCLASS_ATTN, KCLASS_OTHER = 0, 1, 2
 
 
@@ -110,6 +112,17 @@ class RopeDesc(ctypes.Structure):
                 ("rot_dim", c_int32), ("head_dim", c_int32)]
 
 
+# a cache in 8 bits: positions that share a scale
+FP8_BLOCK = 64
+
+
+class PagedKvFp8Desc(ctypes.Structure):
+    _fields_ = [("pool", c_void), ("pool_bytes", ctypes.c_size_t), ("page_bytes", ctypes.c_int64),
+                ("k_offset", ctypes.c_int64), ("v_offset", ctypes.c_int64), ("s_offset", ctypes.c_int64),
+                ("n_pages", c_int32), ("page_tokens", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32)]
+
+
 class RopeAppendArgs(ctypes.Structure):
     _fields_ = [("kv", PagedKvDesc), ("rope", P(RopeDesc)), ("qkv", c_void), ("qkv_dtype", c_int32),
                 ("qkv_stride", ctypes.c_int64), ("tokens", c_int32), ("n_heads", c_int32),
@@ -126,6 +139,21 @@ class PagedAttentionArgs(ctypes.Structure):
                 ("sinks", c_int32), ("out", c_void), ("out_dtype", c_int32),
                 ("out_stride", ctypes.c_int64), ("workspace", c_void),
                 ("workspace_bytes", ctypes.c_size_t), ("err", c_void)]
+
+
+class RopeAppendFp8Args(ctypes.Structure):
+    _fields_ = [("kv", PagedKvFp8Desc)] + RopeAppendArgs._fields_[1:]
+
+
+class PagedAttentionFp8Args(ctypes.Structure):
+    _fields_ = [("kv", PagedKvFp8Desc)] + PagedAttentionArgs._fields_[1:]
+
+
+class PagedReadFp8Args(ctypes.Structure):
+    _fields_ = [("kv", PagedKvFp8Desc), ("block_table", c_void), ("max_pages", c_int32),
+                ("rows", c_int32), ("kv_lens", c_void), ("first", c_void), ("cu", c_void),
+                ("tokens", c_int32), ("k_out", c_void), ("v_out", c_void), ("out_dtype", c_int32),
+                ("out_stride", ctypes.c_int64), ("err", c_void)]
 
 
 class AttentionConfig(ctypes.Structure):
@@ -193,8 +221,13 @@ def lib():
         L.cbt_paged_attention.argtypes = [P(PagedAttentionArgs), c_void]
         L.cbt_paged_attention_workspace.argtypes = [P(PagedAttentionArgs)]
         L.cbt_paged_attention_workspace.restype = ctypes.c_size_t
+        L.cbt_rope_append_fp8.argtypes = [P(RopeAppendFp8Args), c_void]
+        L.cbt_paged_read_fp8.argtypes = [P(PagedReadFp8Args), c_void]
+        L.cbt_paged_attention_fp8.argtypes = [P(PagedAttentionFp8Args), c_void]
+        L.cbt_paged_attention_fp8_workspace.argtypes = [P(PagedAttentionFp8Args)]
+        L.cbt_paged_attention_fp8_workspace.restype = ctypes.c_size_t
         for name in EXPORTS:
-            if name not in ("cbt_paged_attention_workspace",
+            if name not in ("cbt_paged_attention_workspace", "cbt_paged_attention_fp8_workspace",
                             "cbt_status_str", "cbt_slab_bytes", "cbt_slab_bytes_kv8",
                             "cbt_slab_bytes_kvq", "cbt_kernel_launches"):
                 getattr(L, name).restype = c_int32
@@ -401,3 +434,19 @@ def paged_attention(args: PagedAttentionArgs, stream: int = 0) -> None:
 
 def paged_attention_workspace(args: PagedAttentionArgs) -> int:
     return lib().cbt_paged_attention_workspace(ctypes.byref(args))
+
+
+def rope_append_fp8(args: RopeAppendFp8Args, stream: int = 0) -> None:
+    _check(lib().cbt_rope_append_fp8(args, stream), "cbt_rope_append_fp8")
+
+
+def paged_read_fp8(args: PagedReadFp8Args, stream: int = 0) -> None:
+    _check(lib().cbt_paged_read_fp8(args, stream), "cbt_paged_read_fp8")
+
+
+def paged_attention_fp8(args: PagedAttentionFp8Args, stream: int = 0) -> None:
+    _check(lib().cbt_paged_attention_fp8(args, stream), "cbt_paged_attention_fp8")
+
+
+def paged_attention_fp8_workspace(args: PagedAttentionFp8Args) -> int:
+    return lib().cbt_paged_attention_fp8_workspace(ctypes.byref(args))

@@ -1,5 +1,5 @@
 // paged.h -- launchers of the operators on a paged KV cache (host side) and the index helpers
-// their kernels share.
+// their kernels share.  The same operators on a cache in 8 bits: paged_fp8.h.
 #pragma once
 #include "kernels.h"
 
@@ -21,8 +21,9 @@ CBT_HD long long paged_v(const PagedKv& c, int id, int head, int o, int d) {
 
 cudaError_t launch_page_map(const cbt_page_map_args& a, cudaStream_t s);
 
-struct RopeAppend {
-  PagedKv kv;
+template <class Kv>
+struct RopeAppendOn {
+  Kv kv;
   cbt_rope rope;  // rot_dim 0: no rotation
   const void* qkv;
   bool f32;
@@ -35,10 +36,12 @@ struct RopeAppend {
   long long q_ld;
   int* err;
 };
+using RopeAppend = RopeAppendOn<PagedKv>;
 cudaError_t launch_paged_rope(const RopeAppend& a, cudaStream_t s);
 
-struct PagedAttn {
-  PagedKv kv;
+template <class Kv>
+struct PagedAttnOn {
+  Kv kv;
   const int32_t* table;
   int max_pages, rows;
   const int32_t* lens;
@@ -55,6 +58,7 @@ struct PagedAttn {
   size_t ws_bytes;
   int* err;
 };
+using PagedAttn = PagedAttnOn<PagedKv>;
 size_t paged_attn_workspace(const PagedAttn& a);
 cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s);
 // its two forms: one query token per row (max_q == 1), split over the cache's length, and ragged

@@ -2,7 +2,7 @@
 // launch.  Nothing here touches the device before every check has passed.
 #include <math.h>
 
-#include "paged.h"
+#include "paged_fp8.h"
 
 namespace {
 
@@ -41,13 +41,37 @@ cbt_status paged_kv(const cbt_paged_kv& k, PagedKv* out) {
   return CBT_OK;
 }
 
+cbt_status paged_kv(const cbt_paged_kv_fp8& k, PagedKvFp8* out) {
+  if (!k.pool) return CBT_ERR_NULL;
+  if (k.head_dim != 64 && k.head_dim != 128) return CBT_ERR_UNSUPPORTED;
+  if (k.n_pages <= 0 || k.page_tokens <= 0 || k.page_tokens % kBlock || k.n_kv_heads <= 0 || k.page_bytes <= 0 ||
+      k.page_bytes % 256 || k.k_offset < 0 || k.k_offset % 256 || k.v_offset < 0 || k.v_offset % 256 ||
+      k.s_offset < 0 || k.s_offset % 256 || !aligned(k.pool, 256))
+    return CBT_ERR_INVALID;
+  // 256: what the tensor maps count in
+  if ((int64_t)k.n_pages * k.page_tokens > INT32_MAX || k.pool_bytes >= (size_t)256 << 31)
+    return CBT_ERR_LIMIT;
+  if ((uint64_t)k.page_bytes > k.pool_bytes || (uint64_t)k.k_offset > k.pool_bytes ||
+      (uint64_t)k.v_offset > k.pool_bytes || (uint64_t)k.s_offset > k.pool_bytes)
+    return CBT_ERR_INVALID;
+  const double block = (double)k.n_kv_heads * k.page_tokens * k.head_dim;
+  const double scales = 8.0 * k.n_kv_heads * (k.page_tokens / kBlock);
+  const double off = (double)(k.k_offset > k.v_offset ? k.k_offset : k.v_offset) + block;
+  const double end = (double)k.s_offset + scales > off ? (double)k.s_offset + scales : off;
+  if ((double)(k.n_pages - 1) * (double)k.page_bytes + end > (double)k.pool_bytes) return CBT_ERR_INVALID;
+  *out = PagedKvFp8{static_cast<uint8_t*>(k.pool), (long long)k.pool_bytes, k.page_bytes, k.k_offset, k.v_offset,
+                    k.s_offset, k.n_pages, k.page_tokens, k.n_kv_heads, k.head_dim};
+  return CBT_OK;
+}
+
 bool rope_ok(const cbt_rope& r, int head_dim) {
   return (r.layout == CBT_ROPE_HALF || r.layout == CBT_ROPE_INTERLEAVED) && r.head_dim == head_dim &&
          r.rot_dim >= 2 && r.rot_dim <= head_dim && r.rot_dim % 2 == 0;
 }
 
 // the sizes of an attention call, without its pointers
-cbt_status attn_sizes(const cbt_paged_attention_args& a) {
+template <class Args>
+cbt_status attn_sizes(const Args& a) {
   if (a.kv.head_dim != 64 && a.kv.head_dim != 128) return CBT_ERR_UNSUPPORTED;
   if (a.rows < 0 || a.tokens < 0 || a.max_pages <= 0 || a.max_q <= 0 || a.max_kv < 0 ||
       a.n_heads <= 0 || a.kv.n_kv_heads <= 0 || a.n_heads % a.kv.n_kv_heads || a.window < 0 ||
@@ -66,8 +90,9 @@ cbt_status attn_sizes(const cbt_paged_attention_args& a) {
   return CBT_OK;
 }
 
-PagedAttn attn_args(const cbt_paged_attention_args& a, const PagedKv& kv) {
-  PagedAttn p{};
+template <class Args, class Kv>
+PagedAttnOn<Kv> attn_args(const Args& a, const Kv& kv) {
+  PagedAttnOn<Kv> p{};
   p.kv = kv;
   p.table = a.block_table;
   p.max_pages = a.max_pages;
@@ -97,6 +122,81 @@ cudaError_t sm_count(int* n) {
   int dev = 0;
   const cudaError_t rc = cudaGetDevice(&dev);
   return rc == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : rc;
+}
+
+// an append's checks, then its launch
+template <class Kv, class Args>
+cbt_status rope_append(const Args* a, cudaError_t (*launch)(const RopeAppendOn<Kv>&, cudaStream_t), void* stream) {
+  if (!a) return CBT_ERR_NULL;
+  RopeAppendOn<Kv> p{};
+  const cbt_status st = paged_kv(a->kv, &p.kv);
+  if (st != CBT_OK) return st;
+  const int hd = a->kv.head_dim;
+  const int64_t width = ((int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads) * hd;
+  if (a->tokens < 0 || a->n_heads <= 0 || !(a->eps >= 0.f) || !(a->eps <= 3.4e38f) ||
+      (a->qkv_dtype != CBT_DTYPE_BF16 && a->qkv_dtype != CBT_DTYPE_F32) || a->qkv_stride < width ||
+      a->qkv_stride % 8 || a->q_stride < (int64_t)a->n_heads * hd || a->q_stride % 8 ||
+      (a->rope && !rope_ok(*a->rope, hd)))
+    return CBT_ERR_INVALID;
+  // 65535: the launch's limit on its second grid dimension, far above any head count in use
+  if (a->tokens > kMostTokens || width > INT32_MAX / 4 || (int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads > 65535)
+    return CBT_ERR_LIMIT;
+  if (a->tokens == 0) return CBT_OK;
+  if (!a->qkv || !a->q_out || !a->positions || !a->slots || !a->err) return CBT_ERR_NULL;
+  if (!aligned(a->qkv, 16) || !aligned(a->q_out, 16) || !aligned(a->q_gain, 16) ||
+      !aligned(a->k_gain, 16))
+    return CBT_ERR_INVALID;
+  if (a->rope) p.rope = *a->rope;
+  p.qkv = a->qkv;
+  p.f32 = a->qkv_dtype == CBT_DTYPE_F32;
+  p.qkv_ld = a->qkv_stride;
+  p.tokens = a->tokens;
+  p.n_heads = a->n_heads;
+  p.q_gain = static_cast<const uint16_t*>(a->q_gain);
+  p.k_gain = static_cast<const uint16_t*>(a->k_gain);
+  p.eps = a->eps;
+  p.positions = a->positions;
+  p.slots = a->slots;
+  p.q_out = static_cast<uint16_t*>(a->q_out);
+  p.q_ld = a->q_stride;
+  p.err = a->err;
+  return launch(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
+}
+
+template <class Kv, class Args>
+size_t attn_workspace(const Args* a, size_t (*need)(const PagedAttnOn<Kv>&)) {
+  if (!a || attn_sizes(*a) != CBT_OK) return 0;
+  Kv kv{};
+  kv.n_pages = a->kv.n_pages;
+  kv.page_tokens = a->kv.page_tokens;
+  kv.n_kv_heads = a->kv.n_kv_heads;
+  kv.head_dim = a->kv.head_dim;
+  return need(attn_args(*a, kv));
+}
+
+// an attention's checks, then its launch
+template <class Kv, class Args>
+cbt_status attention(const Args* a, size_t (*workspace)(const PagedAttnOn<Kv>&),
+                     cudaError_t (*launch)(const PagedAttnOn<Kv>&, int, cudaStream_t), void* stream) {
+  if (!a) return CBT_ERR_NULL;
+  Kv kv{};
+  cbt_status st = paged_kv(a->kv, &kv);
+  if (st == CBT_OK) st = attn_sizes(*a);
+  if (st != CBT_OK) return st;
+  const int64_t width = (int64_t)a->n_heads * a->kv.head_dim;
+  if (a->q_stride < width || a->q_stride % 8 || a->out_stride < width || a->out_stride % 8 ||
+      (!a->cu_q && (a->tokens != a->rows || a->max_q != 1)))
+    return CBT_ERR_INVALID;
+  if (a->rows == 0 || a->tokens == 0) return CBT_OK;
+  if (!a->q || !a->out || !a->block_table || !a->kv_lens || !a->err) return CBT_ERR_NULL;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16)) return CBT_ERR_INVALID;
+  const PagedAttnOn<Kv> p = attn_args(*a, kv);
+  const size_t need = workspace(p);
+  if (need && !a->workspace) return CBT_ERR_NULL;
+  if (need > a->workspace_bytes || !aligned(a->workspace, 256)) return CBT_ERR_INVALID;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != cudaSuccess) return CBT_ERR_CUDA;
+  return launch(p, num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
 }
 
 }  // namespace
@@ -173,71 +273,52 @@ extern "C" cbt_status cbt_rope_init(const cbt_rope_config* c, int32_t head_dim, 
 }
 
 extern "C" cbt_status cbt_rope_append(const cbt_rope_append_args* a, void* stream) {
-  if (!a) return CBT_ERR_NULL;
-  RopeAppend p{};
-  const cbt_status st = paged_kv(a->kv, &p.kv);
-  if (st != CBT_OK) return st;
-  const int hd = a->kv.head_dim;
-  const int64_t width = ((int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads) * hd;
-  if (a->tokens < 0 || a->n_heads <= 0 || !(a->eps >= 0.f) || !(a->eps <= 3.4e38f) ||
-      (a->qkv_dtype != CBT_DTYPE_BF16 && a->qkv_dtype != CBT_DTYPE_F32) || a->qkv_stride < width ||
-      a->qkv_stride % 8 || a->q_stride < (int64_t)a->n_heads * hd || a->q_stride % 8 ||
-      (a->rope && !rope_ok(*a->rope, hd)))
-    return CBT_ERR_INVALID;
-  // 65535: the launch's limit on its second grid dimension, far above any head count in use
-  if (a->tokens > kMostTokens || width > INT32_MAX / 4 || (int64_t)a->n_heads + 2 * (int64_t)a->kv.n_kv_heads > 65535)
-    return CBT_ERR_LIMIT;
-  if (a->tokens == 0) return CBT_OK;
-  if (!a->qkv || !a->q_out || !a->positions || !a->slots || !a->err) return CBT_ERR_NULL;
-  if (!aligned(a->qkv, 16) || !aligned(a->q_out, 16) || !aligned(a->q_gain, 16) ||
-      !aligned(a->k_gain, 16))
-    return CBT_ERR_INVALID;
-  if (a->rope) p.rope = *a->rope;
-  p.qkv = a->qkv;
-  p.f32 = a->qkv_dtype == CBT_DTYPE_F32;
-  p.qkv_ld = a->qkv_stride;
-  p.tokens = a->tokens;
-  p.n_heads = a->n_heads;
-  p.q_gain = static_cast<const uint16_t*>(a->q_gain);
-  p.k_gain = static_cast<const uint16_t*>(a->k_gain);
-  p.eps = a->eps;
-  p.positions = a->positions;
-  p.slots = a->slots;
-  p.q_out = static_cast<uint16_t*>(a->q_out);
-  p.q_ld = a->q_stride;
-  p.err = a->err;
-  return launch_paged_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
+  return rope_append(a, launch_paged_rope, stream);
+}
+extern "C" cbt_status cbt_rope_append_fp8(const cbt_rope_append_fp8_args* a, void* stream) {
+  return rope_append(a, launch_append_fp8, stream);
 }
 
 extern "C" size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a) {
-  if (!a || attn_sizes(*a) != CBT_OK) return 0;
-  PagedKv kv{};
-  kv.n_pages = a->kv.n_pages;
-  kv.page_tokens = a->kv.page_tokens;
-  kv.n_kv_heads = a->kv.n_kv_heads;
-  kv.head_dim = a->kv.head_dim;
-  return paged_attn_workspace(attn_args(*a, kv));
+  return attn_workspace(a, paged_attn_workspace);
+}
+extern "C" size_t cbt_paged_attention_fp8_workspace(const cbt_paged_attention_fp8_args* a) {
+  return attn_workspace(a, attn_fp8_workspace);
 }
 
 extern "C" cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream) {
+  return attention(a, paged_attn_workspace, launch_paged_attn, stream);
+}
+extern "C" cbt_status cbt_paged_attention_fp8(const cbt_paged_attention_fp8_args* a, void* stream) {
+  return attention(a, attn_fp8_workspace, launch_attn_fp8, stream);
+}
+
+extern "C" cbt_status cbt_paged_read_fp8(const cbt_paged_read_fp8_args* a, void* stream) {
   if (!a) return CBT_ERR_NULL;
-  PagedKv kv{};
-  cbt_status st = paged_kv(a->kv, &kv);
-  if (st == CBT_OK) st = attn_sizes(*a);
+  PagedReadFp8 p{};
+  const cbt_status st = paged_kv(a->kv, &p.kv);
   if (st != CBT_OK) return st;
-  const int64_t width = (int64_t)a->n_heads * a->kv.head_dim;
-  if (a->q_stride < width || a->q_stride % 8 || a->out_stride < width || a->out_stride % 8 ||
-      (!a->cu_q && (a->tokens != a->rows || a->max_q != 1)))
+  const int64_t width = (int64_t)a->kv.n_kv_heads * a->kv.head_dim;
+  if (a->rows < 0 || a->tokens < 0 || a->max_pages <= 0 || a->out_stride < width || a->out_stride % 8 ||
+      (a->out_dtype != CBT_DTYPE_BF16 && a->out_dtype != CBT_DTYPE_F32))
     return CBT_ERR_INVALID;
-  if (a->rows == 0 || a->tokens == 0) return CBT_OK;
-  if (!a->q || !a->out || !a->block_table || !a->kv_lens || !a->err) return CBT_ERR_NULL;
-  if (!aligned(a->q, 16) || !aligned(a->out, 16)) return CBT_ERR_INVALID;
-  const PagedAttn p = attn_args(*a, kv);
-  const size_t need = paged_attn_workspace(p);
-  if (need && !a->workspace) return CBT_ERR_NULL;
-  if (need > a->workspace_bytes || !aligned(a->workspace, 256)) return CBT_ERR_INVALID;
-  int num_sms = 0;
-  if (sm_count(&num_sms) != cudaSuccess) return CBT_ERR_CUDA;
-  return launch_paged_attn(p, num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK
-                                                                                         : CBT_ERR_CUDA;
+  // 32767: the launch's limit on its second grid dimension, K's heads and V's
+  if (a->rows > CBT_PAGED_ATTENTION_MAX_ROWS || a->tokens > kMostTokens || a->kv.n_kv_heads > 32767)
+    return CBT_ERR_LIMIT;
+  if (a->rows == 0 || a->tokens == 0 || (!a->k_out && !a->v_out)) return CBT_OK;
+  if (!a->block_table || !a->kv_lens || !a->cu || !a->err) return CBT_ERR_NULL;
+  if (!aligned(a->k_out, 16) || !aligned(a->v_out, 16)) return CBT_ERR_INVALID;
+  p.table = a->block_table;
+  p.max_pages = a->max_pages;
+  p.rows = a->rows;
+  p.lens = a->kv_lens;
+  p.first = a->first;
+  p.cu = a->cu;
+  p.tokens = a->tokens;
+  p.k_out = a->k_out;
+  p.v_out = a->v_out;
+  p.f32 = a->out_dtype == CBT_DTYPE_F32;
+  p.out_ld = a->out_stride;
+  p.err = a->err;
+  return launch_read_fp8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CBT_OK : CBT_ERR_CUDA;
 }

@@ -1,0 +1,424 @@
+// paged_append_fp8.cu -- per-head RMS norm, rotary positions and the append of K and V to a paged cache
+// in 8 bits, one launch over QKV rows.
+//
+// Every element is read once and written once, q as bf16 and k and v as codes.  q is rotated as for a
+// bf16 cache (a warp per token and run of heads).  A scale belongs to the 64 positions of a block, so k
+// and v go by blocks: a thread block takes the runs (tokens next to each other in the call that lie in
+// one cache block) that begin among its kChunk tokens, to their ends, for one kv head and K or V alone,
+//   1. forms the tokens' values, held in registers, and each run's largest magnitude;
+//   2. settles each run's exponent from that and the scale that the cache block has;
+//   3. where it grows, moves the codes held there down (rare: once a block has a few tokens, most of
+//      those that follow are below its largest);
+//   4. rounds the values to codes; V, whose layout runs along the positions of a dim, is turned around
+//      in shared memory and written 16 positions at a time where a run fills them.
+// No thread block shares a cache block with another, so nothing is exchanged through memory.
+#include "paged_fp8.h"
+#include "paged_rope.cuh"
+
+namespace {
+
+constexpr float kTop = 448.f;
+
+// sin and cos of ph / 2^64 turns to fp32's last place or so: the nearest quarter turn is taken off in
+// whole numbers, and the rest, at most pi / 4, goes through the Taylor series (first terms left out:
+// x^11 / 11! and x^12 / 12!, below 2^-28).  A rounding to three bits of mantissa shows no more than
+// this costs: with the hardware's sine, off by 2^-21, a few more codes in a million fall on the other
+// side of a border than the formula's.
+CBT_D void turn_sincos(uint64_t ph, float* sn, float* cs) {
+  const uint64_t at = ph + (1ull << 61);
+  const int quarter = (int)(at >> 62);
+  const int rest = (int)((long long)((at & ((1ull << 62) - 1)) - (1ull << 61)) >> 30);  // of 2^34 a turn
+  const float x = (float)rest * 0x1.921fb6p-32f;  // 2 pi / 2^34
+  const float z = x * x;
+  float s = fmaf(z, 1.f / 362880, -1.f / 5040);
+  s = fmaf(z, s, 1.f / 120);
+  s = fmaf(z, s, -1.f / 6);
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, -1.f / 3628800, 1.f / 40320);
+  c = fmaf(z, c, -1.f / 720);
+  c = fmaf(z, c, 1.f / 24);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
+  *sn = quarter & 2 ? -a : a;
+  *cs = (quarter + 1) & 2 ? -b : b;
+}
+
+// the exponent of the smallest scale that values up to `top` (finite, >= 0) are within 448 times of
+CBT_D int exponent_for(float top) {
+  const uint32_t u = __float_as_uint(top);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u);  // 448 = 1.75 * 2^8
+  return min(max(e, kLowExp), kHighExp);
+}
+
+// sixteen codes times f, each rounded again
+CBT_D uint32_t move_codes(uint32_t w, float f) {
+  const uint32_t lo = e4m3_to_f16((uint16_t)w), hi = e4m3_to_f16((uint16_t)(w >> 16));
+  return pack_e4m3(f16_lo(lo) * f, f16_hi(lo) * f) | (uint32_t)pack_e4m3(f16_lo(hi) * f, f16_hi(hi) * f) << 16;
+}
+
+constexpr int kMostChunk = 64;             // tokens whose runs a thread block takes
+constexpr int kTokens = 2 * kMostChunk;    // with the last run's further ones (of 64 positions at most)
+struct Runs {
+  int slot[kTokens];               // of each token, -1: not this block's
+  short run[kMostChunk];           // of each of the chunk's tokens, -1: none that begins here
+  int first_slot[kMostChunk];      // of each run
+  int top[kMostChunk];             // its largest magnitude, as bits
+  int anew[kMostChunk];            // it holds its cache block's first position
+  int exponent[kMostChunk];
+  int grown[kMostChunk], down[kMostChunk];  // runs whose cache block moves, and by how much
+  int count, n_grown, last_block;
+  int warp_runs[2];
+  int part[kTokens], warp_parts[kTokens / 32];  // tokens next to each other in 16 aligned slots
+};
+
+template <int HD>
+constexpr size_t kv_smem() {
+  return sizeof(Runs) + (size_t)kTokens * (HD + 4);  // V's codes by token, rows padded by a word
+}
+
+// runs of kv head g that begin in tokens [t0, t0 + chunk), of K or of V
+template <int HD, bool F32, int MODE, bool V>
+CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t* sm, float* xs) {
+  constexpr int LPH = HD / 8, NH = 32 / LPH;  // lanes of a token, tokens of a warp
+  constexpr int kPlaces = kWarps * NH;        // tokens in flight
+  constexpr int kHeld = kTokens / kPlaces;    // of a lane's
+  constexpr int kRow = HD + 4;
+  Runs& r = *reinterpret_cast<Runs*>(sm);
+  uint8_t* tile = sm + sizeof(Runs);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % LPH, sub = lane / LPH;
+  const int page = a.kv.page_tokens;
+  auto slot_of = [&](int t) {
+    if (t < 0 || t >= a.tokens) return -1;
+    const int s = a.slots[t];
+    return slot_ok(a, s, a.positions[t]) ? s : -1;
+  };
+  // ---- the runs: a token begins one where the token before it lies in another cache block
+  if (tid < kMostChunk) {
+    const int s = tid < chunk ? slot_of(t0 + tid) : -1;
+    const int before = tid < chunk ? slot_of(t0 + tid - 1) : -1;
+    const bool first = s >= 0 && (before < 0 || before / kBlock != s / kBlock);
+    const unsigned m = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) r.warp_runs[warp] = __popc(m);
+    r.slot[tid] = s;
+    r.run[tid] = s < 0 ? -1 : (short)(__popc(m & (0xffffffffu >> (31 - lane))) - 1);  // in its warp
+    r.top[tid] = 0;
+    r.anew[tid] = 0;
+  }
+  if (tid == 0) r.n_grown = 0;
+  __syncthreads();
+  if (tid < chunk) {
+    const int run = r.run[tid] + (warp == 1 && r.slot[tid] >= 0 ? r.warp_runs[0] : 0);
+    r.run[tid] = (short)run;
+    if (run >= 0) {
+      const int before = tid == 0 ? -2 : r.slot[tid - 1];
+      if (tid == 0 || before < 0 || before / kBlock != r.slot[tid] / kBlock) r.first_slot[run] = r.slot[tid];
+    }
+    if (tid == chunk - 1) r.last_block = run >= 0 ? r.slot[tid] / kBlock : -1;
+    if (tid == 0) r.count = r.warp_runs[0] + r.warp_runs[1];
+  }
+  __syncthreads();
+  const int count = r.count, last_block = r.last_block;
+  if (count == 0) return;
+  // the last run's tokens behind the chunk (more than 64 only where slots come twice)
+  int tail = 0;
+  if (last_block >= 0) {
+    int seen = 0;
+#pragma unroll 1
+    for (;;) {
+      const int t = t0 + chunk + tail + tid, s = slot_of(t);
+      const bool in = s >= 0 && s / kBlock == last_block;
+      const int at = chunk + tail + tid;
+      if (in && at < kTokens) r.slot[at] = s;
+      const unsigned out = __ballot_sync(0xffffffffu, !in);
+      if (lane == 0) xs[warp] = __int_as_float(out ? __ffs(out) - 1 : 32);
+      __syncthreads();
+      seen = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int n = __float_as_int(xs[w]);
+        if (seen == 32 * w) seen += n;
+      }
+      __syncthreads();
+      tail += seen;
+      if (seen < kThreads) break;
+    }
+  }
+  const int total = chunk + tail;
+  // what each run's cache block has so far
+  float held = 0.f;
+  if (tid < count) {
+    const int s = r.first_slot[tid], id = s / page;
+    held = *fp8_scale(a.kv, id, V, g, s - id * page);
+  }
+
+  // ---- values: lane l of a token holds eight dims
+  const int rot = V ? 0 : a.rope.rot_dim;
+  const LaneDims dims = lane_dims<V ? kNone : MODE>(l, rot);
+  const long long src = (long long)(a.n_heads + (V ? a.kv.n_kv_heads : 0) + g) * HD;
+  auto run_at = [&](int i) { return i >= total ? -1 : i < chunk ? (int)r.run[i] : count - 1; };
+  auto values = [&](int i, bool on, float (&x)[8]) {  // by all lanes: `on` may differ between tokens
+    const int t = t0 + (on ? i : 0);
+    load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e0, x);
+    load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e1, x + 4);
+    if (V) return;
+    if (a.k_gain) scale_head<HD>(x, head_squares<HD>(x), a.eps, a.k_gain, dims);
+    if (MODE == kNone) return;
+    constexpr int kAngles = MODE == kHalfOdd ? 8 : 4;
+    const int pos = on ? a.positions[t] : 0;
+    float cs[kAngles], sn[kAngles];
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) {
+      int pair = 4 * l + k;
+      bool turn = k < dims.turned;
+      if (MODE == kHalfOdd) {
+        const int d = 8 * l + k;
+        turn = d < rot;
+        pair = d < rot / 2 ? d : d - rot / 2;
+      }
+      cs[k] = 1.f;
+      sn[k] = 0.f;
+      if (turn) {
+        turn_sincos((uint64_t)pos * a.rope.turns[pair], &sn[k], &cs[k]);
+        sn[k] *= a.rope.mscale;
+        cs[k] *= a.rope.mscale;
+      }
+    }
+    turn_head<HD, V ? kNone : MODE>(x, cs, sn, l, dims.turned, rot, xs + (warp * NH + sub) * HD);
+  };
+  auto note_top = [&](const float (&x)[8], int run, int slot) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float y = fabsf(x[k]);
+      if (y <= 3.4028235e38f) top = fmaxf(top, y);
+    }
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (l == 0 && run >= 0) {
+      atomicMax(&r.top[run], __float_as_int(top));
+      if (slot % kBlock == 0) r.anew[run] = 1;
+    }
+  };
+  float x[kHeld][8];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int base = k * kPlaces + warp * NH, i = base + sub;
+    if (base >= total) break;
+    const int run = run_at(i);
+    values(i, run >= 0, x[k]);
+    note_top(x[k], run, run >= 0 ? r.slot[i] : 1);
+  }
+#pragma unroll 1
+  for (int base = kHeld * kPlaces + warp * NH; base < total; base += kPlaces) {  // slots came twice
+    float y[8];
+    const int i = base + sub, run = run_at(i);
+    values(i, run >= 0, y);
+    note_top(y, run, run >= 0 ? a.slots[t0 + i] : 1);
+  }
+  __syncthreads();
+
+  // ---- exponents
+  if (tid < count) {
+    const int e_call = exponent_for(__int_as_float(r.top[tid])), e_held = fp8_exponent(held);
+    const bool anew = r.anew[tid] != 0;
+    const int e = anew ? e_call : max(e_call, e_held);
+    r.exponent[tid] = e;
+    const float scale = pow2_of(e);
+    if (scale != held) {
+      const int s = r.first_slot[tid], id = s / page;
+      *fp8_scale(a.kv, id, V, g, s - id * page) = scale;
+    }
+    if (!anew && e > e_held) {
+      const int k = atomicAdd(&r.n_grown, 1);
+      r.grown[k] = tid;
+      r.down[k] = e_held - e;
+    }
+  }
+  __syncthreads();
+  const int n_grown = r.n_grown;
+  if (n_grown) {
+    constexpr int kVecs = kBlock * HD / 16;
+#pragma unroll 1
+    for (int k = tid; k < n_grown * kVecs; k += kThreads) {
+      const int which = k / kVecs, run = r.grown[which], s = r.first_slot[run], id = s / page;
+      const int o = (s - id * page) / kBlock * kBlock;
+      uint4* p = reinterpret_cast<uint4*>(a.kv.pool + (V ? fp8_v(a.kv, id, g, o, 0) : fp8_k(a.kv, id, g, o, 0))) +
+                 k % kVecs;
+      const float f = pow2_of(r.down[which]);
+      uint4 c = *p;
+      c.x = move_codes(c.x, f);
+      c.y = move_codes(c.y, f);
+      c.z = move_codes(c.z, f);
+      c.w = move_codes(c.w, f);
+      *p = c;
+    }
+    __syncthreads();
+  }
+
+  // ---- codes
+  auto codes = [&](const float (&y)[8], int run, uint32_t* w) {
+    const float f = pow2_of(-r.exponent[run]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      w[k] = pack_e4m3(y[4 * k] * f, y[4 * k + 1] * f) | (uint32_t)pack_e4m3(y[4 * k + 2] * f, y[4 * k + 3] * f) << 16;
+  };
+  auto put = [&](const uint32_t* w, int s) {  // straight to the token's slot
+    const int id = s / page, o = s - id * page;
+    if (!V) {
+      uint8_t* dst = a.kv.pool + fp8_k(a.kv, id, g, o, 0);
+      *reinterpret_cast<uint32_t*>(dst + dims.e0) = w[0];
+      *reinterpret_cast<uint32_t*>(dst + dims.e1) = w[1];
+    } else {
+      uint8_t* dst = a.kv.pool + fp8_v(a.kv, id, g, o, 8 * l);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dst[k * kBlock] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    }
+  };
+  // V is turned around where runs are long enough to fill stores
+  const bool turned = V && total >= 16 && total >= 4 * count;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int base = k * kPlaces + warp * NH, i = base + sub;
+    if (base >= total) break;
+    const int run = run_at(i);
+    if (run < 0) {
+      if (turned && l == 0 && i < kTokens) r.slot[i] = -1;
+      continue;
+    }
+    uint32_t w[2];
+    codes(x[k], run, w);
+    if (turned) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(tile + i * kRow + 8 * l);
+      dst[0] = w[0];
+      dst[1] = w[1];
+    } else {
+      put(w, r.slot[i]);
+    }
+  }
+#pragma unroll 1
+  for (int base = kHeld * kPlaces + warp * NH; base < total; base += kPlaces) {
+    float y[8];
+    const int i = base + sub, run = run_at(i);
+    values(i, run >= 0, y);
+    if (run < 0) continue;
+    uint32_t w[2];
+    codes(y, run, w);
+    put(w, a.slots[t0 + i]);
+  }
+  if (!turned) return;
+  __syncthreads();
+  // ---- V: the parts of the runs that lie in 16 aligned slots, four dims a thread; 16 positions in one
+  // store where such a part fills them
+  const int n = min(total, kTokens);
+  bool first = false;
+  int len = 0;
+  unsigned m = 0;
+  if (tid < kTokens) {
+    const int s = tid < n ? r.slot[tid] : -1;
+    first = s >= 0 && (tid == 0 || s % 16 == 0 || r.slot[tid - 1] != s - 1);
+    if (first) {
+      len = 1;
+      while (tid + len < n && (s + len) % 16 && r.slot[tid + len] == s + len) ++len;
+    }
+    m = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) r.warp_parts[warp] = __popc(m);
+  }
+  __syncthreads();
+  if (first) {
+    int at = __popc(m & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += r.warp_parts[w];
+    r.part[at] = tid | (len << 16);
+  }
+  const int parts = r.warp_parts[0] + r.warp_parts[1] + r.warp_parts[2] + r.warp_parts[3];
+  __syncthreads();
+  constexpr int kEights = HD / 32;  // groups of 8 lanes' 4 dims; with 4 parts a warp's stores fill 64-byte rows
+#pragma unroll 1
+  for (int k = warp; k < (parts + 3) / 4 * kEights; k += kWarps) {
+    const int p = k / kEights * 4 + (lane & 3), d = ((k % kEights) * 8 + (lane >> 2)) * 4;
+    if (p >= parts) continue;
+    const int i = r.part[p] & 0xFFFF, size = r.part[p] >> 16;
+    const int s = r.slot[i], id = s / page, o = s - id * page;
+    uint8_t* dst = a.kv.pool + fp8_v(a.kv, id, g, o, d);
+    auto row = [&](int j) { return *reinterpret_cast<const uint32_t*>(tile + (i + j) * kRow + d); };
+    if (size == 16) {
+      uint32_t w[4][4];  // [dim][positions 4j..]
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = row(4 * j + e);
+        transpose4(q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e][j] = q[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(dst + e * kBlock) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < size; ++j) {
+        const uint32_t w = row(j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e * kBlock + j] = (uint8_t)(w >> (8 * e));
+      }
+    }
+  }
+}
+
+// Blocks [0, kv_blocks): runs that begin in `chunk` tokens, of a kv head's K or V; then warps over (token,
+// run of `per` q heads), `cuts` of them a token.
+template <int HD, bool F32, int MODE>
+__global__ void __launch_bounds__(kThreads)
+    k_append_fp8(const __grid_constant__ RopeAppendFp8 a, int kv_blocks, int chunk, int cuts, int per) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  __shared__ float xs[kWarps * 256];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x < kv_blocks) {
+    const int heads = a.kv.n_kv_heads, h = blockIdx.x % (2 * heads), t0 = blockIdx.x / (2 * heads) * chunk;
+    if (h < heads) append_runs<HD, F32, MODE, false>(a, t0, chunk, h, sm, xs);
+    else append_runs<HD, F32, MODE, true>(a, t0, chunk, h - heads, sm, xs);
+  } else {
+    const long long w = (long long)(blockIdx.x - kv_blocks) * kWarps + warp;
+    const int t = (int)(w / cuts), h0 = (int)(w - (long long)t * cuts) * per;
+    if (t < a.tokens && h0 < a.n_heads)
+      rotate_heads<HD, F32, MODE>(a, t, h0, min(a.n_heads, h0 + per), xs + warp * 256);
+  }
+  pdl_launch();
+}
+
+template <int HD, bool F32, int MODE>
+cudaError_t launch(const RopeAppendFp8& a, cudaStream_t s) {
+  constexpr int kStep = 32 / (HD / 8) * kUnroll;  // heads a warp has in flight
+  constexpr size_t smem = kv_smem<HD>();
+  static_assert(smem + kWarps * 256 * sizeof(float) <= 48 * 1024, "shared memory");
+  const int steps = (a.n_heads + kStep - 1) / kStep;
+  int cuts = (kTargetWarps + a.tokens - 1) / a.tokens;
+  cuts = cuts < steps ? cuts : steps;
+  const int per = (steps + cuts - 1) / cuts * kStep;
+  cuts = (a.n_heads + per - 1) / per;
+  const long long q = ((long long)a.tokens * cuts + kWarps - 1) / kWarps;
+  // few tokens are spread over more blocks
+  const int heads2 = 2 * a.kv.n_kv_heads;
+  auto blocks = [&](int chunk) { return (long long)((a.tokens + chunk - 1) / chunk) * heads2; };
+  const int chunk = blocks(kMostChunk) >= 2 * 152 ? kMostChunk : 16;
+  const long long kv = blocks(chunk);
+  if (q + kv > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch_pdl(k_append_fp8<HD, F32, MODE>, dim3((unsigned)(q + kv)), dim3(kThreads), smem, s, a,
+                    (int)kv, chunk, cuts, per);
+}
+
+template <int HD, bool F32>
+cudaError_t launch_mode(const RopeAppendFp8& a, cudaStream_t s) {
+  if (a.rope.rot_dim == 0) return launch<HD, F32, kNone>(a, s);
+  if (a.rope.layout == CBT_ROPE_INTERLEAVED) return launch<HD, F32, kInter>(a, s);
+  return a.rope.rot_dim % 8 ? launch<HD, F32, kHalfOdd>(a, s) : launch<HD, F32, kHalf>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append_fp8(const RopeAppendFp8& a, cudaStream_t s) {
+  if (a.kv.head_dim == 128) return a.f32 ? launch_mode<128, true>(a, s) : launch_mode<128, false>(a, s);
+  return a.f32 ? launch_mode<64, true>(a, s) : launch_mode<64, false>(a, s);
+}

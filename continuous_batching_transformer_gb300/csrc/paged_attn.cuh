@@ -96,7 +96,8 @@ struct RowTokens {
   int t0, n, len;
   bool bad;
 };
-CBT_D RowTokens row_tokens(const PagedAttn& a, int b) {
+template <class Kv>
+CBT_D RowTokens row_tokens(const PagedAttnOn<Kv>& a, int b) {
   RowTokens r{b, 1, a.lens[b], false};
   if (a.cu) {
     r.t0 = a.cu[b];

@@ -2,8 +2,10 @@
 
 For a model of one's own that keeps its KV cache in the engine's page layout: ``PagedKV`` describes
 a pool of pages, ``PageMap`` turns request lengths into block tables and slots, ``RopeAppend``
-normalises and rotates q and k and writes k and v into the pages, ``Attention`` reads them.  The
-handles check what they are given, borrow the tensors they were made with (which must outlive
+normalises and rotates q and k and writes k and v into the pages, ``Attention`` reads them.
+``PagedKVFp8`` in ``PagedKV``'s place holds K and V as 8-bit floats with a scale for every 64 positions
+of a kv head, in half the bytes; the other handles take either, and ``PageRead`` reads positions of such
+a cache back.  The handles check what they are given, borrow the tensors they were made with (which must outlive
 them) and queue their work on the current stream of the pool's device; lengths, tables and the
 free stack stay on the device, so a step can be captured in a CUDA graph.
 
@@ -43,6 +45,17 @@ DEV_ERRORS = {B.DEV_PAGE_ID: "page id outside the pool", B.DEV_PAGES: "too few f
 def page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int, n_layers: int = 1) -> int:
     """Bytes of one page holding `n_layers` layers."""
     return 4 * n_layers * n_kv_heads * page_tokens * head_dim
+
+
+def page_bytes_fp8(page_tokens: int, n_kv_heads: int, head_dim: int, n_layers: int = 1) -> int:
+    """Bytes of one page of a cache in 8 bits holding `n_layers` layers: codes of K and of V, then their
+    scales, each layer's padded to whole 256 bytes."""
+    return n_layers * sum(_layer_fp8(page_tokens, n_kv_heads, head_dim))
+
+
+def _layer_fp8(page_tokens, n_kv_heads, head_dim):
+    """(bytes of K's and V's codes, bytes of the scales with what fills up 256) of a page's layer."""
+    return 2 * n_kv_heads * page_tokens * head_dim, -(-8 * n_kv_heads * (page_tokens // B.FP8_BLOCK) // 256) * 256
 
 
 def size32(v, what: str) -> int:
@@ -177,16 +190,20 @@ class PagedKV:
     """A pool of pages, each holding K and V of `n_layers` layers for `page_tokens` positions.
 
     pool         1-D contiguous bf16 or uint8 tensor, 256-byte aligned; its length gives the pages
+                 (page_bytes each)
     block_table  int32 [rows, max_pages], kv_lens int32 [rows]: which pages a row holds and how
                  many positions (both may be None for a cache that is only appended to by slot)
     """
+
+    _pool_types = (torch.bfloat16, torch.uint8)
+    _page_bytes = staticmethod(page_bytes)
 
     def __init__(self, pool, block_table, kv_lens, *, page_tokens: int, n_kv_heads: int,
                  head_dim: int, n_layers: int = 1):
         for n, what in ((page_tokens, "page_tokens"), (n_kv_heads, "n_kv_heads"), (head_dim, "head_dim"),
                         (n_layers, "n_layers")):
             size32(n, what)
-        _tensor(pool, "pool", (torch.bfloat16, torch.uint8), dims=1)
+        _tensor(pool, "pool", self._pool_types, dims=1)
         self.device = pool.device
         self.index = pool.get_device()
         self.pool, self.block_table, self.kv_lens = pool, block_table, kv_lens
@@ -202,20 +219,43 @@ class PagedKV:
             raise ValueError("page_tokens, n_kv_heads, head_dim and n_layers are positive")
         self.n_layers = n_layers
         size = pool.numel() * pool.element_size()
-        step = page_bytes(page_tokens, n_kv_heads, head_dim, n_layers)
+        step = self._page_bytes(page_tokens, n_kv_heads, head_dim, n_layers)
         self.n_pages = size // step
         if self.n_pages == 0:
             raise ValueError(f"pool: {size} bytes hold no page of {step}")
-        block = step // (2 * n_layers)
-        self.layers = [B.PagedKvDesc(pool.data_ptr(), size, step, 2 * l * block, (2 * l + 1) * block,
-                                     self.n_pages, page_tokens, n_kv_heads, head_dim)
-                       for l in range(n_layers)]
+        self.layers = [self._layer(l, size, step) for l in range(n_layers)]
         self.err = torch.zeros(2, dtype=torch.int32, device=self.device)
         self.call = _Device(self.index, [self.err])
+
+    def _layer(self, l, size, step):
+        block = step // (2 * self.n_layers)
+        return B.PagedKvDesc(self.pool.data_ptr(), size, step, 2 * l * block, (2 * l + 1) * block,
+                             self.n_pages, self.page_tokens, self.n_kv_heads, self.head_dim)
 
     def check(self) -> None:
         """Wait for the work queued on the current stream and raise if a kernel found an error."""
         _read_err(self.err)
+
+
+class PagedKVFp8(PagedKV):
+    """A pool of pages that holds K and V as 8-bit floats (e4m3 codes) with a scale, a power of two, for
+    every 64 positions of a kv head (cbt_paged_kv_fp8); everything else is as in PagedKV.
+
+    pool         1-D contiguous uint8 tensor, 256-byte aligned; its length gives the pages
+                 (page_bytes_fp8 each)
+    RopeAppend writes the codes and sets the scales.  A row starts in the first position of a page
+    whose contents do not matter; one that is to go on within a block of 64 positions that no append
+    has begun needs that page zeroed first.  The tokens of a block stand next to each other in an
+    append, as PageMap deals them."""
+
+    _pool_types = (torch.uint8,)
+    _page_bytes = staticmethod(page_bytes_fp8)
+
+    def _layer(self, l, size, step):
+        codes, scales = _layer_fp8(self.page_tokens, self.n_kv_heads, self.head_dim)
+        at = l * (codes + scales)
+        return B.PagedKvFp8Desc(self.pool.data_ptr(), size, step, at, at + codes // 2, at + codes,
+                                self.n_pages, self.page_tokens, self.n_kv_heads, self.head_dim)
 
 
 class PageMap:
@@ -297,7 +337,8 @@ class PageMap:
 
 
 class RopeAppend:
-    """Per-head norm, rotary positions and KV append (cbt_rope_append).  rope None: no rotation."""
+    """Per-head norm, rotary positions and KV append (cbt_rope_append, and cbt_rope_append_fp8 where
+    the cache is a PagedKVFp8).  rope None: no rotation."""
 
     def __init__(self, cache: PagedKV, rope: Rope | None, *, n_heads: int, eps: float = 1e-6):
         if rope is not None and rope.head_dim != cache.head_dim:
@@ -307,7 +348,8 @@ class RopeAppend:
         self.q_width = n_heads * cache.head_dim
         self._layer = None
         self._lock = threading.Lock()
-        self.args = B.RopeAppendArgs()
+        self.fp8 = isinstance(cache, PagedKVFp8)
+        self.args = B.RopeAppendFp8Args() if self.fp8 else B.RopeAppendArgs()
         self.args.rope = None if rope is None else ctypes.pointer(rope.desc)
         self.args.n_heads = n_heads
         self.args.eps = eps
@@ -334,7 +376,7 @@ class RopeAppend:
             a.k_gain = None if k_gain is None else self._gain(k_gain, "k_gain")
             a.qkv, a.q_out = qkv.data_ptr(), q_out.data_ptr()
             a.qkv_dtype = B.DTYPE_F32 if qkv.dtype is torch.float32 else B.DTYPE_BF16
-            c.call(B.rope_append, a)
+            c.call(B.rope_append_fp8 if self.fp8 else B.rope_append, a)
 
     def _gain(self, t, what):
         if _tensor(t, what, _BF16, self.cache.index, 1).numel() != self.cache.head_dim:
@@ -343,7 +385,8 @@ class RopeAppend:
 
 
 class Attention:
-    """Attention over the cache's pages (cbt_paged_attention), with a workspace of its own.
+    """Attention over the cache's pages (cbt_paged_attention, and cbt_paged_attention_fp8 where the
+    cache is a PagedKVFp8), with a workspace of its own.
 
     max_kv, max_q  upper bounds of a row's positions and query tokens.  With max_q > 1 they also decide how
                  the work is cut: bounds far above the rows cost time.  Weights are then rounded to
@@ -367,7 +410,8 @@ class Attention:
         self._layer = None
         self._lock = threading.Lock()
         self.max_tokens = cache.rows if max_tokens is None else max_tokens
-        a = self.args = B.PagedAttentionArgs()
+        self.fp8 = isinstance(cache, PagedKVFp8)
+        a = self.args = B.PagedAttentionFp8Args() if self.fp8 else B.PagedAttentionArgs()
         a.kv = cache.layers[0]
         a.block_table, a.max_pages, a.rows = (cache.block_table.data_ptr(),
                                               cache.block_table.shape[1], cache.rows)
@@ -376,7 +420,7 @@ class Attention:
         a.scale = 1 / math.sqrt(cache.head_dim) if scale is None else scale
         a.window, a.sinks = window, sinks
         a.err = cache.err.data_ptr()
-        n = B.paged_attention_workspace(a)
+        n = (B.paged_attention_fp8_workspace if self.fp8 else B.paged_attention_workspace)(a)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
         a.workspace = self.workspace.data_ptr() if n else None
         a.workspace_bytes = n
@@ -406,4 +450,48 @@ class Attention:
                 a.cu_q = _vec(cu_q, "cu_q", dev, c.rows + 1)
             a.q, a.out, a.tokens = q.data_ptr(), out.data_ptr(), tokens
             a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
-            self.call(B.paged_attention, a)
+            self.call(B.paged_attention_fp8 if self.fp8 else B.paged_attention, a)
+
+
+class PageRead:
+    """Positions of a cache in 8 bits read back (cbt_paged_read_fp8)."""
+
+    def __init__(self, cache: PagedKVFp8):
+        if not isinstance(cache, PagedKVFp8):
+            raise TypeError("cache: a PagedKVFp8 is wanted")
+        if cache.block_table is None:
+            raise ValueError("the cache has no block table")
+        self.cache = cache
+        self.width = cache.n_kv_heads * cache.head_dim
+        self._layer = None
+        self._lock = threading.Lock()
+        a = self.args = B.PagedReadFp8Args()
+        a.block_table, a.max_pages, a.rows = (cache.block_table.data_ptr(), cache.block_table.shape[1],
+                                              cache.rows)
+        a.kv_lens, a.err = cache.kv_lens.data_ptr(), cache.err.data_ptr()
+
+    def __call__(self, layer: int, k_out, v_out, cu, first=None) -> None:
+        """Row b's positions [first[b], first[b] + n_b), n_b = cu[b + 1] - cu[b], to rows [cu[b], cu[b +
+        1]) of k_out and v_out, [tokens, n_kv_heads, head_dim] (or two dimensions) of one type, bf16 or
+        fp32; their rows may be strided, by the same stride.  Either may be None.  cu int32 [rows + 1],
+        first int32 [rows] (None: 0)."""
+        c, a = self.cache, self.args
+        dev = c.index
+        out = v_out if k_out is None else k_out
+        if out is None:
+            raise ValueError("k_out and v_out: one of them is wanted")
+        with self._lock:
+            a.tokens = tokens = out.shape[0]
+            if layer != self._layer:
+                a.kv = c.layers[layer]
+                self._layer = layer
+            a.out_stride = _rows(out, "v_out" if k_out is None else "k_out", _ROWS, dev, tokens, self.width)
+            if k_out is not None and v_out is not None and \
+                    _rows(v_out, "v_out", (k_out.dtype,), dev, tokens, self.width) != a.out_stride:
+                raise ValueError("k_out and v_out: their rows have different strides")
+            a.cu = _vec(cu, "cu", dev, c.rows + 1)
+            a.first = None if first is None else _vec(first, "first", dev, c.rows)
+            a.k_out = None if k_out is None else k_out.data_ptr()
+            a.v_out = None if v_out is None else v_out.data_ptr()
+            a.out_dtype = B.DTYPE_F32 if out.dtype is torch.float32 else B.DTYPE_BF16
+            c.call(B.paged_read_fp8, a)

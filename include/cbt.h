@@ -578,6 +578,119 @@ cbt_status cbt_paged_attention(const cbt_paged_attention_args* a, void* stream);
  * it needs none or the sizes are not supported. */
 size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
 
+/* ---- The same operators on a cache in 8 bits ----------------------------------------------
+ * cbt_rope_append_fp8, cbt_paged_attention_fp8 and cbt_paged_read_fp8 work on pages that hold K and V
+ * as 8-bit floats (e4m3: four bits of exponent, three of mantissa, largest 448) with a scale for every
+ * block of 64 positions of a kv head, K and V apart: half the bytes of a bf16 cache.  What such a cache
+ * holds is off from what was appended by at most 2^-4 of each value, or 2^-10 of the block's scale where
+ * that is more.  Tables, slots and lengths are as for bf16 pages (cbt_page_map serves both).
+ *
+ * A scale is a power of two, 2^e with e in [-56, 56]: the smallest that all of the block's values are
+ * within 448 times of.  The steps of an 8-bit float are relative, so a finer scale would gain nothing,
+ * and a block whose scale has to grow under later tokens is moved to the new one without another
+ * rounding, but for codes below 2^-6.
+ *
+ * One layer in a pool of n_pages pages, page i at pool + i * page_bytes.  In a page, the codes of K
+ * start at k_offset and those of V at v_offset bytes, each n_kv_heads blocks of page_tokens *
+ * head_dim: K [position][head_dim], V [position / 64][head_dim][64].  The scales start at s_offset
+ * bytes: fp32 [2 (K, V)][n_kv_heads][page_tokens / 64]; one that is not such a power of two is taken as
+ * the one below it, and those out of range as the nearest in it.  pool, page_bytes and the offsets are
+ * multiples of 256 bytes; page_tokens is a multiple of 64; head_dim is 64 or 128; n_pages * page_tokens
+ * < 2^31 and pool_bytes < 256 * 2^31 (CBT_ERR_LIMIT); the last page's codes and scales end within
+ * pool_bytes. */
+#define CBT_FP8_BLOCK 64
+typedef struct {
+  void* pool;
+  size_t pool_bytes;
+  int64_t page_bytes;
+  int64_t k_offset, v_offset, s_offset;
+  int32_t n_pages, page_tokens, n_kv_heads, head_dim;
+} cbt_paged_kv_fp8;
+
+/* cbt_rope_append with K and V rounded to codes.  The norms, the rotation and q_out are those of
+ * cbt_rope_append; k (rotated, in fp32) and v then go to slot slots[t] as codes.  For each block that
+ * the call's tokens lie in, kv head, and K and V apart:
+ *   - where a token lies in the block's first position (slot % 64 == 0) the block starts anew, and what
+ *     its other positions held is lost; else it goes on from the scale that it has;
+ *   - the scale becomes the largest of that and what the call's tokens need (their values that are
+ *     finite); where it grows, the codes held there are rounded to the new one;
+ *   - the tokens are rounded to it once, to nearest even.  An infinity becomes 448 times the scale, as
+ *     does a value above 448 * 2^56; a NaN stays one.
+ * A block that is gone on with has to hold a scale: pages are taken from position 0 on, or zeroed first.
+ * The tokens of one block stand next to each other in the call (as cbt_page_map deals them; tokens that
+ * are skipped do not stand between them): where they do not, what the block then holds is unspecified.
+ * Where two tokens have one slot, each element there is one or the other's.  Everything else is as in
+ * cbt_rope_append, errors among it. */
+typedef struct {
+  cbt_paged_kv_fp8 kv;
+  const cbt_rope* rope;
+  const void* qkv;
+  int32_t qkv_dtype;
+  int64_t qkv_stride;
+  int32_t tokens, n_heads;
+  const void* q_gain;
+  const void* k_gain;
+  float eps;
+  const int32_t* positions;
+  const int32_t* slots;
+  void* q_out;
+  int64_t q_stride;
+  int32_t* err;
+} cbt_rope_append_fp8_args;
+cbt_status cbt_rope_append_fp8(const cbt_rope_append_fp8_args* a, void* stream);
+
+/* Reads positions back: row b's [first[b], first[b] + n_b), n_b = cu[b + 1] - cu[b], go to rows
+ * [cu[b], cu[b + 1]) of k_out and v_out as code * scale (exact in either type).
+ *   block_table, kv_lens  as in cbt_paged_attention; the positions lie within [0, kv_lens[b])
+ *   first        int32 [rows], or NULL: 0
+ *   cu           int32 [rows + 1]
+ *   tokens       rows of k_out and v_out; those past cu[rows] are left as they are
+ *   k_out, v_out bf16 or fp32 (out_dtype) [tokens][n_kv_heads * head_dim], rows out_stride elements
+ *                apart; either may be NULL
+ * A row whose positions leave the row or its table is skipped (CBT_DEV_LENGTH, info: the row); positions
+ * in a page outside the pool are left as they were (CBT_DEV_PAGE_ID).  Where a row's range of cu leaves
+ * [0, tokens] or runs backwards (CBT_DEV_LENGTH), the call's outputs are unspecified.  k_out and v_out
+ * are 16-byte aligned, the stride a multiple of 8; rows <= CBT_PAGED_ATTENTION_MAX_ROWS, tokens <= 2^30
+ * (CBT_ERR_LIMIT).  Other errors: CBT_ERR_NULL, CBT_ERR_INVALID, CBT_ERR_UNSUPPORTED, CBT_ERR_CUDA. */
+typedef struct {
+  cbt_paged_kv_fp8 kv;
+  const int32_t* block_table;
+  int32_t max_pages, rows;
+  const int32_t* kv_lens;
+  const int32_t* first;
+  const int32_t* cu;
+  int32_t tokens;
+  void* k_out;
+  void* v_out;
+  int32_t out_dtype;
+  int64_t out_stride;
+  int32_t* err;
+} cbt_paged_read_fp8_args;
+cbt_status cbt_paged_read_fp8(const cbt_paged_read_fp8_args* a, void* stream);
+
+/* cbt_paged_attention over codes: k_j and v_j are code * scale of position j, everything else is as
+ * there. */
+typedef struct {
+  cbt_paged_kv_fp8 kv;
+  const int32_t* block_table;
+  int32_t max_pages, rows;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int32_t tokens, max_q, max_kv, n_heads;
+  const void* q;
+  int64_t q_stride;
+  float scale;
+  int32_t window, sinks;
+  void* out;
+  int32_t out_dtype;
+  int64_t out_stride;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* err;
+} cbt_paged_attention_fp8_args;
+cbt_status cbt_paged_attention_fp8(const cbt_paged_attention_fp8_args* a, void* stream);
+size_t cbt_paged_attention_fp8_workspace(const cbt_paged_attention_fp8_args* a);
+
 /* The attention form of an engine's layers.  From now on every prefill and decode step of the
  * engine normalises q and k per head, rotates them, appends K and V and attends as cbt_rope_append
  * and cbt_paged_attention do, over the engine's own pages; NULL returns it to its built-in form
