@@ -340,6 +340,19 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, int head_dim, int heads, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_bytes(CUtensorMap* m, const void* base, uint64_t bytes, uint32_t row, uint32_t rows) {
+  auto fn = encode_fn();
+  if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || (row != 64 && row != 128) || rows * row % 256)
+    return false;
+  cuuint64_t dims[3] = {row, 256 / row, bytes / 256};
+  cuuint64_t strides[2] = {row, 256};
+  cuuint32_t box[3] = {row, 256 / row, rows * row / 256};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_kblocks(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows,
                        uint32_t nk, uint64_t pair_rows) {
   auto fn = encode_fn();

@@ -100,6 +100,9 @@ bool make_tmap_kblocks(CUtensorMap* m, const void* base, uint64_t K, uint64_t ro
 // box brings 64 dims of box_heads heads of box_tokens tokens, each (token, head) a 128-byte row
 bool make_tmap_rows(CUtensorMap* m, const void* base, int head_dim, int heads, int tokens,
                     long long row_stride, int box_heads, int box_tokens);
+// `bytes` bytes as rows of 64 or 128, in whole 256 bytes so that a map reaches 2^39: coordinate {0, 0,
+// offset / 256}, a box brings `rows` rows next to each other, in the row size's swizzle
+bool make_tmap_bytes(CUtensorMap* m, const void* base, uint64_t bytes, uint32_t row, uint32_t rows);
 // N tile for hi/lo (split) activations of n rows, and for plain bf16 activations
 int tc_split_bn(int n);
 int tc_plain_bn(int n);

@@ -85,9 +85,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_attn_fp8(const __grid_constant_
 
 }  // namespace
 
-size_t attn_fp8_workspace(const PagedAttnFp8&) { return 0; }
+size_t attn_fp8_workspace(const PagedAttnFp8& a) { return a.max_q == 1 ? decode_fp8_workspace(a) : 0; }
 
 cudaError_t launch_attn_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s) {
+  if (attn_fp8_workspace(a) > a.ws_bytes) return cudaErrorInvalidValue;
+  if (a.max_q == 1) return launch_decode_fp8(a, num_sms, s);
   const long long pairs = (long long)a.max_q * a.n_heads, most = (pairs + kWarps - 1) / kWarps;
   const dim3 grid((unsigned)(most < 64 * num_sms ? most : 64 * num_sms), a.rows);
   return a.kv.head_dim == 128 ? launch_pdl(k_attn_fp8<128>, grid, dim3(32 * kWarps), 0, s, a)

@@ -1,0 +1,509 @@
+// paged_decode_fp8.cu -- attention of one new token per row over a paged cache in 8 bits, split over the
+// cache's length and joined.
+//
+// The contraction is turned around as over bf16 pages (paged_decode.cu): per 128-key chunk, S^T[key]
+// [head] = K . Q^T and O^T[dim][head] = V^T . P^T, with K and V taken by the tensor cores as the codes
+// they are (e4m3, M = 128).  What multiplies them is split into codes too, each part in columns of its
+// own, so that nothing but a last rounding is lost:
+//   q   two parts (bf16 has eight bits of mantissa, a part four): exact down to 2^-12 of the head's largest
+//       element, off by at most 2^-22 of it below;
+//   p   three: 2^-12 of each weight, 2^-26 of the largest.
+// A block's scales are powers of two.  K's multiplies its scores; V's is an addition to them, in units of
+// log2: the weights are 2^(s_j + e_j - m), e_j the exponent of j's block, m the largest s_j + e_j so far,
+// and the sum l takes them times 2^-e_j.  (e in [-56, 56], so both hold in fp32.)
+//
+// Bound by HBM: 2 head_dim bytes of K and V per position and kv head.  Items, runs and their join are
+// those of paged_split.cuh.
+#include "fp8_tc.cuh"
+#include "paged_split.cuh"
+
+namespace {
+
+constexpr int kCompute = 128;  // warps 0..3; warp 4 requests tiles
+constexpr int kIssuers = 2;    // threads that issue half of each contraction's MMAs
+constexpr int kParts = 3;      // of a weight
+using Attn = PagedAttnFp8;
+
+template <int HD, int GT>
+struct Shape {
+  static constexpr int kNQ = 16, kNP = kParts * GT <= 16 ? 16 : 32;  // columns of S^T and of O^T
+  static constexpr int kK = kSub * HD, kVHalf = kBlock * HD, kQ = kNQ * HD, kP = kNP * kSub;
+  static constexpr uint32_t kCols = kIssuers * (kNQ + kNP) <= 64 ? 64 : 128;  // of tensor memory
+  // V^T's halves span M = 128 rows: for head_dim 64 the second one's rows past 64 lie in what follows
+  static constexpr int kTiles = kK + 2 * kVHalf + kQ + kP;
+  static constexpr size_t kSmem = 1024 + (kTiles > kK + 3 * kVHalf ? kTiles : kK + 3 * kVHalf) + 1024;
+  static constexpr int kCtas = GT == 8 ? 4 : 5;  // of an SM
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kCtas * kCols <= 512, "shared and tensor memory");
+};
+
+// What a chunk's requester hands to the softmax: the exponents of each half's K and V scales
+struct Scales {
+  int k[2], v[2];
+};
+
+// GT: the group's q heads rounded up to 1, 2, 4 or 8
+template <int HD, int GT>
+__global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
+    k_decode_fp8(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                 const __grid_constant__ Attn a, float* __restrict__ part_o, float2* __restrict__ part_ml) {
+  using S = Shape<HD, GT>;
+  constexpr uint32_t kIdescS = tc::idesc_e4m3(128, S::kNQ), kIdescO = tc::idesc_e4m3(128, S::kNP);
+  constexpr float kUnit = 256.f;   // a weight of 1 in units of its first part
+  constexpr float kPart = 16.f;    // of one part's unit to the next one's
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sK = smem;                   // [128 keys][HD]
+  uint8_t* sV = sK + S::kK;             // [64-key half][HD dims][64 keys]
+  uint8_t* sP = sV + 2 * S::kVHalf;     // [part, head][128 keys]
+  uint8_t* sQ = sP + S::kP;             // [part, head][HD]
+  uint8_t* end = smem + S::kSmem - 2048;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(end);
+  uint64_t *kfull = bars, *vfull = bars + 1, *kempty = bars + 2, *vempty = bars + 3;
+  uint64_t *bar_s = bars + 4, *bar_o = bars + 5;
+  Scales* scales = reinterpret_cast<Scales*>(bars + 6);  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scales + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* vis = tmem_slot + 2;                        // [4] visible keys of the chunk
+  float* red = reinterpret_cast<float*>(tmem_slot + 6); // [4 warps][8 heads]
+  float* red2 = red + 32;
+  float* l_run = red2 + 32;                             // [8]
+  float* q_unit = l_run + 8;                            // [8] a score's unit, in log2 units
+
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const Layout lay = layout_of(a);
+  const int per_row = a.kv.n_kv_heads * lay.groups;
+  if (tid == 0) {
+    for (int i = 0; i < 6; ++i) tc::mbar_init(&bars[i], i < 2 ? 1 : kIssuers);
+    tc::mbar_init(kempty, kIssuers + 4);  // the MMAs, and every warp has seen that the tile was full
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::tma_prefetch_desc(&tk);
+    tc::tma_prefetch_desc(&tv);
+  }
+  if (warp == 0) tc::tmem_alloc(tmem_slot, S::kCols);
+  // heads and parts that no item fills stay zero
+  for (int i = tid; i < (S::kP + S::kQ) / 16; i += kCompute + 32)
+    reinterpret_cast<uint4*>(sP)[i] = make_uint4(0, 0, 0, 0);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  pdl_wait();
+  Cursor<Attn> cur;
+  cur.load(a, per_row, 0, 0);
+
+  if (warp == 4) {
+    // ---- tile requests: K, then V of each chunk.  The next chunk's pages and scales are looked up while
+    // V's buffer is awaited, so that K's stays empty for a wait only.
+    const uint64_t pol = tc::policy_evict_first();
+    uint32_t n = 0, nk = 0, nv = 0;  // chunks, and tiles of K and of V requested
+    bool ok = true;
+    const int P = a.kv.page_tokens;
+    // a chunk's halves of 64 keys that hold a key the query sees, and where they lie; lane e has half
+    // e's scales
+    struct Chunk {
+      unsigned halves;
+      int k[2], v[2];
+      float ks, vs;
+    };
+    int it = blockIdx.x, i = 0;
+    bool have = cur.seek(a, per_row, it);
+    Item w{};
+    if (have) {
+      w = item_at(cur, a, lay.groups, it);
+      i = w.i0;
+    }
+    auto next = [&]() {  // halves 0: no chunk is left
+      Chunk c{};
+      while (have && i >= w.i1) {
+        it += gridDim.x;
+        have = cur.seek(a, per_row, it);
+        if (have) {
+          w = item_at(cur, a, lay.groups, it);
+          i = w.i0;
+        }
+      }
+      if (!have) return c;
+      // lanes 0 and 1: a half each
+      const int k0 = w.seen.chunk(i++) * kSub + kBlock * lane;
+      int kat = 0, vat = 0;
+      const bool want = lane < 2 && k0 <= w.p && (sees(k0, w.p, a.window, a.sinks) ||
+                                                   sees(min(k0 + 63, w.p), w.p, a.window, a.sinks));
+      if (want) {
+        const int pg = k0 / P, o = k0 - pg * P;
+        int id = a.table[(size_t)w.b * a.max_pages + pg];
+        if (id < 0 || id >= a.kv.n_pages) {
+          set_device_error(a.err, CBT_DEV_PAGE_ID, w.b);
+          id = 0;  // a page that exists: the row's outputs are unspecified
+        }
+        kat = (int)(fp8_k(a.kv, id, w.g, o, 0) >> 8);
+        vat = (int)(fp8_v(a.kv, id, w.g, o, 0) >> 8);
+        c.ks = *fp8_scale(a.kv, id, 0, w.g, o);
+        c.vs = *fp8_scale(a.kv, id, 1, w.g, o);
+      }
+      c.halves = __ballot_sync(0xffffffffu, want);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c.k[e] = __shfl_sync(0xffffffffu, kat, e);
+        c.v[e] = __shfl_sync(0xffffffffu, vat, e);
+      }
+      return c;
+    };
+    Chunk c = next();
+#pragma unroll 1
+    for (; c.halves; ++n) {
+      const uint32_t bytes = __popc(c.halves) * S::kVHalf;
+      ok = __all_sync(0xffffffffu, wait_or_abort(kempty, (n & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (c.halves >> e & 1) tc::tma_load_rows(sK + e * S::kVHalf, &tk, kfull, c.k[e], pol);
+      }
+      // (the tile's bytes may land before they are expected: the phase waits for the arrival)
+      if (lane < 2) {
+        scales[n & 1].k[lane] = fp8_exponent(c.ks);
+        scales[n & 1].v[lane] = fp8_exponent(c.vs);
+      }
+      __syncwarp();
+      if (elect_one()) tc::mbar_expect_tx(kfull, bytes);
+      ++nk;
+      const Chunk nxt = next();
+      ok = __all_sync(0xffffffffu, wait_or_abort(vempty, (n & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (elect_one()) {
+        tc::mbar_expect_tx(vfull, bytes);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (c.halves >> e & 1) tc::tma_load_rows(sV + e * S::kVHalf, &tv, vfull, c.v[e], pol);
+      }
+      ++nv;
+      c = nxt;
+    }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 21);
+    // no copies in flight at exit
+    if (nk) wait_landed(kfull, (nk - 1) & 1);
+    if (nv) wait_landed(vfull, (nv - 1) & 1);
+  } else {
+    uint32_t n = 0;  // chunks done
+    bool ok = true;
+    const float scale2 = a.scale * kLog2e;  // scores in units of log2
+    constexpr int kQUnits = HD / 8;         // 16-byte pieces of a head
+    const int qh = tid / kQUnits, qu = tid % kQUnits;
+    // this thread's piece of the next item's q
+    auto load_q = [&](const Item& w) {
+      return qh < w.heads
+                 ? *reinterpret_cast<const uint4*>(a.q + w.t * a.q_ld + (long long)(w.head0 + qh) * HD + qu * 8)
+                 : make_uint4(0, 0, 0, 0);
+    };
+    // ... as two parts of codes; by all lanes (a head's pieces lie with lanes next to each other)
+    auto store_q = [&](const uint4& v) {
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      float x[8], top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(u[e]);
+        x[2 * e + 1] = bf16_hi(u[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fabsf(x[e]) <= 3.4028235e38f ? fmaxf(top, fabsf(x[e])) : top;
+#pragma unroll
+      for (int o = kQUnits / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int fit = fit_exponent(top);
+      const float f = pow2_of(fit);
+      uint32_t part[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        part[0][e] = part[1][e] = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float z = x[4 * e + 2 * j + k];
+            y[k] = fabsf(z) <= 3.4028235e38f ? z * f : __int_as_float(0x7FC00000);  // infinities: NaN
+          }
+          const uint16_t hi = pack_e4m3(y[0], y[1]);
+          const uint32_t back = e4m3_to_f16(hi);
+          const uint16_t lo = pack_e4m3((y[0] - f16_lo(back)) * kPart, (y[1] - f16_hi(back)) * kPart);
+          part[0][e] |= (uint32_t)hi << (16 * j);
+          part[1][e] |= (uint32_t)lo << (16 * j);
+        }
+      }
+      if (qh < GT) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint2*>(sQ + tc::swz<HD>(k * GT + qh, qu * 8)) = make_uint2(part[k][0], part[k][1]);
+        if (qu == 0) q_unit[qh] = scale2 * pow2_of(-fit);
+      }
+    };
+    int it = blockIdx.x;
+    bool have = cur.seek(a, per_row, it);
+    Item w{}, nxt{};
+    uint4 qv = make_uint4(0, 0, 0, 0);
+    if (have) {
+      nxt = item_at(cur, a, lay.groups, it);
+      qv = load_q(nxt);
+    }
+    while (have && ok) {
+      w = nxt;
+      // the MMAs that read the last item's Q have completed (bar_s)
+      store_q(qv);
+      it += gridDim.x;
+      have = cur.seek(a, per_row, it);
+      if (have) {
+        nxt = item_at(cur, a, lay.groups, it);
+        qv = load_q(nxt);
+      }
+      if (tid < 8) l_run[tid] = 0.f;
+      float m_run[GT], oacc[GT];
+#pragma unroll
+      for (int h = 0; h < GT; ++h) {
+        m_run[h] = -INFINITY;  // kept by every thread, each from the same values in the same order
+        oacc[h] = 0.f;
+      }
+      tc::fence_proxy_async_smem();
+      tc::named_bar_sync(1, kCompute);
+
+      for (int i = w.i0; i < w.i1; ++i, ++n) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(kfull, n & 1, abort_flag))) {
+          if (lane == 0) wait_timeout(a.err, abort_flag, 22);
+        } else {
+          if (lane == 0) tc::mbar_arrive(kempty);
+          if (warp < kIssuers && elect_one()) {
+            tc::tc_fence_after();
+            constexpr int kSteps = HD / 32 / kIssuers;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              const int kk = warp * kSteps + k;
+              tc::mma_e4m3(tmem + S::kNQ * warp, tc::sdesc_rows<HD>(tc::smem_u32(sK)) + 2 * kk,
+                           tc::sdesc_rows<HD>(tc::smem_u32(sQ)) + 2 * kk, kIdescS, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(bar_s);
+            tc::mma_commit(kempty);
+          }
+        }
+        const int k0 = w.seen.chunk(i) * kSub;
+        const bool valid = sees(k0 + tid, w.p, a.window, a.sinks);
+        const uint32_t vb = __ballot_sync(0xffffffffu, valid);
+        if (lane == 0) vis[warp] = vb;
+        const float k_unit = pow2_of(scales[n & 1].k[tid >> 6]);
+        const int ve = scales[n & 1].v[tid >> 6];
+        const bool bad_s = !wait_or_abort(bar_s, n & 1, abort_flag);
+        if (tc::named_bar_any(2, kCompute, bad_s)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t raw[16], raw2[16];
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        tc::tmem_ld16(lane_base, raw);
+        tc::tmem_ld16(lane_base + S::kNQ, raw2);
+        tc::tmem_ld_wait();
+        float s[GT], mx[GT];
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          const float hi = __uint_as_float(raw[h]) + __uint_as_float(raw2[h]);
+          const float lo = __uint_as_float(raw[GT + h]) + __uint_as_float(raw2[GT + h]);
+          s[h] = valid ? fmaf(fmaf(lo, 1.f / kPart, hi) * k_unit, q_unit[h], (float)ve) : -INFINITY;
+          mx[h] = s[h];
+        }
+        warp_reduce_n<GT, true>(mx);
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
+        }
+        tc::named_bar_sync(1, kCompute);
+        float scl[GT];
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          const float mloc = fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h]));
+          const float mo = m_run[h];
+          const float mn = fmaxf(mo, mloc);
+          scl[h] = mo == -INFINITY ? 0.f : ex2(mo - mn);
+          m_run[h] = mn;
+        }
+        float ps[GT];
+        const float v_down = pow2_of(-ve);
+        uint8_t* dst = sP + (tid & 15);
+#pragma unroll
+        for (int h = 0; h < GT; h += 2) {
+          float p[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
+            const int g = h + e < GT ? h + e : h;
+            p[e] = valid ? ex2(s[g] - (m_run[g] == -INFINITY ? 0.f : m_run[g])) : 0.f;
+          }
+          ps[h] = p[0] * v_down;
+          if (h + 1 < GT) ps[h + 1 < GT ? h + 1 : h] = p[1] * v_down;
+          p[0] *= kUnit;
+          p[1] *= kUnit;
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            const uint16_t code = pack_e4m3(p[0], p[1]);
+            dst[tc::swz<128>(k * GT + h, tid & ~15)] = (uint8_t)code;
+            if (h + 1 < GT) dst[tc::swz<128>(k * GT + h + 1, tid & ~15)] = (uint8_t)(code >> 8);
+            const uint32_t back = e4m3_to_f16(code);
+            p[0] = (p[0] - f16_lo(back)) * kPart;
+            p[1] = (p[1] - f16_hi(back)) * kPart;
+          }
+        }
+        warp_reduce_n<GT, false>(ps);
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h) red2[warp * 8 + h] = ps[h];
+        }
+        if (vis[0] + 1 != 0 || vis[1] + 1 != 0 || vis[2] + 1 != 0 || vis[3] + 1 != 0) {
+          // masked keys: their V may hold anything, so it is zeroed (their weights are zero)
+          const bool bad_v = !wait_or_abort(vfull, n & 1, abort_flag);
+          if (tc::named_bar_any(2, kCompute, bad_v)) {
+            if (tid == 0) wait_timeout(a.err, abort_flag, 23);
+            ok = false;
+            break;
+          }
+          if (tid < HD) {
+#pragma unroll 1
+            for (int u = 0; u < 8; ++u) {  // 16 keys of this thread's dim
+              const uint32_t bits = (vis[u >> 1] >> (16 * (u & 1))) & 0xFFFFu;
+              if (bits == 0xFFFFu) continue;
+              uint4* at = reinterpret_cast<uint4*>(sV + (u >> 2) * S::kVHalf + tc::swz<64>(tid, 16 * (u & 3)));
+              const uint4 mk = code_mask(bits);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (bits) v = *at;
+              *at = make_uint4(v.x & mk.x, v.y & mk.y, v.z & mk.z, v.w & mk.w);
+            }
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        tc::named_bar_sync(1, kCompute);
+        if (tid < GT) {
+          float sc = scl[0];
+#pragma unroll
+          for (int h = 1; h < GT; ++h)
+            if (h == tid) sc = scl[h];
+          l_run[tid] = l_run[tid] * sc + red2[tid] + red2[8 + tid] + red2[16 + tid] + red2[24 + tid];
+        }
+        if (warp < kIssuers) {
+          if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
+            if (lane == 0) wait_timeout(a.err, abort_flag, 24);
+          } else if (elect_one()) {
+            tc::tc_fence_after();
+            // issuer e: the half's two steps of 32 keys
+#pragma unroll
+            for (int k = 0; k < kBlock / 32; ++k)
+              tc::mma_e4m3(tmem + kIssuers * S::kNQ + S::kNP * warp,
+                           tc::sdesc_rows<64>(tc::smem_u32(sV + warp * S::kVHalf)) + 2 * k,
+                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * (2 * warp + k), kIdescO, k > 0 ? 1u : 0u);
+            tc::mma_commit(bar_o);
+            tc::mma_commit(vempty);
+          }
+        }
+        const bool bad_o = !wait_or_abort(bar_o, n & 1, abort_flag);
+        if (tc::named_bar_any(2, kCompute, bad_o)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t o1[S::kNP], o2[S::kNP];
+#pragma unroll
+        for (int k = 0; k < S::kNP; k += 16) {
+          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + k, o1 + k);
+          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + S::kNP + k, o2 + k);
+        }
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          float o = 0.f;
+#pragma unroll
+          for (int k = kParts - 1; k >= 0; --k)
+            o = fmaf(o, 1.f / kPart, __uint_as_float(o1[k * GT + h]) + __uint_as_float(o2[k * GT + h]));
+          oacc[h] = fmaf(oacc[h], scl[h], o * (1.f / kUnit));
+        }
+        tc::tc_fence_before();
+      }
+      if (!ok) break;
+      tc::named_bar_sync(1, kCompute);  // l_run is complete
+      if (w.runs == 1) {
+        if (tid < HD) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h) {
+            if (h >= w.heads) break;
+            const float o = w.seen.n ? oacc[h] / l_run[h] : 0.f;
+            const long long at = w.t * a.out_ld + (long long)(w.head0 + h) * HD + tid;
+            if (a.f32) static_cast<float*>(a.out)[at] = o;
+            else static_cast<uint16_t*>(a.out)[at] = round_bf16(o);
+          }
+        }
+      } else {
+        const size_t base = ((size_t)w.b * a.n_heads + w.head0) * lay.max_runs + w.run;
+        if (tid < HD) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h)
+            if (h < w.heads) part_o[(base + (size_t)h * lay.max_runs) * HD + tid] = oacc[h];
+        }
+        if (tid < w.heads) {
+          float mm = m_run[0];
+#pragma unroll
+          for (int h = 1; h < GT; ++h)
+            if (h == tid) mm = m_run[h];
+          part_ml[base + (size_t)tid * lay.max_runs] = make_float2(mm, l_run[tid]);
+        }
+      }
+      tc::named_bar_sync(1, kCompute);
+    }
+  }
+  // only now: the join's blocks, resident early, would take room from those that stream
+  pdl_launch();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+template <int HD, int GT>
+cudaError_t launch_gt(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& a, long long items, int num_sms,
+                      float* po, float2* pml, cudaStream_t s) {
+  using Sh = Shape<HD, GT>;
+  const cudaError_t rc = cudaFuncSetAttribute(k_decode_fp8<HD, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)Sh::kSmem);
+  if (rc != cudaSuccess) return rc;
+  const int most = Sh::kCtas * num_sms;
+  return launch_pdl(k_decode_fp8<HD, GT>, dim3((unsigned)(items < most ? items : most)), dim3(kCompute + 32), Sh::kSmem,
+                    s, tk, tv, a, po, pml);
+}
+
+template <int HD>
+cudaError_t launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& a, int num_sms, cudaStream_t s) {
+  const Layout lay = layout_of(a);
+  if (lay.max_runs > 1 && !a.ws) return cudaErrorInvalidValue;
+  const size_t n = (size_t)a.rows * a.n_heads * lay.max_runs;
+  float* po = reinterpret_cast<float*>(a.ws);
+  float2* pml = reinterpret_cast<float2*>(a.ws + n * HD * sizeof(float));
+  const long long items = (long long)a.rows * a.kv.n_kv_heads * lay.groups * lay.max_runs;
+  const int G = a.n_heads / a.kv.n_kv_heads;
+  const cudaError_t rc = G <= 1   ? launch_gt<HD, 1>(tk, tv, a, items, num_sms, po, pml, s)
+                         : G <= 2 ? launch_gt<HD, 2>(tk, tv, a, items, num_sms, po, pml, s)
+                         : G <= 4 ? launch_gt<HD, 4>(tk, tv, a, items, num_sms, po, pml, s)
+                                  : launch_gt<HD, 8>(tk, tv, a, items, num_sms, po, pml, s);
+  if (rc != cudaSuccess || lay.max_runs == 1) return rc;
+  return launch_pdl(k_paged_merge<HD, Attn>, dim3(a.n_heads, a.rows), dim3(128), 0, s, a, po, pml);
+}
+
+}  // namespace
+
+size_t decode_fp8_workspace(const Attn& a) {
+  const Layout lay = layout_of(a);
+  if (lay.max_runs == 1) return 0;
+  return (size_t)a.rows * a.n_heads * lay.max_runs * (a.kv.head_dim * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_decode_fp8(const Attn& a, int num_sms, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  if (!fp8_maps(a.kv, &tk, &tv)) return cudaErrorInvalidValue;
+  return a.kv.head_dim == 128 ? launch_hd<128>(tk, tv, a, num_sms, s) : launch_hd<64>(tk, tv, a, num_sms, s);
+}

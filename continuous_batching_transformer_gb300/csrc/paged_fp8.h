@@ -86,3 +86,6 @@ cudaError_t launch_read_fp8(const PagedReadFp8& a, cudaStream_t s);
 using PagedAttnFp8 = PagedAttnOn<PagedKvFp8>;
 size_t attn_fp8_workspace(const PagedAttnFp8& a);
 cudaError_t launch_attn_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s);
+// its two forms: one query token per row (max_q == 1), and ragged runs of them
+size_t decode_fp8_workspace(const PagedAttnFp8& a);
+cudaError_t launch_decode_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s);
