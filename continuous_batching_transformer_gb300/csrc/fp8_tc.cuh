@@ -18,12 +18,27 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// Instruction descriptor, kind::f16: fp16 A and B (both K-major), fp32 D, M x N
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 // K-major tile of 64- or 128-byte rows in the swizzle of that size, groups of 8 rows next to each other
 template <int ROW>
 __device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
   static_assert(ROW == 64 || ROW == 128, "rows of 64 or 128 bytes");
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(8 * ROW >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)(ROW == 64 ? 4 : 2) << 61;
+}
+// the same as two words: the high one is every tile's, the low one counts in 16-byte units and is moved by
+// additions
+template <int ROW>
+__device__ __forceinline__ uint32_t rows_lo(const void* p) {
+  return (uint32_t)sdesc_rows<ROW>(smem_u32(p));
+}
+template <int ROW>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t lo) {
+  constexpr uint32_t hi = (uint32_t)((8 * ROW >> 4) | 1 << 14) | (ROW == 64 ? 4u : 2u) << 29;
+  return (uint64_t)hi << 32 | lo;
 }
 // byte offset of (row, byte) in such a tile
 template <int ROW>

@@ -210,6 +210,15 @@ cudaError_t launch_paged_attn(const PagedAttn& a, int num_sms, cudaStream_t s) {
   return a.max_q > 1 ? launch_paged_prefill(a, num_sms, s) : launch_paged_decode(a, num_sms, s);
 }
 
+size_t attn_fp8_workspace(const PagedAttnFp8& a) {
+  return a.max_q == 1 ? decode_fp8_workspace(a) : prefill_fp8_workspace(a);
+}
+
+cudaError_t launch_attn_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s) {
+  if (attn_fp8_workspace(a) > a.ws_bytes) return cudaErrorInvalidValue;
+  return a.max_q > 1 ? launch_prefill_fp8(a, num_sms, s) : launch_decode_fp8(a, num_sms, s);
+}
+
 extern "C" cbt_status cbt_page_map(const cbt_page_map_args* a, void* stream) {
   if (!a) return CBT_ERR_NULL;
   if (a->rows < 0 || a->max_pages <= 0 || a->page_tokens <= 0 || a->n_pages <= 0 || a->max_tokens < 0)

@@ -89,3 +89,5 @@ cudaError_t launch_attn_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s);
 // its two forms: one query token per row (max_q == 1), and ragged runs of them
 size_t decode_fp8_workspace(const PagedAttnFp8& a);
 cudaError_t launch_decode_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s);
+size_t prefill_fp8_workspace(const PagedAttnFp8& a);
+cudaError_t launch_prefill_fp8(const PagedAttnFp8& a, int num_sms, cudaStream_t s);

@@ -1,0 +1,554 @@
+// paged_prefill_fp8.cu -- attention of ragged runs of query tokens over a paged cache in 8 bits.
+//
+// Units, tiles and steps are those of the kernel over bf16 pages (paged_prefill.cu, paged_tiles.cuh): two
+// tiles of 128 (token, q head) rows, steps of 64 keys.  Per step and tile
+//   S = Q K^T     K as the codes it is, Q as the sum of two tiles of codes (q has eight bits of mantissa, a
+//                 code four: exact down to 2^-10 of the row's largest element, off by at most 2^-18 of it
+//                 below), e4m3 at twice the rate of bf16: what a product of bf16 would take
+//   softmax       one thread per row
+//   O += P V      P as fp16 in tensor memory (2^-11 of each weight, 2^-31 of the largest or so), V turned
+//                 from codes to fp16 in shared memory, which is exact
+// The step is a scale's block, and scales are powers of two: K's multiplies the row's score unit, V's
+// exponent e is added to the scores, in units of log2: the weights are 2^(s + e - m) with m a whole number
+// near the largest s + e so far, and the sum takes a step's weights times 2^-e.
+//
+// The codes of K and V come through TMA into a ring of stages.  A warpgroup of its own turns V into fp16
+// (into a ring of its own), clearing keys that no query of the unit sees, and splits the units' Q; it
+// has the registers that requester and issuers do not need.
+#include "fp8_tc.cuh"
+#include "paged_tiles.cuh"
+
+namespace {
+
+using Attn = PagedAttnFp8;
+constexpr int kStages = 6;
+constexpr int kVSlots = 3;      // of V in fp16: two behind the newest scores, one being filled
+constexpr int kThreads = 512;   // warps: requester, issuer 0, issuer 1, idle; 4..7 and 8..11 softmax; 12..15
+// Registers of a thread of each warpgroup, out of kThreads times kRegs at launch
+constexpr int kRegs = 128, kRegsIssue = 72, kRegsSoftmax = 168, kRegsConvert = 104;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * kRegs, "registers");
+// A row's weights are below 2^kHead when its reference is set, and the reference is raised once they pass
+// 2^(kHead + kSlack): far from the largest fp16, 2^16, and small ones as far from the smallest
+constexpr float kHead = 6.f, kSlack = 9.f;
+constexpr int kExps = 16;       // steps whose exponents are kept: more than are under way
+
+// Shared memory: the tiles of Q, K and V, then this
+constexpr int kBars = 3 + 2 * kStages + 2 * kVSlots + 12;
+struct Tail {
+  uint64_t bars[kBars];
+  uint32_t tmem_slot;
+  int abort_flag;
+  int warp_sums[kThreads / 32];
+  int2 exps[kExps];            // of K's and V's scale
+  float row_unit[2][kRows];    // of each row's scores, in log2 units
+  Unit units[kUnits];
+};
+template <int HD>
+constexpr size_t smem_bytes() {  // 1024: the base is rounded up to the tiles' alignment
+  return 1024 + 4 * kRows * HD + kStages * 2 * kStep * HD + kVSlots * HD * 128 + sizeof(Tail);
+}
+static_assert(smem_bytes<128>() <= 227 * 1024, "shared memory");
+
+CBT_D uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prefill_fp8(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                  const __grid_constant__ Attn a, const int runs, const int most, float* __restrict__ part_o,
+                  float2* __restrict__ part_ml) {
+  constexpr uint32_t kPart = kRows * HD;     // one part of a Q tile
+  constexpr uint32_t kKV = kStep * HD;       // codes of K or V of a step
+  constexpr uint32_t kV16 = HD * 128;        // V of a step in fp16
+  constexpr uint32_t kIdescS = tc::idesc_e4m3(128, kStep), kIdescO = tc::idesc_f16(128, HD);
+  constexpr uint32_t kTmem = 512;  // S (P over it): tile x, buffer b at 128 x + 64 b; O: 256 + HD x
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem;                     // [tile][part][128 rows][HD]
+  uint8_t* sK = sQ + 4 * kPart;           // [stage][64 keys][HD]
+  uint8_t* sV = sK + kStages * kKV;       // [stage][HD dims][64 keys]
+  uint8_t* sV16 = sV + kStages * kKV;     // [slot][HD dims][64 keys]
+  Tail& tail = *reinterpret_cast<Tail*>(sV16 + kVSlots * kV16);
+  uint64_t* bars = tail.bars;
+  // Q of a tile is there, all are done with Q; a stage has landed, both tiles and the conversion are done
+  // with it; V in fp16 is there, both tiles are done with it
+  uint64_t *qfull = bars, *qempty = bars + 2, *full = bars + 3, *empty = full + kStages;
+  uint64_t *v_full = empty + kStages, *v_empty = v_full + kVSlots;
+  // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
+  uint64_t *s_full = v_empty + kVSlots, *p_full = s_full + 4, *pv_done = p_full + 4;
+  uint32_t* tmem_slot = &tail.tmem_slot;
+  volatile int* abort_flag = &tail.abort_flag;
+  Unit* units = tail.units;
+
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
+  const int TQ = kRows / G;  // tokens per tile
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&qfull[i], 4);            // the converting warps
+    tc::mbar_init(qempty, 2 + 8);                                       // issuers, softmax warps
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2 + 4);  // issuers, converting warps
+    for (int i = 0; i < kVSlots; ++i) {
+      tc::mbar_init(&v_full[i], 4);
+      tc::mbar_init(&v_empty[i], 2);
+    }
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);           // a tile's softmax warps
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::tma_prefetch_desc(&tk);
+    tc::tma_prefetch_desc(&tv);
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
+  pdl_wait();
+  static_assert(kScratch <= 4 * kPart, "the search fits where Q goes");
+  int count = find_units<kThreads>(a, units, sQ, tail.warp_sums, TQ, runs, most);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  count = uniform(count);
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  const int sinks = a.window ? a.sinks : 0;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0) {
+      // ---- tile requests.  The pages and scales of 32 steps are looked up at once, a lane each.
+      const uint64_t pol = tc::policy_evict_last();
+      const int P = a.kv.page_tokens;
+      int st = 0, n = 0;  // stage, steps requested
+      uint32_t ph = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; k < count && ok; ++k) {
+        const Work<Attn> w(units + k, a);
+        int kat = 0, vat = 0;
+        float ks = 0.f, vs = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < w.steps; ++i) {
+          if ((i & 31) == 0 && i + lane < w.steps) {
+            const int key = w.key(i + lane), pg = key / P, o = key - pg * P;
+            int id = a.table[(size_t)w.u.b * a.max_pages + pg];
+            if (id < 0 || id >= a.kv.n_pages) {
+              set_device_error(a.err, CBT_DEV_PAGE_ID, w.u.b);
+              id = 0;  // a page that exists: the row's outputs are unspecified
+            }
+            kat = (int)(fp8_k(a.kv, id, w.u.g, o, 0) >> 8);
+            vat = (int)(fp8_v(a.kv, id, w.u.g, o, 0) >> 8);
+            ks = *fp8_scale(a.kv, id, 0, w.u.g, o);
+            vs = *fp8_scale(a.kv, id, 1, w.u.g, o);
+          }
+          const int ka = __shfl_sync(0xffffffffu, kat, i & 31), va = __shfl_sync(0xffffffffu, vat, i & 31);
+          ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], ph ^ 1, abort_flag));
+          if (!ok) break;
+          if (elect_one()) {
+            tc::tma_load_rows(sK + st * kKV, &tk, &full[st], ka, pol);
+            tc::tma_load_rows(sV + st * kKV, &tv, &full[st], va, pol);
+          }
+          // (the bytes may land before they are expected: the phase waits for the arrival)
+          if (lane == (i & 31)) tail.exps[n & (kExps - 1)] = make_int2(fp8_exponent(ks), fp8_exponent(vs));
+          __syncwarp();
+          if (elect_one()) tc::mbar_expect_tx(&full[st], 2 * kKV);
+          ++n;
+          st = st + 1 == kStages ? 0 : st + 1;
+          ph ^= st == 0;
+        }
+      }
+      if (lane == 0) {
+        if (!ok) wait_timeout(a.err, abort_flag, 31);
+        // no copies in flight at exit
+#pragma unroll 1
+        for (int i = max(0, n - kStages); i < n; ++i) wait_landed(&full[i % kStages], (i / kStages) & 1);
+      }
+    } else if (warp <= 2) {
+      // ---- MMA issue of tile x: P V of the step kLag before, then S of the step into the buffer this
+      // freed.  So a step's scores are there before the softmax asks for them, and it never waits for
+      // its own P V.
+      const int x = warp - 1;
+      const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
+      const uint32_t dq = tc::rows_lo<HD>(sQ + x * 2 * kPart), dk = tc::rows_lo<HD>(sK), dv = tc::rows_lo<128>(sV16);
+      int st = 0, slot = 0;
+      uint32_t ph = 0, vp = 0, pp = 0, qp = 0;  // phases of stages, slots, p_full (bit b: buffer b) and Q
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; k < count && ok; ++k) {
+        const Work<Attn> w(units + k, a);
+        if (!w.stages) continue;
+        const TileKeys mine(w, a, x, TQ);
+        uint32_t took = 0;  // bit j: the tile took part in the step j before this one
+        uint32_t acc = 0;   // O holds something of this unit
+        ok = __all_sync(0xffffffffu, wait_or_abort(&qfull[x], qp, abort_flag));
+        qp ^= 1;
+#pragma unroll 1
+        for (int i = 0; i < w.stages && ok; ++i) {
+          const int b = i & 1;
+          const bool has_k = i < w.steps, has_v = i >= kLag;
+          const bool need = has_k && mine.need(w.key(i), sinks), due = took >> (kLag - 1) & 1;
+          if (has_k) ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
+          if (has_v) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&v_full[slot], vp, abort_flag));
+          if (due) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&p_full[2 * x + b], pp >> b & 1, abort_flag));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (elect_one()) {
+            if (due) {
+              const uint32_t v = dv + slot * (kV16 >> 4);
+#pragma unroll
+              for (int e = 0; e < kStep / 16; ++e)
+                tc::mma_bf16_ta(o_tm, s_tm + 64 * b + 8 * e, tc::rows_desc<128>(v + 2 * e), kIdescO,
+                                (acc || e > 0) ? 1u : 0u);
+              tc::mma_commit(&pv_done[2 * x + b]);
+            }
+            if (has_v) tc::mma_commit(&v_empty[slot]);
+            if (need) {
+              const uint32_t kd = dk + st * (kKV >> 4);
+#pragma unroll
+              for (int e = 0; e < 2 * (HD / 32); ++e) {
+                const int part = e / (HD / 32), step = e % (HD / 32);
+                tc::mma_e4m3(s_tm + 64 * b, tc::rows_desc<HD>(dq + part * (kPart >> 4) + 2 * step),
+                             tc::rows_desc<HD>(kd + 2 * step), kIdescS, e > 0 ? 1u : 0u);
+              }
+              tc::mma_commit(&s_full[2 * x + b]);
+            }
+            if (has_k) tc::mma_commit(&empty[st]);
+            if (i == w.steps - 1) tc::mma_commit(qempty);
+          }
+          if (due) {
+            pp ^= 1u << b;
+            acc = 1;
+          }
+          took = took << 1 | (need ? 1u : 0u);
+          if (has_v) {
+            slot = slot + 1 == kVSlots ? 0 : slot + 1;
+            vp ^= slot == 0;
+          }
+          if (has_k) {
+            st = st + 1 == kStages ? 0 : st + 1;
+            ph ^= st == 0;
+          }
+        }
+      }
+      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 32);
+    }
+  } else if (warp >= 12) {
+    // ---- Q into two parts of codes, V into fp16.  Thread = row of Q; of V, 16 keys of HD / 32 dims.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    const int row = tid - (kThreads - 128);
+    int st = 0, slot = 0;
+    uint32_t ph = 0, vp = 0, qp = 0;
+    bool ok = true;
+    const float scale2 = fabsf(a.scale) * kLog2e;
+#pragma unroll 1
+    for (int k = 0; k < count && ok; ++k) {
+      const Work<Attn> w(units + k, a);
+      if (!w.stages) continue;
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        const int tok = x * TQ + row / G;
+        const bool tile = x * TQ < w.u.n, live = row < TQ * G && tok < w.u.n;
+        uint32_t c[HD / 2];  // pairs of q; then, of every 8 elements, two words of codes of either part
+        float unit = 0.f;
+        if (tile) {
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.u.t0 + tok) * a.q_ld +
+                                                            (long long)(w.u.g * G + row % G) * HD);
+#pragma unroll
+          for (int j = 0; j < HD / 8; ++j) {
+            const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+            c[4 * j] = v.x;
+            c[4 * j + 1] = v.y;
+            c[4 * j + 2] = v.z;
+            c[4 * j + 3] = v.w;
+          }
+          uint32_t top = 0;  // largest magnitudes, as bf16
+#pragma unroll
+          for (int j = 0; j < HD / 2; ++j) top = __vmaxu2(top, c[j] & 0x7FFF7FFFu);
+          top = max(top >> 16, top & 0xFFFFu);
+          const bool finite = top < 0x7F80u;
+          const int fit = fit_exponent(bf16_lo(finite ? top : 0));
+          const float f = a.scale < 0.f ? -pow2_of(fit) : pow2_of(fit);  // the sign of the scale is q's
+          unit = scale2 * pow2_of(-fit);
+#pragma unroll
+          for (int j = 0; j < HD / 8; ++j) {
+            uint32_t part[2][2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y0 = bf16_lo(c[4 * j + e]) * f, y1 = bf16_hi(c[4 * j + e]) * f;
+              const uint16_t hi = pack_e4m3(y0, y1);
+              const uint32_t back = e4m3_to_f16(hi);
+              const uint16_t lo = pack_e4m3(y0 - f16_lo(back), y1 - f16_hi(back));
+              part[0][e >> 1] = e & 1 ? part[0][e >> 1] | (uint32_t)hi << 16 : hi;
+              part[1][e >> 1] = e & 1 ? part[1][e >> 1] | (uint32_t)lo << 16 : lo;
+            }
+            c[4 * j] = part[0][0];
+            c[4 * j + 1] = part[0][1];
+            c[4 * j + 2] = part[1][0];
+            c[4 * j + 3] = part[1][1];
+          }
+          if (!finite) {  // its scores are not numbers
+#pragma unroll
+            for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
+          }
+        }
+        if (x == 0) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
+          qp ^= 1;
+          if (!ok) break;
+        }
+        if (tile) {
+          uint8_t* q = sQ + x * 2 * kPart;
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int j = 0; j < HD / 16; ++j)
+              *reinterpret_cast<uint4*>(q + p * kPart + tc::swz<HD>(row, 16 * j)) =
+                  make_uint4(c[8 * j + 2 * p], c[8 * j + 2 * p + 1], c[8 * j + 4 + 2 * p], c[8 * j + 5 + 2 * p]);
+          tail.row_unit[x][row] = unit;
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&qfull[x]);
+      }
+#pragma unroll 1
+      for (int i = 0; i < w.steps && ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
+        if (!ok) break;
+        const uint8_t* v = sV + st * kKV;
+        uint4 in[HD / 32];
+#pragma unroll
+        for (int j = 0; j < HD / 32; ++j)
+          in[j] = *reinterpret_cast<const uint4*>(v + tc::swz<64>((row >> 2) + 32 * j, 16 * (row & 3)));
+        uint32_t bits[2];
+        seen_bits(w.key(i), w.pl, w.lo_win, sinks, bits);
+        if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {  // keys that no query of the unit sees
+          const uint4 m = code_mask((row & 2 ? bits[1] : bits[0]) >> (16 * (row & 1)));
+#pragma unroll
+          for (int j = 0; j < HD / 32; ++j)
+            in[j] = make_uint4(in[j].x & m.x, in[j].y & m.y, in[j].z & m.z, in[j].w & m.w);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty[st]);
+        ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[slot], vp ^ 1, abort_flag));
+        if (!ok) break;
+        uint8_t* out = sV16 + slot * kV16;
+#pragma unroll
+        for (int j = 0; j < HD / 32; ++j) {
+          const uint32_t u[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint4*>(out + tc::swz<128>((row >> 2) + 32 * j, 32 * (row & 3) + 16 * e)) =
+                make_uint4(e4m3_to_f16((uint16_t)u[2 * e]), e4m3_to_f16((uint16_t)(u[2 * e] >> 16)),
+                           e4m3_to_f16((uint16_t)u[2 * e + 1]), e4m3_to_f16((uint16_t)(u[2 * e + 1] >> 16)));
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&v_full[slot]);
+        slot = slot + 1 == kVSlots ? 0 : slot + 1;
+        vp ^= slot == 0;
+        st = st + 1 == kStages ? 0 : st + 1;
+        ph ^= st == 0;
+      }
+    }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 33);
+  } else {
+    // ---- softmax of tile x: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + x * 128 + lane_off, o_tm = tmem + 256 + x * HD + lane_off;
+    uint32_t sp = 0, qp = 0;  // phases of s_full to come (bit b: buffer b) and of Q
+    int n = 0;                // steps of the units before
+    bool ok = true;
+    // rows of out on 32-byte boundaries: whole sectors a store
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.out_ld % (a.f32 ? 8 : 16) == 0;
+#pragma unroll 1
+    for (int unit = 0; unit < count && ok; ++unit) {
+      const Work<Attn> w(units + unit, a);
+      const TileKeys mine(w, a, x, TQ);
+      const int tok = x * TQ + row / G;  // token of the unit
+      const bool live = row < TQ * G && tok < w.u.n;
+      const int p = live ? w.u.p0 + tok : -1;  // -1: sees nothing
+      // rows that hold no token are left unmasked: what they compute is not stored
+      const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
+      float m = -INFINITY, l = 0.f;  // the reference (near the largest so far, a whole number) and the sum
+      int done = -1;                 // the last step done
+      float row_unit = 0.f;
+      if (w.stages) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&qfull[x], qp, abort_flag));
+        if (!ok) break;
+        qp ^= 1;
+        row_unit = tail.row_unit[x][row];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(qempty);
+      }
+#pragma unroll 1
+      for (int i = 0; i < w.steps && ok; ++i) {
+        const int k0 = w.key(i);
+        if (!mine.need(k0, sinks)) continue;
+        const int b = i & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
+        if (!ok) break;
+        sp ^= 1u << b;
+        tc::tc_fence_after();
+        const int2 exps = tail.exps[(n + i) & (kExps - 1)];
+        uint32_t s[64];
+        tmem_ld32(s_tm + 64 * b, s);
+        tmem_ld32(s_tm + 64 * b + 32, s + 32);
+        // a score's unit (kept where a masked -inf stays -inf and a zero is one) and the addition to it
+        const float cs = fminf(fmaxf(row_unit * pow2_of(exps.x), 1e-37f), 3e38f), ve = (float)exps.y;
+        tc::tmem_ld_wait();
+        // every row sees every key of the step, or keys are masked one by one
+        if (!__all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64))) {
+          uint32_t bits[2];
+          seen_bits(k0, hi, lo, sinks, bits);
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((bits[e >> 5] >> (e & 31)) & 1)) s[e] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        const float top = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), cs, ve);
+        const bool up = m == -INFINITY ? top > -INFINITY : top > m + (kHead + kSlack);
+        if (__any_sync(0xffffffffu, up)) {
+          // Rows that exceed their reference, or see their first keys, raise it, to a whole number: what
+          // the old one has scaled is multiplied by a power of two, which rounds nothing.
+          const float next = up ? ceilf(top) - kHead : m;
+          const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
+          m = next;
+          l *= f;
+          if (done >= 0) {
+            // O is at rest once the last step's product is in it (S of this step, there already, was
+            // issued after those before)
+            const int d = done & 1;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ (d != b), abort_flag));
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_tm + d, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_tm + d, o);
+            }
+          }
+        }
+        const float add = ve - (m == -INFINITY ? 0.f : m);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), cs, add));
+          const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), cs, add));
+          part[e & 3] += p0;
+          part[(e + 2) & 3] += p1;
+          s[e] = pack_f16(p0, p1);
+        }
+        tc::tmem_st32(s_tm + 64 * b, s);  // over the scores
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
+        l = fmaf((part[0] + part[1]) + (part[2] + part[3]), pow2_of(-exps.y), l);
+        done = i;
+      }
+      n += w.steps;
+      // The row goes straight out.  O is not written again before this tile hands in weights of the next
+      // unit.
+      if (ok && done >= 0) {
+        const int d = done & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ 1, abort_flag));
+        tc::tc_fence_after();
+      }
+      if (!ok) break;
+      // a run of several hands over O as it is, with its reference and sum
+      const int head = w.u.g * G + row % G;
+      const size_t part = ((size_t)(w.u.t0 + tok) * H + head) * runs + units[unit].run;
+      const float inv = runs > 1 ? 1.f : p >= 0 ? 1.f / l : 0.f;
+      if (runs > 1 && live) part_ml[part] = make_float2(m, l);
+      const long long at = (long long)(w.u.t0 + tok) * a.out_ld + (long long)head * HD;
+#pragma unroll 1
+      for (int k = 0; k < HD; k += 16) {
+        uint32_t o[16];
+        if (done >= 0) {
+          tc::tmem_ld16(o_tm + k, o);
+          tc::tmem_ld_wait();
+        }
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = p >= 0 ? __uint_as_float(o[e]) * inv : 0.f;
+        if (!live) continue;
+        if (a.f32 || runs > 1) {
+          float* dst = runs > 1 ? part_o + part * HD + k : static_cast<float*>(a.out) + at + k;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = __float_as_uint(v[e + j]);
+            store32(dst + e, h, wide || runs > 1);
+          }
+        } else {
+          uint32_t h[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          store32(static_cast<uint16_t*>(a.out) + at + k, h, wide);
+        }
+      }
+      tc::tc_fence_before();
+    }
+    if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 34);
+    tc::tc_fence_before();
+  }
+  pdl_launch();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmem);
+  }
+}
+
+template <int HD>
+cudaError_t launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& a, int num_sms, cudaStream_t s) {
+  constexpr size_t smem = smem_bytes<HD>();
+  cudaError_t rc = cudaFuncSetAttribute(k_prefill_fp8<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (rc != cudaSuccess) return rc;
+  // the warpgroups' shares come out of what a block is launched with: with less the kernel would wait
+  cudaFuncAttributes attr;
+  rc = cudaFuncGetAttributes(&attr, k_prefill_fp8<HD>);
+  if (rc != cudaSuccess) return rc;
+  if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;
+  const int G = a.n_heads / a.kv.n_kv_heads, run = 2 * (kRows / G);
+  // most units: every row may end in a partly filled one
+  const long long by_tokens = (long long)a.tokens / run + a.rows;
+  const long long by_rows = (long long)a.rows * ((a.max_q + run - 1) / run);
+  const long long units = by_tokens < by_rows ? by_tokens : by_rows;
+  const int runs = runs_for(a);
+  const long long items = units * a.kv.n_kv_heads * runs, least = (items + kUnits - 1) / kUnits;
+  const long long grid = items < num_sms ? items : least > num_sms ? least : num_sms;
+  float* po = reinterpret_cast<float*>(a.ws);
+  const size_t parts = (size_t)a.tokens * a.n_heads * runs;
+  float2* pml = reinterpret_cast<float2*>(a.ws + parts * HD * sizeof(float));
+  rc = launch_pdl(k_prefill_fp8<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tk, tv, a, runs, (int)units, po,
+                  pml);
+  if (rc != cudaSuccess || runs == 1) return rc;
+  const long long pairs = (long long)a.tokens * a.n_heads;
+  if (pairs <= kFewPairs && runs > kManyRuns)
+    return launch_pdl(k_prefill_merge<HD, 4, Attn>, dim3((unsigned)pairs), dim3(128), 0, s, a, runs, po, pml);
+  return launch_pdl(k_prefill_merge<HD, 1, Attn>, dim3((unsigned)((pairs + 3) / 4)), dim3(128), 0, s, a, runs, po, pml);
+}
+
+}  // namespace
+
+size_t prefill_fp8_workspace(const Attn& a) {
+  const int runs = runs_for(a);
+  return runs == 1 ? 0 : (size_t)a.tokens * a.n_heads * runs * (a.kv.head_dim * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_prefill_fp8(const Attn& a, int num_sms, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  if (!fp8_maps(a.kv, &tk, &tv)) return cudaErrorInvalidValue;
+  return a.kv.head_dim == 128 ? launch_hd<128>(tk, tv, a, num_sms, s) : launch_hd<64>(tk, tv, a, num_sms, s);
+}
