@@ -22,15 +22,16 @@ namespace {
 
 using Attn = PagedAttnFp8;
 constexpr int kStages = 6;
-constexpr int kVSlots = 3;      // of V in fp16: two behind the newest scores, one being filled
-constexpr int kThreads = 512;   // warps: requester, issuer 0, issuer 1, idle; 4..7 and 8..11 softmax; 12..15
-// Registers of a thread of each warpgroup, out of kThreads times kRegs at launch
-constexpr int kRegs = 128, kRegsIssue = 72, kRegsSoftmax = 168, kRegsConvert = 104;
+constexpr int kVSlots = 3;      // of V in fp16
+// warps: issuers of S of tile 0, S of tile 1 and P V of both, requester of tiles; 4..7 and 8..11 softmax;
+// 12..15 conversion
+constexpr int kThreads = 512;
+// Registers of a thread of the four warpgroups, out of what a block's threads have at launch (kRegs each)
+constexpr int kRegs = 128, kRegsIssue = 64, kRegsSoftmax = 168, kRegsConvert = 112;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * kRegs, "registers");
 // A row's weights are below 2^kHead when its reference is set, and the reference is raised once they pass
 // 2^(kHead + kSlack): far from the largest fp16, 2^16, and small ones as far from the smallest
 constexpr float kHead = 6.f, kSlack = 9.f;
-constexpr int kExps = 16;       // steps whose exponents are kept: more than are under way
 
 // Shared memory: the tiles of Q, K and V, then this
 constexpr int kBars = 3 + 2 * kStages + 2 * kVSlots + 12;
@@ -39,7 +40,8 @@ struct Tail {
   uint32_t tmem_slot;
   int abort_flag;
   int warp_sums[kThreads / 32];
-  int2 exps[kExps];            // of K's and V's scale
+  int2 exps[kStages];          // of K's and V's scale of a stage's step
+  int2 s_exps[2][2];           // [tile]: of its last steps
   float row_unit[2][kRows];    // of each row's scores, in log2 units
   Unit units[kUnits];
 };
@@ -49,10 +51,53 @@ constexpr size_t smem_bytes() {  // 1024: the base is rounded up to the tiles' a
 }
 static_assert(smem_bytes<128>() <= 227 * 1024, "shared memory");
 
+// every key of the step from k0 on is seen, by queries up to hi whose windows start at lo
+CBT_D bool sees_all(int k0, int hi, int lo, int sinks) {
+  return k0 + kStep - 1 <= hi && (lo <= k0 || sinks >= k0 + kStep);
+}
+// The steps of an item that tile x of its unit takes part in: those before `end`, without [hole0, hole1)
+// (behind the sinks, before the window of the tile's first token)
+struct TileSteps {
+  int end, hole0, hole1;
+  CBT_D TileSteps(const Work<Attn>& w, const Attn& a, int x, int TQ, int sinks) {
+    const TileKeys t(w, a, x, TQ);
+    const int last = t.last >= 0 ? t.last / kStep : -1, lo = t.lo / kStep, sink = (sinks + kStep - 1) / kStep;
+    const Seen& s = w.seen;
+    end = min(s.ns, last + 1) + max(0, last - s.ws + 1) - w.u.s0;
+    hole0 = s.ns + max(0, sink - s.ws) - w.u.s0;
+    hole1 = s.ns + lo - s.ws - w.u.s0;
+  }
+  CBT_D bool need(int i) const { return i < end && !(i >= hole0 && i < hole1); }
+};
+
 CBT_D uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+CBT_D uint16_t f16_to_e4m3(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+CBT_D uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// a * b + c and a + b on two numbers, one instruction
+CBT_D void fma2(float& x, float& y, float a, float b, float2 m, float2 c) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n mov.b64 r, {%6, %7};\n"
+      " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(m.x), "f"(m.y), "f"(c.x), "f"(c.y));
+}
+CBT_D void add2(float2& s, float a, float b) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n"
+      " mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(s.x), "+f"(s.y)
+      : "f"(a), "f"(b));
 }
 
 template <int HD>
@@ -64,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kKV = kStep * HD;       // codes of K or V of a step
   constexpr uint32_t kV16 = HD * 128;        // V of a step in fp16
   constexpr uint32_t kIdescS = tc::idesc_e4m3(128, kStep), kIdescO = tc::idesc_f16(128, HD);
-  constexpr uint32_t kTmem = 512;  // S (P over it): tile x, buffer b at 128 x + 64 b; O: 256 + HD x
+  constexpr uint32_t kTmem = 512;  // tile x: S at 128 x, P of buffer b at 128 x + 64 + 32 b; O: 256 + HD x
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -78,8 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // with it; V in fp16 is there, both tiles are done with it
   uint64_t *qfull = bars, *qempty = bars + 2, *full = bars + 3, *empty = full + kStages;
   uint64_t *v_full = empty + kStages, *v_empty = v_full + kVSlots;
-  // [tile][buffer]: S is there, P is there, P has been read (and its product is in O)
-  uint64_t *s_full = v_empty + kVSlots, *p_full = s_full + 4, *pv_done = p_full + 4;
+  // [tile]: S is there, S has been taken; [tile][buffer]: P is there, P has been read (and its product is
+  // in O)
+  uint64_t *s_full = v_empty + kVSlots, *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 4;
   uint32_t* tmem_slot = &tail.tmem_slot;
   volatile int* abort_flag = &tail.abort_flag;
   Unit* units = tail.units;
@@ -92,11 +138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) tc::mbar_init(&qfull[i], 4);            // the converting warps
     tc::mbar_init(qempty, 2 + 8);                                       // issuers, softmax warps
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2 + 4);  // issuers, converting warps
-    for (int i = 0; i < kVSlots; ++i) {
-      tc::mbar_init(&v_full[i], 4);
-      tc::mbar_init(&v_empty[i], 2);
-    }
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);           // a tile's softmax warps
+    for (int i = 0; i < kVSlots; ++i) tc::mbar_init(&v_full[i], 4);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&s_free[i], 4);           // a tile's softmax warps
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tk);
@@ -115,13 +159,104 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0) {
+    bool ok = true;
+    if (warp < 2) {
+      // ---- S of tile x, as soon as the softmax has taken the last one
+      const int x = warp;
+      const uint32_t s_tm = tmem + x * 128;
+      const uint32_t dq = tc::rows_lo<HD>(sQ + x * 2 * kPart), dk = tc::rows_lo<HD>(sK);
+      int st = 0, n = 0;  // stage, steps that the tile took part in
+      uint32_t ph = 0, qp = 0;
+#pragma unroll 1
+      for (int k = 0; k < count && ok; ++k) {
+        const Work<Attn> w(units + k, a);
+        if (!w.steps) continue;
+        const TileSteps mine(w, a, x, TQ, sinks);
+        ok = __all_sync(0xffffffffu, wait_or_abort(&qfull[x], qp, abort_flag));
+        if (!ok) break;
+        qp ^= 1;
+#pragma unroll 1
+        for (int i = 0; i < w.steps; ++i) {
+          const bool need = mine.need(i);
+          // K has landed; S has been taken; P of the step two before has been read, so that the softmax may
+          // write there again
+          bool got = wait_or_abort(&full[st], ph, abort_flag);
+          if (need)
+            got = got && wait_or_abort(&pv_done[2 * x + (n & 1)], (n >> 1 & 1) ^ 1, abort_flag) &&
+                  wait_or_abort(&s_free[x], (n & 1) ^ 1, abort_flag);
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const int2 exps = tail.exps[st];
+          if (elect_one()) {
+            if (need) {
+              const uint32_t kd = dk + st * (kKV >> 4);
+#pragma unroll
+              for (int e = 0; e < 2 * (HD / 32); ++e) {
+                const int part = e / (HD / 32), step = e % (HD / 32);
+                tc::mma_e4m3(s_tm, tc::rows_desc<HD>(dq + part * (kPart >> 4) + 2 * step),
+                             tc::rows_desc<HD>(kd + 2 * step), kIdescS, e > 0 ? 1u : 0u);
+              }
+              tail.s_exps[x][n & 1] = exps;
+              tc::mma_commit(&s_full[x]);
+            }
+            tc::mma_commit(&empty[st]);
+            if (i == w.steps - 1) tc::mma_commit(qempty);
+          }
+          n += need;
+          st = st + 1 == kStages ? 0 : st + 1;
+          ph ^= st == 0;
+        }
+      }
+      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 32);
+    } else if (warp == 2) {
+      // ---- P V of both tiles
+      const uint32_t dv = tc::rows_lo<128>(sV16);
+      int slot = 0, n[2] = {0, 0};
+      uint32_t vp = 0;
+#pragma unroll 1
+      for (int k = 0; k < count && ok; ++k) {
+        const Work<Attn> w(units + k, a);
+        const TileSteps tile[2] = {TileSteps(w, a, 0, TQ, sinks), TileSteps(w, a, 1, TQ, sinks)};
+        uint32_t acc[2] = {0, 0};  // O holds something of this unit
+#pragma unroll 1
+        for (int i = 0; i < w.steps && ok; ++i) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bool need = tile[x].need(i);
+            const int b = n[x] & 1;
+            if (x == 0 || need) {
+              bool got = x > 0 || wait_or_abort(&v_full[slot], vp, abort_flag);
+              if (need) got = got && wait_or_abort(&p_full[2 * x + b], n[x] >> 1 & 1, abort_flag);
+              ok = __all_sync(0xffffffffu, got);
+              if (!ok) break;
+              tc::tc_fence_after();
+            }
+            if (need && elect_one()) {
+              const uint32_t v = dv + slot * (kV16 >> 4);
+#pragma unroll
+              for (int e = 0; e < kStep / 16; ++e)
+                tc::mma_bf16_ta(tmem + 256 + x * HD, tmem + 128 * x + 64 + 32 * b + 8 * e, tc::rows_desc<128>(v + 2 * e),
+                                kIdescO, (acc[x] || e > 0) ? 1u : 0u);
+              tc::mma_commit(&pv_done[2 * x + b]);
+            }
+            if (need) {
+              acc[x] = 1;
+              ++n[x];
+            }
+          }
+          if (ok && elect_one()) tc::mma_commit(&v_empty[slot]);
+          slot = slot + 1 == kVSlots ? 0 : slot + 1;
+          vp ^= slot == 0;
+        }
+      }
+      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 35);
+    } else {
       // ---- tile requests.  The pages and scales of 32 steps are looked up at once, a lane each.
       const uint64_t pol = tc::policy_evict_last();
       const int P = a.kv.page_tokens;
       int st = 0, n = 0;  // stage, steps requested
       uint32_t ph = 0;
-      bool ok = true;
 #pragma unroll 1
       for (int k = 0; k < count && ok; ++k) {
         const Work<Attn> w(units + k, a);
@@ -149,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tma_load_rows(sV + st * kKV, &tv, &full[st], va, pol);
           }
           // (the bytes may land before they are expected: the phase waits for the arrival)
-          if (lane == (i & 31)) tail.exps[n & (kExps - 1)] = make_int2(fp8_exponent(ks), fp8_exponent(vs));
+          if (lane == (i & 31)) tail.exps[st] = make_int2(fp8_exponent(ks), fp8_exponent(vs));
           __syncwarp();
           if (elect_one()) tc::mbar_expect_tx(&full[st], 2 * kKV);
           ++n;
@@ -163,140 +298,82 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = max(0, n - kStages); i < n; ++i) wait_landed(&full[i % kStages], (i / kStages) & 1);
       }
-    } else if (warp <= 2) {
-      // ---- MMA issue of tile x: P V of the step kLag before, then S of the step into the buffer this
-      // freed.  So a step's scores are there before the softmax asks for them, and it never waits for
-      // its own P V.
-      const int x = warp - 1;
-      const uint32_t s_tm = tmem + x * 128, o_tm = tmem + 256 + x * HD;
-      const uint32_t dq = tc::rows_lo<HD>(sQ + x * 2 * kPart), dk = tc::rows_lo<HD>(sK), dv = tc::rows_lo<128>(sV16);
-      int st = 0, slot = 0;
-      uint32_t ph = 0, vp = 0, pp = 0, qp = 0;  // phases of stages, slots, p_full (bit b: buffer b) and Q
-      bool ok = true;
-#pragma unroll 1
-      for (int k = 0; k < count && ok; ++k) {
-        const Work<Attn> w(units + k, a);
-        if (!w.stages) continue;
-        const TileKeys mine(w, a, x, TQ);
-        uint32_t took = 0;  // bit j: the tile took part in the step j before this one
-        uint32_t acc = 0;   // O holds something of this unit
-        ok = __all_sync(0xffffffffu, wait_or_abort(&qfull[x], qp, abort_flag));
-        qp ^= 1;
-#pragma unroll 1
-        for (int i = 0; i < w.stages && ok; ++i) {
-          const int b = i & 1;
-          const bool has_k = i < w.steps, has_v = i >= kLag;
-          const bool need = has_k && mine.need(w.key(i), sinks), due = took >> (kLag - 1) & 1;
-          if (has_k) ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
-          if (has_v) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&v_full[slot], vp, abort_flag));
-          if (due) ok = ok && __all_sync(0xffffffffu, wait_or_abort(&p_full[2 * x + b], pp >> b & 1, abort_flag));
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (elect_one()) {
-            if (due) {
-              const uint32_t v = dv + slot * (kV16 >> 4);
-#pragma unroll
-              for (int e = 0; e < kStep / 16; ++e)
-                tc::mma_bf16_ta(o_tm, s_tm + 64 * b + 8 * e, tc::rows_desc<128>(v + 2 * e), kIdescO,
-                                (acc || e > 0) ? 1u : 0u);
-              tc::mma_commit(&pv_done[2 * x + b]);
-            }
-            if (has_v) tc::mma_commit(&v_empty[slot]);
-            if (need) {
-              const uint32_t kd = dk + st * (kKV >> 4);
-#pragma unroll
-              for (int e = 0; e < 2 * (HD / 32); ++e) {
-                const int part = e / (HD / 32), step = e % (HD / 32);
-                tc::mma_e4m3(s_tm + 64 * b, tc::rows_desc<HD>(dq + part * (kPart >> 4) + 2 * step),
-                             tc::rows_desc<HD>(kd + 2 * step), kIdescS, e > 0 ? 1u : 0u);
-              }
-              tc::mma_commit(&s_full[2 * x + b]);
-            }
-            if (has_k) tc::mma_commit(&empty[st]);
-            if (i == w.steps - 1) tc::mma_commit(qempty);
-          }
-          if (due) {
-            pp ^= 1u << b;
-            acc = 1;
-          }
-          took = took << 1 | (need ? 1u : 0u);
-          if (has_v) {
-            slot = slot + 1 == kVSlots ? 0 : slot + 1;
-            vp ^= slot == 0;
-          }
-          if (has_k) {
-            st = st + 1 == kStages ? 0 : st + 1;
-            ph ^= st == 0;
-          }
-        }
-      }
-      if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 32);
     }
   } else if (warp >= 12) {
     // ---- Q into two parts of codes, V into fp16.  Thread = row of Q; of V, 16 keys of HD / 32 dims.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    const int row = tid - (kThreads - 128);
+    const int row = tid - 384;
     int st = 0, slot = 0;
     uint32_t ph = 0, vp = 0, qp = 0;
     bool ok = true;
     const float scale2 = fabsf(a.scale) * kLog2e;
+    // A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part.  The
+    // next unit's first tile is fetched and split while the last steps of this one run.
+    uint32_t c[HD / 2];
+    float unit = 0.f;
+    bool ahead = false;  // c holds the unit's first tile
+    auto fetch = [&](const Work<Attn>& w, int x) {
+      const int tok = x * TQ + row / G;
+      const bool live = row < TQ * G && tok < w.u.n;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.u.t0 + tok) * a.q_ld +
+                                                        (long long)(w.u.g * G + row % G) * HD);
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j) {
+        const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        c[4 * j] = v.x;
+        c[4 * j + 1] = v.y;
+        c[4 * j + 2] = v.z;
+        c[4 * j + 3] = v.w;
+      }
+    };
+    auto split = [&]() {
+      uint32_t top = 0;  // largest magnitudes, as bf16
+#pragma unroll
+      for (int j = 0; j < HD / 2; ++j) top = __vmaxu2(top, c[j] & 0x7FFF7FFFu);
+      top = max(top >> 16, top & 0xFFFFu);
+      const bool finite = top < 0x7F80u;
+      const int fit = fit_exponent(bf16_lo(finite ? top : 0));
+      const float f = a.scale < 0.f ? -pow2_of(fit) : pow2_of(fit);  // the sign of the scale is q's
+      unit = scale2 * pow2_of(-fit);
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j) {
+        uint32_t part[2][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // in fp16 from here, which the scaled element's eight bits fit
+          const uint32_t y = pack_f16(bf16_lo(c[4 * j + e]) * f, bf16_hi(c[4 * j + e]) * f);
+          const uint16_t hi = f16_to_e4m3(y), lo = f16_to_e4m3(sub_f16(y, e4m3_to_f16(hi)));
+          part[0][e >> 1] = e & 1 ? part[0][e >> 1] | (uint32_t)hi << 16 : hi;
+          part[1][e >> 1] = e & 1 ? part[1][e >> 1] | (uint32_t)lo << 16 : lo;
+        }
+        c[4 * j] = part[0][0];
+        c[4 * j + 1] = part[0][1];
+        c[4 * j + 2] = part[1][0];
+        c[4 * j + 3] = part[1][1];
+      }
+      if (!finite) {  // its scores are not numbers
+#pragma unroll
+        for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
+      }
+    };
 #pragma unroll 1
     for (int k = 0; k < count && ok; ++k) {
       const Work<Attn> w(units + k, a);
-      if (!w.stages) continue;
+      if (!w.steps) continue;
+      if (!ahead) {
+        fetch(w, 0);
+        split();
+      }
+      ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
+      if (!ok) break;
+      qp ^= 1;
 #pragma unroll 1
-      for (int x = 0; x < 2 && ok; ++x) {
-        const int tok = x * TQ + row / G;
-        const bool tile = x * TQ < w.u.n, live = row < TQ * G && tok < w.u.n;
-        uint32_t c[HD / 2];  // pairs of q; then, of every 8 elements, two words of codes of either part
-        float unit = 0.f;
-        if (tile) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.u.t0 + tok) * a.q_ld +
-                                                            (long long)(w.u.g * G + row % G) * HD);
-#pragma unroll
-          for (int j = 0; j < HD / 8; ++j) {
-            const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-            c[4 * j] = v.x;
-            c[4 * j + 1] = v.y;
-            c[4 * j + 2] = v.z;
-            c[4 * j + 3] = v.w;
+      for (int x = 0; x < 2; ++x) {
+        if (x * TQ < w.u.n) {
+          if (x) {
+            fetch(w, 1);
+            split();
           }
-          uint32_t top = 0;  // largest magnitudes, as bf16
-#pragma unroll
-          for (int j = 0; j < HD / 2; ++j) top = __vmaxu2(top, c[j] & 0x7FFF7FFFu);
-          top = max(top >> 16, top & 0xFFFFu);
-          const bool finite = top < 0x7F80u;
-          const int fit = fit_exponent(bf16_lo(finite ? top : 0));
-          const float f = a.scale < 0.f ? -pow2_of(fit) : pow2_of(fit);  // the sign of the scale is q's
-          unit = scale2 * pow2_of(-fit);
-#pragma unroll
-          for (int j = 0; j < HD / 8; ++j) {
-            uint32_t part[2][2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y0 = bf16_lo(c[4 * j + e]) * f, y1 = bf16_hi(c[4 * j + e]) * f;
-              const uint16_t hi = pack_e4m3(y0, y1);
-              const uint32_t back = e4m3_to_f16(hi);
-              const uint16_t lo = pack_e4m3(y0 - f16_lo(back), y1 - f16_hi(back));
-              part[0][e >> 1] = e & 1 ? part[0][e >> 1] | (uint32_t)hi << 16 : hi;
-              part[1][e >> 1] = e & 1 ? part[1][e >> 1] | (uint32_t)lo << 16 : lo;
-            }
-            c[4 * j] = part[0][0];
-            c[4 * j + 1] = part[0][1];
-            c[4 * j + 2] = part[1][0];
-            c[4 * j + 3] = part[1][1];
-          }
-          if (!finite) {  // its scores are not numbers
-#pragma unroll
-            for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
-          }
-        }
-        if (x == 0) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
-          qp ^= 1;
-          if (!ok) break;
-        }
-        if (tile) {
           uint8_t* q = sQ + x * 2 * kPart;
 #pragma unroll
           for (int p = 0; p < 2; ++p)
@@ -310,18 +387,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&qfull[x]);
       }
+      const Work<Attn> next(units + min(k + 1, count - 1), a);
+      ahead = k + 1 < count && next.steps;
+      const int fetch_at = ahead ? max(0, w.steps - 4) : w.steps, split_at = min(fetch_at + 1, w.steps - 1);
 #pragma unroll 1
       for (int i = 0; i < w.steps && ok; ++i) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag));
+        // the step has landed, and its slot is free again
+        ok = __all_sync(0xffffffffu, wait_or_abort(&full[st], ph, abort_flag) &&
+                                         wait_or_abort(&v_empty[slot], vp ^ 1, abort_flag));
         if (!ok) break;
         const uint8_t* v = sV + st * kKV;
         uint4 in[HD / 32];
 #pragma unroll
         for (int j = 0; j < HD / 32; ++j)
           in[j] = *reinterpret_cast<const uint4*>(v + tc::swz<64>((row >> 2) + 32 * j, 16 * (row & 3)));
-        uint32_t bits[2];
-        seen_bits(w.key(i), w.pl, w.lo_win, sinks, bits);
-        if ((bits[0] & bits[1]) != 0xFFFFFFFFu) {  // keys that no query of the unit sees
+        const int k0 = w.key(i);
+        if (!sees_all(k0, w.pl, w.lo_win, sinks)) {  // keys that no query of the unit sees
+          uint32_t bits[2];
+          seen_bits(k0, w.pl, w.lo_win, sinks, bits);
           const uint4 m = code_mask((row & 2 ? bits[1] : bits[0]) >> (16 * (row & 1)));
 #pragma unroll
           for (int j = 0; j < HD / 32; ++j)
@@ -329,8 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&empty[st]);
-        ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[slot], vp ^ 1, abort_flag));
-        if (!ok) break;
         uint8_t* out = sV16 + slot * kV16;
 #pragma unroll
         for (int j = 0; j < HD / 32; ++j) {
@@ -348,6 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         vp ^= slot == 0;
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0;
+        if (i == fetch_at) fetch(next, 0);
+        if (i == split_at && ahead) split();
       }
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 33);
@@ -357,24 +440,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tmem + x * 128 + lane_off, o_tm = tmem + 256 + x * HD + lane_off;
-    uint32_t sp = 0, qp = 0;  // phases of s_full to come (bit b: buffer b) and of Q
-    int n = 0;                // steps of the units before
+    uint32_t qp = 0;  // phase of Q
+    int done = 0;     // steps that the tile took part in
     bool ok = true;
     // rows of out on 32-byte boundaries: whole sectors a store
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.out_ld % (a.f32 ? 8 : 16) == 0;
 #pragma unroll 1
     for (int unit = 0; unit < count && ok; ++unit) {
       const Work<Attn> w(units + unit, a);
-      const TileKeys mine(w, a, x, TQ);
+      const TileSteps mine(w, a, x, TQ, sinks);
       const int tok = x * TQ + row / G;  // token of the unit
       const bool live = row < TQ * G && tok < w.u.n;
       const int p = live ? w.u.p0 + tok : -1;  // -1: sees nothing
       // rows that hold no token are left unmasked: what they compute is not stored
       const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
+      const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
       float m = -INFINITY, l = 0.f;  // the reference (near the largest so far, a whole number) and the sum
-      int done = -1;                 // the last step done
+      const int before = done;
       float row_unit = 0.f;
-      if (w.stages) {
+      if (w.steps) {
         ok = __all_sync(0xffffffffu, wait_or_abort(&qfull[x], qp, abort_flag));
         if (!ok) break;
         qp ^= 1;
@@ -384,22 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll 1
       for (int i = 0; i < w.steps && ok; ++i) {
-        const int k0 = w.key(i);
-        if (!mine.need(k0, sinks)) continue;
-        const int b = i & 1;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[2 * x + b], sp >> b & 1, abort_flag));
+        if (!mine.need(i)) continue;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[x], done & 1, abort_flag));
         if (!ok) break;
-        sp ^= 1u << b;
         tc::tc_fence_after();
-        const int2 exps = tail.exps[(n + i) & (kExps - 1)];
+        const int2 exps = tail.s_exps[x][done & 1];
         uint32_t s[64];
-        tmem_ld32(s_tm + 64 * b, s);
-        tmem_ld32(s_tm + 64 * b + 32, s + 32);
+        tmem_ld32(s_tm, s);
+        tmem_ld32(s_tm + 32, s + 32);
         // a score's unit (kept where a masked -inf stays -inf and a zero is one) and the addition to it
         const float cs = fminf(fmaxf(row_unit * pow2_of(exps.x), 1e-37f), 3e38f), ve = (float)exps.y;
         tc::tmem_ld_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_free[x]);
         // every row sees every key of the step, or keys are masked one by one
-        if (!__all_sync(0xffffffffu, hi >= k0 + 63 && (lo <= k0 || sinks >= k0 + 64))) {
+        const int k0 = w.key(i);
+        if (!sees_all(k0, hi_all, lo_all, sinks)) {
           uint32_t bits[2];
           seen_bits(k0, hi, lo, sinks, bits);
 #pragma unroll
@@ -419,11 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
           m = next;
           l *= f;
-          if (done >= 0) {
-            // O is at rest once the last step's product is in it (S of this step, there already, was
-            // issued after those before)
-            const int d = done & 1;
-            ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ (d != b), abort_flag));
+          if (done > before) {
+            // O is at rest once the last step's product is in it
+            const int d = done - 1;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + (d & 1)], d >> 1 & 1, abort_flag));
             if (!ok) break;
             tc::tc_fence_after();
 #pragma unroll 1
@@ -438,29 +522,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float add = ve - (m == -INFINITY ? 0.f : m);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cs2 = make_float2(cs, cs), add_2 = make_float2(add, add);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[2 * e]), cs, add));
-          const float p1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), cs, add));
-          part[e & 3] += p0;
-          part[(e + 2) & 3] += p1;
+          float p0, p1;
+          fma2(p0, p1, __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), cs2, add_2);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          add2(part[e & 1], p0, p1);
           s[e] = pack_f16(p0, p1);
         }
-        tc::tmem_st32(s_tm + 64 * b, s);  // over the scores
+        tc::tmem_st32(s_tm + 64 + 32 * (done & 1), s);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + b]);
-        l = fmaf((part[0] + part[1]) + (part[2] + part[3]), pow2_of(-exps.y), l);
-        done = i;
+        if (lane == 0) tc::mbar_arrive(&p_full[2 * x + (done & 1)]);
+        l = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), pow2_of(-exps.y), l);
+        ++done;
       }
-      n += w.steps;
       // The row goes straight out.  O is not written again before this tile hands in weights of the next
       // unit.
-      if (ok && done >= 0) {
-        const int d = done & 1;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + d], (sp >> d & 1) ^ 1, abort_flag));
+      if (ok && done > before) {
+        const int d = done - 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&pv_done[2 * x + (d & 1)], d >> 1 & 1, abort_flag));
         tc::tc_fence_after();
       }
       if (!ok) break;
@@ -473,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int k = 0; k < HD; k += 16) {
         uint32_t o[16];
-        if (done >= 0) {
+        if (done > before) {
           tc::tmem_ld16(o_tm + k, o);
           tc::tmem_ld_wait();
         }
