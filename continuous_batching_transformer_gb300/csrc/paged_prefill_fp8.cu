@@ -21,8 +21,8 @@
 namespace {
 
 using Attn = PagedAttnFp8;
-constexpr int kStages = 6;
-constexpr int kVSlots = 3;      // of V in fp16
+constexpr int kStages = 5;
+constexpr int kVSlots = 4;      // of V in fp16
 // warps: issuers of S of tile 0, S of tile 1 and P V of both, requester of tiles; 4..7 and 8..11 softmax;
 // 12..15 conversion
 constexpr int kThreads = 512;
@@ -85,6 +85,74 @@ CBT_D uint32_t sub_f16(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// of each of two pairs the larger magnitude (some sign; NaN where one is)
+CBT_D uint32_t largest_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part
+template <int HD>
+struct QRow {
+  uint32_t c[HD / 2];
+  float unit;  // of the row's scores, in log2 units
+  CBT_D void fetch(const Attn& a, const Unit& u, int x, int TQ, int G, int row) {
+    const int tok = x * TQ + row / G;
+    const bool live = row < TQ * G && tok < u.n;
+    const uint4* src =
+        reinterpret_cast<const uint4*>(a.q + (u.t0 + tok) * a.q_ld + (long long)(u.g * G + row % G) * HD);
+#pragma unroll
+    for (int j = 0; j < HD / 8; ++j) {
+      const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+      c[4 * j] = v.x;
+      c[4 * j + 1] = v.y;
+      c[4 * j + 2] = v.z;
+      c[4 * j + 3] = v.w;
+    }
+  }
+  CBT_D void split(const Attn& a) {
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int j = 0; j < HD / 2; ++j) top2 = largest_bf16(top2, c[j]);
+    const uint32_t top = max(top2 >> 16 & 0x7FFFu, top2 & 0x7FFFu);
+    const bool finite = top < 0x7F80u;
+    const int fit = fit_exponent(bf16_lo(finite ? top : 0));
+    const float f = a.scale < 0.f ? -pow2_of(fit) : pow2_of(fit);  // the sign of the scale is q's
+    unit = fabsf(a.scale) * kLog2e * pow2_of(-fit);
+#pragma unroll
+    for (int j = 0; j < HD / 8; ++j) {
+      uint32_t part[2][2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // in fp16 from here, which the scaled element's eight bits fit: the first four of them, and the rest
+        const uint32_t y = pack_f16(bf16_lo(c[4 * j + e]) * f, bf16_hi(c[4 * j + e]) * f), y_hi = y & 0xFF80FF80u;
+        const uint16_t hi = f16_to_e4m3(y_hi), lo = f16_to_e4m3(sub_f16(y, y_hi));
+        part[0][e >> 1] = e & 1 ? part[0][e >> 1] | (uint32_t)hi << 16 : hi;
+        part[1][e >> 1] = e & 1 ? part[1][e >> 1] | (uint32_t)lo << 16 : lo;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[4 * j + e] = part[e >> 1][e & 1];
+    }
+    if (!finite) {  // its scores are not numbers
+#pragma unroll
+      for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
+    }
+  }
+  CBT_D void store(uint8_t* q, uint32_t part_bytes, int row) const {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < HD / 16; ++j)
+        *reinterpret_cast<uint4*>(q + p * part_bytes + tc::swz<HD>(row, 16 * j)) =
+            make_uint4(c[8 * j + 2 * p], c[8 * j + 2 * p + 1], c[8 * j + 4 + 2 * p], c[8 * j + 5 + 2 * p]);
+  }
+};
+// the first unit behind k that has steps, or count
+CBT_D int next_with_steps(const Unit* units, int k, int count) {
+  do ++k;
+  while (k < count && units[k].s1 <= units[k].s0);
+  return k;
 }
 // a * b + c and a + b on two numbers, one instruction
 CBT_D void fma2(float& x, float& y, float a, float b, float2 m, float2 c) {
@@ -306,90 +374,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     int st = 0, slot = 0;
     uint32_t ph = 0, vp = 0, qp = 0;
     bool ok = true;
-    const float scale2 = fabsf(a.scale) * kLog2e;
-    // A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part.  The
-    // next unit's first tile is fetched and split while the last steps of this one run.
-    uint32_t c[HD / 2];
-    float unit = 0.f;
-    bool ahead = false;  // c holds the unit's first tile
-    auto fetch = [&](const Work<Attn>& w, int x) {
-      const int tok = x * TQ + row / G;
-      const bool live = row < TQ * G && tok < w.u.n;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (w.u.t0 + tok) * a.q_ld +
-                                                        (long long)(w.u.g * G + row % G) * HD);
-#pragma unroll
-      for (int j = 0; j < HD / 8; ++j) {
-        const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-        c[4 * j] = v.x;
-        c[4 * j + 1] = v.y;
-        c[4 * j + 2] = v.z;
-        c[4 * j + 3] = v.w;
-      }
-    };
-    auto split = [&]() {
-      uint32_t top = 0;  // largest magnitudes, as bf16
-#pragma unroll
-      for (int j = 0; j < HD / 2; ++j) top = __vmaxu2(top, c[j] & 0x7FFF7FFFu);
-      top = max(top >> 16, top & 0xFFFFu);
-      const bool finite = top < 0x7F80u;
-      const int fit = fit_exponent(bf16_lo(finite ? top : 0));
-      const float f = a.scale < 0.f ? -pow2_of(fit) : pow2_of(fit);  // the sign of the scale is q's
-      unit = scale2 * pow2_of(-fit);
-#pragma unroll
-      for (int j = 0; j < HD / 8; ++j) {
-        uint32_t part[2][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // in fp16 from here, which the scaled element's eight bits fit
-          const uint32_t y = pack_f16(bf16_lo(c[4 * j + e]) * f, bf16_hi(c[4 * j + e]) * f);
-          const uint16_t hi = f16_to_e4m3(y), lo = f16_to_e4m3(sub_f16(y, e4m3_to_f16(hi)));
-          part[0][e >> 1] = e & 1 ? part[0][e >> 1] | (uint32_t)hi << 16 : hi;
-          part[1][e >> 1] = e & 1 ? part[1][e >> 1] | (uint32_t)lo << 16 : lo;
-        }
-        c[4 * j] = part[0][0];
-        c[4 * j + 1] = part[0][1];
-        c[4 * j + 2] = part[1][0];
-        c[4 * j + 3] = part[1][1];
-      }
-      if (!finite) {  // its scores are not numbers
-#pragma unroll
-        for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
-      }
-    };
+    // The next unit's first tile of Q is fetched and split while the last steps of this one run; the first
+    // unit's are the softmax's
+    QRow<HD> q;
+    const int first = next_with_steps(units, -1, count);
 #pragma unroll 1
-    for (int k = 0; k < count && ok; ++k) {
+    for (int k = first; k < count && ok;) {
       const Work<Attn> w(units + k, a);
-      if (!w.steps) continue;
-      if (!ahead) {
-        fetch(w, 0);
-        split();
-      }
-      ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp ^ 1, abort_flag));
-      if (!ok) break;
-      qp ^= 1;
+      if (k != first) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp, abort_flag));
+        if (!ok) break;
+        qp ^= 1;
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (x * TQ < w.u.n) {
-          if (x) {
-            fetch(w, 1);
-            split();
+        for (int x = 0; x < 2; ++x) {
+          if (x * TQ < w.u.n) {
+            if (x) {
+              q.fetch(a, w.u, 1, TQ, G, row);
+              q.split(a);
+            }
+            q.store(sQ + x * 2 * kPart, kPart, row);
+            tail.row_unit[x][row] = q.unit;
+            tc::fence_proxy_async_smem();
           }
-          uint8_t* q = sQ + x * 2 * kPart;
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int j = 0; j < HD / 16; ++j)
-              *reinterpret_cast<uint4*>(q + p * kPart + tc::swz<HD>(row, 16 * j)) =
-                  make_uint4(c[8 * j + 2 * p], c[8 * j + 2 * p + 1], c[8 * j + 4 + 2 * p], c[8 * j + 5 + 2 * p]);
-          tail.row_unit[x][row] = unit;
-          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&qfull[x]);
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&qfull[x]);
       }
-      const Work<Attn> next(units + min(k + 1, count - 1), a);
-      ahead = k + 1 < count && next.steps;
-      const int fetch_at = ahead ? max(0, w.steps - 4) : w.steps, split_at = min(fetch_at + 1, w.steps - 1);
+      k = uniform(next_with_steps(units, k, count));
+      const int fetch_at = k < count ? max(0, w.steps - 6) : w.steps, split_at = min(fetch_at + 1, w.steps - 1);
 #pragma unroll 1
       for (int i = 0; i < w.steps && ok; ++i) {
         // the step has landed, and its slot is free again
@@ -429,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         vp ^= slot == 0;
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0;
-        if (i == fetch_at) fetch(next, 0);
-        if (i == split_at && ahead) split();
+        if (i == fetch_at) q.fetch(a, units[k], 0, TQ, G, row);
+        if (i == split_at && k < count) q.split(a);
       }
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 33);
@@ -443,6 +455,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qp = 0;  // phase of Q
     int done = 0;     // steps that the tile took part in
     bool ok = true;
+    // the first unit's Q, which nothing runs ahead of
+    if (const int first = next_with_steps(units, -1, count); first < count) {
+      const Unit u = units[first];
+      if (x * TQ < u.n) {
+        QRow<HD> q;
+        q.fetch(a, u, x, TQ, G, row);
+        q.split(a);
+        q.store(sQ + x * 2 * kPart, kPart, row);
+        tail.row_unit[x][row] = q.unit;
+        tc::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&qfull[x]);
+    }
     // rows of out on 32-byte boundaries: whole sectors a store
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.out_ld % (a.f32 ? 8 : 16) == 0;
 #pragma unroll 1
@@ -562,9 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_ld16(o_tm + k, o);
           tc::tmem_ld_wait();
         }
-        float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = p >= 0 ? __uint_as_float(o[e]) * inv : 0.f;
+        for (int e = 0; e < 16; ++e) o[e] = p >= 0 ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
         if (!live) continue;
         if (a.f32 || runs > 1) {
           float* dst = runs > 1 ? part_o + part * HD + k : static_cast<float*>(a.out) + at + k;
@@ -572,13 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; e += 8) {
             uint32_t h[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = __float_as_uint(v[e + j]);
+            for (int j = 0; j < 8; ++j) h[j] = o[e + j];
             store32(dst + e, h, wide || runs > 1);
           }
         } else {
           uint32_t h[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 8; ++j) h[j] = pack_bf16(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
           store32(static_cast<uint16_t*>(a.out) + at + k, h, wide);
         }
       }
