@@ -19,16 +19,15 @@ namespace {
 
 constexpr float kTop = 448.f;
 
-// sin and cos of ph / 2^64 turns to fp32's last place or so: the nearest quarter turn is taken off in
-// whole numbers, and the rest, at most pi / 4, goes through the Taylor series (first terms left out:
-// x^11 / 11! and x^12 / 12!, below 2^-28).  A rounding to three bits of mantissa shows no more than
-// this costs: with the hardware's sine, off by 2^-21, a few more codes in a million fall on the other
-// side of a border than the formula's.
-CBT_D void turn_sincos(uint64_t ph, float* sn, float* cs) {
-  const uint64_t at = ph + (1ull << 61);
-  const int quarter = (int)(at >> 62);
-  const int rest = (int)((long long)((at & ((1ull << 62) - 1)) - (1ull << 61)) >> 30);  // of 2^34 a turn
-  const float x = (float)rest * 0x1.921fb6p-32f;  // 2 pi / 2^34
+// sin and cos of the 256 whole fractions of a turn, for turn_sincos
+struct Circle {
+  float2 at[256];
+};
+// One entry: within an eighth of a turn of a whole number of quarters, the Taylor series (first terms left
+// out: x^11 / 11! and x^12 / 12!, below 2^-28).
+CBT_D float2 circle_at(int k) {
+  const int quarter = (k + 32) >> 6;
+  const float x = (float)(k - 64 * quarter) * 0x1.921fb6p-6f;  // 2 pi / 256
   const float z = x * x;
   float s = fmaf(z, 1.f / 362880, -1.f / 5040);
   s = fmaf(z, s, 1.f / 120);
@@ -40,9 +39,30 @@ CBT_D void turn_sincos(uint64_t ph, float* sn, float* cs) {
   c = fmaf(z, c, -0.5f);
   c = fmaf(z, c, 1.f);
   const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
-  *sn = quarter & 2 ? -a : a;
-  *cs = (quarter + 1) & 2 ? -b : b;
+  return make_float2(quarter & 2 ? -a : a, (quarter + 1) & 2 ? -b : b);
 }
+// sin and cos of pos * turns (a fraction of a turn, 2^64 a whole) to fp32's last place or so: the nearest
+// entry, turned by the rest (at most pi / 256, where two terms of the series are enough).  A rounding to
+// three bits of mantissa shows no more than this costs: with the hardware's sine, off by 2^-21, a few more
+// codes in a million fall on the other side of a border than the formula's.
+CBT_D void turn_sincos(const Circle& circle, uint32_t pos, uint64_t turns, float* sn, float* cs) {
+  const uint32_t ph = pos * (uint32_t)(turns >> 32) + __umulhi(pos, (uint32_t)turns);  // 2^32 a turn
+  const uint32_t k = ph + (1u << 23);
+  const float r = (float)(int)((k & 0xFFFFFFu) - (1u << 23)) * 0x1.921fb6p-30f;  // 2 pi / 2^32
+  const float2 e = circle.at[k >> 24];
+  const float z = r * r;
+  const float s = r * fmaf(z, -1.f / 6, 1.f), c1 = z * fmaf(z, 1.f / 24, -0.5f);  // sin r, cos r - 1
+  *sn = e.x + fmaf(e.x, c1, e.y * s);
+  *cs = e.y + fmaf(e.y, c1, -e.x * s);
+}
+
+// A number's first 16 bits, the last of them set where anything behind it is ("rounded to odd"): what is
+// rounded from that to a code's four bits is rounded as the number itself.
+CBT_D uint32_t odd16(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u | ((u & 0xFFFFu) + 0xFFFFu);
+}
+CBT_D uint32_t pack_odd(float lo, float hi) { return __byte_perm(odd16(lo), odd16(hi), 0x7632); }
 
 // the exponent of the smallest scale that values up to `top` (finite, >= 0) are within 448 times of
 CBT_D int exponent_for(float top) {
@@ -68,24 +88,31 @@ struct Runs {
   int exponent[kMostChunk];
   int grown[kMostChunk], down[kMostChunk];  // runs whose cache block moves, and by how much
   int count, n_grown, last_block;
-  int warp_runs[2];
+  int warp_runs[2], scan[kWarps];
   int part[kTokens], warp_parts[kTokens / 32];  // tokens next to each other in 16 aligned slots
 };
 
+// Shared memory of a block for k and v: the runs, the tokens' values (rows padded by 16 bytes), the circle,
+// and what heads with odd pairs exchange through
 template <int HD>
+constexpr int kRowBytes = 2 * HD + 16;
+constexpr size_t kRunsBytes = (sizeof(Runs) + 15) / 16 * 16;
+template <int HD, int MODE>
 constexpr size_t kv_smem() {
-  return sizeof(Runs) + (size_t)kTokens * (HD + 4);  // V's codes by token, rows padded by a word
+  return kRunsBytes + (size_t)kTokens * kRowBytes<HD> + (MODE == kNone ? 0 : sizeof(Circle)) +
+         (MODE == kHalfOdd ? kWarps * 256 * sizeof(float) : 0);
 }
 
 // runs of kv head g that begin in tokens [t0, t0 + chunk), of K or of V
 template <int HD, bool F32, int MODE, bool V>
-CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t* sm, float* xs) {
+CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t* sm) {
   constexpr int LPH = HD / 8, NH = 32 / LPH;  // lanes of a token, tokens of a warp
   constexpr int kPlaces = kWarps * NH;        // tokens in flight
-  constexpr int kHeld = kTokens / kPlaces;    // of a lane's
-  constexpr int kRow = HD + 4;
+  constexpr int kRow = kRowBytes<HD>;
   Runs& r = *reinterpret_cast<Runs*>(sm);
-  uint8_t* tile = sm + sizeof(Runs);
+  uint8_t* tile = sm + kRunsBytes;
+  Circle& circle = *reinterpret_cast<Circle*>(tile + kTokens * kRow);
+  float* xs = reinterpret_cast<float*>(&circle + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % LPH, sub = lane / LPH;
   const int page = a.kv.page_tokens;
   auto slot_of = [&](int t) {
@@ -106,6 +133,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     r.anew[tid] = 0;
   }
   if (tid == 0) r.n_grown = 0;
+  if (!V && MODE != kNone) circle.at[tid] = circle_at(tid);
   __syncthreads();
   if (tid < chunk) {
     const int run = r.run[tid] + (warp == 1 && r.slot[tid] >= 0 ? r.warp_runs[0] : 0);
@@ -131,12 +159,12 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
       const int at = chunk + tail + tid;
       if (in && at < kTokens) r.slot[at] = s;
       const unsigned out = __ballot_sync(0xffffffffu, !in);
-      if (lane == 0) xs[warp] = __int_as_float(out ? __ffs(out) - 1 : 32);
+      if (lane == 0) r.scan[warp] = out ? __ffs(out) - 1 : 32;
       __syncthreads();
       seen = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const int n = __float_as_int(xs[w]);
+        const int n = r.scan[w];
         if (seen == 32 * w) seen += n;
       }
       __syncthreads();
@@ -179,7 +207,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
       cs[k] = 1.f;
       sn[k] = 0.f;
       if (turn) {
-        turn_sincos((uint64_t)pos * a.rope.turns[pair], &sn[k], &cs[k]);
+        turn_sincos(circle, pos, a.rope.turns[pair], &sn[k], &cs[k]);
         sn[k] *= a.rope.mscale;
         cs[k] *= a.rope.mscale;
       }
@@ -200,17 +228,18 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
       if (slot % kBlock == 0) r.anew[run] = 1;
     }
   };
-  float x[kHeld][8];
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int base = k * kPlaces + warp * NH, i = base + sub;
-    if (base >= total) break;
-    const int run = run_at(i);
-    values(i, run >= 0, x[k]);
-    note_top(x[k], run, run >= 0 ? r.slot[i] : 1);
+  const int held_tokens = min(total, kTokens);
+#pragma unroll 2
+  for (int base = warp * NH; base < held_tokens; base += kPlaces) {
+    const int i = base + sub, run = run_at(i);
+    float x[8];
+    values(i, run >= 0, x);
+    note_top(x, run, run >= 0 ? r.slot[i] : 1);
+    *reinterpret_cast<uint4*>(tile + i * kRow + 16 * l) =
+        make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
   }
 #pragma unroll 1
-  for (int base = kHeld * kPlaces + warp * NH; base < total; base += kPlaces) {  // slots came twice
+  for (int base = kTokens + warp * NH; base < total; base += kPlaces) {  // slots came twice
     float y[8];
     const int i = base + sub, run = run_at(i);
     values(i, run >= 0, y);
@@ -277,27 +306,23 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
   };
   // V is turned around where runs are long enough to fill stores
   const bool turned = V && total >= 16 && total >= 4 * count;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int base = k * kPlaces + warp * NH, i = base + sub;
-    if (base >= total) break;
-    const int run = run_at(i);
-    if (run < 0) {
-      if (turned && l == 0 && i < kTokens) r.slot[i] = -1;
-      continue;
-    }
-    uint32_t w[2];
-    codes(x[k], run, w);
-    if (turned) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(tile + i * kRow + 8 * l);
-      dst[0] = w[0];
-      dst[1] = w[1];
-    } else {
+  if (turned) {
+    if (tid < held_tokens && run_at(tid) < 0) r.slot[tid] = -1;
+  } else {
+#pragma unroll 2
+    for (int base = warp * NH; base < held_tokens; base += kPlaces) {
+      const int i = base + sub, run = run_at(i);
+      if (run < 0) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + i * kRow + 16 * l);
+      const float y[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                          bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+      uint32_t w[2];
+      codes(y, run, w);
       put(w, r.slot[i]);
     }
   }
 #pragma unroll 1
-  for (int base = kHeld * kPlaces + warp * NH; base < total; base += kPlaces) {
+  for (int base = kTokens + warp * NH; base < total; base += kPlaces) {
     float y[8];
     const int i = base + sub, run = run_at(i);
     values(i, run >= 0, y);
@@ -310,7 +335,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
   __syncthreads();
   // ---- V: the parts of the runs that lie in 16 aligned slots, four dims a thread; 16 positions in one
   // store where such a part fills them
-  const int n = min(total, kTokens);
+  const int n = held_tokens;
   bool first = false;
   int len = 0;
   unsigned m = 0;
@@ -340,7 +365,11 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     const int i = r.part[p] & 0xFFFF, size = r.part[p] >> 16;
     const int s = r.slot[i], id = s / page, o = s - id * page;
     uint8_t* dst = a.kv.pool + fp8_v(a.kv, id, g, o, d);
-    auto row = [&](int j) { return *reinterpret_cast<const uint32_t*>(tile + (i + j) * kRow + d); };
+    const float f = pow2_of(-r.exponent[run_at(i)]);
+    auto row = [&](int j) {
+      const uint2 v = *reinterpret_cast<const uint2*>(tile + (i + j) * kRow + 2 * d);
+      return pack_e4m3(bf16_lo(v.x) * f, bf16_hi(v.x) * f) | (uint32_t)pack_e4m3(bf16_lo(v.y) * f, bf16_hi(v.y) * f) << 16;
+    };
     if (size == 16) {
       uint32_t w[4][4];  // [dim][positions 4j..]
 #pragma unroll
@@ -369,21 +398,20 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
 // Blocks [0, kv_blocks): runs that begin in `chunk` tokens, of a kv head's K or V; then warps over (token,
 // run of `per` q heads), `cuts` of them a token.
 template <int HD, bool F32, int MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     k_append_fp8(const __grid_constant__ RopeAppendFp8 a, int kv_blocks, int chunk, int cuts, int per) {
   extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ float xs[kWarps * 256];
   pdl_wait();
   const int warp = threadIdx.x >> 5;
   if ((int)blockIdx.x < kv_blocks) {
     const int heads = a.kv.n_kv_heads, h = blockIdx.x % (2 * heads), t0 = blockIdx.x / (2 * heads) * chunk;
-    if (h < heads) append_runs<HD, F32, MODE, false>(a, t0, chunk, h, sm, xs);
-    else append_runs<HD, F32, MODE, true>(a, t0, chunk, h - heads, sm, xs);
+    if (h < heads) append_runs<HD, F32, MODE, false>(a, t0, chunk, h, sm);
+    else append_runs<HD, F32, MODE, true>(a, t0, chunk, h - heads, sm);
   } else {
     const long long w = (long long)(blockIdx.x - kv_blocks) * kWarps + warp;
     const int t = (int)(w / cuts), h0 = (int)(w - (long long)t * cuts) * per;
     if (t < a.tokens && h0 < a.n_heads)
-      rotate_heads<HD, F32, MODE>(a, t, h0, min(a.n_heads, h0 + per), xs + warp * 256);
+      rotate_heads<HD, F32, MODE>(a, t, h0, min(a.n_heads, h0 + per), reinterpret_cast<float*>(sm) + warp * 256);
   }
   pdl_launch();
 }
@@ -391,8 +419,8 @@ __global__ void __launch_bounds__(kThreads)
 template <int HD, bool F32, int MODE>
 cudaError_t launch(const RopeAppendFp8& a, cudaStream_t s) {
   constexpr int kStep = 32 / (HD / 8) * kUnroll;  // heads a warp has in flight
-  constexpr size_t smem = kv_smem<HD>();
-  static_assert(smem + kWarps * 256 * sizeof(float) <= 48 * 1024, "shared memory");
+  constexpr size_t smem = kv_smem<HD, MODE>();
+  static_assert(smem >= kWarps * 256 * sizeof(float) && smem <= 48 * 1024, "shared memory");
   const int steps = (a.n_heads + kStep - 1) / kStep;
   int cuts = (kTargetWarps + a.tokens - 1) / a.tokens;
   cuts = cuts < steps ? cuts : steps;
