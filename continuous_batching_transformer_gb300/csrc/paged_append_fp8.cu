@@ -56,13 +56,18 @@ CBT_D void turn_sincos(const Circle& circle, uint32_t pos, uint64_t turns, float
   *cs = e.y + fmaf(e.y, c1, -e.x * s);
 }
 
-// A number's first 16 bits, the last of them set where anything behind it is ("rounded to odd"): what is
-// rounded from that to a code's four bits is rounded as the number itself.
-CBT_D uint32_t odd16(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u | ((u & 0xFFFFu) + 0xFFFFu);
+// Two numbers' first 16 bits each, the last of them set where anything is behind it ("rounded to odd"):
+// what is rounded from that to a code's four bits is rounded as the number itself.
+CBT_D uint32_t pack_odd(float lo, float hi) {
+  const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+  return __byte_perm(a, b, 0x7632) | __vminu2(__byte_perm(a, b, 0x5410), 0x00010001u);
 }
-CBT_D uint32_t pack_odd(float lo, float hi) { return __byte_perm(odd16(lo), odd16(hi), 0x7632); }
+// of each of two pairs of bf16 the larger magnitude (some sign; a NaN only where both are)
+CBT_D uint32_t larger_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // the exponent of the smallest scale that values up to `top` (finite, >= 0) are within 448 times of
 CBT_D int exponent_for(float top) {
@@ -83,12 +88,13 @@ struct Runs {
   int slot[kTokens];               // of each token, -1: not this block's
   short run[kMostChunk];           // of each of the chunk's tokens, -1: none that begins here
   int first_slot[kMostChunk];      // of each run
+  uint8_t* block[kMostChunk];      // its cache block's codes
   int top[kMostChunk];             // its largest magnitude, as bits
   int anew[kMostChunk];            // it holds its cache block's first position
   int exponent[kMostChunk];
   int grown[kMostChunk], down[kMostChunk];  // runs whose cache block moves, and by how much
-  int count, n_grown, last_block;
-  int warp_runs[2], scan[kWarps];
+  int count, lead, n_grown, last_block;
+  int warp_runs[2], warp_lead[2], scan[kWarps];
   int part[kTokens], warp_parts[kTokens / 32];  // tokens next to each other in 16 aligned slots
 };
 
@@ -126,7 +132,10 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     const int before = tid < chunk ? slot_of(t0 + tid - 1) : -1;
     const bool first = s >= 0 && (before < 0 || before / kBlock != s / kBlock);
     const unsigned m = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) r.warp_runs[warp] = __popc(m);
+    if (lane == 0) {
+      r.warp_runs[warp] = __popc(m);
+      r.warp_lead[warp] = m ? 32 * warp + __ffs(m) - 1 : kMostChunk;
+    }
     r.slot[tid] = s;
     r.run[tid] = s < 0 ? -1 : (short)(__popc(m & (0xffffffffu >> (31 - lane))) - 1);  // in its warp
     r.top[tid] = 0;
@@ -143,10 +152,14 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
       if (tid == 0 || before < 0 || before / kBlock != r.slot[tid] / kBlock) r.first_slot[run] = r.slot[tid];
     }
     if (tid == chunk - 1) r.last_block = run >= 0 ? r.slot[tid] / kBlock : -1;
-    if (tid == 0) r.count = r.warp_runs[0] + r.warp_runs[1];
+    if (tid == 0) {
+      r.count = r.warp_runs[0] + r.warp_runs[1];
+      r.lead = min(r.warp_lead[0], r.warp_lead[1]);
+    }
   }
   __syncthreads();
   const int count = r.count, last_block = r.last_block;
+  const int lead = r.lead;  // the tokens before belong to a run that began earlier
   if (count == 0) return;
   // the last run's tokens behind the chunk (more than 64 only where slots come twice)
   int tail = 0;
@@ -175,9 +188,12 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
   const int total = chunk + tail;
   // what each run's cache block has so far
   float held = 0.f;
+  float* scale_at = nullptr;
   if (tid < count) {
-    const int s = r.first_slot[tid], id = s / page;
-    held = *fp8_scale(a.kv, id, V, g, s - id * page);
+    const int s = r.first_slot[tid], id = s / page, o = (s - id * page) & ~(kBlock - 1);
+    scale_at = fp8_scale(a.kv, id, V, g, o);
+    held = *scale_at;
+    r.block[tid] = a.kv.pool + (V ? fp8_v(a.kv, id, g, o, 0) : fp8_k(a.kv, id, g, o, 0));
   }
 
   // ---- values: lane l of a token holds eight dims
@@ -185,65 +201,93 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
   const LaneDims dims = lane_dims<V ? kNone : MODE>(l, rot);
   const long long src = (long long)(a.n_heads + (V ? a.kv.n_kv_heads : 0) + g) * HD;
   auto run_at = [&](int i) { return i >= total ? -1 : i < chunk ? (int)r.run[i] : count - 1; };
+  // a lane's pairs (kHalfOdd: the pair of each of its dims) and gains are the same for all of its tokens
+  constexpr int kAngles = V || MODE == kNone ? 1 : MODE == kHalfOdd ? 8 : 4;
+  uint64_t turns[kAngles];
+  float gain[8];
+  if (!V) {
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) {
+      const int d = 8 * l + k, pair = MODE == kHalfOdd ? (d < rot / 2 ? d : d - rot / 2) : 4 * l + k;
+      const bool turn = MODE == kHalfOdd ? d < rot : MODE != kNone && k < dims.turned;
+      turns[k] = turn ? a.rope.turns[pair] : 0;
+    }
+    if (a.k_gain) load_gain(a.k_gain, dims, gain);
+  }
   auto values = [&](int i, bool on, float (&x)[8]) {  // by all lanes: `on` may differ between tokens
     const int t = t0 + (on ? i : 0);
     load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e0, x);
     load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e1, x + 4);
     if (V) return;
-    if (a.k_gain) scale_head<HD>(x, head_squares<HD>(x), a.eps, a.k_gain, dims);
+    const int pos = MODE != kNone && on ? a.positions[t] : 0;
+    if (a.k_gain) scale_head<HD>(x, head_squares<HD>(x), a.eps, gain);
     if (MODE == kNone) return;
-    constexpr int kAngles = MODE == kHalfOdd ? 8 : 4;
-    const int pos = on ? a.positions[t] : 0;
     float cs[kAngles], sn[kAngles];
 #pragma unroll
-    for (int k = 0; k < kAngles; ++k) {
-      int pair = 4 * l + k;
-      bool turn = k < dims.turned;
-      if (MODE == kHalfOdd) {
-        const int d = 8 * l + k;
-        turn = d < rot;
-        pair = d < rot / 2 ? d : d - rot / 2;
-      }
-      cs[k] = 1.f;
-      sn[k] = 0.f;
-      if (turn) {
-        turn_sincos(circle, pos, a.rope.turns[pair], &sn[k], &cs[k]);
-        sn[k] *= a.rope.mscale;
-        cs[k] *= a.rope.mscale;
-      }
+    for (int k = 0; k < kAngles; ++k) {  // dims that are not turned: by no angle, and not scaled either
+      turn_sincos(circle, pos, turns[k], &sn[k], &cs[k]);
+      sn[k] *= a.rope.mscale;
+      cs[k] *= a.rope.mscale;
     }
     turn_head<HD, V ? kNone : MODE>(x, cs, sn, l, dims.turned, rot, xs + (warp * NH + sub) * HD);
   };
-  auto note_top = [&](const float (&x)[8], int run, int slot) {
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float y = fabsf(x[k]);
-      if (y <= 3.4028235e38f) top = fmaxf(top, y);
-    }
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  auto note_top = [&](float top, int run, int slot) {  // of a token, at its first lane
     if (l == 0 && run >= 0) {
       atomicMax(&r.top[run], __float_as_int(top));
       if (slot % kBlock == 0) r.anew[run] = 1;
     }
   };
+  auto top_of = [&](const float (&x)[8]) {  // the largest finite magnitude of a token, by all lanes
+    auto over_lanes = [&](float y) {
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+      return y;
+    };
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));  // (NaN are passed over)
+    top = over_lanes(top);
+    if (__any_sync(0xffffffffu, top == INFINITY)) {
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y = fmaxf(y, fabsf(x[k]) == INFINITY ? 0.f : fabsf(x[k]));
+      top = over_lanes(y);
+    }
+    return top;
+  };
   const int held_tokens = min(total, kTokens);
 #pragma unroll 2
-  for (int base = warp * NH; base < held_tokens; base += kPlaces) {
-    const int i = base + sub, run = run_at(i);
-    float x[8];
-    values(i, run >= 0, x);
-    note_top(x, run, run >= 0 ? r.slot[i] : 1);
-    *reinterpret_cast<uint4*>(tile + i * kRow + 16 * l) =
-        make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
+  for (int base = lead + warp * NH; base < held_tokens; base += kPlaces) {
+    const int i = base + sub, run = i < held_tokens ? run_at(i) : -1;
+    uint4 v;
+    float top;
+    if (V && !F32) {  // as it lies there
+      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.qkv) + (t0 + (run >= 0 ? i : 0)) * a.qkv_ld +
+                                               src + 8 * l));
+      uint32_t m = larger_bf16(larger_bf16(v.x, v.y), larger_bf16(v.z, v.w));
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) m = larger_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
+      top = fmaxf(fmaxf(0.f, fabsf(bf16_lo(m))), fabsf(bf16_hi(m)));
+      if (__any_sync(0xffffffffu, top == INFINITY)) {
+        const float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                            bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+        top = top_of(x);
+      }
+    } else {
+      float x[8];
+      values(i, run >= 0, x);
+      top = top_of(x);
+      v = make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
+    }
+    note_top(top, run, run >= 0 ? r.slot[i] : 1);
+    if (i < held_tokens) *reinterpret_cast<uint4*>(tile + i * kRow + 16 * l) = v;
   }
 #pragma unroll 1
   for (int base = kTokens + warp * NH; base < total; base += kPlaces) {  // slots came twice
     float y[8];
     const int i = base + sub, run = run_at(i);
     values(i, run >= 0, y);
-    note_top(y, run, run >= 0 ? a.slots[t0 + i] : 1);
+    note_top(top_of(y), run, run >= 0 ? a.slots[t0 + i] : 1);
   }
   __syncthreads();
 
@@ -254,10 +298,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     const int e = anew ? e_call : max(e_call, e_held);
     r.exponent[tid] = e;
     const float scale = pow2_of(e);
-    if (scale != held) {
-      const int s = r.first_slot[tid], id = s / page;
-      *fp8_scale(a.kv, id, V, g, s - id * page) = scale;
-    }
+    if (scale != held) *scale_at = scale;
     if (!anew && e > e_held) {
       const int k = atomicAdd(&r.n_grown, 1);
       r.grown[k] = tid;
@@ -270,10 +311,8 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     constexpr int kVecs = kBlock * HD / 16;
 #pragma unroll 1
     for (int k = tid; k < n_grown * kVecs; k += kThreads) {
-      const int which = k / kVecs, run = r.grown[which], s = r.first_slot[run], id = s / page;
-      const int o = (s - id * page) / kBlock * kBlock;
-      uint4* p = reinterpret_cast<uint4*>(a.kv.pool + (V ? fp8_v(a.kv, id, g, o, 0) : fp8_k(a.kv, id, g, o, 0))) +
-                 k % kVecs;
+      const int which = k / kVecs, run = r.grown[which];
+      uint4* p = reinterpret_cast<uint4*>(r.block[run]) + k % kVecs;
       const float f = pow2_of(r.down[which]);
       uint4 c = *p;
       c.x = move_codes(c.x, f);
@@ -292,14 +331,14 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     for (int k = 0; k < 2; ++k)
       w[k] = pack_e4m3(y[4 * k] * f, y[4 * k + 1] * f) | (uint32_t)pack_e4m3(y[4 * k + 2] * f, y[4 * k + 3] * f) << 16;
   };
-  auto put = [&](const uint32_t* w, int s) {  // straight to the token's slot
-    const int id = s / page, o = s - id * page;
+  auto put = [&](const uint32_t* w, int run, int s) {  // straight to the token's slot
+    const int o = s % kBlock;
     if (!V) {
-      uint8_t* dst = a.kv.pool + fp8_k(a.kv, id, g, o, 0);
+      uint8_t* dst = r.block[run] + o * HD;
       *reinterpret_cast<uint32_t*>(dst + dims.e0) = w[0];
       *reinterpret_cast<uint32_t*>(dst + dims.e1) = w[1];
     } else {
-      uint8_t* dst = a.kv.pool + fp8_v(a.kv, id, g, o, 8 * l);
+      uint8_t* dst = r.block[run] + 8 * l * kBlock + o;
 #pragma unroll
       for (int k = 0; k < 8; ++k) dst[k * kBlock] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
     }
@@ -310,15 +349,15 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     if (tid < held_tokens && run_at(tid) < 0) r.slot[tid] = -1;
   } else {
 #pragma unroll 2
-    for (int base = warp * NH; base < held_tokens; base += kPlaces) {
-      const int i = base + sub, run = run_at(i);
+    for (int base = lead + warp * NH; base < held_tokens; base += kPlaces) {
+      const int i = base + sub, run = i < held_tokens ? run_at(i) : -1;
       if (run < 0) continue;
       const uint4 v = *reinterpret_cast<const uint4*>(tile + i * kRow + 16 * l);
       const float y[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
                           bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
       uint32_t w[2];
       codes(y, run, w);
-      put(w, r.slot[i]);
+      put(w, run, r.slot[i]);
     }
   }
 #pragma unroll 1
@@ -329,7 +368,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     if (run < 0) continue;
     uint32_t w[2];
     codes(y, run, w);
-    put(w, a.slots[t0 + i]);
+    put(w, run, a.slots[t0 + i]);
   }
   if (!turned) return;
   __syncthreads();
@@ -363,9 +402,9 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     const int p = k / kEights * 4 + (lane & 3), d = ((k % kEights) * 8 + (lane >> 2)) * 4;
     if (p >= parts) continue;
     const int i = r.part[p] & 0xFFFF, size = r.part[p] >> 16;
-    const int s = r.slot[i], id = s / page, o = s - id * page;
-    uint8_t* dst = a.kv.pool + fp8_v(a.kv, id, g, o, d);
-    const float f = pow2_of(-r.exponent[run_at(i)]);
+    const int run = run_at(i);
+    uint8_t* dst = r.block[run] + d * kBlock + r.slot[i] % kBlock;
+    const float f = pow2_of(-r.exponent[run]);
     auto row = [&](int j) {
       const uint2 v = *reinterpret_cast<const uint2*>(tile + (i + j) * kRow + 2 * d);
       return pack_e4m3(bf16_lo(v.x) * f, bf16_hi(v.x) * f) | (uint32_t)pack_e4m3(bf16_lo(v.y) * f, bf16_hi(v.y) * f) << 16;
@@ -396,7 +435,7 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
 }
 
 // Blocks [0, kv_blocks): runs that begin in `chunk` tokens, of a kv head's K or V; then warps over (token,
-// run of `per` q heads), `cuts` of them a token.
+// run of `per` q heads), `cuts` of them a token.  (Dealt among one another they took as long.)
 template <int HD, bool F32, int MODE>
 __global__ void __launch_bounds__(kThreads, 4)
     k_append_fp8(const __grid_constant__ RopeAppendFp8 a, int kv_blocks, int chunk, int cuts, int per) {

@@ -1,6 +1,8 @@
 // paged_rope.cuh -- per-head norm and rotary positions of QKV rows: what the appends to a bf16 and to an
 // 8-bit paged cache share.
 #pragma once
+#include <type_traits>
+
 #include "paged.h"
 
 namespace {
@@ -84,13 +86,14 @@ CBT_D float head_squares(const float (&x)[8]) {
   return s;
 }
 template <int HD>
-CBT_D void scale_head(float (&x)[8], float squares, float eps, const uint16_t* gain, const LaneDims& d) {
+CBT_D void scale_head(float (&x)[8], float squares, float eps, const float (&g)[8]) {
   const float r = rsqrtf(squares * (1.f / HD) + eps);
-  float g[8];
-  load4<false>(gain, d.e0, g);
-  load4<false>(gain, d.e1, g + 4);
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
+}
+CBT_D void load_gain(const uint16_t* gain, const LaneDims& d, float (&g)[8]) {
+  load4<false>(gain, d.e0, g);
+  load4<false>(gain, d.e1, g + 4);
 }
 // turns a head's pairs; kHalfOdd exchanges through hx, HD floats of shared memory of the head's own
 template <int HD, int MODE>
@@ -180,7 +183,12 @@ CBT_D void rotate_heads(const A& a, int t, int h0, int h1, float* xs) {
   const int page = a.kv.page_tokens, id = slot / page, o = slot - id * page, H = a.n_heads;
   uint16_t* qdst = a.q_out + t * a.q_ld;
   uint16_t* kdst = k_row(a, id, o);
-  const bool norm = a.q_gain || a.k_gain;
+  // One gain for all heads is held; two take their turns (held, their registers cost more than the loads:
+  // 41 us for 39.4 in the append to bf16 pages).
+  constexpr bool kQOnly = !std::is_same<A, RopeAppend>::value;
+  const bool norm = a.q_gain || (!kQOnly && a.k_gain);
+  float g[8];
+  if (kQOnly && a.q_gain) load_gain(a.q_gain, dims, g);
   for (int hb = h0; hb < h1; hb += NH * kUnroll) {
     Four<F32> now[kUnroll][2];
 #pragma unroll
@@ -198,7 +206,10 @@ CBT_D void rotate_heads(const A& a, int t, int h0, int h1, float* xs) {
       if (norm) {
         const float s = head_squares<HD>(x);
         const uint16_t* gain = h < H ? a.q_gain : a.k_gain;
-        if (gain) scale_head<HD>(x, s, a.eps, gain, dims);
+        if (gain) {
+          if (!kQOnly) load_gain(gain, dims, g);
+          scale_head<HD>(x, s, a.eps, g);
+        }
       }
       turn_head<HD, MODE>(x, cs, sn, l, turned, rot, xs + sub * HD);
       if (h < h1) {
