@@ -34,7 +34,7 @@ static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * kRegs, "regist
 constexpr float kHead = 6.f, kSlack = 9.f;
 
 // Shared memory: the tiles of Q, K and V, then this
-constexpr int kBars = 3 + 2 * kStages + 2 * kVSlots + 12;
+constexpr int kBars = 5 + 2 * kStages + 2 * kVSlots + 12;
 struct Tail {
   uint64_t bars[kBars];
   uint32_t tmem_slot;
@@ -92,19 +92,17 @@ CBT_D uint32_t largest_bf16(uint32_t a, uint32_t b) {
   asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part
+// A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part.  A tile
+// lands as rows of q in the bytes that its codes take: boxes of 64 dims, [128 rows][128 bytes], swizzled.
+constexpr int kQBox = kRows * 128;
 template <int HD>
 struct QRow {
   uint32_t c[HD / 2];
   float unit;  // of the row's scores, in log2 units
-  CBT_D void fetch(const Attn& a, const Unit& u, int x, int TQ, int G, int row) {
-    const int tok = x * TQ + row / G;
-    const bool live = row < TQ * G && tok < u.n;
-    const uint4* src =
-        reinterpret_cast<const uint4*>(a.q + (u.t0 + tok) * a.q_ld + (long long)(u.g * G + row % G) * HD);
+  CBT_D void load(const uint8_t* q, int row) {
 #pragma unroll
     for (int j = 0; j < HD / 8; ++j) {
-      const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+      const uint4 v = *reinterpret_cast<const uint4*>(q + j / 8 * kQBox + tc::swz<128>(row, 16 * (j % 8)));
       c[4 * j] = v.x;
       c[4 * j + 1] = v.y;
       c[4 * j + 2] = v.z;
@@ -139,7 +137,9 @@ struct QRow {
       for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
     }
   }
-  CBT_D void store(uint8_t* q, uint32_t part_bytes, int row) const {
+  // the whole tile has been loaded where a row's codes lie among other rows' q (head_dim 64)
+  CBT_D void store(uint8_t* q, int row) const {
+    constexpr int part_bytes = kRows * HD;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -148,6 +148,25 @@ struct QRow {
             make_uint4(c[8 * j + 2 * p], c[8 * j + 2 * p + 1], c[8 * j + 4 + 2 * p], c[8 * j + 5 + 2 * p]);
   }
 };
+// a tile of Q from q to codes, by 128 threads (which meet at named barrier `id`), thread = row
+template <int HD>
+CBT_D void split_tile(const Attn& a, uint8_t* tile, float* row_unit, int row, int id) {
+  QRow<HD> q;
+  q.load(tile, row);
+  if (HD == 64) tc::named_bar_sync(id, 128);
+  q.split(a);
+  q.store(tile, row);
+  row_unit[row] = q.unit;
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
+CBT_D void tma_load_q(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int head, int tok) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(head), "r"(tok)
+      : "memory");
+}
 // the first unit behind k that has steps, or count
 CBT_D int next_with_steps(const Unit* units, int k, int count) {
   do ++k;
@@ -170,7 +189,8 @@ CBT_D void add2(float2& s, float a, float b) {
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_prefill_fp8(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    k_prefill_fp8(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ Attn a, const int runs, const int most, float* __restrict__ part_o,
                   float2* __restrict__ part_ml) {
   constexpr uint32_t kPart = kRows * HD;     // one part of a Q tile
@@ -187,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sV16 = sV + kStages * kKV;     // [slot][HD dims][64 keys]
   Tail& tail = *reinterpret_cast<Tail*>(sV16 + kVSlots * kV16);
   uint64_t* bars = tail.bars;
-  // Q of a tile is there, all are done with Q; a stage has landed, both tiles and the conversion are done
-  // with it; V in fp16 is there, both tiles are done with it
-  uint64_t *qfull = bars, *qempty = bars + 2, *full = bars + 3, *empty = full + kStages;
+  // q of a tile has landed, it is split, all are done with Q; a stage has landed, both tiles and the
+  // conversion are done with it; V in fp16 is there, both tiles are done with it
+  uint64_t *q_in = bars, *qfull = bars + 2, *qempty = bars + 4, *full = bars + 5, *empty = full + kStages;
   uint64_t *v_full = empty + kStages, *v_empty = v_full + kVSlots;
   // [tile]: S is there, S has been taken; [tile][buffer]: P is there, P has been read (and its product is
   // in O)
@@ -203,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int TQ = kRows / G;  // tokens per tile
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&qfull[i], 4);            // the converting warps
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&qfull[i], 4);            // the warps that split it
     tc::mbar_init(qempty, 2 + 8);                                       // issuers, softmax warps
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2 + 4);  // issuers, converting warps
     for (int i = 0; i < kVSlots; ++i) tc::mbar_init(&v_full[i], 4);
@@ -211,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);
     *abort_flag = 0;
     tc::mbar_fence_init();
+    tc::tma_prefetch_desc(&tq);
     tc::tma_prefetch_desc(&tk);
     tc::tma_prefetch_desc(&tv);
   }
@@ -374,34 +395,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     int st = 0, slot = 0;
     uint32_t ph = 0, vp = 0, qp = 0;
     bool ok = true;
-    // The next unit's first tile of Q is fetched and split while the last steps of this one run; the first
-    // unit's are the softmax's
-    QRow<HD> q;
+    uint32_t qi = 0, asked = 0;  // phases of q_in, and which have been asked for
     const int first = next_with_steps(units, -1, count);
 #pragma unroll 1
-    for (int k = first; k < count && ok;) {
+    for (int k = first; k < count && ok; k = uniform(next_with_steps(units, k, count))) {
       const Work<Attn> w(units + k, a);
-      if (k != first) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp, abort_flag));
-        if (!ok) break;
-        qp ^= 1;
+      const int tiles = w.u.n > TQ ? 2 : 1;
+      if (k != first) ok = __all_sync(0xffffffffu, wait_or_abort(qempty, qp, abort_flag));
+      if (!ok) break;
+      if (k != first) qp ^= 1;
+      if (warp == 12 && elect_one()) {
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          if (x * TQ < w.u.n) {
-            if (x) {
-              q.fetch(a, w.u, 1, TQ, G, row);
-              q.split(a);
-            }
-            q.store(sQ + x * 2 * kPart, kPart, row);
-            tail.row_unit[x][row] = q.unit;
-            tc::fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&qfull[x]);
+        for (int x = 0; x < tiles; ++x) {
+          tc::mbar_expect_tx(&q_in[x], HD / 64 * G * TQ * 128);
+#pragma unroll
+          for (int h = 0; h < HD / 64; ++h)
+            tma_load_q(sQ + x * 2 * kPart + h * kQBox, &tq, &q_in[x], h * 64, w.u.g * G, w.u.t0 + x * TQ);
         }
       }
-      k = uniform(next_with_steps(units, k, count));
-      const int fetch_at = k < count ? max(0, w.steps - 6) : w.steps, split_at = min(fetch_at + 1, w.steps - 1);
+      qi ^= tiles == 2 ? 3 : 1;
+      asked |= tiles == 2 ? 3 : 1;
+      // the first unit's are split by the softmax's warps, which have nothing else to do
+#pragma unroll 1
+      for (int x = 0; x < 2 && k != first && ok; ++x) {
+        if (x < tiles) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(&q_in[x], (qi >> x & 1) ^ 1, abort_flag));
+          if (!ok) break;
+          split_tile<HD>(a, sQ + x * 2 * kPart, tail.row_unit[x], row, 1);
+        }
+        if (lane == 0) tc::mbar_arrive(&qfull[x]);
+      }
 #pragma unroll 1
       for (int i = 0; i < w.steps && ok; ++i) {
         // the step has landed, and its slot is free again
@@ -441,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         vp ^= slot == 0;
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0;
-        if (i == fetch_at) q.fetch(a, units[k], 0, TQ, G, row);
-        if (i == split_at && k < count) q.split(a);
       }
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 33);
+    // no copies in flight at exit
+    if (warp == 12 && lane < 2 && asked >> lane & 1) wait_landed(&q_in[lane], (qi >> lane & 1) ^ 1);
   } else {
     // ---- softmax of tile x: thread = row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -455,18 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qp = 0;  // phase of Q
     int done = 0;     // steps that the tile took part in
     bool ok = true;
-    // the first unit's Q, which nothing runs ahead of
-    if (const int first = next_with_steps(units, -1, count); first < count) {
-      const Unit u = units[first];
-      if (x * TQ < u.n) {
-        QRow<HD> q;
-        q.fetch(a, u, x, TQ, G, row);
-        q.split(a);
-        q.store(sQ + x * 2 * kPart, kPart, row);
-        tail.row_unit[x][row] = q.unit;
-        tc::fence_proxy_async_smem();
+    if (const int first = next_with_steps(units, -1, count); first < count) {  // the first unit's Q
+      if (x * TQ < units[first].n) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&q_in[x], 0, abort_flag));
+        if (ok) split_tile<HD>(a, sQ + x * 2 * kPart, tail.row_unit[x], row, 2 + x);
       }
-      __syncwarp();
       if (lane == 0) tc::mbar_arrive(&qfull[x]);
     }
     // rows of out on 32-byte boundaries: whole sectors a store
@@ -621,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HD>
-cudaError_t launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Attn& a, int num_sms,
+                      cudaStream_t s) {
   constexpr size_t smem = smem_bytes<HD>();
   cudaError_t rc = cudaFuncSetAttribute(k_prefill_fp8<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (rc != cudaSuccess) return rc;
@@ -641,8 +658,8 @@ cudaError_t launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Attn& 
   float* po = reinterpret_cast<float*>(a.ws);
   const size_t parts = (size_t)a.tokens * a.n_heads * runs;
   float2* pml = reinterpret_cast<float2*>(a.ws + parts * HD * sizeof(float));
-  rc = launch_pdl(k_prefill_fp8<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tk, tv, a, runs, (int)units, po,
-                  pml);
+  rc = launch_pdl(k_prefill_fp8<HD>, dim3((unsigned)grid), dim3(kThreads), smem, s, tq, tk, tv, a, runs, (int)units,
+                  po, pml);
   if (rc != cudaSuccess || runs == 1) return rc;
   const long long pairs = (long long)a.tokens * a.n_heads;
   if (pairs <= kFewPairs && runs > kManyRuns)
@@ -658,7 +675,10 @@ size_t prefill_fp8_workspace(const Attn& a) {
 }
 
 cudaError_t launch_prefill_fp8(const Attn& a, int num_sms, cudaStream_t s) {
-  CUtensorMap tk, tv;
-  if (!fp8_maps(a.kv, &tk, &tv)) return cudaErrorInvalidValue;
-  return a.kv.head_dim == 128 ? launch_hd<128>(tk, tv, a, num_sms, s) : launch_hd<64>(tk, tv, a, num_sms, s);
+  CUtensorMap tq, tk, tv;
+  const int G = a.n_heads / a.kv.n_kv_heads;
+  if (!fp8_maps(a.kv, &tk, &tv) ||
+      !make_tmap_rows(&tq, a.q, a.kv.head_dim, a.n_heads, a.tokens, a.q_ld, G, kRows / G))
+    return cudaErrorInvalidValue;
+  return a.kv.head_dim == 128 ? launch_hd<128>(tq, tk, tv, a, num_sms, s) : launch_hd<64>(tq, tk, tv, a, num_sms, s);
 }
