@@ -7,10 +7,10 @@
 // own, so that nothing but a last rounding is lost:
 //   q   two parts (bf16 has eight bits of mantissa, a part four): exact down to 2^-12 of the head's largest
 //       element, off by at most 2^-22 of it below;
-//   p   three: 2^-12 of each weight, 2^-26 of the largest.
+//   p   four, of the weight in fp16: 2^-11 of each weight, 2^-22 of the reference's.
 // A block's scales are powers of two.  K's multiplies its scores; V's is an addition to them, in units of
-// log2: the weights are 2^(s_j + e_j - m), e_j the exponent of j's block, m the largest s_j + e_j so far,
-// and the sum l takes them times 2^-e_j.  (e in [-56, 56], so both hold in fp32.)
+// log2: the weights are 2^(s_j + e_j - m), e_j the exponent of j's block, m near the largest s_j + e_j so
+// far, and the sum l takes them times 2^-e_j.  (e in [-56, 56], so both hold in fp32.)
 //
 // Bound by HBM: 2 head_dim bytes of K and V per position and kv head.  Items, runs and their join are
 // those of paged_split.cuh.
@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kCompute = 128;  // warps 0..3; warp 4 requests tiles
 constexpr int kIssuers = 2;    // threads that issue half of each contraction's MMAs
-constexpr int kParts = 3;      // of a weight
+constexpr int kParts = 4;      // of a weight
 using Attn = PagedAttnFp8;
 
 template <int HD, int GT>
@@ -36,6 +36,28 @@ struct Shape {
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kCtas * kCols <= 512, "shared and tensor memory");
 };
 
+// By how many powers of two weights may pass 1 (one whose score is the reference) before the reference is
+// raised: 2^8 is below the largest code.
+constexpr float kSlack = 8.f;
+constexpr float kPart = 16.f;  // of one part's unit to the next one's
+
+CBT_D uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+CBT_D uint16_t f16_to_e4m3(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// 16 (a - b), of two pairs of fp16
+CBT_D uint32_t rest16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}\n" : "=r"(r) : "r"(a), "r"(b), "r"(0x4C004C00u));
+  return r;
+}
+
 // What a chunk's requester hands to the softmax: the exponents of each half's K and V scales
 struct Scales {
   int k[2], v[2];
@@ -48,8 +70,6 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
                  const __grid_constant__ Attn a, float* __restrict__ part_o, float2* __restrict__ part_ml) {
   using S = Shape<HD, GT>;
   constexpr uint32_t kIdescS = tc::idesc_e4m3(128, S::kNQ), kIdescO = tc::idesc_e4m3(128, S::kNP);
-  constexpr float kUnit = 256.f;   // a weight of 1 in units of its first part
-  constexpr float kPart = 16.f;    // of one part's unit to the next one's
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -64,10 +84,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
   Scales* scales = reinterpret_cast<Scales*>(bars + 6);  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scales + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* vis = tmem_slot + 2;                        // [4] visible keys of the chunk
-  float* red = reinterpret_cast<float*>(tmem_slot + 6); // [4 warps][8 heads]
-  float* red2 = red + 32;
-  float* l_run = red2 + 32;                             // [8]
+  float* red = reinterpret_cast<float*>(tmem_slot + 2); // [4 warps][8 heads]
+  float* l_run = red + 32;                              // [8]
   float* q_unit = l_run + 8;                            // [8] a score's unit, in log2 units
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -188,6 +206,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
   } else {
     uint32_t n = 0;  // chunks done
     bool ok = true;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const float scale2 = a.scale * kLog2e;  // scores in units of log2
     constexpr int kQUnits = HD / 8;         // 16-byte pieces of a head
     const int qh = tid / kQUnits, qu = tid % kQUnits;
@@ -256,13 +275,34 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         nxt = item_at(cur, a, lay.groups, it);
         qv = load_q(nxt);
       }
-      if (tid < 8) l_run[tid] = 0.f;
-      float m_run[GT], oacc[GT];
+      // The reference is the first chunk's largest s + e, and is raised where one passes it by more than
+      // kSlack: so O stays in tensor memory over the item's chunks, and most chunks look for no maximum.
+      // m_run is kept by every thread, each from the same values in the same order; l_own are its own keys'
+      float m_run[GT], oacc[GT], l_own[GT];
+      uint32_t acc = 0;  // O in tensor memory holds something
 #pragma unroll
       for (int h = 0; h < GT; ++h) {
-        m_run[h] = -INFINITY;  // kept by every thread, each from the same values in the same order
-        oacc[h] = 0.f;
+        m_run[h] = -INFINITY;
+        oacc[h] = l_own[h] = 0.f;
       }
+      // this thread's dim of O, from its parts
+      auto add_o = [&]() {
+        uint32_t o1[S::kNP], o2[S::kNP];
+#pragma unroll
+        for (int k = 0; k < S::kNP; k += 16) {
+          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + k, o1 + k);
+          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + S::kNP + k, o2 + k);
+        }
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          float o = 0.f;
+#pragma unroll
+          for (int k = kParts - 1; k >= 0; --k)
+            o = fmaf(o, 1.f / kPart, __uint_as_float(o1[k * GT + h]) + __uint_as_float(o2[k * GT + h]));
+          oacc[h] += o;
+        }
+      };
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(1, kCompute);
 
@@ -287,105 +327,108 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         const int k0 = w.seen.chunk(i) * kSub;
         const bool valid = sees(k0 + tid, w.p, a.window, a.sinks);
         const uint32_t vb = __ballot_sync(0xffffffffu, valid);
-        if (lane == 0) vis[warp] = vb;
         const float k_unit = pow2_of(scales[n & 1].k[tid >> 6]);
         const int ve = scales[n & 1].v[tid >> 6];
-        const bool bad_s = !wait_or_abort(bar_s, n & 1, abort_flag);
-        if (tc::named_bar_any(2, kCompute, bad_s)) {
-          ok = false;
-          break;
-        }
+        const float v_down = pow2_of(-ve);
+        bool bad = !wait_or_abort(bar_s, n & 1, abort_flag);
+        __syncwarp();
         tc::tc_fence_after();
         uint32_t raw[16], raw2[16];
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         tc::tmem_ld16(lane_base, raw);
         tc::tmem_ld16(lane_base + S::kNQ, raw2);
         tc::tmem_ld_wait();
-        float s[GT], mx[GT];
+        tc::tc_fence_before();
+        float s[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
           const float hi = __uint_as_float(raw[h]) + __uint_as_float(raw2[h]);
           const float lo = __uint_as_float(raw[GT + h]) + __uint_as_float(raw2[GT + h]);
           s[h] = valid ? fmaf(fmaf(lo, 1.f / kPart, hi) * k_unit, q_unit[h], (float)ve) : -INFINITY;
-          mx[h] = s[h];
         }
-        warp_reduce_n<GT, true>(mx);
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
-        }
-        tc::named_bar_sync(1, kCompute);
-        float scl[GT];
-#pragma unroll
-        for (int h = 0; h < GT; ++h) {
-          const float mloc = fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h]));
-          const float mo = m_run[h];
-          const float mn = fmaxf(mo, mloc);
-          scl[h] = mo == -INFINITY ? 0.f : ex2(mo - mn);
-          m_run[h] = mn;
-        }
-        float ps[GT];
-        const float v_down = pow2_of(-ve);
-        uint8_t* dst = sP + (tid & 15);
-#pragma unroll
-        for (int h = 0; h < GT; h += 2) {
-          float p[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
-            const int g = h + e < GT ? h + e : h;
-            p[e] = valid ? ex2(s[g] - (m_run[g] == -INFINITY ? 0.f : m_run[g])) : 0.f;
-          }
-          ps[h] = p[0] * v_down;
-          if (h + 1 < GT) ps[h + 1 < GT ? h + 1 : h] = p[1] * v_down;
-          p[0] *= kUnit;
-          p[1] *= kUnit;
-#pragma unroll
-          for (int k = 0; k < kParts; ++k) {
-            const uint16_t code = pack_e4m3(p[0], p[1]);
-            dst[tc::swz<128>(k * GT + h, tid & ~15)] = (uint8_t)code;
-            if (h + 1 < GT) dst[tc::swz<128>(k * GT + h + 1, tid & ~15)] = (uint8_t)(code >> 8);
-            const uint32_t back = e4m3_to_f16(code);
-            p[0] = (p[0] - f16_lo(back)) * kPart;
-            p[1] = (p[1] - f16_hi(back)) * kPart;
-          }
-        }
-        warp_reduce_n<GT, false>(ps);
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < GT; ++h) red2[warp * 8 + h] = ps[h];
-        }
-        if (vis[0] + 1 != 0 || vis[1] + 1 != 0 || vis[2] + 1 != 0 || vis[3] + 1 != 0) {
-          // masked keys: their V may hold anything, so it is zeroed (their weights are zero)
-          const bool bad_v = !wait_or_abort(vfull, n & 1, abort_flag);
-          if (tc::named_bar_any(2, kCompute, bad_v)) {
-            if (tid == 0) wait_timeout(a.err, abort_flag, 23);
-            ok = false;
-            break;
-          }
-          if (tid < HD) {
+        // the weights of the chunk before have been read
+        if (n) bad = bad || !wait_or_abort(bar_o, (n - 1) & 1, abort_flag);
+        __syncwarp();
+        if (vb != 0xffffffffu) {
+          // masked keys: their V may hold anything, so it is zeroed (their weights are zero), each warp its own
+          bad = bad || !wait_or_abort(vfull, n & 1, abort_flag);
+          __syncwarp();
+          uint8_t* v = sV + (warp >> 1) * S::kVHalf;
 #pragma unroll 1
-            for (int u = 0; u < 8; ++u) {  // 16 keys of this thread's dim
-              const uint32_t bits = (vis[u >> 1] >> (16 * (u & 1))) & 0xFFFFu;
-              if (bits == 0xFFFFu) continue;
-              uint4* at = reinterpret_cast<uint4*>(sV + (u >> 2) * S::kVHalf + tc::swz<64>(tid, 16 * (u & 3)));
-              const uint4 mk = code_mask(bits);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (bits) v = *at;
-              *at = make_uint4(v.x & mk.x, v.y & mk.y, v.z & mk.z, v.w & mk.w);
+          for (int u = 0; u < 2; ++u) {  // 16 keys
+            const uint32_t bits = (vb >> (16 * u)) & 0xFFFFu;
+            if (bits == 0xFFFFu) continue;
+            const uint4 mk = code_mask(bits);
+            for (int d = lane; d < HD; d += 32) {
+              uint4* at = reinterpret_cast<uint4*>(v + tc::swz<64>(d, 32 * (warp & 1) + 16 * u));
+              uint4 z = make_uint4(0, 0, 0, 0);
+              if (bits) z = *at;
+              *at = make_uint4(z.x & mk.x, z.y & mk.y, z.z & mk.z, z.w & mk.w);
             }
           }
         }
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        tc::named_bar_sync(1, kCompute);
-        if (tid < GT) {
-          float sc = scl[0];
+        bool raise = i == w.i0;
+#pragma unroll 1
+        for (;;) {
+          if (raise) {
+            float mx[GT];
 #pragma unroll
-          for (int h = 1; h < GT; ++h)
-            if (h == tid) sc = scl[h];
-          l_run[tid] = l_run[tid] * sc + red2[tid] + red2[8 + tid] + red2[16 + tid] + red2[24 + tid];
+            for (int h = 0; h < GT; ++h) mx[h] = s[h];
+            warp_reduce_n<GT, true>(mx);
+            if (lane == 0) {
+#pragma unroll
+              for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
+            }
+            tc::named_bar_sync(1, kCompute);
+            if (acc) {
+              tc::tc_fence_after();
+              add_o();
+              tc::tc_fence_before();
+              acc = 0;
+            }
+#pragma unroll
+            for (int h = 0; h < GT; ++h) {
+              const float mo = m_run[h];
+              const float mn = fmaxf(mo, fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])));
+              const float scl = mo == -INFINITY ? 0.f : ex2(mo - mn);
+              oacc[h] *= scl;
+              l_own[h] *= scl;
+              m_run[h] = mn;
+            }
+          }
+          bool over = false;
+          uint8_t* dst = sP + (tid & 15);
+          float p[GT];
+#pragma unroll
+          for (int h = 0; h < GT; ++h) {
+            // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
+            p[h] = valid ? ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h])) : 0.f;
+            over = over || s[h] > m_run[h] + kSlack;
+          }
+#pragma unroll
+          for (int h = 0; h < GT; h += 2) {
+            uint32_t y = pack_f16(p[h], h + 1 < GT ? p[h + 1 < GT ? h + 1 : h] : 0.f);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+              const uint16_t code = f16_to_e4m3(y);
+              dst[tc::swz<128>(k * GT + h, tid & ~15)] = (uint8_t)code;
+              if (h + 1 < GT) dst[tc::swz<128>(k * GT + h + 1, tid & ~15)] = (uint8_t)(code >> 8);
+              if (k + 1 < kParts) y = rest16(y, e4m3_to_f16(code));
+            }
+          }
+          tc::fence_proxy_async_smem();
+          if (!tc::named_bar_any(2, kCompute, bad || (over && !raise))) {
+#pragma unroll
+            for (int h = 0; h < GT; ++h) l_own[h] = fmaf(p[h], v_down, l_own[h]);
+            break;
+          }
+          // something has passed a reference, or has failed
+          if (tc::named_bar_any(2, kCompute, bad)) {
+            ok = false;
+            break;
+          }
+          raise = true;
         }
+        if (!ok) break;
         if (warp < kIssuers) {
           if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
             if (lane == 0) wait_timeout(a.err, abort_flag, 24);
@@ -396,36 +439,33 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
             for (int k = 0; k < kBlock / 32; ++k)
               tc::mma_e4m3(tmem + kIssuers * S::kNQ + S::kNP * warp,
                            tc::sdesc_rows<64>(tc::smem_u32(sV + warp * S::kVHalf)) + 2 * k,
-                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * (2 * warp + k), kIdescO, k > 0 ? 1u : 0u);
+                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * (2 * warp + k), kIdescO,
+                           acc || k > 0 ? 1u : 0u);
             tc::mma_commit(bar_o);
             tc::mma_commit(vempty);
           }
         }
-        const bool bad_o = !wait_or_abort(bar_o, n & 1, abort_flag);
-        if (tc::named_bar_any(2, kCompute, bad_o)) {
+        acc = 1;
+      }
+      if (!ok) break;
+      if (acc) {
+        const bool bad = !wait_or_abort(bar_o, (n - 1) & 1, abort_flag);
+        if (tc::named_bar_any(2, kCompute, bad)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        uint32_t o1[S::kNP], o2[S::kNP];
-#pragma unroll
-        for (int k = 0; k < S::kNP; k += 16) {
-          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + k, o1 + k);
-          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + S::kNP + k, o2 + k);
-        }
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int h = 0; h < GT; ++h) {
-          float o = 0.f;
-#pragma unroll
-          for (int k = kParts - 1; k >= 0; --k)
-            o = fmaf(o, 1.f / kPart, __uint_as_float(o1[k * GT + h]) + __uint_as_float(o2[k * GT + h]));
-          oacc[h] = fmaf(oacc[h], scl[h], o * (1.f / kUnit));
-        }
+        add_o();
         tc::tc_fence_before();
       }
-      if (!ok) break;
-      tc::named_bar_sync(1, kCompute);  // l_run is complete
+      warp_reduce_n<GT, false>(l_own);
+      if (lane == 0) {
+#pragma unroll
+        for (int h = 0; h < GT; ++h) red[warp * 8 + h] = l_own[h];
+      }
+      tc::named_bar_sync(1, kCompute);
+      if (tid < GT) l_run[tid] = (red[tid] + red[8 + tid]) + (red[16 + tid] + red[24 + tid]);
+      tc::named_bar_sync(1, kCompute);
       if (w.runs == 1) {
         if (tid < HD) {
 #pragma unroll
