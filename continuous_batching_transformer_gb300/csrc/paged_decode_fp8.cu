@@ -20,7 +20,6 @@
 namespace {
 
 constexpr int kCompute = 128;  // warps 0..3; warp 4 requests tiles
-constexpr int kIssuers = 2;    // threads that issue half of each contraction's MMAs
 constexpr int kParts = 4;      // of a weight
 using Attn = PagedAttnFp8;
 
@@ -28,11 +27,11 @@ template <int HD, int GT>
 struct Shape {
   static constexpr int kNQ = 16, kNP = kParts * GT <= 16 ? 16 : 32;  // columns of S^T and of O^T
   static constexpr int kK = kSub * HD, kVHalf = kBlock * HD, kQ = kNQ * HD, kP = kNP * kSub;
-  static constexpr uint32_t kCols = kIssuers * (kNQ + kNP) <= 64 ? 64 : 128;  // of tensor memory
+  static constexpr uint32_t kCols = kNQ + kNP <= 32 ? 32 : 64;  // of tensor memory: S^T, then O^T
   // V^T's halves span M = 128 rows: for head_dim 64 the second one's rows past 64 lie in what follows
   static constexpr int kTiles = kK + 2 * kVHalf + kQ + kP;
   static constexpr size_t kSmem = 1024 + (kTiles > kK + 3 * kVHalf ? kTiles : kK + 3 * kVHalf) + 1024;
-  static constexpr int kCtas = GT == 8 ? 4 : 5;  // of an SM
+  static constexpr int kCtas = 4;  // of an SM (five, with fewer registers, took up to 11 % longer, three 3 %)
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kCtas * kCols <= 512, "shared and tensor memory");
 };
 
@@ -92,8 +91,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
   const Layout lay = layout_of(a);
   const int per_row = a.kv.n_kv_heads * lay.groups;
   if (tid == 0) {
-    for (int i = 0; i < 6; ++i) tc::mbar_init(&bars[i], i < 2 ? 1 : kIssuers);
-    tc::mbar_init(kempty, kIssuers + 4);  // the MMAs, and every warp has seen that the tile was full
+    for (int i = 0; i < 6; ++i) tc::mbar_init(&bars[i], 1);
+    tc::mbar_init(kempty, 1 + 4);  // the MMAs, and every warp has seen that the tile was full
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tk);
@@ -287,19 +286,15 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
       }
       // this thread's dim of O, from its parts
       auto add_o = [&]() {
-        uint32_t o1[S::kNP], o2[S::kNP];
+        uint32_t part[S::kNP];
 #pragma unroll
-        for (int k = 0; k < S::kNP; k += 16) {
-          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + k, o1 + k);
-          tc::tmem_ld16(lane_base + kIssuers * S::kNQ + S::kNP + k, o2 + k);
-        }
+        for (int k = 0; k < S::kNP; k += 16) tc::tmem_ld16(lane_base + S::kNQ + k, part + k);
         tc::tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
           float o = 0.f;
 #pragma unroll
-          for (int k = kParts - 1; k >= 0; --k)
-            o = fmaf(o, 1.f / kPart, __uint_as_float(o1[k * GT + h]) + __uint_as_float(o2[k * GT + h]));
+          for (int k = kParts - 1; k >= 0; --k) o = fmaf(o, 1.f / kPart, __uint_as_float(part[k * GT + h]));
           oacc[h] += o;
         }
       };
@@ -311,15 +306,12 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
           if (lane == 0) wait_timeout(a.err, abort_flag, 22);
         } else {
           if (lane == 0) tc::mbar_arrive(kempty);
-          if (warp < kIssuers && elect_one()) {
+          if (warp == 0 && elect_one()) {
             tc::tc_fence_after();
-            constexpr int kSteps = HD / 32 / kIssuers;
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              const int kk = warp * kSteps + k;
-              tc::mma_e4m3(tmem + S::kNQ * warp, tc::sdesc_rows<HD>(tc::smem_u32(sK)) + 2 * kk,
-                           tc::sdesc_rows<HD>(tc::smem_u32(sQ)) + 2 * kk, kIdescS, k > 0 ? 1u : 0u);
-            }
+            for (int k = 0; k < HD / 32; ++k)
+              tc::mma_e4m3(tmem, tc::sdesc_rows<HD>(tc::smem_u32(sK)) + 2 * k,
+                           tc::sdesc_rows<HD>(tc::smem_u32(sQ)) + 2 * k, kIdescS, k > 0 ? 1u : 0u);
             tc::mma_commit(bar_s);
             tc::mma_commit(kempty);
           }
@@ -333,17 +325,15 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         bool bad = !wait_or_abort(bar_s, n & 1, abort_flag);
         __syncwarp();
         tc::tc_fence_after();
-        uint32_t raw[16], raw2[16];
+        uint32_t raw[16];
         tc::tmem_ld16(lane_base, raw);
-        tc::tmem_ld16(lane_base + S::kNQ, raw2);
         tc::tmem_ld_wait();
         tc::tc_fence_before();
         float s[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float hi = __uint_as_float(raw[h]) + __uint_as_float(raw2[h]);
-          const float lo = __uint_as_float(raw[GT + h]) + __uint_as_float(raw2[GT + h]);
-          s[h] = valid ? fmaf(fmaf(lo, 1.f / kPart, hi) * k_unit, q_unit[h], (float)ve) : -INFINITY;
+          const float both = fmaf(__uint_as_float(raw[GT + h]), 1.f / kPart, __uint_as_float(raw[h]));
+          s[h] = valid ? fmaf(both * k_unit, q_unit[h], (float)ve) : -INFINITY;
         }
         // the weights of the chunk before have been read
         if (n) bad = bad || !wait_or_abort(bar_o, (n - 1) & 1, abort_flag);
@@ -429,18 +419,15 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
           raise = true;
         }
         if (!ok) break;
-        if (warp < kIssuers) {
+        if (warp == 0) {
           if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
             if (lane == 0) wait_timeout(a.err, abort_flag, 24);
           } else if (elect_one()) {
             tc::tc_fence_after();
-            // issuer e: the half's two steps of 32 keys
 #pragma unroll
-            for (int k = 0; k < kBlock / 32; ++k)
-              tc::mma_e4m3(tmem + kIssuers * S::kNQ + S::kNP * warp,
-                           tc::sdesc_rows<64>(tc::smem_u32(sV + warp * S::kVHalf)) + 2 * k,
-                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * (2 * warp + k), kIdescO,
-                           acc || k > 0 ? 1u : 0u);
+            for (int k = 0; k < kSub / 32; ++k)
+              tc::mma_e4m3(tmem + S::kNQ, tc::sdesc_rows<64>(tc::smem_u32(sV + (k >> 1) * S::kVHalf)) + 2 * (k & 1),
+                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * k, kIdescO, acc || k > 0 ? 1u : 0u);
             tc::mma_commit(bar_o);
             tc::mma_commit(vempty);
           }
