@@ -3,8 +3,15 @@
 #pragma once
 #include "kernels.h"
 
+// How attention of single tokens cuts a row of n 128-key chunks into runs: up to `one` chunks are one run;
+// below `two` they go singly, below `four` by twos, from there on by fours (paged_split.cuh).
+struct RunRule {
+  int one, two, four;
+};
+
 // One layer's K and V in a pool of pages (cbt_paged_kv with every offset in bf16 elements)
 struct PagedKv {
+  static constexpr RunRule kRuns{3, 32, 96};
   uint16_t* pool;
   long long pool_elems, page_elems, k_off, v_off;
   int n_pages, page_tokens, n_kv_heads, head_dim;

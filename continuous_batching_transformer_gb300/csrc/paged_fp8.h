@@ -5,6 +5,7 @@
 
 // One layer's K and V in a pool of pages (cbt_paged_kv_fp8)
 struct PagedKvFp8 {
+  static constexpr RunRule kRuns{4, 5, 33};
   uint8_t* pool;
   long long pool_bytes, page_bytes, k_off, v_off, s_off;
   int n_pages, page_tokens, n_kv_heads, head_dim;

@@ -11,18 +11,28 @@ constexpr int kGroup = 8;      // q heads per item
 
 // Chunks of a run, by the chunks n that the row sees alone (so that its result does not depend on the
 // other rows).  Longer runs halve the partial outputs and their join; shorter ones spread a few rows
-// over the SMs: in us, 32 rows of 64 to 128 chunks 244 by fours, 251 by twos; one row of 64 chunks
-// 11.3 by fours, 10.4 by twos; 16 rows of 33 chunks 47.0 by twos, 48.3 singly.  Up to three chunks are
-// one run, which needs no join (one row of two chunks 6.4 against 7.4).
-CBT_HD int chunks_per_run(int n) { return n >= 96 ? 4 : n >= 32 ? 2 : n > 3 ? 1 : n > 0 ? n : 1; }
+// over the SMs.  Over bf16 pages, in us: 32 rows of 64 to 128 chunks 244 by fours, 251 by twos; one row of 64
+// chunks 11.3 by fours, 10.4 by twos; 16 rows of 33 chunks 47.0 by twos, 48.3 singly; one row of two chunks
+// 6.4 in one run, which needs no join, against 7.4.  Over 8-bit pages, where a chunk takes half the time and
+// its partial output as long: 32 rows of 64 to 128 chunks 126 by fours, 128 by twos; 16 rows of 33 chunks
+// 28.5 by fours, 29.3 by twos; 64 rows of 4 to 8 chunks 25.4 by twos, 31.6 singly; 256 rows of 1 to 4 chunks
+// 47.7 in one run, 54.0 singly from 4 on; one row of 8 chunks 8.3 by twos, 7.3 singly.
+template <class A>
+CBT_HD int chunks_per_run(int n) {
+  constexpr RunRule r = decltype(A::kv)::kRuns;
+  return n >= r.four ? 4 : n >= r.two ? 2 : n > r.one ? 1 : n > 0 ? n : 1;
+}
+template <class A>
 CBT_HD int runs_of(int n) {  // a row that sees nothing has one run, which writes its zeros
-  const int per = chunks_per_run(n);
+  const int per = chunks_per_run<A>(n);
   return n <= 0 ? 1 : (n + per - 1) / per;
 }
+template <class A>
 CBT_HD int most_runs(int n) {  // of any row that sees n chunks or fewer
-  int r = runs_of(n);
-  if (n >= 32) r = r > 31 ? r : 31;
-  if (n >= 96) r = r > 48 ? r : 48;
+  constexpr RunRule rule = decltype(A::kv)::kRuns;
+  int r = runs_of<A>(n);
+  for (const int below : {rule.two, rule.four})
+    if (n >= below && runs_of<A>(below - 1) > r) r = runs_of<A>(below - 1);
   return r;
 }
 
@@ -39,7 +49,7 @@ __host__ __device__ inline Layout layout_of(const A& a) {
     const long long w = ((long long)a.sinks + kSub - 1) / kSub + (a.window + kSub - 2) / kSub + 1;
     n = w < n ? (int)w : n;
   }
-  return {(G + kGroup - 1) / kGroup, most_runs(n)};
+  return {(G + kGroup - 1) / kGroup, most_runs<A>(n)};
 }
 
 // The rows' items in flat order, walked forward by a whole warp: lane i keeps row w0 + i and the
@@ -63,7 +73,7 @@ struct Cursor {
       if (row.bad && blockIdx.x == 0) set_device_error(a.err, CBT_DEV_LENGTH, b);
       if (row.n == 1) {
         seen = seen_chunks<kSub>(row.len - 1, row.len - 1, a.window, a.sinks);
-        n = runs_of(seen.n) * per_row;
+        n = runs_of<A>(seen.n) * per_row;
       }
     }
     int inc = n;
@@ -106,14 +116,14 @@ CBT_D Item item_at(const Cursor<A>& c, const A& a, int groups, int it) {
   w.seen.ns = __shfl_sync(0xffffffffu, c.seen.ns, src);
   w.seen.ws = __shfl_sync(0xffffffffu, c.seen.ws, src);
   w.seen.n = __shfl_sync(0xffffffffu, c.seen.n, src);
-  w.runs = runs_of(w.seen.n);
+  w.runs = runs_of<A>(w.seen.n);
   w.run = k % w.runs;
   k /= w.runs;
   const int G = a.n_heads / a.kv.n_kv_heads, j = k % groups;
   w.g = k / groups;
   w.head0 = w.g * G + j * kGroup;
   w.heads = min(kGroup, G - j * kGroup);
-  const int per = chunks_per_run(w.seen.n);
+  const int per = chunks_per_run<A>(w.seen.n);
   w.i0 = w.run * per;
   w.i1 = min(w.seen.n, w.i0 + per);
   return w;
@@ -146,7 +156,7 @@ __global__ void __launch_bounds__(128)
   const RowTokens row = row_tokens(a, b);
   if (row.n != 1) return;
   const Seen seen = seen_chunks<kSub>(row.len - 1, row.len - 1, a.window, a.sinks);
-  const int runs = runs_of(seen.n);
+  const int runs = runs_of<A>(seen.n);
   if (runs == 1) return;
   const size_t base = ((size_t)b * a.n_heads + h) * layout_of(a).max_runs;
   float m = -INFINITY, l = 0.f, acc[R];
