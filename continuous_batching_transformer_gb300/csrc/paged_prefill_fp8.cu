@@ -95,7 +95,8 @@ CBT_D uint32_t largest_bf16(uint32_t a, uint32_t b) {
   return r;
 }
 // A row of Q on its way: pairs of q; then, of every 8 elements, two words of codes of either part.  A tile
-// lands as rows of q in the bytes that its codes take: boxes of 64 dims, [128 rows][128 bytes], swizzled.
+// lands as rows of q, boxes of 64 dims, [128 rows][128 bytes], swizzled.  A row's codes take the bytes that
+// its q took: the parts one box each, or (head_dim 64) either half of a row.
 constexpr int kQBox = kRows * 128;
 template <int HD>
 struct QRow {
@@ -139,23 +140,25 @@ struct QRow {
       for (int j = 0; j < HD / 2; ++j) c[j] = 0x7F7F7F7Fu;
     }
   }
-  // the whole tile has been loaded where a row's codes lie among other rows' q (head_dim 64)
   CBT_D void store(uint8_t* q, int row) const {
-    constexpr int part_bytes = kRows * HD;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int j = 0; j < HD / 16; ++j)
-        *reinterpret_cast<uint4*>(q + p * part_bytes + tc::swz<HD>(row, 16 * j)) =
+        *reinterpret_cast<uint4*>(q + (HD == 128 ? p * kQBox : 0) + tc::swz<128>(row, (HD == 128 ? 0 : 64 * p) + 16 * j)) =
             make_uint4(c[8 * j + 2 * p], c[8 * j + 2 * p + 1], c[8 * j + 4 + 2 * p], c[8 * j + 5 + 2 * p]);
   }
 };
-// a tile of Q from q to codes, by 128 threads (which meet at named barrier `id`), thread = row
+// the 32-deep step `step` of a part, from the tile's start in 16-byte units
 template <int HD>
-CBT_D void split_tile(const Attn& a, uint8_t* tile, float* row_unit, int row, int id) {
+CBT_HD constexpr uint32_t q_step(int part, int step) {
+  return (uint32_t)(HD == 128 ? part * (kQBox >> 4) + 2 * step : 4 * part + 2 * step);
+}
+// a tile of Q from q to codes, by 128 threads, thread = row
+template <int HD>
+CBT_D void split_tile(const Attn& a, uint8_t* tile, float* row_unit, int row) {
   QRow<HD> q;
   q.load(tile, row);
-  if (HD == 64) tc::named_bar_sync(id, 128);
   q.split(a);
   q.store(tile, row);
   row_unit[row] = q.unit;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ Attn a, const int runs, const int most, float* __restrict__ part_o,
                   float2* __restrict__ part_ml) {
-  constexpr uint32_t kPart = kRows * HD;     // one part of a Q tile
+  constexpr uint32_t kTile = kRows * HD * 2; // of Q
   constexpr uint32_t kKV = kStep * HD;       // codes of K or V of a step
   constexpr uint32_t kV16 = HD * 128;        // V of a step in fp16
   constexpr uint32_t kIdescS = tc::idesc_e4m3(128, kStep), kIdescO = tc::idesc_f16(128, HD);
@@ -203,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sQ = smem;                     // [tile][part][128 rows][HD]
-  uint8_t* sK = sQ + 4 * kPart;           // [stage][64 keys][HD]
+  uint8_t* sQ = smem;                     // [tile]
+  uint8_t* sK = sQ + 2 * kTile;           // [stage][64 keys][HD]
   uint8_t* sV = sK + kStages * kKV;       // [stage][HD dims][64 keys]
   uint8_t* sV16 = sV + kStages * kKV;     // [slot][HD dims][64 keys]
   Tail& tail = *reinterpret_cast<Tail*>(sV16 + kVSlots * kV16);
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmem);
   pdl_wait();
-  static_assert(kScratch <= 4 * kPart, "the search fits where Q goes");
+  static_assert(kScratch <= 2 * kTile, "the search fits where Q goes");
   int count = find_units<kThreads>(a, units, sQ, tail.warp_sums, TQ, runs, most);
   tc::tc_fence_before();
   __syncthreads();
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- S of tile x, as soon as the softmax has taken the last one
       const int x = warp;
       const uint32_t s_tm = tmem + x * 128;
-      const uint32_t dq = tc::rows_lo<HD>(sQ + x * 2 * kPart), dk = tc::rows_lo<HD>(sK);
+      const uint32_t dq = tc::rows_lo<128>(sQ + x * kTile), dk = tc::rows_lo<HD>(sK);
       int st = 0, n = 0;  // stage, steps that the tile took part in
       uint32_t ph = 0, qp = 0;
 #pragma unroll 1
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 2 * (HD / 32); ++e) {
                 const int part = e / (HD / 32), step = e % (HD / 32);
-                tc::mma_e4m3(s_tm, tc::rows_desc<HD>(dq + part * (kPart >> 4) + 2 * step),
+                tc::mma_e4m3(s_tm, tc::rows_desc<128>(dq + q_step<HD>(part, step)),
                              tc::rows_desc<HD>(kd + 2 * step), kIdescS, e > 0 ? 1u : 0u);
               }
               tail.s_exps[x][n & 1] = exps;
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mbar_expect_tx(&q_in[x], HD / 64 * G * TQ * 128);
 #pragma unroll
           for (int h = 0; h < HD / 64; ++h)
-            tma_load_q(sQ + x * 2 * kPart + h * kQBox, &tq, &q_in[x], h * 64, w.u.g * G, w.u.t0 + x * TQ);
+            tma_load_q(sQ + x * kTile + h * kQBox, &tq, &q_in[x], h * 64, w.u.g * G, w.u.t0 + x * TQ);
         }
       }
       qi ^= tiles == 2 ? 3 : 1;
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x < tiles) {
           ok = __all_sync(0xffffffffu, wait_or_abort(&q_in[x], (qi >> x & 1) ^ 1, abort_flag));
           if (!ok) break;
-          split_tile<HD>(a, sQ + x * 2 * kPart, tail.row_unit[x], row, 1);
+          split_tile<HD>(a, sQ + x * kTile, tail.row_unit[x], row);
         }
         if (lane == 0) tc::mbar_arrive(&qfull[x]);
       }
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (const int first = next_with_steps(units, -1, count); first < count) {  // the first unit's Q
       if (x * TQ < units[first].n) {
         ok = __all_sync(0xffffffffu, wait_or_abort(&q_in[x], 0, abort_flag));
-        if (ok) split_tile<HD>(a, sQ + x * 2 * kPart, tail.row_unit[x], row, 2 + x);
+        if (ok) split_tile<HD>(a, sQ + x * kTile, tail.row_unit[x], row);
       }
       if (lane == 0) tc::mbar_arrive(&qfull[x]);
     }
@@ -651,10 +654,11 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   cudaError_t rc = cudaFuncSetAttribute(k_prefill_fp8<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (rc != cudaSuccess) return rc;
   // the warpgroups' shares come out of what a block is launched with: with less the kernel would wait
-  cudaFuncAttributes attr;
-  rc = cudaFuncGetAttributes(&attr, k_prefill_fp8<HD>);
-  if (rc != cudaSuccess) return rc;
-  if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;
+  static const int regs = [] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, k_prefill_fp8<HD>) == cudaSuccess ? attr.numRegs : 0;
+  }();
+  if (regs < kRegs) return cudaErrorInvalidConfiguration;
   const int G = a.n_heads / a.kv.n_kv_heads, run = 2 * (kRows / G);
   // most units: every row may end in a partly filled one
   const long long by_tokens = (long long)a.tokens / run + a.rows;
