@@ -154,7 +154,7 @@ class _Device:
         raw = torch._C._cuda_getCurrentRawStream(self.index)
         if raw not in self.streams:
             self.join(raw)
-        if torch.cuda.current_device() == self.index:
+        if torch._C._cuda_getDevice() == self.index:  # (torch.cuda.current_device without its checks)
             fn(args, raw)
         else:
             with torch.cuda.device(self.index):
@@ -486,7 +486,9 @@ class PageRead:
                 a.kv = c.layers[layer]
                 self._layer = layer
             a.out_stride = _rows(out, "v_out" if k_out is None else "k_out", _ROWS, dev, tokens, self.width)
-            if k_out is not None and v_out is not None and \
+            if k_out is not None and v_out is not None and not (
+                    v_out.shape == k_out.shape and v_out.dtype is k_out.dtype and v_out.get_device() == dev and
+                    v_out.is_contiguous() and k_out.is_contiguous()) and \
                     _rows(v_out, "v_out", (k_out.dtype,), dev, tokens, self.width) != a.out_stride:
                 raise ValueError("k_out and v_out: their rows have different strides")
             a.cu = _vec(cu, "cu", dev, c.rows + 1)
