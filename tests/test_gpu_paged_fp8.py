@@ -682,3 +682,95 @@ def test_another_stream():
         outs.append((out, k, v))
     for x, y in zip(*outs):
         assert torch.equal(x, y)
+
+
+# ---- far sizes ---------------------------------------------------------------------------------------
+def test_offsets_past_32_bits():
+    """A pool of more than 4 GB, its rows in the last pages: append, read back and attend there."""
+    H, kv, hd, page = 4, 2, 128, 64
+    lay = F.Layout(kv, hd, page)
+    n_pages = (1 << 32) // lay.page_bytes + 40
+    if torch.cuda.mem_get_info()[0] < 2 * n_pages * lay.page_bytes:
+        pytest.skip("not enough memory")
+    pool = torch.empty(n_pages * lay.page_bytes, dtype=torch.uint8, device=dev())
+    n = 300
+    ids = list(range(n_pages - 1, n_pages - 1 - 5, -1))
+    table = torch.tensor([ids], dtype=torch.int32, device=dev())
+    cache = paged.PagedKVFp8(pool, table, i32([n]), page_tokens=page, n_kv_heads=kv, head_dim=hd)
+    x = torch.randn(n, (H + 2 * kv) * hd, generator=torch.Generator().manual_seed(2)).bfloat16()
+    q = torch.empty(n, H, hd, dtype=torch.bfloat16, device=dev())
+    paged.RopeAppend(cache, None, n_heads=H)(0, x.to(dev()), i32(list(range(n))),
+                                             i32([ids[j // page] * page + j % page for j in range(n)]), q)
+    k, v = (torch.zeros(n, kv, hd, device=dev()) for _ in range(2))
+    paged.PageRead(cache)(0, k, v, i32([0, n]))
+    out = {}
+    for new in (1, 70):
+        out[new] = torch.zeros(new, H, hd, device=dev())
+        paged.Attention(cache, n_heads=H, max_kv=n, max_q=new, max_tokens=new)(
+            0, q[n - new:], out[new], None if new == 1 else i32([0, new]))
+    cache.check()
+    small = np.zeros(5 * lay.page_bytes, np.uint8)
+    heads = x.double().numpy().reshape(n, -1, hd)
+    F.append(small, lay, heads[:, H:H + kv], heads[:, H + kv:], list(range(n)))
+    want_k, want_v = F.values(small, lay, np.arange(5), n)
+    assert (k.double().cpu().numpy() == want_k.transpose(1, 0, 2)).all()
+    assert (v.double().cpu().numpy() == want_v.transpose(1, 0, 2)).all()
+    for new, o in out.items():
+        ref, mag = R.attention(heads[n - new:, :H], want_k, want_v, n - new, 0, 0, 1 / math.sqrt(hd))
+        check_attention(o, ref, mag, np.full(mag.shape[:2], 2.0 ** -12), torch.float32)
+
+
+def test_many_rows():
+    """More rows than are ranked, and more units than one round of them a block holds."""
+    run_attention([(i % 7, 1 + i % 3) for i in range(90)], 2, 1, 64, 64, seed=5)
+    r = random.Random(3)
+    run_attention([(r.randint(0, 3), r.randint(0, 2)) for _ in range(4096)], 2, 2, 64, 64, max_q=2, seed=6)
+    run_attention([(r.randint(0, 200), 1) for _ in range(500)], 3, 1, 64, 64, decode=True, seed=7)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 9, 20, 64])
+def test_heads_of_a_kv_head(G):
+    run_attention([(130, 1), (64, 1)], 2 * G, 2, 128, 64, decode=True, seed=G)
+    run_attention([(130, 40), (0, 70)], 2 * G, 2, 128, 64, seed=G)
+    run_attention([(130, 40)], G, 1, 64, 64, seed=G, window=50, sinks=3)
+
+
+@pytest.mark.parametrize("sinks", [0, 1, 64, 65, 200])
+@pytest.mark.parametrize("window", [1, 63, 64, 65, 200])
+def test_windows_and_sinks(window, sinks):
+    """Tiles whose tokens' windows begin in different steps, sinks that reach into them, runs cut anywhere."""
+    run_attention([(700, 100), (0, 300), (129, 1)], 2, 1, 64, 64, window=window, sinks=sinks, seed=window)
+    run_attention([(3000, 4)], 2, 1, 64, 64, window=window * 10, sinks=sinks, seed=sinks)
+    run_attention([(700, 1), (0, 1), (129, 1)], 2, 1, 64, 64, window=window, sinks=sinks, seed=window, decode=True)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_scores_that_rise_along_the_row(decode):
+    """Each step's scores pass the last one's reference, V's exponents change with every block."""
+    hd, n = 64, 1400
+    r = np.random.default_rng(8)
+    sharp = np.zeros(hd)
+    sharp[3] = 1.0
+    pool, table, k, v = planted(n, hd, lambda j: sharp * (j // 64) * 12.0,
+                                lambda j: r.standard_normal(hd) * 2.0 ** (j // 64 * 7 % 23 - 11))
+    q = torch.zeros(1, 2, hd, dtype=torch.bfloat16)
+    q[0, 0, 3], q[0, 1, 3] = 8.0, -8.0   # rising, and falling
+    got = attend(pool, table, n, q, 1, hd, decode)
+    ref, mag = R.attention(q.double().numpy(), k, v, n - 1, 0, 0, 1 / math.sqrt(hd))
+    # scores up to 252: a few dozen roundings of 2^-24 of that
+    assert (np.abs(got - ref) <= (WEIGHT + 4 * SCORE) * mag + 2.0 ** -20 * mag.max()).all()
+
+
+def test_append_of_every_rotary_form():
+    for hd in (64, 128):
+        for mode, rot in (("none", hd), ("half", hd), ("half", 8), ("half", hd // 2), ("half", 22), ("interleaved", hd),
+                          ("interleaved", 10), ("interleaved", 2)):
+            for dtype in (torch.float32, torch.bfloat16):
+                run_append(runs=[span(9, 30), span(70, 100), [200]], hd=hd, page=64, mode=mode, rot=rot, dtype=dtype,
+                           H=3, kv=1, seed=rot)
+
+
+def test_append_far_positions():
+    """Angles of positions up to 2^31 - 1 keep their fraction of a turn."""
+    run_append(runs=[[5], [70], [130], [195], [260]], hd=128, page=64,
+               positions=[2 ** 31 - 1, 2 ** 30 + 12345, 1000003, 7, 0])
