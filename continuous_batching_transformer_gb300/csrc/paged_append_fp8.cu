@@ -15,16 +15,14 @@
 //      on the way and written 16 positions at a time where a run fills them.
 // No thread block shares a cache block with another, so nothing is exchanged through memory.
 //
-// HBM is the floor.  8192 tokens of 32 q and 8 kv heads of 128 with norms take 49.5 us, 2.9 TB/s, over bf16
-// pages 40: issue slots (62 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
-// 31 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 7.5 us: one
+// HBM is the floor.  8192 tokens of 32 q and 8 kv heads of 128 with norms take 52 us, 2.8 TB/s, over bf16
+// pages 40: issue slots (68 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
+// 35 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 8 us: one
 // such chain.
 #include "paged_fp8.h"
 #include "paged_rope.cuh"
 
 namespace {
-
-constexpr float kTop = 448.f;
 
 // sin and cos of the 256 whole fractions of a turn, for turn_sincos
 struct Circle {
@@ -49,9 +47,9 @@ CBT_D float2 circle_at(int k) {
   return make_float2(quarter & 2 ? -a : a, (quarter + 1) & 2 ? -b : b);
 }
 // sin and cos of pos * turns (a fraction of a turn, 2^64 a whole) to fp32's last place or so: the nearest
-// entry, turned by the rest (at most pi / 256, where two terms of the series are enough).  A rounding to
-// three bits of mantissa shows no more than this costs: with the hardware's sine, off by 2^-21, a few more
-// codes in a million fall on the other side of a border than the formula's.
+// entry, turned by the rest (at most pi / 256, where two terms of the series are enough).  (The hardware's sine,
+// off by 2^-21, takes 1.5 us less for 8192 tokens of 8 heads of 128, and with it 45 codes of 8.4 million lie beside
+// the formula's for 5.)
 CBT_D void turn_sincos(const Circle& circle, uint32_t pos, uint64_t turns, float* sn, float* cs) {
   const uint32_t ph = pos * (uint32_t)(turns >> 32) + __umulhi(pos, (uint32_t)turns);  // 2^32 a turn
   const uint32_t k = ph + (1u << 23);
@@ -87,6 +85,62 @@ CBT_D int exponent_for(float top) {
 CBT_D uint32_t move_codes(uint32_t w, float f) {
   const uint32_t lo = e4m3_to_f16((uint16_t)w), hi = e4m3_to_f16((uint16_t)(w >> 16));
   return pack_e4m3(f16_lo(lo) * f, f16_hi(lo) * f) | (uint32_t)pack_e4m3(f16_lo(hi) * f, f16_hi(hi) * f) << 16;
+}
+
+// How far above the start of the range around the middle between two codes (of any scale: a code's last bit is
+// the fourth of its mantissa) in which what fp32 is off by may decide where it is rounded to
+// Such values are formed again in 64 bits (a warp has one in 400 of its steps): what is left are a few small
+// members of their pairs, where fp32 is off by more steps.  8.4 million codes: 5 beside the formula's for 13, at 2 us
+// of 62 for the look at each value.
+constexpr uint32_t kNear = 6;  // steps of fp32 on either side
+CBT_D uint32_t above_middle(float x) { return __float_as_uint(x) * 4096u + ((kNear - 0x80000u) << 12); }
+CBT_D bool near_middle(uint32_t above) { return above < (2 * kNear) << 12; }
+template <bool F32>
+CBT_D double element(const void* p, long long i) {
+  return F32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
+}
+// The values of K head g of token t that lie so, from 64 bits rounded to odd; by all lanes of a warp
+template <int HD, bool F32, int MODE>
+CBT_D void settle(const RopeAppendFp8& a, int t, int g, int l, const LaneDims& dims, bool on, float (&x)[8]) {
+  unsigned near = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (on && near_middle(above_middle(x[k]))) near |= 1u << k;
+  const long long row = t * a.qkv_ld + (long long)(a.n_heads + g) * HD;
+  double r = 1.0;
+  if (a.k_gain) {
+    double s = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const double y = element<F32>(a.qkv, row + 8 * l + k);
+      s = fma(y, y, s);
+    }
+#pragma unroll 1
+    for (int w = HD / 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    r = rsqrt(s / HD + (double)a.eps);
+  }
+  auto value = [&](int d) {
+    const double y = element<F32>(a.qkv, row + d) * r;
+    return a.k_gain ? y * element<false>(a.k_gain, d) : y;
+  };
+  const int rot = MODE == kNone ? 0 : a.rope.rot_dim;
+#pragma unroll 1
+  for (; near; near &= near - 1) {
+    const int k = __ffs(near) - 1, d = k < 4 ? dims.e0 + k : dims.e1 + k - 4;
+    double y = value(d);
+    if (d < rot) {
+      const bool second = MODE == kInter ? d & 1 : d >= rot / 2;
+      const int pair = MODE == kInter ? d / 2 : second ? d - rot / 2 : d;
+      const int other = MODE == kInter ? d ^ 1 : second ? pair : d + rot / 2;
+      double sn, cs;  // of a phase of 2^64 a turn
+      sincospi((double)(int64_t)((uint64_t)a.positions[t] * a.rope.turns[pair]) * 0x1p-63, &sn, &cs);
+      y = (y * cs + (second ? sn : -sn) * value(other)) * a.rope.mscale;
+    }
+    float f = __double2float_rz(y);
+    if ((double)f != y) f = __uint_as_float(__float_as_uint(f) | 1u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j == k ? f : x[j];
+  }
 }
 
 constexpr int kMostChunk = 64;             // tokens whose runs a thread block takes
@@ -332,6 +386,13 @@ CBT_D void append_runs(const RopeAppendFp8& a, int t0, int chunk, int g0, int g1
           }
         } else {
           turn(x[u], pos[u]);
+          if (!V && (MODE != kNone || a.k_gain)) {
+            uint32_t least = above_middle(x[u][0]);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) least = min(least, above_middle(x[u][k]));
+            if (__any_sync(0xffffffffu, near_middle(least)))
+              settle<HD, F32, MODE>(a, t0 + (run[u] >= 0 ? i : 0), g, l, dims, run[u] >= 0, x[u]);
+          }
           top = top_of(x[u]);
           v[u] = make_uint4(pack_odd(x[u][0], x[u][1]), pack_odd(x[u][2], x[u][3]), pack_odd(x[u][4], x[u][5]),
                             pack_odd(x[u][6], x[u][7]));
