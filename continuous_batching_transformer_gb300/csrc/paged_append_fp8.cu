@@ -16,8 +16,8 @@
 // No thread block shares a cache block with another, so nothing is exchanged through memory.
 //
 // HBM is the floor.  8192 tokens of 32 q and 8 kv heads of 128 with norms take 52 us, 2.8 TB/s, over bf16
-// pages 40: issue slots (68 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
-// 35 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 8 us: one
+// pages 40: issue slots (67 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
+// 34 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 8 us: one
 // such chain.
 #include "paged_fp8.h"
 #include "paged_rope.cuh"
