@@ -48,16 +48,6 @@ struct Shape {
 constexpr float kSlack = 8.f;
 constexpr float kPart = 16.f;  // of one part's unit to the next one's
 
-CBT_D uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-CBT_D uint16_t f16_to_e4m3(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
 // 16 (a - b), of two pairs of fp16
 CBT_D uint32_t rest16(uint32_t a, uint32_t b) {
   uint32_t r;

@@ -83,17 +83,6 @@ struct TileSteps {
   CBT_D bool need(int i) const { return i < end && !(i >= hole0 && i < hole1); }
 };
 
-CBT_D uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-CBT_D uint16_t f16_to_e4m3(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
 CBT_D uint32_t sub_f16(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
