@@ -390,7 +390,7 @@ class Attention:
 
     max_kv, max_q  upper bounds of a row's positions and query tokens.  With max_q > 1 they also decide how
                  the work is cut: bounds far above the rows cost time.  Weights are then rounded to
-                 bf16, which with max_q == 1 they are not
+                 bf16, which with max_q == 1 they are not (over a PagedKVFp8: to fp16 in either case)
     max_tokens     most rows of q in a call (default: the cache's rows, one token each)
     window, sinks  0: causal; else position p sees j > p - window and j < sinks
     Calls of one handle share its workspace: they may not overlap on the GPU (two streams, or two
