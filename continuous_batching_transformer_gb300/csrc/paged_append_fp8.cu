@@ -17,7 +17,7 @@
 //
 // HBM is the floor.  8192 tokens of 32 q and 8 kv heads of 128 with norms take 52 us, 2.8 TB/s, over bf16
 // pages 40: issue slots (67 % taken) and the chains of loads and barriers of a block bound it together, DRAM is
-// 34 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 8 us: one
+// 34 % busy.  8 tokens of them take 4 us, 800 tokens of 12 and 4 heads of 64 in runs of up to 177 7.3 us: one
 // such chain.
 #include "paged_fp8.h"
 #include "paged_rope.cuh"
@@ -49,7 +49,7 @@ CBT_D float2 circle_at(int k) {
 // sin and cos of pos * turns (a fraction of a turn, 2^64 a whole) to fp32's last place or so: the nearest
 // entry, turned by the rest (at most pi / 256, where two terms of the series are enough).  (The hardware's sine,
 // off by 2^-21, takes 1.5 us less for 8192 tokens of 8 heads of 128, and with it 45 codes of 8.4 million lie beside
-// the formula's for 5.)
+// the formula's for 6.)
 CBT_D void turn_sincos(const Circle& circle, uint32_t pos, uint64_t turns, float* sn, float* cs) {
   const uint32_t ph = pos * (uint32_t)(turns >> 32) + __umulhi(pos, (uint32_t)turns);  // 2^32 a turn
   const uint32_t k = ph + (1u << 23);
@@ -89,17 +89,55 @@ CBT_D uint32_t move_codes(uint32_t w, float f) {
 
 // How far above the start of the range around the middle between two codes (of any scale: a code's last bit is
 // the fourth of its mantissa) in which what fp32 is off by may decide where it is rounded to
-// Such values are formed again in 64 bits (a warp has one in 400 of its steps): what is left are a few small
-// members of their pairs, where fp32 is off by more steps.  8.4 million codes: 5 beside the formula's for 13, at 2 us
+// Such values are formed again from pairs of fp32 (a warp has one in 500 of its steps): what is left are a few small
+// members of their pairs, where fp32 is off by more steps.  8.4 million codes: 6 beside the formula's for 13, at 2 us
 // of 62 for the look at each value.
-constexpr uint32_t kNear = 6;  // steps of fp32 on either side
+constexpr uint32_t kNear = 4;  // steps of fp32 on either side
 CBT_D uint32_t above_middle(float x) { return __float_as_uint(x) * 4096u + ((kNear - 0x80000u) << 12); }
 CBT_D bool near_middle(uint32_t above) { return above < (2 * kNear) << 12; }
 template <bool F32>
-CBT_D double element(const void* p, long long i) {
+CBT_D float element(const void* p, long long i) {
   return F32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
 }
-// The values of K head g of token t that lie so, from 64 bits rounded to odd; by all lanes of a warp
+// A value as the sum of two fp32, some 44 bits: settle's arithmetic, which in 64 bits waits for that pipe
+// (with the read-back a call of 256 tokens takes 10.9 us without settle, 14.5 with it in 64 bits, 12.0 so).
+struct Pair {
+  float hi, lo;
+};
+CBT_D Pair both(float a, float b) {  // a + b
+  const float s = a + b, v = s - a;
+  return {s, (a - (s - v)) + (b - v)};
+}
+CBT_D Pair plus(Pair a, Pair b) {
+  const Pair s = both(a.hi, b.hi);
+  return both(s.hi, s.lo + (a.lo + b.lo));
+}
+CBT_D Pair times(Pair a, Pair b) {
+  const float p = a.hi * b.hi;
+  return both(p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi));
+}
+// sin and cos of a phase of 2^64 a turn: Taylor's series around the nearest quarter, x within pi / 4.  The terms
+// from x^4 on are below 2^-5 and are summed in fp32; first ones left out: x^13 / 13! and x^12 / 12!.  Off by less
+// than 2^-28.
+CBT_D void turn_pairs(uint64_t ph, Pair* sn, Pair* cs) {
+  const uint64_t up = ph + (1ull << 61);
+  const int64_t rest = (int64_t)(up & ((1ull << 62) - 1)) - (1ll << 61);
+  const float top = (float)rest;
+  const Pair x = times({top, (float)(rest - (int64_t)top)}, {0x1.921fb6p-62f, -0x1.777a5cp-87f});  // 2 pi / 2^64
+  const Pair z = times(x, x);
+  const float w = z.hi;
+  const float s = w * w * fmaf(w, fmaf(w, fmaf(w, -1.f / 39916800, 1.f / 362880), -1.f / 5040), 1.f / 120);
+  const float c = w * w * fmaf(w, fmaf(w, fmaf(w, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24);
+  const Pair sixth = times(z, {-0x1.555556p-3f, 0x1.555556p-28f});  // -1 / 6
+  const Pair sine = times(x, plus({1.f, 0.f}, plus(sixth, {s, 0.f})));
+  const Pair cosine = plus({1.f, 0.f}, plus({-0.5f * z.hi, -0.5f * z.lo}, {c, 0.f}));
+  const int quarter = (int)(up >> 62);
+  const Pair p = quarter & 1 ? cosine : sine, q = quarter & 1 ? sine : cosine;
+  const float ps = quarter & 2 ? -1.f : 1.f, qs = (quarter + 1) & 2 ? -1.f : 1.f;
+  *sn = {ps * p.hi, ps * p.lo};
+  *cs = {qs * q.hi, qs * q.lo};
+}
+// The values of K head g of token t that lie so, formed anew and rounded to odd; by all lanes of a warp
 template <int HD, bool F32, int MODE>
 CBT_D void settle(const RopeAppendFp8& a, int t, int g, int l, const LaneDims& dims, bool on, float (&x)[8]) {
   unsigned near = 0;
@@ -107,39 +145,45 @@ CBT_D void settle(const RopeAppendFp8& a, int t, int g, int l, const LaneDims& d
   for (int k = 0; k < 8; ++k)
     if (on && near_middle(above_middle(x[k]))) near |= 1u << k;
   const long long row = t * a.qkv_ld + (long long)(a.n_heads + g) * HD;
-  double r = 1.0;
+  Pair r = {1.f, 0.f};
   if (a.k_gain) {
-    double s = 0.0;
+    float y[8];
+    load4<F32>(a.qkv, row + 8 * l, y);
+    load4<F32>(a.qkv, row + 8 * l + 4, y + 4);
+    Pair s = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = plus(s, times({y[k], 0.f}, {y[k], 0.f}));
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-      const double y = element<F32>(a.qkv, row + 8 * l + k);
-      s = fma(y, y, s);
-    }
-#pragma unroll 1
-    for (int w = HD / 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    r = rsqrt(s / HD + (double)a.eps);
+    for (int w = HD / 16; w > 0; w >>= 1)
+      s = plus(s, {__shfl_xor_sync(0xffffffffu, s.hi, w), __shfl_xor_sync(0xffffffffu, s.lo, w)});
+    s = plus({s.hi * (1.f / HD), s.lo * (1.f / HD)}, {a.eps, 0.f});
+    const float r0 = rsqrtf(s.hi);
+    const Pair off = plus({1.f, 0.f}, times(s, times({-r0, 0.f}, {r0, 0.f})));  // Newton: twice the places
+    r = both(r0, 0.5f * r0 * off.hi);
   }
-  auto value = [&](int d) {
-    const double y = element<F32>(a.qkv, row + d) * r;
-    return a.k_gain ? y * element<false>(a.k_gain, d) : y;
-  };
   const int rot = MODE == kNone ? 0 : a.rope.rot_dim;
+  auto value = [&](int d) {
+    const float y = element<F32>(a.qkv, row + d);
+    return a.k_gain ? times({y, 0.f}, {element<false>(a.k_gain, d), 0.f}) : Pair{y, 0.f};
+  };
 #pragma unroll 1
   for (; near; near &= near - 1) {
     const int k = __ffs(near) - 1, d = k < 4 ? dims.e0 + k : dims.e1 + k - 4;
-    double y = value(d);
+    Pair y = value(d);
     if (d < rot) {
       const bool second = MODE == kInter ? d & 1 : d >= rot / 2;
       const int pair = MODE == kInter ? d / 2 : second ? d - rot / 2 : d;
       const int other = MODE == kInter ? d ^ 1 : second ? pair : d + rot / 2;
-      double sn, cs;  // of a phase of 2^64 a turn
-      sincospi((double)(int64_t)((uint64_t)a.positions[t] * a.rope.turns[pair]) * 0x1p-63, &sn, &cs);
-      y = (y * cs + (second ? sn : -sn) * value(other)) * a.rope.mscale;
+      Pair sn, cs;
+      turn_pairs((uint64_t)a.positions[t] * a.rope.turns[pair], &sn, &cs);
+      if (!second) sn = {-sn.hi, -sn.lo};
+      y = times(plus(times(y, cs), times(value(other), sn)), {a.rope.mscale, 0.f});
     }
-    float f = __double2float_rz(y);
-    if ((double)f != y) f = __uint_as_float(__float_as_uint(f) | 1u);
+    y = times(y, r);
+    uint32_t f = __float_as_uint(y.hi);
+    if (y.lo != 0.f) f = (f - ((y.lo < 0.f) != (y.hi < 0.f) ? 1u : 0u)) | 1u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j == k ? f : x[j];
+    for (int q = 0; q < 8; ++q) x[q] = q == k ? __uint_as_float(f) : x[q];
   }
 }
 
