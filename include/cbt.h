@@ -616,6 +616,8 @@ typedef struct {
  *     finite); where it grows, the codes held there are rounded to the new one;
  *   - the tokens are rounded to it once, to nearest even.  An infinity becomes 448 times the scale, as
  *     does a value above 448 * 2^56; a NaN stays one.
+ * k is formed in fp32, and to 2^-28 of the pair that is rotated where it lies beside the middle between two
+ * codes, so that nearly every code is the one of k in full.
  * A block that is gone on with has to hold a scale: pages are taken from position 0 on, or zeroed first.
  * The tokens of one block stand next to each other in the call (as cbt_page_map deals them; tokens that
  * are skipped do not stand between them): where they do not, what the block then holds is unspecified.

@@ -157,6 +157,10 @@ APPENDS = [
     dict(runs=[span(7, 701), [-1] * 3, span(1024, 333), span(1601, 200)], hd=64, page=64, kv=37, H=37, rot=54),
     dict(runs=[span(64 * i + i % 58, 3 + i % 4) for i in range(260)], hd=64, page=64, kv=37, H=37, dtype=torch.float32),
     dict(runs=[span(33, 1300)], hd=128, page=128, kv=33, H=33, mode="interleaved", strided=True),
+    # norms alone; enough values that some lie beside a border between two codes
+    dict(runs=[span(33, 1300)], hd=128, page=128, kv=8, H=8, mode="none"),
+    dict(runs=[span(5, 1300)], hd=64, page=128, kv=8, H=8, mode="none", dtype=torch.float32),
+    dict(runs=[span(0, 1500)], hd=128, page=64, kv=8, H=8, rot=54, dtype=torch.float32),
     # skipped tokens between runs and at the ends; nothing but skipped tokens
     dict(runs=[[-1], span(30, 3), [-1, -1], span(64, 2), [-1]], hd=64, page=64),
     dict(runs=[[-1] * 20], hd=64, page=64),
@@ -778,3 +782,37 @@ def test_append_far_positions():
     """Angles of positions up to 2^31 - 1 keep their fraction of a turn."""
     run_append(runs=[[5], [70], [130], [195], [260]], hd=128, page=64,
                positions=[2 ** 31 - 1, 2 ** 30 + 12345, 1000003, 7, 0])
+
+
+def test_append_settles_values_beside_a_border():
+    """Rotated values that lie within 2^-24 of the middle between two codes, relative, are rounded as the formula's.
+
+    Those that are the larger part of their pair (0.9 of its size): fp32 forms them with errors of at most 1.1 2^-24
+    of each element for the angle, half a step for the product and half a step at last, 2.6 steps in all, with the
+    distance 3.6, and four steps on either side are looked at.  Closer than 2^-26 is left out: the pairs of fp32
+    are good to 2^-28 of the pair."""
+    hd, r = 64, np.random.default_rng(7)
+    freqs = np.asarray(R.rope_freqs(hd, 1e4, "none", 1.0, 0)[0])
+    heads, positions, dims = [], [], []
+    for pos in r.integers(1, 5000, 10):
+        x = torch.from_numpy(r.standard_normal((50000, hd))).to(torch.bfloat16)
+        a, b = (v.double().numpy() for v in (x[:, :hd // 2], x[:, hd // 2:]))
+        c, s = np.cos(pos * freqs), np.sin(pos * freqs)
+        y = np.concatenate([a * c - b * s, b * c + a * s], 1)
+        size = np.tile(np.sqrt(a * a + b * b), 2)
+        m, _ = np.frexp(np.abs(y))             # [0.5, 1): codes' middles at odd 32nds
+        off = np.abs(m * 32 - (2 * np.floor(m * 16) + 1)) / (m * 32)
+        ok = (off > 2.0 ** -26) & (off < 2.0 ** -24) & (np.abs(y) > 0.9 * size)
+        ok &= np.abs(y) > 0.1 * np.abs(y).max(1, keepdims=True)  # codes of full length
+        for i, d in np.argwhere(ok):
+            heads.append(x[i])
+            positions.append(int(pos))
+            dims.append((d, y[i, d], np.abs(y[i]).max()))
+    n = len(heads)
+    assert n >= 3
+    def edit(x):
+        x[:, 1] = torch.stack(heads)
+    pool = run_append([[64 * i] for i in range(n)], H=1, kv=1, hd=hd, page=64, norm=False, edit=edit, positions=positions)
+    K = F.Layout(1, hd, 64).views(pool.cpu().numpy())[0]
+    for i, (d, y, top) in enumerate(dims):
+        assert K[i, 0, 0, d] == F.encode(y * 2.0 ** -F.exponent_for(top)), (i, d, y)
