@@ -88,7 +88,7 @@ CBT_D uint32_t move_codes(uint32_t w, float f) {
 }
 
 // How far above the start of the range around the middle between two codes (of any scale: a code's last bit is
-// the fourth of its mantissa) in which what fp32 is off by may decide where it is rounded to
+// the fourth of its mantissa) in which what fp32 is off by may decide where it is rounded to.
 // Such values are formed again from pairs of fp32 (a warp has one in 500 of its steps): what is left are a few small
 // members of their pairs, where fp32 is off by more steps.  8.4 million codes: 6 beside the formula's for 13, at 2 us
 // of 62 for the look at each value.
@@ -183,7 +183,8 @@ CBT_D void settle(const RopeAppendFp8& a, int t, int g, int l, const LaneDims& d
     uint32_t f = __float_as_uint(y.hi);
     if (y.lo != 0.f) f = (f - ((y.lo < 0.f) != (y.hi < 0.f) ? 1u : 0u)) | 1u;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = q == k ? __uint_as_float(f) : x[q];
+    for (int q = 0; q < 8; ++q)  // (a product on the way may pass fp32's range where the value does not)
+      x[q] = q == k && y.lo - y.lo == 0.f ? __uint_as_float(f) : x[q];
   }
 }
 

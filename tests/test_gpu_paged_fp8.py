@@ -816,3 +816,21 @@ def test_append_settles_values_beside_a_border():
     K = F.Layout(1, hd, 64).views(pool.cpu().numpy())[0]
     for i, (d, y, top) in enumerate(dims):
         assert K[i, 0, 0, d] == F.encode(y * 2.0 ** -F.exponent_for(top)), (i, d, y)
+
+
+def test_append_products_past_the_range():
+    """Norms of large rows with a large gain: k is finite, though x times the gain is not, and is held as the largest
+    code, never as NaN."""
+    n, kv, hd = 1300, 8, 64
+    pool = torch.zeros(-(-n // 64) * F.Layout(kv, hd, 64).page_bytes, dtype=torch.uint8, device=dev())
+    cache = paged.PagedKVFp8(pool, None, None, page_tokens=64, n_kv_heads=kv, head_dim=hd)
+    r = np.random.default_rng(3)
+    x = r.choice([-1.0, 1.0], (n, 1 + 2 * kv, hd)) * (1 + 99 * r.random((n, 1 + 2 * kv, hd))) * 2.0 ** 50
+    qkv = torch.from_numpy(x.reshape(n, -1)).to(device=dev(), dtype=torch.bfloat16)
+    q = torch.empty(n, 1, hd, dtype=torch.bfloat16, device=dev())
+    gain = torch.full((hd,), 2.0 ** 100, dtype=torch.bfloat16, device=dev())
+    paged.RopeAppend(cache, None, n_heads=1)(0, qkv, i32(list(range(n))), i32(list(range(n))), q, None, gain)
+    cache.check()
+    K = F.Layout(kv, hd, 64).views(pool.cpu().numpy())[0]
+    held = K.transpose(0, 2, 1, 3).reshape(-1, kv, hd)[:n]
+    assert (held == np.where(x[:, 1:1 + kv] < 0, 0xFE, 0x7E)).all()
