@@ -96,12 +96,13 @@ struct RowTokens {
   int t0, n, len;
   bool bad;
 };
-template <class Kv>
+template <bool L2 = false, class Kv>  // L2: what this SM holds of them is not asked
 CBT_D RowTokens row_tokens(const PagedAttnOn<Kv>& a, int b) {
-  RowTokens r{b, 1, a.lens[b], false};
+  auto at = [](const int32_t* p) { return L2 ? __ldcg(p) : *p; };
+  RowTokens r{b, 1, at(a.lens + b), false};
   if (a.cu) {
-    r.t0 = a.cu[b];
-    const int t1 = a.cu[b + 1];
+    r.t0 = at(a.cu + b);
+    const int t1 = at(a.cu + b + 1);
     r.bad = r.t0 < 0 || t1 < r.t0 || t1 > a.tokens || t1 - r.t0 > a.max_q;
     r.n = t1 - r.t0;
   }
