@@ -7,14 +7,17 @@
 // own, so that nothing but a last rounding is lost:
 //   q   two parts (bf16 has eight bits of mantissa, a part four): exact down to 2^-12 of the head's largest
 //       element, off by at most 2^-22 of it below;
-//   p   four, of the weight in fp16: 2^-11 of each weight, 2^-22 of the reference's.
+//   p   four, of the weight in fp16: 2^-11 of each weight, 2^-20 of the item's largest.
 // A block's scales are powers of two.  K's multiplies its scores; V's is an addition to them, in units of
-// log2: the weights are 2^(s_j + e_j - m), e_j the exponent of j's block, m near the largest s_j + e_j so
-// far, and the sum l takes them times 2^-e_j.  (e in [-56, 56], so both hold in fp32.)
+// log2: the weights are 2^(s_j + e_j - u - m), e_j the exponent of j's block, m near the largest s_j so far and u
+// a unit that O is summed in, and the sum l takes them times 2^(u - e_j).  u follows V's exponents (0 <= u - e_j <=
+// kSpread), so that a weight beside a block of a far larger scale has the bits that it has alone: where a
+// chunk's exponents leave that, O goes to registers in whole units first.  A chunk whose two halves lie further apart
+// than kSpread takes them one after the other.
 //
 // The reference m is the item's first chunk's largest, and is raised only where a score passes it by kSlack:
 // so most chunks look for no maximum, the sums stay with the keys' threads, and O stays in tensor memory
-// until the item ends or the reference moves.
+// until the item ends or the reference or the unit moves.
 //
 // Bound by HBM: 2 head_dim bytes of K and V per position and kv head, while a chunk's instructions hide under
 // them (up to 8 q heads of 128 on a kv head; heads of 64 have half the bytes for as many).  Items, runs and
@@ -22,6 +25,8 @@
 // positions, 32 / 8 heads of 128, 126.5 us = 6.4 TB/s, 96 % of the measured copy rate; with 64 q heads 133, with
 // heads of 64 87 us (70 %), 64 of them 125 (49 %); 16 rows through a window of 4096 27.8 us (72 %); 8 rows of
 // 512 to 4096 11.5 us; one row of 100 4.6 us.
+#include <type_traits>
+
 #include "fp8_tc.cuh"
 #include "paged_split.cuh"
 
@@ -46,19 +51,35 @@ struct Shape {
 // By how many powers of two weights may pass 1 (one whose score is the reference) before the reference is
 // raised: 2^8 is below the largest code.
 constexpr float kSlack = 8.f;
-constexpr float kPart = 16.f;  // of one part's unit to the next one's
+// How far V's exponents may lie below the unit.  2^-24 of the unit is what the parts lose of a weight and 2^-25 what
+// fp16 does, so that 2^-20 of the reference's weight holds.  (Real blocks differ by less, so that the unit rarely
+// moves.)
+constexpr int kSpread = 3;
+constexpr float kPart = 16.f;  // of one part of q to the next one's unit
+// ... of a weight: a code leaves a rest of a 16th of itself, or 2^-10; with eleven bits in all a 64th or nothing
+// is left behind the second and third one, but for 2^-10.
+CBT_HD constexpr float part_unit(int k) { return k == 0 ? 16.f : k == 1 ? 32.f : 256.f; }
 
-// 16 (a - b), of two pairs of fp16
-CBT_D uint32_t rest16(uint32_t a, uint32_t b) {
+// part_unit(k) (a - b), of two pairs of fp16
+CBT_D uint32_t rest_of(uint32_t a, uint32_t b, int k) {
   uint32_t r;
-  asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}\n" : "=r"(r) : "r"(a), "r"(b), "r"(0x4C004C00u));
+  asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}\n"
+      : "=r"(r)
+      : "r"(a), "r"(b), "r"(k == 0 ? 0x4C004C00u : k == 1 ? 0x50005000u : 0x5C005C00u));
   return r;
 }
 
-// What a chunk's requester hands to the softmax: the exponents of each half's K and V scales
+// What a chunk's requester hands to the softmax of each half's K and V scales, and V's unit
 struct Scales {
-  int k[2], v[2];
+  struct Half {
+    float k_unit;  // K's scale
+    float ve;      // V's exponent, from the unit
+    float v_down;  // 2^-ve
+  } half[2];
+  int unit[2];  // V's, of the chunk; where the halves lie too far apart for one, of either
+  int moves;    // 0: the unit is that of the chunk before; kMoves, or kApart
 };
+constexpr int kMoves = 1, kApart = 2;
 
 // GT: the group's q heads rounded up to 1, 2, 4 or 8
 template <int HD, int GT>
@@ -113,6 +134,10 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
     // V's buffer is awaited, so that K's stays empty for a wait only.
     const uint64_t pol = tc::policy_evict_first();
     uint32_t n = 0, nk = 0, nv = 0;  // chunks, and tiles of K and of V requested
+    // what is handed over of the next chunk's scales: V's unit (below any scale's: none yet) and its first half's,
+    // and, lane 0 and 1, a half's own
+    int unit = kLowExp - 1, unit0 = 0, moves = 0;
+    float k_unit = 0.f, v_down = 0.f, ve = 0.f;
     bool ok = true;
     const int P = a.kv.page_tokens;
     // a chunk's halves of 64 keys that hold a key the query sees, and where they lie; lane e has half
@@ -165,7 +190,27 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
       }
       return c;
     };
+    // (where its scales are awaited: behind the requests for the chunk before)
+    auto scales_of = [&](const Chunk& c) {
+      const int e = fp8_exponent(c.vs);
+      // a half that is not there has the other one's scale
+      const int v0 = __shfl_sync(0xffffffffu, e, c.halves == 2), v1 = __shfl_sync(0xffffffffu, e, c.halves != 1);
+      const int lo = min(v0, v1), hi = max(v0, v1);
+      moves = hi - lo > kSpread ? kApart : hi > unit || lo < unit - kSpread ? kMoves : 0;
+      if (moves) unit = min(lo + kSpread, hi + 1);
+      unit0 = unit;
+      int off = (lane ? v1 : v0) - unit;
+      if (moves == kApart) {
+        unit0 = v0;
+        unit = v1;
+        off = 0;
+      }
+      k_unit = pow2_of(fp8_exponent(c.ks));
+      ve = (float)off;
+      v_down = pow2_of(-off);
+    };
     Chunk c = next();
+    scales_of(c);
 #pragma unroll 1
     for (; c.halves; ++n) {
       const uint32_t bytes = __popc(c.halves) * S::kVHalf;
@@ -177,9 +222,12 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
           if (c.halves >> e & 1) tc::tma_load_rows(sK + e * S::kVHalf, &tk, kfull, c.k[e], pol);
       }
       // (the tile's bytes may land before they are expected: the phase waits for the arrival)
+      Scales& out = scales[n & 1];
       if (lane < 2) {
-        scales[n & 1].k[lane] = fp8_exponent(c.ks);
-        scales[n & 1].v[lane] = fp8_exponent(c.vs);
+        out.half[lane] = {k_unit, ve, v_down};
+        out.unit[lane] = lane ? unit : unit0;
+      } else if (lane == 2) {
+        out.moves = moves;
       }
       __syncwarp();
       if (elect_one()) tc::mbar_expect_tx(kfull, bytes);
@@ -195,13 +243,15 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
       }
       ++nv;
       c = nxt;
+      if (c.halves) scales_of(c);
     }
     if (!ok && lane == 0) wait_timeout(a.err, abort_flag, 21);
     // no copies in flight at exit
     if (nk) wait_landed(kfull, (nk - 1) & 1);
     if (nv) wait_landed(vfull, (nv - 1) & 1);
   } else {
-    uint32_t n = 0;  // chunks done
+    uint32_t n = 0, no = 0;     // chunks done, products with V asked for
+    int unit = kLowExp - 1;     // V's, of the product in tensor memory (below any scale's: none yet)
     bool ok = true;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const float scale2 = a.scale * kLog2e;  // scores in units of log2
@@ -272,8 +322,6 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         nxt = item_at(cur, a, lay.groups, it);
         qv = load_q(nxt);
       }
-      // The reference is the first chunk's largest s + e, and is raised where one passes it by more than
-      // kSlack: so O stays in tensor memory over the item's chunks, and most chunks look for no maximum.
       // m_run is kept by every thread, each from the same values in the same order; l_own are its own keys'
       float m_run[GT], oacc[GT], l_own[GT];
       uint32_t acc = 0;  // O in tensor memory holds something
@@ -292,8 +340,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         for (int h = 0; h < GT; ++h) {
           float o = 0.f;
 #pragma unroll
-          for (int k = kParts - 1; k >= 0; --k) o = fmaf(o, 1.f / kPart, __uint_as_float(part[k * GT + h]));
-          oacc[h] += o;
+          for (int k = kParts - 1; k >= 0; --k) o = fmaf(o, 1.f / part_unit(k), __uint_as_float(part[k * GT + h]));
+          oacc[h] = fmaf(o, pow2_of(unit), oacc[h]);
         }
       };
       tc::fence_proxy_async_smem();
@@ -317,9 +365,10 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         const int k0 = w.seen.chunk(i) * kSub;
         const bool valid = sees(k0 + tid, w.p, a.window, a.sinks);
         const uint32_t vb = __ballot_sync(0xffffffffu, valid);
-        const float k_unit = pow2_of(scales[n & 1].k[tid >> 6]);
-        const int ve = scales[n & 1].v[tid >> 6];
-        const float v_down = pow2_of(-ve);
+        const Scales& sc = scales[n & 1];
+        const Scales::Half& mine = sc.half[tid >> 6];
+        const float k_unit = mine.k_unit, ve = mine.ve;
+        const int moves = sc.moves;
         bool bad = !wait_or_abort(bar_s, n & 1, abort_flag);
         __syncwarp();
         tc::tc_fence_after();
@@ -331,10 +380,10 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
           const float both = fmaf(__uint_as_float(raw[GT + h]), 1.f / kPart, __uint_as_float(raw[h]));
-          s[h] = valid ? fmaf(both * k_unit, q_unit[h], (float)ve) : -INFINITY;
+          s[h] = valid ? fmaf(both * k_unit, q_unit[h], ve) : -INFINITY;
         }
-        // the weights of the chunk before have been read
-        if (n) bad = bad || !wait_or_abort(bar_o, (n - 1) & 1, abort_flag);
+        // the weights of the product before have been read
+        if (no) bad = bad || !wait_or_abort(bar_o, (no - 1) & 1, abort_flag);
         __syncwarp();
         if (vb != 0xffffffffu) {
           // masked keys: their V may hold anything, so it is zeroed (their weights are zero), each warp its own
@@ -354,87 +403,118 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
             }
           }
         }
-        bool raise = i == w.i0;
-#pragma unroll 1
-        for (;;) {
-          if (raise) {
-            float mx[GT];
-#pragma unroll
-            for (int h = 0; h < GT; ++h) mx[h] = s[h];
-            warp_reduce_n<GT, true>(mx);
-            if (lane == 0) {
-#pragma unroll
-              for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
-            }
-            tc::named_bar_sync(1, kCompute);
-            if (acc) {
+        // O += P V, by one thread; `last`: of the chunk
+        auto multiply = [&](bool last) {
+          if (warp == 0) {
+            if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
+              if (lane == 0) wait_timeout(a.err, abort_flag, 24);
+            } else if (elect_one()) {
               tc::tc_fence_after();
-              add_o();
-              tc::tc_fence_before();
-              acc = 0;
+#pragma unroll
+              for (int k = 0; k < kSub / 32; ++k)
+                tc::mma_e4m3(tmem + S::kNQ, tc::sdesc_rows<64>(tc::smem_u32(sV + (k >> 1) * S::kVHalf)) + 2 * (k & 1),
+                             tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * k, kIdescO, acc || k > 0 ? 1u : 0u);
+              tc::mma_commit(bar_o);
+              if (last) tc::mma_commit(vempty);
             }
+          }
+          acc = 1;
+          ++no;
+        };
+        // O leaves tensor memory
+        auto take_o = [&]() {
+          if (!acc) return;
+          tc::tc_fence_after();
+          add_o();
+          tc::tc_fence_before();
+          acc = 0;
+        };
+        // The chunk's weights and their product.  (Two copies of the code: in one, with the unit's moves in it, 32 rows
+        // of 8192 to 16384 took 135 us for 133 with 64 q heads, and 94 for 91 with heads of 64.)
+        auto weigh = [&](auto moving) {
+          bool raise = i == w.i0, turn = valid;
+          bool halves = false;  // the first one's turn, of two
+          if (moving.value) {
+            take_o();
+            unit = sc.unit[0];
+            halves = moves == kApart;
+            if (halves) turn = valid && tid < 64;
+          }
+#pragma unroll 1
+          for (;;) {
+            if (raise) {
+              float mx[GT];
+#pragma unroll
+              for (int h = 0; h < GT; ++h) mx[h] = s[h] - mine.ve;
+              warp_reduce_n<GT, true>(mx);
+              if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
+              }
+              tc::named_bar_sync(1, kCompute);
+              take_o();
+#pragma unroll
+              for (int h = 0; h < GT; ++h) {
+                const float mo = m_run[h];
+                const float mn = fmaxf(mo, fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])));
+                const float scl = mo == -INFINITY ? 0.f : ex2(mo - mn);
+                oacc[h] *= scl;
+                l_own[h] *= scl;
+                m_run[h] = mn;
+              }
+            }
+            bool over = false;
+            uint8_t* dst = sP + (tid & 15);
+            float p[GT];
 #pragma unroll
             for (int h = 0; h < GT; ++h) {
-              const float mo = m_run[h];
-              const float mn = fmaxf(mo, fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])));
-              const float scl = mo == -INFINITY ? 0.f : ex2(mo - mn);
-              oacc[h] *= scl;
-              l_own[h] *= scl;
-              m_run[h] = mn;
+              // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
+              p[h] = turn ? ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h])) : 0.f;
+              over = over || s[h] > m_run[h] + kSlack;
             }
-          }
-          bool over = false;
-          uint8_t* dst = sP + (tid & 15);
-          float p[GT];
 #pragma unroll
-          for (int h = 0; h < GT; ++h) {
-            // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
-            p[h] = valid ? ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h])) : 0.f;
-            over = over || s[h] > m_run[h] + kSlack;
-          }
+            for (int h = 0; h < GT; h += 2) {
+              uint32_t y = pack_f16(p[h], h + 1 < GT ? p[h + 1 < GT ? h + 1 : h] : 0.f);
 #pragma unroll
-          for (int h = 0; h < GT; h += 2) {
-            uint32_t y = pack_f16(p[h], h + 1 < GT ? p[h + 1 < GT ? h + 1 : h] : 0.f);
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-              const uint16_t code = f16_to_e4m3(y);
-              dst[tc::swz<128>(k * GT + h, tid & ~15)] = (uint8_t)code;
-              if (h + 1 < GT) dst[tc::swz<128>(k * GT + h + 1, tid & ~15)] = (uint8_t)(code >> 8);
-              if (k + 1 < kParts) y = rest16(y, e4m3_to_f16(code));
+              for (int k = 0; k < kParts; ++k) {
+                const uint16_t code = f16_to_e4m3(y);
+                dst[tc::swz<128>(k * GT + h, tid & ~15)] = (uint8_t)code;
+                if (h + 1 < GT) dst[tc::swz<128>(k * GT + h + 1, tid & ~15)] = (uint8_t)(code >> 8);
+                if (k + 1 < kParts) y = rest_of(y, e4m3_to_f16(code), k);
+              }
             }
-          }
-          tc::fence_proxy_async_smem();
-          if (!tc::named_bar_any(2, kCompute, bad || (over && !raise))) {
+            tc::fence_proxy_async_smem();
+            if (!tc::named_bar_any(2, kCompute, bad || (over && !raise))) {
 #pragma unroll
-            for (int h = 0; h < GT; ++h) l_own[h] = fmaf(p[h], v_down, l_own[h]);
-            break;
+              for (int h = 0; h < GT; ++h) l_own[h] = fmaf(p[h], mine.v_down, l_own[h]);
+              if (!moving.value || !halves) break;
+              // the second half's turn, once the first one's weights have been read
+              multiply(false);
+              bad = !wait_or_abort(bar_o, (no - 1) & 1, abort_flag);
+              __syncwarp();
+              take_o();
+              unit = sc.unit[1];
+              turn = valid && tid >= 64;
+              raise = false;
+              halves = false;
+              continue;
+            }
+            // something has passed a reference, or has failed
+            if (tc::named_bar_any(2, kCompute, bad)) {
+              ok = false;
+              break;
+            }
+            raise = true;
           }
-          // something has passed a reference, or has failed
-          if (tc::named_bar_any(2, kCompute, bad)) {
-            ok = false;
-            break;
-          }
-          raise = true;
-        }
+          if (ok) multiply(true);
+        };
+        if (moves) weigh(std::true_type());
+        else weigh(std::false_type());
         if (!ok) break;
-        if (warp == 0) {
-          if (!__all_sync(0xffffffffu, wait_or_abort(vfull, n & 1, abort_flag))) {
-            if (lane == 0) wait_timeout(a.err, abort_flag, 24);
-          } else if (elect_one()) {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kSub / 32; ++k)
-              tc::mma_e4m3(tmem + S::kNQ, tc::sdesc_rows<64>(tc::smem_u32(sV + (k >> 1) * S::kVHalf)) + 2 * (k & 1),
-                           tc::sdesc_rows<128>(tc::smem_u32(sP)) + 2 * k, kIdescO, acc || k > 0 ? 1u : 0u);
-            tc::mma_commit(bar_o);
-            tc::mma_commit(vempty);
-          }
-        }
-        acc = 1;
       }
       if (!ok) break;
       if (acc) {
-        const bool bad = !wait_or_abort(bar_o, (n - 1) & 1, abort_flag);
+        const bool bad = !wait_or_abort(bar_o, (no - 1) & 1, abort_flag);
         if (tc::named_bar_any(2, kCompute, bad)) {
           ok = false;
           break;
