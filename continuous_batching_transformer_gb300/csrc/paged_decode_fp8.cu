@@ -7,17 +7,19 @@
 // own, so that nothing but a last rounding is lost:
 //   q   two parts (bf16 has eight bits of mantissa, a part four): exact down to 2^-12 of the head's largest
 //       element, off by at most 2^-22 of it below;
-//   p   four, of the weight in fp16: 2^-11 of each weight, 2^-20 of the item's largest.
+//   p   four, of the weight in fp16: 2^-11 of each weight, and 2^-24 of what the reference stands for.
 // A block's scales are powers of two.  K's multiplies its scores; V's is an addition to them, in units of
-// log2: the weights are 2^(s_j + e_j - u - m), e_j the exponent of j's block, m near the largest s_j so far and u
-// a unit that O is summed in, and the sum l takes them times 2^(u - e_j).  u follows V's exponents (0 <= u - e_j <=
-// kSpread), so that a weight beside a block of a far larger scale has the bits that it has alone: where a
-// chunk's exponents leave that, O goes to registers in whole units first.  A chunk whose two halves lie further apart
-// than kSpread takes them one after the other.
+// log2: the weights are 2^(s_j + e_j - u - m), e_j the exponent of j's block, u a unit that O is summed in and m a
+// reference, and the sum l takes them times 2^(u - e_j).
 //
-// The reference m is the item's first chunk's largest, and is raised only where a score passes it by kSlack:
-// so most chunks look for no maximum, the sums stay with the keys' threads, and O stays in tensor memory
-// until the item ends or the reference or the unit moves.
+// The reference is the item's first chunk's largest s_j + e_j - u, and is raised where one passes it by kSlack: so
+// most chunks look for no maximum, the sums stay with the keys' threads, and O stays in tensor memory until the
+// item ends or reference or unit move.  The unit follows V's exponents, 0 <= u - e_j <= kSpread: a weight beside a
+// block of a far larger scale has the bits that it has alone.  Where a chunk's exponents leave that, O goes to
+// registers first, and a reference that stood above what it needs for the scales so far is lowered as the unit
+// rises: a block of small weights and large values keeps its bits as well.  (m <= s_max and m + u <= the largest
+// s + e: what is lost of a weight is 2^-20 of the row's largest at most, of weight times scale 2^-20 of
+// the largest of those.)  A chunk whose two halves lie further apart than kSpread takes them one after the other.
 //
 // Bound by HBM: 2 head_dim bytes of K and V per position and kv head, while a chunk's instructions hide under
 // them (up to 8 q heads of 128 on a kv head; heads of 64 have half the bytes for as many).  Items, runs and
@@ -51,9 +53,8 @@ struct Shape {
 // By how many powers of two weights may pass 1 (one whose score is the reference) before the reference is
 // raised: 2^8 is below the largest code.
 constexpr float kSlack = 8.f;
-// How far V's exponents may lie below the unit.  2^-24 of the unit is what the parts lose of a weight and 2^-25 what
-// fp16 does, so that 2^-20 of the reference's weight holds.  (Real blocks differ by less, so that the unit rarely
-// moves.)
+// How far V's exponents may lie below the unit: see above; the parts lose 2^-24 and fp16 2^-25.  (Real blocks differ
+// by less, so that the unit rarely moves.)
 constexpr int kSpread = 3;
 constexpr float kPart = 16.f;  // of one part of q to the next one's unit
 // ... of a weight: a code leaves a rest of a 16th of itself, or 2^-10; with eleven bits in all a 64th or nothing
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
   float* red = reinterpret_cast<float*>(tmem_slot + 2); // [4 warps][8 heads]
   float* l_run = red + 32;                              // [8]
   float* q_unit = l_run + 8;                            // [8] a score's unit, in log2 units
+  float* most = q_unit + 8;                             // [8] the highest m + u before the unit moved
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const Layout lay = layout_of(a);
@@ -330,19 +332,27 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         m_run[h] = -INFINITY;
         oacc[h] = l_own[h] = 0.f;
       }
+      if (tid < GT) most[tid] = -INFINITY;
       // this thread's dim of O, from its parts
       auto add_o = [&]() {
-        uint32_t part[S::kNP];
+        constexpr int kAtOnce = 16 / GT < kParts ? 16 / GT : kParts;  // parts in 16 columns
+        float o[GT];
 #pragma unroll
-        for (int k = 0; k < S::kNP; k += 16) tc::tmem_ld16(lane_base + S::kNQ + k, part + k);
-        tc::tmem_ld_wait();
+        for (int k0 = kParts - kAtOnce; k0 >= 0; k0 -= kAtOnce) {
+          uint32_t part[16];
+          tc::tmem_ld16(lane_base + S::kNQ + k0 * GT, part);
+          tc::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) {
-          float o = 0.f;
+          for (int h = 0; h < GT; ++h) {
 #pragma unroll
-          for (int k = kParts - 1; k >= 0; --k) o = fmaf(o, 1.f / part_unit(k), __uint_as_float(part[k * GT + h]));
-          oacc[h] = fmaf(o, pow2_of(unit), oacc[h]);
+            for (int k = kAtOnce - 1; k >= 0; --k) {
+              const float x = __uint_as_float(part[k * GT + h]);
+              o[h] = k0 + k == kParts - 1 ? x : fmaf(o[h], 1.f / part_unit(k0 + k), x);
+            }
+          }
         }
+#pragma unroll
+        for (int h = 0; h < GT; ++h) oacc[h] = fmaf(o[h], pow2_of(unit), oacc[h]);
       };
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(1, kCompute);
@@ -429,34 +439,34 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
           tc::tc_fence_before();
           acc = 0;
         };
-        // The chunk's weights and their product.  (Two copies of the code: in one, with the unit's moves in it, 32 rows
-        // of 8192 to 16384 took 135 us for 133 with 64 q heads, and 94 for 91 with heads of 64.)
+        // The chunk's weights and their product.  (Two copies of the code: with the unit's moves in the one that most
+        // chunks take, that one had a tenth more instructions.)
         auto weigh = [&](auto moving) {
-          bool raise = i == w.i0, turn = valid;
-          bool halves = false;  // the first one's turn, of two
-          if (moving.value) {
-            take_o();
-            unit = sc.unit[0];
-            halves = moves == kApart;
-            if (halves) turn = valid && tid < 64;
-          }
+          bool raise = i == w.i0 || moving.value, second = false;  // second: half's turn, of two
 #pragma unroll 1
           for (;;) {
+            const bool turn = valid && (!moving.value || moves != kApart || tid >> 6 == (int)second);
             if (raise) {
               float mx[GT];
 #pragma unroll
-              for (int h = 0; h < GT; ++h) mx[h] = s[h] - mine.ve;
+              for (int h = 0; h < GT; ++h) mx[h] = !moving.value || turn ? s[h] : -INFINITY;
               warp_reduce_n<GT, true>(mx);
               if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < GT; ++h) red[warp * 8 + h] = mx[h];
               }
+              if (moving.value && tid == 0) {
+#pragma unroll
+                for (int h = 0; h < GT; ++h) most[h] = fmaxf(most[h], m_run[h] + (float)unit);
+              }
               tc::named_bar_sync(1, kCompute);
               take_o();
+              if (moving.value) unit = sc.unit[second];
 #pragma unroll
               for (int h = 0; h < GT; ++h) {
-                const float mo = m_run[h];
-                const float mn = fmaxf(mo, fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])));
+                // (O and l, in units of 2^m, stay in fp32's range: O's elements are below 2^(most - m + 18 + kSlack))
+                const float mo = m_run[h], low = moving.value ? fminf(mo, most[h] - (float)unit) : mo;
+                const float mn = fmaxf(low, fmaxf(fmaxf(red[h], red[8 + h]), fmaxf(red[16 + h], red[24 + h])));
                 const float scl = mo == -INFINITY ? 0.f : ex2(mo - mn);
                 oacc[h] *= scl;
                 l_own[h] *= scl;
@@ -468,8 +478,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
             float p[GT];
 #pragma unroll
             for (int h = 0; h < GT; ++h) {
-              // (scores of -inf alone so far: weights of 0, not of exp(-inf + inf))
-              p[h] = turn ? ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h])) : 0.f;
+              // (scores of -inf, as masked keys have, alone so far: weights of 0, not of exp(-inf + inf))
+              p[h] = moving.value && !turn ? 0.f : ex2(s[h] - (m_run[h] == -INFINITY ? 0.f : m_run[h]));
               over = over || s[h] > m_run[h] + kSlack;
             }
 #pragma unroll
@@ -487,16 +497,12 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
             if (!tc::named_bar_any(2, kCompute, bad || (over && !raise))) {
 #pragma unroll
               for (int h = 0; h < GT; ++h) l_own[h] = fmaf(p[h], mine.v_down, l_own[h]);
-              if (!moving.value || !halves) break;
+              if (!moving.value || moves != kApart || second) break;
               // the second half's turn, once the first one's weights have been read
               multiply(false);
               bad = !wait_or_abort(bar_o, (no - 1) & 1, abort_flag);
               __syncwarp();
-              take_o();
-              unit = sc.unit[1];
-              turn = valid && tid >= 64;
-              raise = false;
-              halves = false;
+              second = true;
               continue;
             }
             // something has passed a reference, or has failed

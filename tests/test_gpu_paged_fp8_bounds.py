@@ -1,11 +1,12 @@
 """Bounds that the operators on a paged cache in 8 bits state, each where it is hardest to hold.
 
-Attention of single tokens: a weight is off by at most 2^-11 of itself and 2^-20 of its row's largest, whatever V's
-scales are.  A dim that is zero in the
-blocks of the largest scale shows it: what is lost of the others' weights is lost of its whole output.  Each dim has a
+Attention of single tokens: a weight is off by at most 2^-11 of itself and 2^-20 of its row's largest, and times its scale of V by no
+more than 2^-20 of the largest such product, whatever V's scales are.  A dim that is zero in the blocks of the largest scale shows the first: what is lost of the others'
+weights is lost of its whole output.  Blocks of a large scale and small weights show the second.  Each dim has a
 tolerance of its own here, made from what it sums itself.
 """
 import math
+import random
 
 import numpy as np
 import pytest
@@ -18,7 +19,7 @@ from tests.test_gpu_paged_fp8 import SCORE, WEIGHT, attend
 
 pytestmark = pytest.mark.gpu
 
-FLOOR = 2.0 ** -20  # of the row's largest weight
+FLOOR = 2.0 ** -20  # of the row's largest weight, or weight times scale
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -26,13 +27,14 @@ def built():
     ensure_built()
 
 
-def row_of(n, hd, exponents, seed):
+def row_of(n, hd, exponents, seed, below):
     """A row whose block b has a V scale near 2^exponents[b]: blocks above the smallest have their values in one
-    dim each alone.  Returns pool, table, k, v."""
+    dim each alone, and K's first dim -below.  Returns pool, table, k, v and the exponents of V's scales by position."""
     r = np.random.default_rng(seed)
     lay = F.Layout(1, hd, 64)
     blocks = -(-n // 64)
     k = r.integers(-8, 9, (n, 1, hd)) / 16.0
+    k[..., 0] = 0
     v = r.standard_normal((n, 1, hd))
     least = min(exponents)
     for b in range(blocks):
@@ -42,18 +44,21 @@ def row_of(n, hd, exponents, seed):
             keep = v[rows, 0, b % 5].copy()
             v[rows] = 0
             v[rows, 0, b % 5] = keep
+            k[rows, 0, 0] = -below
         v[rows] *= 2.0 ** e
     pool = np.full(blocks * lay.page_bytes, 0x7F, np.uint8)
     F.append(pool, lay, k, v, list(range(n)))
     table = np.arange(blocks, dtype=np.int32)
-    return pool, table, *F.values(pool, lay, table, n)
+    held = np.log2(lay.views(pool)[2][:, 1, 0, 0]).repeat(64)[:n]
+    return pool, table, *F.values(pool, lay, table, n), held
 
 
-def check(n, new, hd, exponents, decode, seed=0, heads=3, spread=1.0, dtype=torch.float32):
-    pool, table, k, v = row_of(n, hd, exponents, seed)
+def check(n, new, hd, exponents, decode, seed=0, heads=3, spread=1.0, dtype=torch.float32, below=0):
+    pool, table, k, v, held = row_of(n, hd, exponents, seed, below)
     g = torch.Generator().manual_seed(seed + 1)
     # whole 8ths below 16: two parts of four bits hold them
     q = (torch.randint(-8, 9, (new, heads, hd), generator=g) / 8 * spread).bfloat16()
+    q[..., 0] = 8.0
     got = attend(pool, table, n, q, new, hd, decode, dtype=dtype)
     x, scale = q.double().numpy(), 1 / math.sqrt(hd)
     ref, mag = R.attention(x, k, v, n - new, 0, 0, scale)
@@ -61,9 +66,10 @@ def check(n, new, hd, exponents, decode, seed=0, heads=3, spread=1.0, dtype=torc
         p = n - new + t
         s = scale * (x[t] @ k[0, :p + 1].T)
         w = np.exp(s - s.max(-1, keepdims=True))
-        largest = 1 / w.sum(-1)  # of the normalised weights
-        # the last rounding, the sum in fp32, each weight's own rounding, and 2^-20 of the largest a position
-        tol = (2.0 ** -18 + WEIGHT + SCORE) * mag[t] + FLOOR * largest[:, None] * np.abs(v[0, :p + 1]).sum(0)
+        product = (w * 2.0 ** held[:p + 1]).max(-1, keepdims=True)  # the largest weight is 1
+        floor = FLOOR * np.minimum(1, product / 2.0 ** held[:p + 1]) / w.sum(-1, keepdims=True)
+        # the last rounding, the sum in fp32, each weight's own rounding, and what is lost of it beside others
+        tol = (2.0 ** -18 + WEIGHT + SCORE) * mag[t] + floor @ np.abs(v[0, :p + 1])
         if dtype == torch.bfloat16:
             tol += R.BF16_STEP * np.abs(ref[t])
         off = np.abs(got[t] - ref[t])
@@ -96,3 +102,24 @@ def test_scales_as_far_apart_as_there_are(exponents):
     for n in (300, 2500):
         check(n, 1, 128, exponents, decode=True, seed=3)
         check(n, 1, 64, exponents, decode=True, seed=4, heads=8)
+
+
+@pytest.mark.parametrize("below", [4, 10, 15])
+@pytest.mark.parametrize("exponents", [[0, 18], [0, 0, 0, 0, 20, 20, 0, 0], [24, 24, 0, 0], [0, 8, 16, 24]], ids=str)
+@pytest.mark.parametrize("n,new", [(700, 1), (4000, 1)])
+def test_small_weights_on_large_blocks(n, new, exponents, below):
+    """Blocks whose values are large and whose weights are 2^-6 to 2^-22 of the others' (in heads of 64; 2^-4 to
+    2^-15 in those of 128) and still carry the output."""
+    for hd in (64, 128):
+        check(n, new, hd, exponents, decode=new == 1, seed=below, below=below)
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_drawn_scales(seed):
+    """Any order of scales, within 2^50 of one another, and of weights."""
+    r = random.Random(seed)
+    for hd in (64, 128):
+        exponents = [r.choice([-20, -10, -4, 0, 2, 9, 17, 30]) for _ in range(r.randint(2, 12))]
+        for n in (r.randint(65, 1200), r.randint(2500, 5000)):
+            check(n, 1, hd, exponents, decode=True, seed=seed, heads=r.choice([1, 2, 5, 8]), below=r.choice([0, 3, 12]),
+                  spread=r.choice([1.0, 4.0]))
