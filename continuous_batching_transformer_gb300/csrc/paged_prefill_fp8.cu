@@ -6,11 +6,14 @@
 //                 code four: exact down to 2^-10 of the row's largest element, off by at most 2^-18 of it
 //                 below), e4m3 at twice the rate of bf16: what a product of bf16 would take
 //   softmax       one thread per row
-//   O += P V      P as fp16 in tensor memory (2^-11 of each weight, 2^-31 of the largest or so), V turned
-//                 from codes to fp16 in shared memory, which is exact
+//   O += P V      P as fp16 in tensor memory (2^-11 of each weight, 2^-25 of what a weight of 1 stands for),
+//                 V turned from codes to fp16 in shared memory, which is exact
 // The step is a scale's block, and scales are powers of two: K's multiplies the row's score unit, V's
 // exponent e is added to the scores, in units of log2: the weights are 2^(s + e - m) with m a whole number
-// near the largest s + e so far, and the sum takes a step's weights times 2^-e.
+// near the largest s + e so far, and the sum takes a step's weights times 2^-e.  Where a block's scale lies so far
+// below others that a key there would lose bits of a weight as large as any, m is lowered: m <= s_max + e + kLow
+// in every step, so that what is lost of a weight is 2^-22 of the row's largest at most, and of weight times scale
+// 2^-25 of the largest of those.
 //
 // The codes of K and V come through TMA into a ring of stages.  A warpgroup of its own turns V into fp16
 // (into a ring of its own), clearing keys that no query of the unit sees, and splits the units' Q; it
@@ -45,6 +48,10 @@ static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 4 * kRegs, "regist
 // A row's weights are below 2^kHead when its reference is set, and the reference is raised once they pass
 // 2^(kHead + kSlack): far from the largest fp16, 2^16, and small ones as far from the smallest
 constexpr float kHead = 6.f, kSlack = 9.f;
+constexpr float kLow = 3.f;
+// A reference goes no further than this below its highest, so that O (65504 * 448 for each of 2^31 positions at
+// most, at the highest) stays in fp32's range
+constexpr float kReach = 64.f;
 
 // Shared memory: the tiles of Q, K and V, then this
 constexpr int kBars = 5 + 2 * kStages + 2 * kVSlots + 12;
@@ -56,6 +63,7 @@ struct Tail {
   int2 exps[kStages];          // of K's and V's scale of a stage's step
   int2 s_exps[2][2];           // [tile]: of its last steps
   float row_unit[2][kRows];    // of each row's scores, in log2 units
+  float most[2][kRows];        // a row's highest reference; its thread's own
   Unit units[kUnits];
 };
 template <int HD>
@@ -503,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = live ? p : 0x3FFFFFFF, lo = live ? first_in_window(max(0, p), a.window) : 0;
       const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
       float m = -INFINITY, l = 0.f;  // the reference (near the largest so far, a whole number) and the sum
+      float s_max = -INFINITY;       // the largest score so far
       const int before = done;
       float row_unit = 0.f;
       if (w.steps) {
@@ -543,12 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e)
             mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
           const float top = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), cs, ve);
-          const bool up = m == -INFINITY ? top > -INFINITY : top > m + (kHead + kSlack);
-          if (__any_sync(0xffffffffu, up)) {
+          s_max = fmaxf(s_max, top - ve);
+          const bool up = m == -INFINITY ? top > -INFINITY : top > m + (kHead + kSlack), down = m > s_max + (ve + kLow);
+          if (__any_sync(0xffffffffu, up || down)) {
             // Rows that exceed their reference, or see their first keys, raise it, to a whole number: what
             // the old one has scaled is multiplied by a power of two, which rounds nothing.
-            const float next = up ? ceilf(top) - kHead : m;
-            const float f = m == -INFINITY ? 0.f : pow2_down(next - m);  // m = -inf: l and O are zero
+            float& most = tail.most[x][row];
+            float next = up ? ceilf(top) - kHead : m;
+            if (down) next = fmaxf(ceilf(s_max + ve) - kHead, most - kReach);
+            // m = -inf: l and O are zero
+            const float f = m == -INFINITY ? 0.f : next < m ? pow2_of((int)(m - next)) : pow2_down(next - m);
+            most = m == -INFINITY ? next : fmaxf(most, next);
             m = next;
             l *= f;
             if (done > before) {

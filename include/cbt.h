@@ -674,9 +674,9 @@ cbt_status cbt_paged_read_fp8(const cbt_paged_read_fp8_args* a, void* stream);
  * but for the roundings on the way:
  *   - q takes part to 2^-18 of the largest element of its head, or as bf16 holds it where that is finer;
  *     a head of q with an element that is not finite gets NaN;
- *   - the weights that multiply V are rounded to fp16 once.  With max_q == 1 they are off by at most 2^-11 of each
- *     and what is less of 2^-20 of the row's largest weight and, with V's scale in both, 2^-20 of the row's largest
- *     product of weight and scale, whatever V's scales are. */
+ *   - the weights that multiply V are rounded to fp16 once: 2^-11 of each, and at most 2^-20 of the row's largest
+ *     weight and, with V's scale in both, 2^-20 of the row's largest product of weight and scale, whichever is
+ *     less.  (max_q > 1: where V's scales lie further apart than 2^64, 2^-84 of that product if that is more.) */
 typedef struct {
   cbt_paged_kv_fp8 kv;
   const int32_t* block_table;

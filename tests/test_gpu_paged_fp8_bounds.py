@@ -1,7 +1,8 @@
 """Bounds that the operators on a paged cache in 8 bits state, each where it is hardest to hold.
 
-Attention of single tokens: a weight is off by at most 2^-11 of itself and 2^-20 of its row's largest, and times its scale of V by no
-more than 2^-20 of the largest such product, whatever V's scales are.  A dim that is zero in the blocks of the largest scale shows the first: what is lost of the others'
+Attention: a weight is off by at most 2^-11 of itself and 2^-20 of its row's largest, and times its scale of V by no
+more than 2^-20 of the largest such product, whatever V's scales are (with more than one token a row: or, where that is
+more, 2^-84 of the largest product).  A dim that is zero in the blocks of the largest scale shows the first: what is lost of the others'
 weights is lost of its whole output.  Blocks of a large scale and small weights show the second.  Each dim has a
 tolerance of its own here, made from what it sums itself.
 """
@@ -67,7 +68,8 @@ def check(n, new, hd, exponents, decode, seed=0, heads=3, spread=1.0, dtype=torc
         s = scale * (x[t] @ k[0, :p + 1].T)
         w = np.exp(s - s.max(-1, keepdims=True))
         product = (w * 2.0 ** held[:p + 1]).max(-1, keepdims=True)  # the largest weight is 1
-        floor = FLOOR * np.minimum(1, product / 2.0 ** held[:p + 1]) / w.sum(-1, keepdims=True)
+        part = product / 2.0 ** held[:p + 1]
+        floor = FLOOR * np.minimum(np.maximum(1, 0 if decode else part * 2.0 ** -64), part) / w.sum(-1, keepdims=True)
         # the last rounding, the sum in fp32, each weight's own rounding, and what is lost of it beside others
         tol = (2.0 ** -18 + WEIGHT + SCORE) * mag[t] + floor @ np.abs(v[0, :p + 1])
         if dtype == torch.bfloat16:
@@ -84,10 +86,12 @@ APART = [[0, 18], [18, 0], [0, 0, 24, 24], [24, 24, 0, 0], [0, 3, 6, 9, 12, 15, 
 
 @pytest.mark.parametrize("exponents", APART, ids=str)
 @pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("n,new", [(500, 1), (4000, 1)])
+@pytest.mark.parametrize("n,new", [(500, 1), (4000, 1), (200, 70), (700, 130), (3000, 4)])
 def test_weights_beside_a_far_larger_scale(n, new, hd, exponents):
-    """(whole rows and rows cut into runs that are joined)"""
-    check(n, new, hd, exponents, decode=True, seed=len(exponents))
+    """(one token a row, and more; whole rows and rows cut into runs that are joined)"""
+    check(n, new, hd, exponents, decode=new == 1, seed=len(exponents))
+    if new == 1:
+        check(n, 1, hd, exponents, decode=False, seed=7, heads=8)
 
 
 @pytest.mark.parametrize("heads", [1, 2, 4, 8, 11])
@@ -95,18 +99,21 @@ def test_every_number_of_heads_beside_a_far_larger_scale(heads):
     for exponents in ([0, 30], [30, 30, 0, 0, 15, 0], [0, 5]):
         check(900, 1, 128, exponents, decode=True, heads=heads, seed=heads, spread=6.0)
         check(900, 1, 64, exponents, decode=True, heads=heads, seed=heads, dtype=torch.bfloat16)
+        check(300, 40, 64, exponents, decode=False, heads=heads, seed=heads, spread=6.0)
 
 
 @pytest.mark.parametrize("exponents", [[-60, 40], [40, -60], [40, 40, -60, -60], [-60, -30, 0, 40]], ids=str)
 def test_scales_as_far_apart_as_there_are(exponents):
     for n in (300, 2500):
+        check(n, 9, 128, exponents, decode=False, seed=5)
+        check(n, 150, 64, exponents, decode=False, seed=6, heads=8)
         check(n, 1, 128, exponents, decode=True, seed=3)
         check(n, 1, 64, exponents, decode=True, seed=4, heads=8)
 
 
 @pytest.mark.parametrize("below", [4, 10, 15])
 @pytest.mark.parametrize("exponents", [[0, 18], [0, 0, 0, 0, 20, 20, 0, 0], [24, 24, 0, 0], [0, 8, 16, 24]], ids=str)
-@pytest.mark.parametrize("n,new", [(700, 1), (4000, 1)])
+@pytest.mark.parametrize("n,new", [(700, 1), (4000, 1), (300, 70), (3000, 4)])
 def test_small_weights_on_large_blocks(n, new, exponents, below):
     """Blocks whose values are large and whose weights are 2^-6 to 2^-22 of the others' (in heads of 64; 2^-4 to
     2^-15 in those of 128) and still carry the output."""
@@ -120,6 +127,6 @@ def test_drawn_scales(seed):
     r = random.Random(seed)
     for hd in (64, 128):
         exponents = [r.choice([-20, -10, -4, 0, 2, 9, 17, 30]) for _ in range(r.randint(2, 12))]
-        for n in (r.randint(65, 1200), r.randint(2500, 5000)):
-            check(n, 1, hd, exponents, decode=True, seed=seed, heads=r.choice([1, 2, 5, 8]), below=r.choice([0, 3, 12]),
+        for n, new in ((r.randint(65, 1200), 1), (r.randint(2500, 5000), 1), (r.randint(200, 800), r.randint(2, 150))):
+            check(n, new, hd, exponents, decode=new == 1, seed=seed, heads=r.choice([1, 2, 5, 8]), below=r.choice([0, 3, 12]),
                   spread=r.choice([1.0, 4.0]))
