@@ -583,7 +583,9 @@ size_t cbt_paged_attention_workspace(const cbt_paged_attention_args* a);
  * as 8-bit floats (e4m3: four bits of exponent, three of mantissa, largest 448) with a scale for every
  * block of 64 positions of a kv head, K and V apart: half the bytes of a bf16 cache.  What such a cache
  * holds is off from what was appended by at most 2^-4 of each value, or 2^-10 of the block's scale where
- * that is more.  Tables, slots and lengths are as for bf16 pages (cbt_page_map serves both).
+ * that is more; where the scale has grown since, by at most 2^-4 of the value and 2^-9 of the scale
+ * together.  (Values past 448 * 2^56 and infinities aside.)  Tables, slots and lengths are as for bf16 pages
+ * (cbt_page_map serves both).
  *
  * A scale is a power of two, 2^e with e in [-56, 56]: the smallest that all of the block's values are
  * within 448 times of.  The steps of an 8-bit float are relative, so a finer scale would gain nothing,

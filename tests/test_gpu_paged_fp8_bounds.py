@@ -13,10 +13,12 @@ import numpy as np
 import pytest
 import torch
 
+from continuous_batching_transformer_gb300 import paged
 from tests import fp8_reference as F
 from tests import paged_reference as R
 from tests.gpu_harness import ensure_built
-from tests.test_gpu_paged_fp8 import SCORE, WEIGHT, attend
+from tests.test_gpu_paged_fp8 import SCORE, WEIGHT, attend, dev, i32
+from tests.test_paged_fp8_bounds_host import growing, off_at_most
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +132,26 @@ def test_drawn_scales(seed):
         for n, new in ((r.randint(65, 1200), 1), (r.randint(2500, 5000), 1), (r.randint(200, 800), r.randint(2, 150))):
             check(n, new, hd, exponents, decode=new == 1, seed=seed, heads=r.choice([1, 2, 5, 8]), below=r.choice([0, 3, 12]),
                   spread=r.choice([1.0, 4.0]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_what_a_growing_block_holds(dtype):
+    """Tokens appended one by one, every other one of which raises its block's scale: what is read back is within 2^-4 of
+    each value and 2^-9 of the block's scale."""
+    hd = 64
+    for seed in range(4):
+        x = torch.from_numpy(growing(seed)).to(dtype)
+        n, lay = len(x), F.Layout(1, hd, 64)
+        pool = torch.zeros(lay.page_bytes, dtype=torch.uint8, device=dev())
+        cache = paged.PagedKVFp8(pool, i32([[0]]), i32([n]), page_tokens=64, n_kv_heads=1, head_dim=hd)
+        app, q = paged.RopeAppend(cache, None, n_heads=1), torch.empty(1, hd, dtype=torch.bfloat16, device=dev())
+        qkv = torch.cat([torch.zeros(n, hd, dtype=dtype), x.reshape(n, 2 * hd)], 1).to(dev())
+        for t in range(n):
+            app(0, qkv[t:t + 1], i32([t]), i32([t]), q)
+        out = [torch.empty(n, hd, device=dev()) for _ in range(2)]
+        paged.PageRead(cache)(0, *out, i32([0, n]))
+        cache.check()
+        scales = lay.views(pool.cpu().numpy())[2][0, :, 0, 0]
+        for which in (0, 1):
+            value, held = x[:, which, 0].double().numpy(), out[which].double().cpu().numpy()
+            assert off_at_most(value, held, scales[which]).all()
