@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
   const Layout lay = layout_of(a);
   const int per_row = a.kv.n_kv_heads * lay.groups;
   if (tid == 0) {
-    for (int i = 0; i < 6; ++i) tc::mbar_init(&bars[i], 1);
-    tc::mbar_init(kempty, 1 + 4);  // the MMAs, and every warp has seen that the tile was full
+    // kempty: the MMAs, and every warp has seen that the tile was full
+    for (int i = 0; i < 6; ++i) tc::mbar_init(&bars[i], &bars[i] == kempty ? 1 + 4 : 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tk);

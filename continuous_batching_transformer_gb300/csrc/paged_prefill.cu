@@ -98,10 +98,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
   const int TQ = kRows / G;  // tokens per tile
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2);  // both issuers
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);       // a tile's softmax warps
-    tc::mbar_init(qempty, 2);
+    // empty, qempty: both issuers; p_full: a tile's softmax warps; else one arrival
+    for (uint64_t* b = bars; b < bars + kBars; ++b)
+      tc::mbar_init(b, b == qempty || (b >= empty && b < empty + kStages) ? 2 : b >= p_full && b < p_full + 4 ? 4 : 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tq);

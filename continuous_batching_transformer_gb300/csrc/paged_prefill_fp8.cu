@@ -235,13 +235,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int H = a.n_heads, Hkv = a.kv.n_kv_heads, G = H / Hkv;
   const int TQ = kRows / G;  // tokens per tile
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(&bars[i], 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&qfull[i], 4);            // the warps that split it
-    tc::mbar_init(qempty, 2 + 8);                                       // issuers, softmax warps
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&empty[i], 2 + 4);  // issuers, converting warps
-    for (int i = 0; i < kVSlots; ++i) tc::mbar_init(&v_full[i], 4);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&s_free[i], 4);           // a tile's softmax warps
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&p_full[i], 4);
+    auto init = [](uint64_t* b, int n, int arrivals) {
+      for (int i = 0; i < n; ++i) tc::mbar_init(b + i, arrivals);
+    };
+    init(q_in, 2, 1);
+    init(qfull, 2, 4);             // the warps that split it
+    init(qempty, 1, 2 + 8);        // issuers, softmax warps
+    init(full, kStages, 1);
+    init(empty, kStages, 2 + 4);   // issuers, converting warps
+    init(v_full, kVSlots, 4);
+    init(v_empty, kVSlots, 1);
+    init(s_full, 2, 1);
+    init(s_free, 2, 4);            // a tile's softmax warps
+    init(p_full, 4, 4);
+    init(pv_done, 4, 1);
     *abort_flag = 0;
     tc::mbar_fence_init();
     tc::tma_prefetch_desc(&tq);
