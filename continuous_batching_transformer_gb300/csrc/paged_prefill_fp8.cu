@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(empty, kStages, 2 + 4);   // issuers, converting warps
     init(v_full, kVSlots, 4);
     init(v_empty, kVSlots, 1);
-    init(s_full, 2, 1);
+    init(s_full, 2, 1 + 1);        // the product, and the issuer has stored the step's exponents
     init(s_free, 2, 4);            // a tile's softmax warps
     init(p_full, 4, 4);
     init(pv_done, 4, 1);
@@ -296,9 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, got);
           if (!ok) break;
           tc::tc_fence_after();
-          const int2 exps = tail.exps[st];
           if (elect_one()) {
             if (need) {
+              tail.s_exps[x][n & 1] = tail.exps[st];
+              tc::mbar_arrive(&s_full[x]);
               const uint32_t kd = dk + st * (kKV >> 4);
 #pragma unroll
               for (int e = 0; e < 2 * (HD / 32); ++e) {
@@ -306,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_e4m3(s_tm, tc::rows_desc<128>(dq + q_step<HD>(part, step)),
                              tc::rows_desc<HD>(kd + 2 * step), kIdescS, e > 0 ? 1u : 0u);
               }
-              tail.s_exps[x][n & 1] = exps;
               tc::mma_commit(&s_full[x]);
             }
             tc::mma_commit(&empty[st]);
