@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(kThreads) k_read_fp8(const __grid_constant__ P
   const int t0 = r.t0, from = r.from, count = r.t1 - r.t0;
   const long long p0 = (from / kBlock + nth) * kBlock;
   if (count == 0 || p0 >= (long long)from + count) return;
-  const int begin = max(from, (int)p0), end = min(from + count, (int)p0 + kBlock);  // positions
   const int page = a.kv.page_tokens, pg = (int)p0 / page, o = (int)p0 - pg * page;
   int id = a.table[(size_t)b * a.max_pages + pg];
   if (id < 0 || id >= a.kv.n_pages) {
@@ -104,7 +103,8 @@ __global__ void __launch_bounds__(kThreads) k_read_fp8(const __grid_constant__ P
   uint8_t* out = static_cast<uint8_t*>(v ? a.v_out : a.k_out) +
                  ((t0 - from + p0) * a.out_ld + (long long)g * HD + 8 * part) * kSize;
   const long long step = a.out_ld * kSize;
-  const int lo_p = begin - (int)p0, hi_p = end - (int)p0;  // the block's positions
+  // the block's positions (the last block's end, as one, may be past 32 bits)
+  const int lo_p = max(from - (int)p0, 0), hi_p = min(from + count - (int)p0, kBlock);
   if (!v) {
     const uint2* src = reinterpret_cast<const uint2*>(a.kv.pool + fp8_k(a.kv, id, g, o, 0)) + tid;
     uint2 w[kBlock / kAtOnce];

@@ -155,3 +155,24 @@ def test_what_a_growing_block_holds(dtype):
         for which in (0, 1):
             value, held = x[:, which, 0].double().numpy(), out[which].double().cpu().numpy()
             assert off_at_most(value, held, scales[which]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_read_of_the_last_positions(dtype):
+    """Positions up to 2^31 - 2, the last that 32 bits count with their length: a row whose table names one page over
+    and over."""
+    kv, hd, n = 2, 64, 150
+    lay = F.Layout(kv, hd, 64)
+    pool = np.zeros(lay.page_bytes, np.uint8)
+    r = np.random.default_rng(3)
+    F.append(pool, lay, r.standard_normal((64, kv, hd)), r.standard_normal((64, kv, hd)), list(range(64)))
+    want = [x.transpose(1, 0, 2) for x in F.values(pool, lay, [0], 64)]
+    table = torch.zeros(1, 1 << 25, dtype=torch.int32, device=dev())
+    last = 2 ** 31 - 1
+    cache = paged.PagedKVFp8(torch.from_numpy(pool).to(dev()), table, i32([last]), page_tokens=64, n_kv_heads=kv, head_dim=hd)
+    out = [torch.full((n, kv, hd), 0.7, dtype=dtype, device=dev()) for _ in range(2)]
+    paged.PageRead(cache)(0, *out, i32([0, n]), i32([last - n]))
+    cache.check()
+    slots = [(last - n + j) % 64 for j in range(n)]
+    for got, w in zip(out, want):
+        assert (got.double().cpu().numpy() == w[slots]).all()
