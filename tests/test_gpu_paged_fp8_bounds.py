@@ -17,7 +17,7 @@ from continuous_batching_transformer_gb300 import paged
 from tests import fp8_reference as F
 from tests import paged_reference as R
 from tests.gpu_harness import ensure_built
-from tests.test_gpu_paged_fp8 import SCORE, WEIGHT, attend, dev, i32
+from tests.test_gpu_paged_fp8 import SCORE, WEIGHT, attend, dev, i32, run_append
 from tests.test_paged_fp8_bounds_host import growing, off_at_most
 
 pytestmark = pytest.mark.gpu
@@ -176,3 +176,42 @@ def test_read_of_the_last_positions(dtype):
     slots = [(last - n + j) % 64 for j in range(n)]
     for got, w in zip(out, want):
         assert (got.double().cpu().numpy() == w[slots]).all()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("mode,rot", [("half", 64), ("interleaved", 32), ("half", 22), ("none", 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_q_beside_heads_that_are_not_finite(dtype, mode, rot, norm):
+    """Infinities and NaN in some of q's heads: they stay what the formula makes of them, and everything else is what it
+    is without them."""
+    H, kv, hd, n = 5, 1, 64, 40
+    r = np.random.default_rng(rot)
+    x = torch.from_numpy(r.standard_normal((n, H + 2 * kv, hd))).to(dtype)
+    x[::2, 1, 3] = float("inf")
+    x[::3, 1, 40] = float("-inf")
+    x[::2, 3, 17] = float("nan")
+    pos = [int(p) for p in r.integers(0, 5000, n)]
+    gain = (1 + 0.1 * torch.from_numpy(r.standard_normal(hd))).to(torch.bfloat16)
+    pool = torch.zeros(F.Layout(kv, hd, 64).page_bytes, dtype=torch.uint8, device=dev())
+    cache = paged.PagedKVFp8(pool, None, None, page_tokens=64, n_kv_heads=kv, head_dim=hd)
+    rope = None if mode == "none" else paged.Rope(hd, rot_dim=rot, layout=mode, theta=1e4)
+    q = torch.empty(n, H, hd, dtype=torch.bfloat16, device=dev())
+    paged.RopeAppend(cache, rope, n_heads=H, eps=1e-6)(0, x.reshape(n, -1).to(dev()), i32(pos), i32(list(range(n))), q,
+                                                       gain.to(dev()) if norm else None)
+    cache.check()
+    with np.errstate(invalid="ignore"):
+        want = R.rope_heads(x[:, :H].double().numpy(), gain.double().numpy() if norm else None, 1e-6, np.array(pos),
+                            0 if mode == "none" else rot, mode, R.rope_freqs(rot, 1e4, "none", 1.0, 0)[0], 1.0)
+    got, fine = q.double().cpu().numpy(), np.isfinite(want)
+    assert not fine.all() and fine[:, [0, 2, 4]].all()
+    assert np.array_equal(got[~fine], want[~fine], equal_nan=True)
+    got, want = np.where(fine, got, 0), np.where(fine, want, 0)
+    size = np.abs(want).max(-1, keepdims=True)
+    assert (np.abs(got - want) <= R.BF16_STEP * 1.01 * np.abs(want) + 2.0 ** -18 * size).all()
+
+
+def test_a_zeroed_page_is_gone_on_with():
+    """A block that no append has begun, in a zeroed page, has the smallest scale there is until its first tokens."""
+    for page, start in ((64, 9), (128, 70), (64, 63)):
+        run_append(runs=[list(range(start, start + 40))], hd=64, page=page, norm=False, mode="none", fill=False)
+        run_append(runs=[[start]], hd=128, page=page, fill=False)
