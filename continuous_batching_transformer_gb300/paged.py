@@ -154,7 +154,7 @@ class _Device:
         raw = torch._C._cuda_getCurrentRawStream(self.index)
         if raw not in self.streams:
             self.join(raw)
-        if torch._C._cuda_getDevice() == self.index:  # (torch.cuda.current_device without its checks)
+        if torch.cuda.current_device() == self.index:
             fn(args, raw)
         else:
             with torch.cuda.device(self.index):
