@@ -136,9 +136,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
     // V's buffer is awaited, so that K's stays empty for a wait only.
     const uint64_t pol = tc::policy_evict_first();
     uint32_t n = 0, nk = 0, nv = 0;  // chunks, and tiles of K and of V requested
-    // what is handed over of the next chunk's scales: V's unit (below any scale's: none yet) and its first half's,
-    // and, lane 0 and 1, a half's own
-    int unit = kLowExp - 1, unit0 = 0, moves = 0;
+    // what is handed over of the next chunk's scales: V's unit and its first half's, and, lane 0 and 1, a half's own
+    int unit = 0, unit0 = 0, moves = 0;
     float k_unit = 0.f, v_down = 0.f, ve = 0.f;
     bool ok = true;
     const int P = a.kv.page_tokens;
@@ -146,6 +145,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
     // e's scales
     struct Chunk {
       unsigned halves;
+      bool first;  // of an item: any unit will do, since nothing has been summed
       int k[2], v[2];
       float ks, vs;
     };
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
         }
       }
       if (!have) return c;
+      c.first = i == w.i0;
       // lanes 0 and 1: a half each
       const int k0 = w.seen.chunk(i++) * kSub + kBlock * lane;
       int kat = 0, vat = 0;
@@ -198,8 +199,8 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
       // a half that is not there has the other one's scale
       const int v0 = __shfl_sync(0xffffffffu, e, c.halves == 2), v1 = __shfl_sync(0xffffffffu, e, c.halves != 1);
       const int lo = min(v0, v1), hi = max(v0, v1);
-      moves = hi - lo > kSpread ? kApart : hi > unit || lo < unit - kSpread ? kMoves : 0;
-      if (moves) unit = min(lo + kSpread, hi + 1);
+      moves = hi - lo > kSpread ? kApart : !c.first && (hi > unit || lo < unit - kSpread) ? kMoves : 0;
+      if (moves || c.first) unit = min(lo + kSpread, hi + 1);
       unit0 = unit;
       int off = (lane ? v1 : v0) - unit;
       if (moves == kApart) {
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
     if (nv) wait_landed(vfull, (nv - 1) & 1);
   } else {
     uint32_t n = 0, no = 0;     // chunks done, products with V asked for
-    int unit = kLowExp - 1;     // V's, of the product in tensor memory (below any scale's: none yet)
+    int unit = 0;               // V's, of the product in tensor memory
     bool ok = true;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const float scale2 = a.scale * kLog2e;  // scores in units of log2
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kCompute + 32, (Shape<HD, GT>::kCtas))
               }
               tc::named_bar_sync(1, kCompute);
               take_o();
-              if (moving.value) unit = sc.unit[second];
+              unit = sc.unit[second];
 #pragma unroll
               for (int h = 0; h < GT; ++h) {
                 // (O and l, in units of 2^m, stay in fp32's range: O's elements are below 2^(most - m + 18 + kSlack))

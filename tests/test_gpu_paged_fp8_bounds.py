@@ -215,3 +215,35 @@ def test_a_zeroed_page_is_gone_on_with():
     for page, start in ((64, 9), (128, 70), (64, 63)):
         run_append(runs=[list(range(start, start + 40))], hd=64, page=page, norm=False, mode="none", fill=False)
         run_append(runs=[[start]], hd=128, page=page, fill=False)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("new", [1, 3])
+def test_a_row_does_not_depend_on_the_others(new, hd):
+    """Rows of every scale, enough of them for several a thread block: each has the bits that it has alone."""
+    r = np.random.default_rng(hd + new)
+    rows, kv, H, n = 500, 4, 8, 200
+    pages = -(-n // 64)
+    lay = F.Layout(kv, hd, 64)
+    pool = r.integers(0, 256, rows * pages * lay.page_bytes, dtype=np.uint8)
+    K, V, S = lay.views(pool)
+    for codes in (K, V):
+        codes[...] &= 0xBF  # finite, below 2
+    S[:, 0] = 2.0 ** -2
+    S[:, 1] = 2.0 ** r.integers(-12, 13, (rows * pages, kv, 1))
+    S[::7, 1] = 2.0 ** r.integers(-50, 51, (len(S[::7]), kv, 1))
+    dpool, table = torch.from_numpy(pool).to(dev()), torch.arange(rows * pages, dtype=torch.int32, device=dev()).view(rows, pages)
+    q = torch.randn(rows * new, H, hd, generator=torch.Generator().manual_seed(hd)).bfloat16().to(dev())
+
+    def attend(first, count):
+        cache = paged.PagedKVFp8(dpool, table[first:first + count].contiguous(), i32([n] * count), page_tokens=64, n_kv_heads=kv,
+                                 head_dim=hd)
+        out = torch.empty(count * new, H, hd, device=dev())
+        paged.Attention(cache, n_heads=H, max_kv=n, max_q=new, max_tokens=count * new)(
+            0, q[first * new:(first + count) * new], out, None if new == 1 else i32([new * i for i in range(count + 1)]))
+        cache.check()
+        return out
+    all_rows = attend(0, rows)
+    assert torch.isfinite(all_rows).all()
+    for b in range(0, rows, 9):
+        assert torch.equal(attend(b, 1), all_rows[b * new:(b + 1) * new]), b
