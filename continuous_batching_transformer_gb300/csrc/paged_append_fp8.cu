@@ -81,7 +81,7 @@ CBT_D int exponent_for(float top) {
   return min(max(e, kLowExp), kHighExp);
 }
 
-// sixteen codes times f, each rounded again
+// four codes times f, each rounded again
 CBT_D uint32_t move_codes(uint32_t w, float f) {
   const uint32_t lo = e4m3_to_f16((uint16_t)w), hi = e4m3_to_f16((uint16_t)(w >> 16));
   return pack_e4m3(f16_lo(lo) * f, f16_hi(lo) * f) | (uint32_t)pack_e4m3(f16_lo(hi) * f, f16_hi(hi) * f) << 16;

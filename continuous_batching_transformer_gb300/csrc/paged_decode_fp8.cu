@@ -24,9 +24,10 @@
 // Bound by HBM: 2 head_dim bytes of K and V per position and kv head, while a chunk's instructions hide under
 // them (up to 8 q heads of 128 on a kv head; heads of 64 have half the bytes for as many).  Items, runs and
 // their join are those of paged_split.cuh.  Measured (graph replays, join included): 32 rows of 8192 to 16384
-// positions, 32 / 8 heads of 128, 126.5 us = 6.4 TB/s, 96 % of the measured copy rate; with 64 q heads 133, with
-// heads of 64 87 us (70 %), 64 of them 125 (49 %); 16 rows through a window of 4096 27.8 us (72 %); 8 rows of
-// 512 to 4096 11.5 us; one row of 100 4.6 us.
+// positions, 32 / 8 heads of 128, 125 us = 6.5 TB/s, 97 % of the measured copy rate; with 64 q heads 138, with
+// heads of 64 91 us (67 %), 64 of them 128 (47 %); 16 rows through a window of 4096 27.8 us (72 %); 8 rows of
+// 512 to 4096 11.7 us; one row of 100 4.9 us.  Where every chunk's halves lie apart 32 rows of 12288 take 155 us
+// for 127, where every other chunk's scales lie far from the last one's as long as with one scale.
 #include <type_traits>
 
 #include "fp8_tc.cuh"

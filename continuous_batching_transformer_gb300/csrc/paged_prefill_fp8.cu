@@ -22,11 +22,13 @@
 // P has two, so that its product is never waited for.
 //
 // Neither pipe is full (issue 53 %, tensor 49 % in long units): a step takes what the softmax warps' own chain
-// of waits, loads and exponentials takes, 0.95 us, next to the conversion's instructions; a unit another 3
-// us to write out its rows and begin.  Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 50.7 us
-// (678 TFLOP/s; over bf16 pages 41); four chunks of 500 to 1030 tokens over 3000 to 9000 positions, window
-// 4096, 194 us (957 TFLOP/s; 169.5); 19 rows of 64 tokens over 16000 positions 236 us (1350 TFLOP/s; 224).
-// Tried: the largest score of a step not looked for unless the weights add up to too much (243 us), Q as
+// of waits, loads and exponentials takes, 0.97 us, next to the conversion's instructions; a unit another 3
+// us to write out its rows and begin.  Measured, 32 q and 8 kv heads of 128: four prompts of 1024 tokens 51.7 us
+// (665 TFLOP/s; over bf16 pages 41); four chunks of 500 to 1030 tokens over 3000 to 9000 positions, window
+// 4096, 198 us (936 TFLOP/s; 169.5); 19 rows of 64 tokens over 16000 positions 241 us (1325 TFLOP/s; 224).
+// To look whether a reference is to be lowered is 2 % of that; where references are, at every other step (scales 2^12
+// apart from two steps to the next two), four rows of 512 tokens over 3584 take 151 us for 116.
+// Tried: the largest score of a step not looked for unless the weights add up to too much (243 us for 236), Q as
 // fp16 with K turned into it as well (not built: as much conversion again), a third tile of Q (261 us: two
 // stages fewer).
 #include <type_traits>

@@ -13,10 +13,18 @@ constexpr int kGroup = 8;      // q heads per item
 // other rows).  Longer runs halve the partial outputs and their join; shorter ones spread a few rows
 // over the SMs.  Over bf16 pages, in us: 32 rows of 64 to 128 chunks 244 by fours, 251 by twos; one row of 64
 // chunks 11.3 by fours, 10.4 by twos; 16 rows of 33 chunks 47.0 by twos, 48.3 singly; one row of two chunks
-// 6.4 in one run, which needs no join, against 7.4.  Over 8-bit pages, where a chunk takes half the time and
-// its partial output as long: 32 rows of 64 to 128 chunks 126 by fours, 128 by twos; 16 rows of 33 chunks
-// 28.5 by fours, 29.3 by twos; 64 rows of 4 to 8 chunks 25.4 by twos, 31.6 singly; 256 rows of 1 to 4 chunks
-// 47.7 in one run, 54.0 singly from 4 on; one row of 8 chunks 8.3 by twos, 7.3 singly.
+// 6.4 in one run, which needs no join, against 7.4.
+// Over 8-bit pages a chunk takes half the time and its partial output as long.  Rows alike, 32 q and 8 kv heads of
+// 128, all in one run / singly / by twos / by fours:
+//   chunks   1 row                   8 rows                  32 rows                 128 rows
+//   4        8.9   6.6  7.6  8.7     9.1   7.6  8.0  8.9     10.3  14.4 11.5 10.0    24.4  37.1  32.6  24.3
+//   8        13.2  6.7  7.6  9.9     13.4  9.2  8.7  10.3    15.7  19.7 16.3 14.8    43.9  62.5  54.5  50.6
+//   16       22.2  7.4  7.7  9.9     22.3  13.1 11.0 11.2    26.7  33.3 28.1 26.9    81.8  114   96.9  90.5
+//   32       40.0  8.7  8.4  10.1    40.9  20.0 16.1 14.2    49.2  58.8 50.6 47.8    157   216   184   171
+//   64       75.9  10.9 10.0 10.7    80.2  34.1 29.8 27.2    93.8  106  93.7 87.6
+// No rule on the row alone has the best of every column.  One run of up to four, twos from 5 and fours from 33 on
+// are within 5 % of the best of the four ways in half of 120 such shapes and within 20 % in nine tenths; the
+// furthest behind are a row of four chunks (8.9 for 6.6 singly) and 64 rows of five (22.6 for 14.6 in one run).
 template <class A>
 CBT_HD int chunks_per_run(int n) {
   constexpr RunRule r = decltype(A::kv)::kRuns;

@@ -331,7 +331,9 @@ constexpr int kFewPairs = 20 * kSms, kManyRuns = 8;  // up to, and above which, 
 // chosen was at worst 2 % behind whole (two rows of 700 tokens over 6000: 157 and 155 us).  Bounds above
 // the rows mislead it: one prompt of 512 tokens takes 15 us, 27 with max_kv 8192 and 31 with 131072; and
 // rows of one token over 65536 next to that prompt stay whole, 735 us.  One item for each SM instead:
-// ten rows of 4 over 8192 stay whole, 100 for 77 us.
+// ten rows of 4 over 8192 stay whole, 100 for 77 us.  (All of these over bf16 pages.)  Over 8-bit pages, where
+// a step takes 0.97 us, the same counts chose a cut that was nowhere behind whole in 25 shapes, up to 5.8 times
+// faster (4 tokens over 16000 positions: 31 and 181 us), and at worst 7 % behind the best of nine (the same: 29).
 template <class A>
 int runs_for(const A& a) {
   const int G = a.n_heads / a.kv.n_kv_heads, width = 2 * (kRows / G);  // tokens of a unit
