@@ -58,8 +58,9 @@ constexpr float kSlack = 8.f;
 // by less, so that the unit rarely moves.)
 constexpr int kSpread = 3;
 constexpr float kPart = 16.f;  // of one part of q to the next one's unit
-// ... of a weight: a code leaves a rest of a 16th of itself, or 2^-10; with eleven bits in all a 64th or nothing
-// is left behind the second and third one, but for 2^-10.
+// ... of a weight: a code leaves a rest of a 16th of its power of two, of eleven bits the second one a 32nd of its
+// unit's and the third one nothing, or 2^-10 each.  (Weights up to 2^8: parts of at most 256, 128, 128 and 1/4,
+// whose sum is off by 2^-24 at most.)
 CBT_HD constexpr float part_unit(int k) { return k == 0 ? 16.f : k == 1 ? 32.f : 256.f; }
 
 // part_unit(k) (a - b), of two pairs of fp16
@@ -79,7 +80,7 @@ struct Scales {
     float v_down;  // 2^-ve
   } half[2];
   int unit[2];  // V's, of the chunk; where the halves lie too far apart for one, of either
-  int moves;    // 0: the unit is that of the chunk before; kMoves, or kApart
+  int moves;    // 0: the unit is that of the chunk before, or an item begins with it; kMoves, or kApart
 };
 constexpr int kMoves = 1, kApart = 2;
 

@@ -44,3 +44,18 @@ def test_what_a_growing_block_holds():
             value = x[:, which, 0]
             assert (np.abs(got[0] - value) <= np.maximum(2.0 ** -4 * np.abs(value), 2.0 ** -10 * scales[which])).all()
     assert worst > 1.2  # one rounding's bound does not hold for a block that has grown
+
+
+def test_a_weight_as_four_codes():
+    """Every fp16 up to 2^8 as the sum of four codes in units of 1, 1 / 16, 1 / 512 and 1 / 131072: each part, formed
+    from the last one's rest in fp16, is exact in fp16 and fits a code, and the sum is off by 2^-24 at most."""
+    x = np.arange(0x7C00, dtype=np.uint16).view(np.float16).astype(np.float64)
+    x = x[x <= 256]
+    y, unit, total = x, 1.0, np.zeros_like(x)
+    for step in (16, 32, 256, 1):
+        assert (y.astype(np.float16).astype(np.float64) == y).all() and np.abs(y).max() <= F.TOP
+        code = F.VALUES[F.encode(y)]
+        total += code * unit
+        y, unit = (y - code) * step, unit / step
+    assert np.abs(total - x).max() <= 2.0 ** -24
+    assert np.abs(total - x)[x >= 2.0 ** -6].max() == 0
